@@ -568,6 +568,178 @@ int ssd_state_passing_validate(int64_t nchunks, int64_t batch, int64_t nheads, i
 int ssd_chunk_scan(const ssd_scan_args_t *args, int64_t chunk_size, const float *carried, void *hip_stream);
 int ssd_chunk_scan_validate(const ssd_scan_args_t *args, int64_t chunk_size, const float *carried);
 
+/* ---------------------------------------------------------------------------
+ * Packed tokens: a Mamba-2 mixer's short convolution, scan and step, for
+ * prompts of several lengths in one call, for single tokens, and in training.
+ *
+ * The tokens of nseq sequences lie one after another, (total, ...), and
+ * cu_seqlens (nseq + 1) int32 on the device holds each sequence's first
+ * token, cu_seqlens[nseq] = total; a sequence may be empty.  Edges out of
+ * order or outside [0, total] give unspecified results, never an access
+ * outside the tensors.  Rows of equal length are the case cu_seqlens[s] = s l.
+ *
+ * A *_stride is the number of elements from a token to the next; what a token
+ * holds is dense.  x, B and C may so be parts of one row, as the input
+ * projection and the convolution leave them.
+ *
+ * Caches hold one entry per request.  Sequence s uses entry slots[s] (s itself
+ * when slots is NULL); an entry outside the cache is neither read nor
+ * written, and the sequence starts from nothing.  Two sequences of a call must
+ * not share an entry.  cache_seqlens[s] (int32, device) is the number of
+ * tokens that the request has seen before the call: where it is 0, or
+ * cache_seqlens is NULL, the entry is not read, so a new request needs no
+ * clearing.  The caller advances cache_seqlens.
+ *   conv_state (state_slots, channels, state_len) io: the last inputs as a
+ *     ring, position p (from 0) at p % state_len; positions before 0 are zero;
+ *   ssm_state (state_slots, nheads, headdim, dstate) fp32.
+ * ------------------------------------------------------------------------- */
+
+/* Arguments of causal_conv1d_varlen_fwd and causal_conv1d_varlen_bwd. */
+typedef struct causal_conv1d_varlen_args {
+  int64_t total, nseq, channels;
+  int32_t width, io_dtype, act;                 /* width: SSM_CONV_WIDTH */
+  const void *x; int64_t x_stride;              /* (total, channels) io */
+  const float *weight;                          /* (channels, width) fp32 */
+  const float *bias;                            /* (channels) fp32 or NULL */
+  const int32_t *cu_seqlens;                    /* (nseq + 1) */
+  /* forward */
+  void *out; int64_t out_stride;                /* (total, channels) io */
+  void *conv_state;                             /* ring cache or NULL */
+  int64_t state_slots, state_len;               /* width <= state_len <= SSM_MAX_CONV_STATE */
+  const int32_t *cache_seqlens, *slots;         /* (nseq) or NULL */
+  /* backward */
+  const void *dout; int64_t dout_stride;        /* (total, channels) io */
+  void *dx; int64_t dx_stride;                  /* (total, channels) io */
+  float *dweight;                               /* (channels, width) fp32 */
+  float *dbias;                                 /* (channels) fp32, required iff bias */
+  void *workspace; size_t workspace_bytes;      /* causal_conv1d_varlen_bwd_workspace_size */
+} causal_conv1d_varlen_args_t;
+
+/* The causal depthwise conv of causal_conv1d_fwd over packed tokens:
+ *   out[t,c] = round_io(act(bias[c] + sum_k weight[c,k] x[t-(width-1)+k,c]))
+ * where the inputs before a sequence's first token come from its ring (zero
+ * without one).  Afterwards the ring holds the sequence's last inputs.  `out`
+ * and conv_state must not overlap x. */
+int causal_conv1d_varlen_fwd(const causal_conv1d_varlen_args_t *args, void *hip_stream);
+int causal_conv1d_varlen_fwd_validate(const causal_conv1d_varlen_args_t *args);
+
+/* Its gradient, for sequences that start from nothing (no cache is read):
+ * with da = dout act'(pre),
+ *   dx[t,c] = sum_k weight[c,k] da[t+(width-1)-k,c]   (inside the sequence)
+ *   dweight[c,k] = sum_t da[t,c] x[t-(width-1)+k,c],  dbias[c] = sum_t da[t,c]
+ * summed in a fixed order (bit-for-bit repeatable). */
+int causal_conv1d_varlen_bwd(const causal_conv1d_varlen_args_t *args, void *hip_stream);
+int causal_conv1d_varlen_bwd_validate(const causal_conv1d_varlen_args_t *args);
+int causal_conv1d_varlen_bwd_workspace_size(const causal_conv1d_varlen_args_t *args, size_t *bytes);
+
+/* Arguments of ssd_varlen_fwd.  x, B, C, z and out must be 16-byte aligned,
+ * their strides multiples of 8. */
+typedef struct ssd_varlen_args {
+  int64_t total, nseq, max_seqlen;              /* max_seqlen: at least the longest sequence */
+  int64_t nheads, headdim, dstate, ngroups;
+  int32_t io_dtype;                             /* SSM_BF16 */
+  const void *x; int64_t x_stride;              /* (total, h, p) io */
+  const void *dt; int64_t dt_stride;            /* (total, h) io */
+  const float *A;                               /* (h) fp32 */
+  const void *B; int64_t B_stride;              /* (total, g, n) io */
+  const void *C; int64_t C_stride;              /* (total, g, n) io */
+  const float *D; int32_t D_per_channel;        /* (h) or (h,p) fp32, or NULL */
+  const void *z; int64_t z_stride;              /* (total, h, p) io or NULL (forward only) */
+  const float *dt_bias;                         /* (h) fp32 or NULL */
+  int32_t dt_softplus, dt_limit;                /* as ssd_scan_args_t */
+  float dt_min, dt_max;
+  const int32_t *cu_seqlens;                    /* (nseq + 1) */
+  void *out; int64_t out_stride;                /* (total, h, p) io */
+  float *ssm_state; int64_t state_slots;        /* cache or NULL: read and written */
+  const int32_t *cache_seqlens, *slots;         /* (nseq) or NULL */
+  /* The state entering every chunk of SSD_CHUNK tokens, in 8 bits, for
+   * ssd_varlen_bwd (NULL: not kept).  Chunk c of sequence s is entry
+   * floor(cu_seqlens[s] / SSD_CHUNK) + s + c of ssd_checkpoint_slots entries;
+   * entries of no chunk are not written.  A state is code * scale with one
+   * scale per channel, the smallest power of two for which the channel's
+   * states are within +-127 scale (at least 2^-100; NaN where one of them is
+   * not finite). */
+  int8_t *checkpoints;                          /* (entries, h, p, n) */
+  float *checkpoint_scales;                     /* (entries, h, p) */
+  void *workspace; size_t workspace_bytes;      /* ssd_varlen_fwd_workspace_size */
+  int32_t seq_segments;                         /* as ssd_scan_args_t */
+} ssd_varlen_args_t;
+
+/* ssd_scan_fwd over packed tokens: the same recurrence for every sequence,
+ * from the cached state (or zero) to the cached state. */
+int ssd_varlen_fwd(const ssd_varlen_args_t *args, void *hip_stream);
+int ssd_varlen_fwd_validate(const ssd_varlen_args_t *args);
+int ssd_varlen_fwd_workspace_size(const ssd_varlen_args_t *args, size_t *bytes);
+
+/* Checkpoint entries of packed tokens: floor(total / SSD_CHUNK) + nseq. */
+int64_t ssd_checkpoint_slots(int64_t total, int64_t nseq);
+
+/* Arguments of ssd_varlen_bwd: the forward's (fwd.z must be NULL: with the
+ * gate outside the scan, as where a gated norm follows, its gradient belongs
+ * there; fwd.out, ssm_state, cache_seqlens, slots and workspace are ignored;
+ * fwd.checkpoints and scales are those that the forward wrote), and the
+ * gradients, caller-allocated and fully overwritten. */
+typedef struct ssd_varlen_bwd_args {
+  ssd_varlen_args_t fwd;
+  const void *dout; int64_t dout_stride;        /* (total, h, p) io */
+  const float *dfinal_states;                   /* (nseq, h, p, n) fp32 or NULL (zero) */
+  void *dx; int64_t dx_stride;                  /* (total, h, p) io */
+  void *ddt; int64_t ddt_stride;                /* (total, h) io */
+  void *dB; int64_t dB_stride;                  /* (total, g, n) io */
+  void *dC; int64_t dC_stride;                  /* (total, g, n) io */
+  float *dA;                                    /* (h) fp32 */
+  float *dD;                                    /* as D, required iff D */
+  float *ddt_bias;                              /* (h) fp32, required iff dt_bias */
+  float *dinitial_states;                       /* (nseq, h, p, n) fp32 or NULL */
+  void *workspace; size_t workspace_bytes;      /* ssd_varlen_bwd_workspace_size */
+} ssd_varlen_bwd_args_t;
+
+/* Gradients of ssd_varlen_fwd.  Every chunk is re-evaluated from its 8-bit
+ * state; the adjoint of the state goes backwards in 32 bits.  With dt' the
+ * step, cs its running sum times A inside the chunk, H the chunk's entering
+ * state, dH the adjoint of its leaving state, g = dout, and for i >= j
+ * L_ij = exp(cs_i - cs_j), S_ij = C_i . B_j, M_ij = g_i . x_j:
+ *   dx_j  = dt'_j (sum_i S_ij L_ij g_i + exp(cs_end - cs_j) dH B_j) + D g_j
+ *   dB_j  = dt'_j (sum_i M_ij L_ij C_i + exp(cs_end - cs_j) dH^T x_j)  (summed over the group's heads)
+ *   dC_i  = sum_j M_ij L_ij dt'_j B_j + exp(cs_i) H^T g_i              (summed over the group's heads)
+ *   dH   <- exp(cs_end) dH + sum_i exp(cs_i) g_i C_i^T
+ * and ddt, dA through the weights and every decay.  Where dt_limit clamps a
+ * step its gradient is zero.  Sums are taken in a fixed order (bit-for-bit
+ * repeatable). */
+int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *args, void *hip_stream);
+int ssd_varlen_bwd_validate(const ssd_varlen_bwd_args_t *args);
+int ssd_varlen_bwd_workspace_size(const ssd_varlen_bwd_args_t *args, size_t *bytes);
+
+/* Arguments of conv1d_ssd_update. */
+typedef struct conv1d_ssd_update_args {
+  int64_t batch, nheads, headdim, dstate, ngroups;
+  int32_t io_dtype, act, width;                 /* width: SSM_CONV_WIDTH */
+  const void *xBC; int64_t xBC_stride;          /* (batch, h p + 2 g n) io: x | B | C before the conv */
+  const void *dt; int64_t dt_stride;            /* (batch, h) io */
+  const float *A;                               /* (h) fp32 */
+  const float *conv_weight;                     /* (h p + 2 g n, width) fp32 */
+  const float *conv_bias;                       /* (h p + 2 g n) fp32 or NULL */
+  const float *D; int32_t D_per_channel;        /* (h) or (h,p) fp32, or NULL */
+  const void *z; int64_t z_stride;              /* (batch, h p) io or NULL */
+  const float *dt_bias;                         /* (h) fp32 or NULL */
+  int32_t dt_softplus, dt_limit;
+  float dt_min, dt_max;
+  void *conv_state; int64_t state_len;          /* ring cache, width <= state_len <= SSM_MAX_CONV_STATE */
+  float *ssm_state;                             /* cache */
+  int64_t state_slots;                          /* entries of both caches */
+  const int32_t *cache_seqlens;                 /* (batch) or NULL (every request is new) */
+  const int32_t *slots;                         /* (batch) or NULL */
+  void *out; int64_t out_stride;                /* (batch, h p) io */
+} conv1d_ssd_update_args_t;
+
+/* One token of every request, in one launch: u = act(conv(xBC)) against the
+ * ring (kept in fp32, not rounded to io), then ssd_varlen_fwd's recurrence for
+ * that token against the cached state, both caches updated.  An entry outside
+ * the cache (a padding row) gives the output of a new request and writes
+ * nothing.  headdim SSD_HEADDIM, dstate 32, 64 or 128; io fp32, bf16 or fp16. */
+int conv1d_ssd_update(const conv1d_ssd_update_args_t *args, void *hip_stream);
+int conv1d_ssd_update_validate(const conv1d_ssd_update_args_t *args);
+
 /* Static text for a status code. */
 const char *ssm_status_str(int status);
 

@@ -9,8 +9,14 @@ from ._lib import SsmError, EXPORTS  # noqa: F401
 from .binding import (  # noqa: F401
     causal_conv1d_fn,
     causal_conv1d_fwd,
+    causal_conv1d_varlen_bwd,
+    causal_conv1d_varlen_fwd,
+    conv1d_ssd_update,
     conv1d_selective_scan_fn,
     selective_scan_fn,
+    ssd_checkpoint_slots,
+    ssd_varlen_bwd,
+    ssd_varlen_fwd,
     ssm_scan_fwd,
     ssm_scan_fwd_complex,
 )

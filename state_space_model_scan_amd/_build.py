@@ -41,6 +41,10 @@ SOURCES = [
     ("scan_complex.hip", True),
     ("decode.hip", True),
     ("ssd.hip", True),
+    ("ssd_varlen.hip", True),
+    ("ssd_varlen_bwd.hip", True),
+    ("conv_varlen.hip", True),
+    ("step.hip", True),
     ("bwd.hip", True),
     ("bwd_complex.hip", True),
     ("validate.cpp", False),

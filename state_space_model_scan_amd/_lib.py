@@ -31,6 +31,11 @@ EXPORTS = (
     "ssd_chunk_scan", "ssd_chunk_scan_validate",
     "ssm_scan_bwd", "ssm_scan_bwd_validate", "ssm_scan_bwd_workspace_size",
     "ssm_scan_bwd_complex", "ssm_scan_bwd_complex_validate", "ssm_scan_bwd_complex_workspace_size",
+    "causal_conv1d_varlen_fwd", "causal_conv1d_varlen_fwd_validate",
+    "causal_conv1d_varlen_bwd", "causal_conv1d_varlen_bwd_validate", "causal_conv1d_varlen_bwd_workspace_size",
+    "ssd_varlen_fwd", "ssd_varlen_fwd_validate", "ssd_varlen_fwd_workspace_size", "ssd_checkpoint_slots",
+    "ssd_varlen_bwd", "ssd_varlen_bwd_validate", "ssd_varlen_bwd_workspace_size",
+    "conv1d_ssd_update", "conv1d_ssd_update_validate",
     "ssm_status_str", "ssm_last_hip_error", "ssm_abi_version",
 )
 
@@ -122,6 +127,48 @@ class SsdArgs(ctypes.Structure):
     ]
 
 
+def _fields(spec: str):
+    """Structure fields from "type name" pairs: p pointer, i int32, q int64,
+    f float, z size_t."""
+    kind = {"p": _vp, "i": ctypes.c_int32, "q": ctypes.c_int64, "f": ctypes.c_float, "z": ctypes.c_size_t}
+    words = spec.split()
+    return [(name, kind[k]) for k, name in zip(words[::2], words[1::2])]
+
+
+class ConvVarlenArgs(ctypes.Structure):
+    """Mirror of causal_conv1d_varlen_args_t."""
+    _fields_ = _fields("""
+        q total q nseq q channels i width i io_dtype i act p x q x_stride p weight p bias p cu_seqlens
+        p out q out_stride p conv_state q state_slots q state_len p cache_seqlens p slots
+        p dout q dout_stride p dx q dx_stride p dweight p dbias p workspace z workspace_bytes""")
+
+
+class SsdVarlenArgs(ctypes.Structure):
+    """Mirror of ssd_varlen_args_t."""
+    _fields_ = _fields("""
+        q total q nseq q max_seqlen q nheads q headdim q dstate q ngroups i io_dtype
+        p x q x_stride p dt q dt_stride p A p B q B_stride p C q C_stride p D i D_per_channel
+        p z q z_stride p dt_bias i dt_softplus i dt_limit f dt_min f dt_max p cu_seqlens
+        p out q out_stride p ssm_state q state_slots p cache_seqlens p slots
+        p checkpoints p checkpoint_scales p workspace z workspace_bytes i seq_segments""")
+
+
+class SsdVarlenBwdArgs(ctypes.Structure):
+    """Mirror of ssd_varlen_bwd_args_t."""
+    _fields_ = [("fwd", SsdVarlenArgs)] + _fields("""
+        p dout q dout_stride p dfinal_states p dx q dx_stride p ddt q ddt_stride p dB q dB_stride
+        p dC q dC_stride p dA p dD p ddt_bias p dinitial_states p workspace z workspace_bytes""")
+
+
+class ConvSsdUpdateArgs(ctypes.Structure):
+    """Mirror of conv1d_ssd_update_args_t."""
+    _fields_ = _fields("""
+        q batch q nheads q headdim q dstate q ngroups i io_dtype i act i width p xBC q xBC_stride
+        p dt q dt_stride p A p conv_weight p conv_bias p D i D_per_channel p z q z_stride p dt_bias
+        i dt_softplus i dt_limit f dt_min f dt_max p conv_state q state_len p ssm_state q state_slots
+        p cache_seqlens p slots p out q out_stride""")
+
+
 class SsmError(ValueError):
     """A non-zero status from libssmscan."""
 
@@ -206,6 +253,18 @@ def lib() -> ctypes.CDLL:
         L.ssm_scan_bwd_complex_validate.restype = ctypes.c_int
         L.ssm_scan_bwd_complex_workspace_size.argtypes = [ctypes.POINTER(BwdArgs), ctypes.POINTER(ctypes.c_size_t)]
         L.ssm_scan_bwd_complex_workspace_size.restype = ctypes.c_int
+        for name, args in (("causal_conv1d_varlen_fwd", ConvVarlenArgs), ("causal_conv1d_varlen_bwd", ConvVarlenArgs),
+                           ("ssd_varlen_fwd", SsdVarlenArgs), ("ssd_varlen_bwd", SsdVarlenBwdArgs),
+                           ("conv1d_ssd_update", ConvSsdUpdateArgs)):
+            getattr(L, name).argtypes = [ctypes.POINTER(args), _vp]
+            getattr(L, name).restype = ctypes.c_int
+            getattr(L, name + "_validate").argtypes = [ctypes.POINTER(args)]
+            getattr(L, name + "_validate").restype = ctypes.c_int
+            if name + "_workspace_size" in EXPORTS:
+                getattr(L, name + "_workspace_size").argtypes = [ctypes.POINTER(args), ctypes.POINTER(ctypes.c_size_t)]
+                getattr(L, name + "_workspace_size").restype = ctypes.c_int
+        L.ssd_checkpoint_slots.argtypes = [i64, i64]
+        L.ssd_checkpoint_slots.restype = i64
         L.ssm_status_str.argtypes = [ctypes.c_int]
         L.ssm_status_str.restype = ctypes.c_char_p
         L.ssm_last_hip_error.argtypes = []

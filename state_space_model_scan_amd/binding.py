@@ -932,3 +932,351 @@ def ssd_scan_workspace_size(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
     need = ctypes.c_size_t(0)
     check(_lib.lib().ssd_scan_workspace_size(ctypes.byref(a), ctypes.byref(need)))
     return need.value
+
+
+# ---------------------------------------------------------------------------
+# Packed tokens: a Mamba-2 mixer's conv, scan and step
+# ---------------------------------------------------------------------------
+
+def _tokens(t: Optional[torch.Tensor], vec: int = 0) -> Optional[torch.Tensor]:
+    """t as the library takes a packed tensor: whatever a token holds dense,
+    any stride from token to token; with ``vec``, the first element 16-byte
+    aligned and the stride a multiple of ``vec`` elements.  A tensor that is
+    not so is copied."""
+    if t is None:
+        return None
+    want, ok = 1, t.shape[0] <= 1 or t.stride(0) >= 1
+    for d in range(t.dim() - 1, 0, -1):
+        ok = ok and (t.shape[d] == 1 or t.stride(d) == want)
+        want *= t.shape[d]
+    ok = ok and (t.shape[0] <= 1 or t.stride(0) >= want)
+    if ok and vec:
+        ok = t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or t.stride(0) % vec == 0)
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    """Elements from a token to the next."""
+    n = 1
+    for d in t.shape[1:]:
+        n *= d
+    return t.stride(0) if t.shape[0] > 1 else n
+
+
+def _tokens_out(t: Optional[torch.Tensor], name: str, shape, dtype, dev: torch.device, vec: int = 0) -> torch.Tensor:
+    """An output given by the caller (checked) or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _spec(t, name, shape, dtype, dev)
+    if dev.type == "cuda" and _tokens(t, vec) is not t:
+        raise ValueError(f"{name} is written in place: what a token holds must be dense"
+                         + (f", its start 16-byte aligned and its token stride a multiple of {vec}" if vec else ""))
+    return t
+
+
+def _int32(t: Optional[torch.Tensor], name: str, count: int, dev: torch.device) -> Optional[torch.Tensor]:
+    _spec(t, name, (count,), torch.int32, dev)
+    return _dense(t)
+
+
+def _cu_spec(cu: torch.Tensor, dev: torch.device) -> int:
+    """Checks cu_seqlens and returns the number of sequences."""
+    if cu.dim() != 1 or cu.shape[0] < 2:
+        raise ValueError(f"cu_seqlens must have shape (nseq + 1,) with nseq >= 1, got {tuple(cu.shape)}")
+    _int32(cu, "cu_seqlens", cu.shape[0], dev)
+    return cu.shape[0] - 1
+
+
+def _cache_spec(t: Optional[torch.Tensor], name: str, tail, dtype, dev: torch.device) -> None:
+    if t is None:
+        return
+    if t.dim() != len(tail) + 1:
+        raise ValueError(f"{name} must have shape (entries,) + {tuple(tail)}, got {tuple(t.shape)}")
+    _out_spec(t, name, (t.shape[0],) + tuple(tail), dtype, dev)
+
+
+def _limit(a, dt_limit) -> None:
+    if dt_limit is not None:
+        a.dt_limit, a.dt_min, a.dt_max = 1, float(dt_limit[0]), float(dt_limit[1])
+
+
+def _workspace(size_fn, a, given: Optional[torch.Tensor], dev: torch.device) -> Optional[torch.Tensor]:
+    """The caller's scratch, or as much as the call needs; set in a."""
+    ws = given
+    if ws is None:
+        need = ctypes.c_size_t(0)
+        check(size_fn(ctypes.byref(a), ctypes.byref(need)))
+        if need.value:
+            ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    if ws is not None:
+        _workspace_spec(ws, dev)
+        a.workspace, a.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
+    return ws
+
+
+def _conv_varlen_args(x, weight, cu_seqlens, bias, activation):
+    io = _io_of(x, "x", 2)
+    total, channels = x.shape
+    weight, bias, dev = _dense(weight), _dense(bias), x.device
+    _conv_params_spec(weight, bias, channels, dev)
+    nseq = _cu_spec(cu_seqlens, dev)
+    x, cu_seqlens = _tokens(x), _dense(cu_seqlens)
+    a = _lib.ConvVarlenArgs()
+    a.total, a.nseq, a.channels = total, nseq, channels
+    a.width, a.io_dtype, a.act = weight.shape[1], io, _act_code(activation)
+    a.x, a.x_stride, a.weight, a.bias, a.cu_seqlens = _ptr(x), _token_stride(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens)
+    return a, (x, weight, bias, cu_seqlens)
+
+
+def causal_conv1d_varlen_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor,
+                             bias: Optional[torch.Tensor] = None, activation=None,
+                             conv_state: Optional[torch.Tensor] = None,
+                             cache_seqlens: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal conv over packed tokens; returns ``out`` (total, channels).
+
+    x: (total, channels), any token stride; weight: (channels, 4) float32;
+    cu_seqlens: (nseq + 1,) int32.  ``conv_state`` (entries, channels,
+    state_len >= 4) in x's dtype is the requests' ring cache: a sequence
+    continues from entry ``slots[s]`` (s without ``slots``; an entry outside
+    the cache is skipped) if ``cache_seqlens[s]`` > 0 tokens went before it,
+    and leaves its last inputs there."""
+    a, keep = _conv_varlen_args(x, weight, cu_seqlens, bias, activation)
+    dev, nseq = x.device, a.nseq
+    cache_seqlens, slots = _int32(cache_seqlens, "cache_seqlens", nseq, dev), _int32(slots, "slots", nseq, dev)
+    if conv_state is not None:
+        _cache_spec(conv_state, "conv_state", (x.shape[1], conv_state.shape[-1]), x.dtype, dev)
+        a.conv_state, a.state_slots, a.state_len = _ptr(conv_state), conv_state.shape[0], conv_state.shape[2]
+    out = _tokens_out(out, "out", x.shape, x.dtype, dev)
+    _on_gpu(dev)
+    a.out, a.out_stride = _ptr(out), _token_stride(out)
+    a.cache_seqlens, a.slots = _ptr(cache_seqlens), _ptr(slots)
+    check(_lib.lib().causal_conv1d_varlen_fwd(ctypes.byref(a), _stream(dev, stream)))
+    return out
+
+
+def causal_conv1d_varlen_bwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor, dout: torch.Tensor,
+                             bias: Optional[torch.Tensor] = None, activation=None,
+                             dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                             stream=None) -> dict:
+    """Gradient of causal_conv1d_varlen_fwd for sequences that start from
+    nothing: dx (x's dtype; written into ``dx`` when given), dweight and dbias
+    (float32)."""
+    a, keep = _conv_varlen_args(x, weight, cu_seqlens, bias, activation)
+    dev, f32 = x.device, torch.float32
+    _spec(dout, "dout", x.shape, x.dtype, dev)
+    dout = _tokens(dout)
+    dx = _tokens_out(dx, "dx", x.shape, x.dtype, dev)
+    if workspace is not None:
+        _workspace_spec(workspace, dev)
+    _on_gpu(dev)
+    dweight = torch.empty(weight.shape, dtype=f32, device=dev)
+    dbias = None if bias is None else torch.empty(bias.shape, dtype=f32, device=dev)
+    a.dout, a.dout_stride, a.dx, a.dx_stride = _ptr(dout), _token_stride(dout), _ptr(dx), _token_stride(dx)
+    a.dweight, a.dbias = _ptr(dweight), _ptr(dbias)
+    L = _lib.lib()
+    ws = _workspace(L.causal_conv1d_varlen_bwd_workspace_size, a, workspace, dev)
+    check(L.causal_conv1d_varlen_bwd(ctypes.byref(a), _stream(dev, stream)))
+    return {"dx": dx, "dweight": dweight, "dbias": dbias}
+
+
+def ssd_checkpoint_slots(total: int, nseq: int) -> int:
+    """Checkpoint entries of ``total`` packed tokens in ``nseq`` sequences."""
+    return total // _lib.SSD_CHUNK + nseq
+
+
+def _ssd_varlen_args(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_softplus, dt_limit, checkpoints,
+                     seq_segments):
+    """ssd_varlen_args_t without outputs and caches; returns (args, tensors
+    kept alive until the call)."""
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"the packed scan takes bfloat16 io, got {x.dtype}")
+    if x.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be (total, nheads, headdim) and B (total, ngroups, dstate)")
+    total, nheads, headdim = x.shape
+    ngroups, dstate = B.shape[1], B.shape[2]
+    dev, f32 = x.device, torch.float32
+    _spec(z, "z", x.shape, x.dtype, dev)
+    _spec(dt, "dt", (total, nheads), x.dtype, dev)
+    _spec(B, "B", (total, ngroups, dstate), x.dtype, dev)
+    _spec(C, "C", (total, ngroups, dstate), x.dtype, dev)
+    _spec(A, "A", (nheads,), f32, dev)
+    _spec(dt_bias, "dt_bias", (nheads,), f32, dev)
+    if D is not None:
+        _spec(D, "D", (nheads,) if D.dim() == 1 else (nheads, headdim), f32, dev)
+    nseq = _cu_spec(cu_seqlens, dev)
+    if not 0 <= int(max_seqlen) <= total:
+        raise ValueError(f"max_seqlen must be the longest sequence's length, at most {total}, got {max_seqlen}")
+    if checkpoints is not None:
+        rows = (ssd_checkpoint_slots(total, nseq), nheads, headdim)
+        _out_spec(checkpoints[0], "checkpoints[0]", rows + (dstate,), torch.int8, dev)
+        _out_spec(checkpoints[1], "checkpoints[1]", rows, f32, dev)
+    a = _lib.SsdVarlenArgs()
+    x, B, C, z, dt = _tokens(x, 8), _tokens(B, 8), _tokens(C, 8), _tokens(z, 8), _tokens(dt)
+    A, D, dt_bias, cu_seqlens = _dense(A), _dense(D), _dense(dt_bias), _dense(cu_seqlens)
+    a.total, a.nseq, a.max_seqlen = total, nseq, int(max_seqlen)
+    a.nheads, a.headdim, a.dstate, a.ngroups, a.io_dtype = nheads, headdim, dstate, ngroups, _lib.SSM_BF16
+    a.x, a.x_stride, a.dt, a.dt_stride = _ptr(x), _token_stride(x), _ptr(dt), _token_stride(dt)
+    a.A, a.B, a.B_stride, a.C, a.C_stride = _ptr(A), _ptr(B), _token_stride(B), _ptr(C), _token_stride(C)
+    a.D, a.D_per_channel = _ptr(D), int(D is not None and D.dim() == 2)
+    if z is not None:
+        a.z, a.z_stride = _ptr(z), _token_stride(z)
+    a.dt_bias, a.dt_softplus = _ptr(dt_bias), int(bool(dt_softplus))
+    _limit(a, dt_limit)
+    a.cu_seqlens, a.seq_segments = _ptr(cu_seqlens), int(seq_segments)
+    if checkpoints is not None:
+        a.checkpoints, a.checkpoint_scales = _ptr(checkpoints[0]), _ptr(checkpoints[1])
+    return a, (x, dt, A, B, C, D, z, dt_bias, cu_seqlens)
+
+
+def ssd_varlen_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                   cu_seqlens: torch.Tensor, max_seqlen: int, D: Optional[torch.Tensor] = None,
+                   z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = False,
+                   dt_limit: Optional[Tuple[float, float]] = None, ssm_state: Optional[torch.Tensor] = None,
+                   cache_seqlens: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                   checkpoints: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   seq_segments: int = 0, stream=None) -> torch.Tensor:
+    """Mamba-2 chunked scan of packed tokens; returns ``out`` (total, nheads,
+    headdim).
+
+    x, z: (total, nheads, 64) bf16; dt: (total, nheads) bf16; B, C: (total,
+    ngroups, dstate) bf16, all with any token stride (x, B and C may be parts of
+    the conv's output rows); A, dt_bias: (nheads,) float32; D: (nheads,) or
+    (nheads, headdim) float32; cu_seqlens: (nseq + 1,) int32; ``max_seqlen``:
+    the longest sequence.  ``ssm_state`` (entries, nheads, headdim, dstate)
+    float32 is the requests' cache, read where ``cache_seqlens[s]`` > 0 and
+    written, at entry ``slots[s]``.  ``checkpoints``: (int8 (entries, nheads,
+    headdim, dstate), float32 (entries, nheads, headdim)) with
+    ``ssd_checkpoint_slots(total, nseq)`` entries receives every chunk's
+    entering state in 8 bits for ``ssd_varlen_bwd``."""
+    a, keep = _ssd_varlen_args(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_softplus, dt_limit,
+                               checkpoints, seq_segments)
+    dev, nseq = x.device, a.nseq
+    _cache_spec(ssm_state, "ssm_state", (a.nheads, a.headdim, a.dstate), torch.float32, dev)
+    cache_seqlens, slots = _int32(cache_seqlens, "cache_seqlens", nseq, dev), _int32(slots, "slots", nseq, dev)
+    out = _tokens_out(out, "out", x.shape, x.dtype, dev, 8)
+    if workspace is not None:
+        _workspace_spec(workspace, dev)
+    _on_gpu(dev)
+    a.out, a.out_stride = _ptr(out), _token_stride(out)
+    if ssm_state is not None:
+        a.ssm_state, a.state_slots = _ptr(ssm_state), ssm_state.shape[0]
+    a.cache_seqlens, a.slots = _ptr(cache_seqlens), _ptr(slots)
+    L = _lib.lib()
+    ws = _workspace(L.ssd_varlen_fwd_workspace_size, a, workspace, dev)
+    check(L.ssd_varlen_fwd(ctypes.byref(a), _stream(dev, stream)))
+    return out
+
+
+def ssd_varlen_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+                   cu_seqlens: torch.Tensor, max_seqlen: int, dout: torch.Tensor,
+                   checkpoints: Tuple[torch.Tensor, torch.Tensor], D: Optional[torch.Tensor] = None,
+                   dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = False,
+                   dt_limit: Optional[Tuple[float, float]] = None, dfinal_states: Optional[torch.Tensor] = None,
+                   want_dinitial_states: bool = False, dx: Optional[torch.Tensor] = None,
+                   dB: Optional[torch.Tensor] = None, dC: Optional[torch.Tensor] = None,
+                   ddt: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   seq_segments: int = 0, stream=None) -> dict:
+    """Gradients of ssd_varlen_fwd (without z) in a dict.
+
+    ``dout``: (total, nheads, headdim) bf16; ``checkpoints``: what the forward
+    wrote.  dx, ddt, dB and dC come in bf16 (into the tensors given, which may
+    be parts of one row, or new ones), dA, dD and ddt_bias in float32.
+    ``dfinal_states`` (nseq, nheads, headdim, dstate) float32 is the gradient
+    of the sequences' last states; with ``want_dinitial_states`` that of their
+    first ones is returned."""
+    if checkpoints is None:
+        raise ValueError("the backward needs the checkpoints that the forward wrote")
+    a = _lib.SsdVarlenBwdArgs()
+    a.fwd, keep = _ssd_varlen_args(x, dt, A, B, C, cu_seqlens, max_seqlen, D, None, dt_bias, dt_softplus, dt_limit,
+                                   checkpoints, seq_segments)
+    dev, f32, io = x.device, torch.float32, x.dtype
+    states = (a.fwd.nseq,) + (a.fwd.nheads, a.fwd.headdim, a.fwd.dstate)
+    _spec(dout, "dout", x.shape, io, dev)
+    _spec(dfinal_states, "dfinal_states", states, f32, dev)
+    dout, dfinal_states = _tokens(dout, 8), _dense(dfinal_states)
+    g = {"dx": _tokens_out(dx, "dx", x.shape, io, dev, 8), "ddt": _tokens_out(ddt, "ddt", dt.shape, io, dev),
+         "dB": _tokens_out(dB, "dB", B.shape, io, dev, 8), "dC": _tokens_out(dC, "dC", C.shape, io, dev, 8)}
+    if workspace is not None:
+        _workspace_spec(workspace, dev)
+    _on_gpu(dev)
+    g["dA"] = torch.empty(A.shape, dtype=f32, device=dev)
+    if D is not None:
+        g["dD"] = torch.empty(D.shape, dtype=f32, device=dev)
+    if dt_bias is not None:
+        g["ddt_bias"] = torch.empty(dt_bias.shape, dtype=f32, device=dev)
+    if want_dinitial_states:
+        g["dinitial_states"] = torch.empty(states, dtype=f32, device=dev)
+    a.dout, a.dout_stride, a.dfinal_states = _ptr(dout), _token_stride(dout), _ptr(dfinal_states)
+    for k in ("dx", "ddt", "dB", "dC"):
+        setattr(a, k, _ptr(g[k]))
+        setattr(a, k + "_stride", _token_stride(g[k]))
+    for k in ("dA", "dD", "ddt_bias", "dinitial_states"):
+        setattr(a, k, _ptr(g.get(k)))
+    L = _lib.lib()
+    ws = _workspace(L.ssd_varlen_bwd_workspace_size, a, workspace, dev)
+    check(L.ssd_varlen_bwd(ctypes.byref(a), _stream(dev, stream)))
+    return g
+
+
+def conv1d_ssd_update(xBC: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, conv_weight: torch.Tensor,
+                      conv_state: torch.Tensor, ssm_state: torch.Tensor, cache_seqlens: Optional[torch.Tensor],
+                      conv_bias: Optional[torch.Tensor] = None, D: Optional[torch.Tensor] = None,
+                      z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
+                      dt_softplus: bool = False, dt_limit: Optional[Tuple[float, float]] = None,
+                      slots: Optional[torch.Tensor] = None, activation="silu",
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """One token of every request through the conv and the state update, in
+    one launch; returns ``out`` (batch, nheads * headdim).
+
+    xBC: (batch, nheads * headdim + 2 * ngroups * dstate), a row's x | B | C
+    before the conv; dt: (batch, nheads); z: (batch, nheads * headdim), any row
+    stride, float32, bfloat16 or float16.  ``conv_state`` (entries, channels,
+    state_len >= 4) in xBC's dtype and ``ssm_state`` (entries, nheads, headdim,
+    dstate) float32 are the caches that causal_conv1d_varlen_fwd and
+    ssd_varlen_fwd fill; request b uses entry ``slots[b]`` and has seen
+    ``cache_seqlens[b]`` tokens (None: every request is new).  A row whose entry is outside the cache
+    is padding."""
+    io = _io_of(xBC, "xBC", 2)
+    if ssm_state.dim() != 4:
+        raise ValueError(f"ssm_state must be (entries, nheads, headdim, dstate), got shape {tuple(ssm_state.shape)}")
+    entries, nheads, headdim, dstate = ssm_state.shape
+    batch, channels = xBC.shape
+    dev, f32, hp = xBC.device, torch.float32, nheads * headdim
+    ngroups = (channels - hp) // (2 * dstate)
+    if channels <= hp or (channels - hp) % (2 * dstate) != 0:
+        raise ValueError(f"xBC must have nheads * headdim + 2 * ngroups * dstate columns, got {channels} "
+                         f"for {nheads} heads of {headdim} and dstate {dstate}")
+    _cache_spec(ssm_state, "ssm_state", (nheads, headdim, dstate), f32, dev)
+    if conv_state.dim() != 3:
+        raise ValueError(f"conv_state must be (entries, channels, state_len), got shape {tuple(conv_state.shape)}")
+    _out_spec(conv_state, "conv_state", (entries, channels, conv_state.shape[2]), xBC.dtype, dev)
+    conv_weight, conv_bias, A, D, dt_bias = (_dense(t) for t in (conv_weight, conv_bias, A, D, dt_bias))
+    _conv_params_spec(conv_weight, conv_bias, channels, dev)
+    _spec(dt, "dt", (batch, nheads), xBC.dtype, dev)
+    _spec(z, "z", (batch, hp), xBC.dtype, dev)
+    _spec(A, "A", (nheads,), f32, dev)
+    _spec(dt_bias, "dt_bias", (nheads,), f32, dev)
+    if D is not None:
+        _spec(D, "D", (nheads,) if D.dim() == 1 else (nheads, headdim), f32, dev)
+    cache_seqlens, slots = _int32(cache_seqlens, "cache_seqlens", batch, dev), _int32(slots, "slots", batch, dev)
+    out = _tokens_out(out, "out", (batch, hp), xBC.dtype, dev)
+    act = _act_code(activation)
+    _on_gpu(dev)
+    xBC, dt, z = _tokens(xBC), _tokens(dt), _tokens(z)
+    a = _lib.ConvSsdUpdateArgs()
+    a.batch, a.nheads, a.headdim, a.dstate, a.ngroups = batch, nheads, headdim, dstate, ngroups
+    a.io_dtype, a.act, a.width = io, act, conv_weight.shape[1]
+    a.xBC, a.xBC_stride, a.dt, a.dt_stride = _ptr(xBC), _token_stride(xBC), _ptr(dt), _token_stride(dt)
+    a.A, a.conv_weight, a.conv_bias = _ptr(A), _ptr(conv_weight), _ptr(conv_bias)
+    a.D, a.D_per_channel, a.dt_bias = _ptr(D), int(D is not None and D.dim() == 2), _ptr(dt_bias)
+    if z is not None:
+        a.z, a.z_stride = _ptr(z), _token_stride(z)
+    a.dt_softplus = int(bool(dt_softplus))
+    _limit(a, dt_limit)
+    a.conv_state, a.state_len, a.ssm_state, a.state_slots = _ptr(conv_state), conv_state.shape[2], _ptr(ssm_state), entries
+    a.cache_seqlens, a.slots = _ptr(cache_seqlens), _ptr(slots)
+    a.out, a.out_stride = _ptr(out), _token_stride(out)
+    check(_lib.lib().conv1d_ssd_update(ctypes.byref(a), _stream(dev, stream)))
+    return out

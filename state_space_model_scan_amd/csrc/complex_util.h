@@ -63,12 +63,4 @@ __device__ __forceinline__ void cexp_turns(float dt, float ar2, float hi, float 
   ei = mag * __builtin_amdgcn_sinf(r);
 }
 
-// softplus(v) = log(1 + e^v) to a few ulp at every v (no cancellation in 1 + w)
-__device__ __forceinline__ float softplus_acc(float v) {
-  const float w = fast_exp2(-fabsf(v) * kLog2e);
-  const float u = 1.0f + w;
-  const float c = (u - 1.0f) - w;
-  return fmaxf(v, 0.0f) + fmaf(fast_log2(u), kLn2, -c * fast_rcp(u));
-}
-
 }  // namespace ssm

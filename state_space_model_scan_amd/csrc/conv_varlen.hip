@@ -1,0 +1,419 @@
+// conv_varlen.hip -- the causal depthwise conv over packed token-major rows
+// (causal_conv1d_varlen_fwd) and its gradient (causal_conv1d_varlen_bwd).
+//
+// Both stream: the forward reads and writes every element once (4 bytes an
+// element in 16 bits), the backward reads two and writes one.  A wave owns 64
+// runs of NV neighbouring channels (16 bytes each where the rows allow it, so
+// a token's load is one KiB) and walks a run of tokens with the last inputs in
+// registers.  The tokens before the run are read again: 3 of kFwdRun + 3.
+// What a token may see is decided by wave-uniform scalars: its place in its
+// sequence, found once per run by a binary search of cu_seqlens and then
+// counted.  The run's loads are issued together before the first is used.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "device_util.h"
+#include "host_util.h"
+#include "ssmscan.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kW = SSM_CONV_WIDTH;
+constexpr int kFwdRun = 16;        // tokens of a wave's run, forward
+constexpr int kBwdRun = 32;        // tokens of a wave's run, backward
+constexpr int kStep = 8;           // tokens whose loads are in flight together, backward
+constexpr int kRows = 4;           // waves (runs) of a workgroup
+
+// NV neighbouring io elements (NV = 1: any alignment)
+template <int IO, int NV>
+struct Vec {
+  RawV<IO, NV> r;
+  __device__ __forceinline__ void load(const void *p, int64_t i) { r.load_vec(p, i); }
+  __device__ __forceinline__ float get(int k) const { return r.get(k); }
+  __device__ __forceinline__ void zero() { r.zero(); }
+};
+template <int IO>
+struct Vec<IO, 1> {
+  float v;
+  __device__ __forceinline__ void load(const void *p, int64_t i) { v = load_io<IO>(p, i); }
+  __device__ __forceinline__ float get(int) const { return v; }
+  __device__ __forceinline__ void zero() { v = 0.0f; }
+};
+template <int IO, int NV>
+__device__ __forceinline__ void put(void *p, int64_t i, const float (&v)[NV]) {
+  if constexpr (NV == 1) store_one<IO>(p, i, v[0]);
+  else store_n<IO, NV>(p, i, v, NV, true);
+}
+
+struct ConvVarParams {
+  const void *x, *dout;
+  void *out, *dx, *ring;
+  const float *w, *bias;
+  const int32_t *cu, *seen, *slots;
+  float *part;                       // backward: (blocks of runs, kW + 1, channels)
+  int64_t total, nseq, channels, xs, os, dos, dxs, nslots, ring_len;
+  int silu;
+};
+
+// The sequence of token t: the last s with cu[s] <= t (uniform).
+__device__ __forceinline__ int64_t find_seq(const int32_t *cu, int64_t nseq, int64_t t) {
+  int64_t lo = 0, hi = nseq;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The input j + 1 tokens before a sequence's first one, from its ring.
+template <int IO, int NV>
+__device__ __forceinline__ void ring_input(const ConvVarParams &p, int64_t s, int back, int64_t c0, float (&v)[NV]) {
+  const int64_t pos = (p.seen ? p.seen[s] : 0) - back;
+  const int64_t slot = p.slots ? p.slots[s] : s;
+  const bool there = p.ring && pos >= 0 && slot >= 0 && slot < p.nslots;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    v[k] = there ? load_io<IO>(p.ring, (slot * p.channels + c0 + k) * p.ring_len + pos % p.ring_len) : 0.0f;
+}
+
+template <int NV>
+__device__ __forceinline__ void load_params(const ConvVarParams &p, int64_t c0, float (&w)[kW][NV], float (&b)[NV]) {
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const float *wr = p.w + (c0 + k) * kW;
+#pragma unroll
+    for (int j = 0; j < kW; ++j) w[j][k] = wr[j];
+    b[k] = p.bias ? p.bias[c0 + k] : 0.0f;
+  }
+}
+
+template <int IO, int NV>
+__global__ void __launch_bounds__(64 * kRows) conv_var_fwd_kernel(const ConvVarParams p) {
+  const int lane = threadIdx.x & 63;
+  const int row = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRows + row) * kFwdRun;
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * NV;
+  if (t0 >= p.total || c0 >= p.channels) return;
+  const int n = static_cast<int>(p.total - t0 < kFwdRun ? p.total - t0 : kFwdRun);
+
+  Vec<IO, NV> in[kFwdRun + kW - 1];
+#pragma unroll
+  for (int i = 0; i < kFwdRun + kW - 1; ++i) {
+    const int64_t t = t0 + i - (kW - 1);
+    if (t >= 0 && i < n + kW - 1) in[i].load(p.x, t * p.xs + c0);
+    else in[i].zero();
+  }
+  float w[kW][NV], bias[NV];
+  load_params<NV>(p, c0, w, bias);
+  int64_t s = find_seq(p.cu, p.nseq, t0);
+  int64_t end = p.cu[s + 1];
+  int64_t pos = t0 - p.cu[s];
+#pragma unroll
+  for (int i = 0; i < kFwdRun; ++i) {
+    if (i >= n) break;
+    while (t0 + i >= end && s + 1 < p.nseq) {
+      ++s;
+      end = p.cu[s + 1];
+      pos = t0 + i - p.cu[s];
+    }
+    float acc[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) acc[k] = fmaf(w[kW - 1][k], in[i + kW - 1].get(k), bias[k]);
+#pragma unroll
+    for (int back = 1; back < kW; ++back) {
+      if (pos >= back) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) acc[k] = fmaf(w[kW - 1 - back][k], in[i + kW - 1 - back].get(k), acc[k]);
+      } else if (p.ring) {
+        float h[NV];
+        ring_input<IO, NV>(p, s, back - static_cast<int>(pos), c0, h);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) acc[k] = fmaf(w[kW - 1 - back][k], h[k], acc[k]);
+      }
+    }
+    if (p.silu) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) acc[k] = silu_f(acc[k]);
+    }
+    put<IO, NV>(p.out, (t0 + i) * p.os + c0, acc);
+    ++pos;
+  }
+}
+
+// The last inputs of every sequence into its ring (a launch of its own: the
+// forward's first tokens still read the ring's old entries).
+template <int IO>
+__global__ void __launch_bounds__(256) conv_var_ring_kernel(const ConvVarParams p) {
+  const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;
+  if (c >= p.channels) return;
+  for (int64_t s = blockIdx.x; s < p.nseq; s += gridDim.x) {
+    int64_t lo = p.cu[s], hi = p.cu[s + 1];
+    lo = lo < 0 ? 0 : lo;
+    hi = hi > p.total ? p.total : hi;
+    const int64_t slot = p.slots ? p.slots[s] : s;
+    if (hi <= lo || slot < 0 || slot >= p.nslots) continue;
+    int64_t seen = p.seen ? p.seen[s] : 0;
+    if (seen < 0) seen = 0;
+    const int64_t from = hi - lo > p.ring_len ? hi - p.ring_len : lo;
+    for (int64_t t = from; t < hi; ++t) {
+      const int64_t at = (slot * p.channels + c) * p.ring_len + (seen + t - lo) % p.ring_len;
+      if constexpr (IO != 0)
+        static_cast<uint16_t *>(p.ring)[at] = static_cast<const uint16_t *>(p.x)[t * p.xs + c];
+      else
+        static_cast<uint32_t *>(p.ring)[at] = static_cast<const uint32_t *>(p.x)[t * p.xs + c];
+    }
+  }
+}
+
+// Backward.  At token t the pre-activation is formed again from x, and
+// da_t = dout_t act'(pre_t) goes to the gradients of the inputs it saw: the
+// run's pending dx of tokens t-3..t are in registers, and token t-3's is
+// complete.  The three tokens after the run are walked for what they give to
+// the run's last ones; their weight gradients belong to the next run.  The
+// weight and bias gradients of the workgroup's four runs meet in LDS and go
+// out as one row of partial sums.
+template <int IO, int NV>
+__global__ void __launch_bounds__(64 * kRows) conv_var_bwd_kernel(const ConvVarParams p) {
+  __shared__ float sum[kRows - 1][kW + 1][NV][64];
+  const int lane = threadIdx.x & 63;
+  const int row = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRows + row) * kBwdRun;
+  const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * NV;
+  const bool live = c0 < p.channels;
+  float dw[kW + 1][NV];
+#pragma unroll
+  for (int j = 0; j <= kW; ++j)
+#pragma unroll
+    for (int k = 0; k < NV; ++k) dw[j][k] = 0.0f;
+
+  if (live && t0 < p.total) {
+    const int64_t stop = t0 + kBwdRun < p.total ? t0 + kBwdRun : p.total;              // end of the run
+    const int64_t walk = stop + kW - 1 < p.total ? stop + kW - 1 : p.total;            // and of the walk
+    float w[kW][NV], bias[NV];
+    load_params<NV>(p, c0, w, bias);
+    // the last three inputs, oldest first, and the pending gradients
+    float win[kW][NV], pend[kW][NV];
+#pragma unroll
+    for (int j = 0; j < kW - 1; ++j) {
+      const int64_t t = t0 - (kW - 1) + j;
+      Vec<IO, NV> v;
+      if (t >= 0) v.load(p.x, t * p.xs + c0);
+      else v.zero();
+#pragma unroll
+      for (int k = 0; k < NV; ++k) win[j][k] = v.get(k);
+    }
+#pragma unroll
+    for (int j = 0; j < kW; ++j)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) pend[j][k] = 0.0f;
+    int64_t s = find_seq(p.cu, p.nseq, t0);
+    int64_t end = p.cu[s + 1];
+    int64_t pos = t0 - p.cu[s];
+    for (int64_t tb = t0; tb < walk + kW - 1; tb += kStep) {
+      Vec<IO, NV> xv[kStep], gv[kStep];
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        if (tb + i < walk) {
+          xv[i].load(p.x, (tb + i) * p.xs + c0);
+          gv[i].load(p.dout, (tb + i) * p.dos + c0);
+        } else {
+          xv[i].zero();
+          gv[i].zero();
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+        const int64_t t = tb + i;
+        if (t < walk) {
+          while (t >= end && s + 1 < p.nseq) {
+            ++s;
+            end = p.cu[s + 1];
+            pos = t - p.cu[s];
+          }
+          float da[NV];
+#pragma unroll
+          for (int k = 0; k < NV; ++k) {
+            win[kW - 1][k] = xv[i].get(k);
+            da[k] = fmaf(w[kW - 1][k], win[kW - 1][k], bias[k]);
+          }
+#pragma unroll
+          for (int back = 1; back < kW; ++back)
+            if (pos >= back) {
+#pragma unroll
+              for (int k = 0; k < NV; ++k) da[k] = fmaf(w[kW - 1 - back][k], win[kW - 1 - back][k], da[k]);
+            }
+#pragma unroll
+          for (int k = 0; k < NV; ++k) {
+            const float pre = da[k];
+            float d = gv[i].get(k);
+            if (p.silu) {
+              const float sg = fast_rcp(1.0f + fast_exp2(-pre * kLog2e));
+              d *= fmaf(pre * sg, 1.0f - sg, sg);
+            }
+            da[k] = d;
+          }
+          const bool mine = t < stop;
+#pragma unroll
+          for (int back = 0; back < kW; ++back)
+            if (pos >= back) {
+#pragma unroll
+              for (int k = 0; k < NV; ++k) {
+                pend[kW - 1 - back][k] = fmaf(w[kW - 1 - back][k], da[k], pend[kW - 1 - back][k]);
+                if (mine) dw[kW - 1 - back][k] = fmaf(da[k], win[kW - 1 - back][k], dw[kW - 1 - back][k]);
+              }
+            }
+          if (mine) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) dw[kW][k] += da[k];
+          }
+          ++pos;
+        }
+        const int64_t done = t - (kW - 1);   // its gradient is complete
+        if (done >= t0 && done < stop) put<IO, NV>(p.dx, done * p.dxs + c0, pend[0]);
+#pragma unroll
+        for (int j = 0; j < kW - 1; ++j)
+#pragma unroll
+          for (int k = 0; k < NV; ++k) {
+            pend[j][k] = pend[j + 1][k];
+            win[j][k] = win[j + 1][k];
+          }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) pend[kW - 1][k] = 0.0f;
+      }
+    }
+  }
+  if (row > 0) {
+#pragma unroll
+    for (int j = 0; j <= kW; ++j)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) sum[row - 1][j][k][lane] = dw[j][k];
+  }
+  __syncthreads();
+  if (row == 0 && live) {
+#pragma unroll
+    for (int j = 0; j <= kW; ++j)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float v = dw[j][k];
+#pragma unroll
+        for (int q = 0; q < kRows - 1; ++q) v += sum[q][j][k][lane];
+        p.part[(static_cast<int64_t>(blockIdx.x) * (kW + 1) + j) * p.channels + c0 + k] = v;
+      }
+  }
+}
+
+// Sum of the partial rows, four threads a column, each its quarter in order;
+// in 64 bits, so that the sum over many tokens keeps 32.
+__global__ void __launch_bounds__(256) conv_var_reduce_kernel(const float *part, float *dweight, float *dbias,
+                                                              int64_t rows, int64_t channels) {
+  __shared__ double sum[4][64];
+  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane, cols = (kW + 1) * channels;
+  double v = 0.0;
+  if (col < cols)
+    for (int64_t r = rows * q / 4; r < rows * (q + 1) / 4; ++r) v += part[r * cols + col];
+  sum[q][lane] = v;
+  __syncthreads();
+  if (q == 0 && col < cols) {
+    const float total = static_cast<float>((sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]));
+    const int64_t j = col / channels, c = col - j * channels;
+    if (j < kW) dweight[c * kW + j] = total;
+    else if (dbias) dbias[c] = total;
+  }
+}
+
+ConvVarParams conv_params(const causal_conv1d_varlen_args_t *a) {
+  ConvVarParams p{};
+  p.x = a->x; p.xs = a->x_stride;
+  p.w = a->weight; p.bias = a->bias; p.cu = a->cu_seqlens;
+  p.total = a->total; p.nseq = a->nseq; p.channels = a->channels;
+  p.silu = a->act == SSM_ACT_SILU;
+  return p;
+}
+
+int64_t bwd_blocks(int64_t total) { return (total + kRows * kBwdRun - 1) / (kRows * kBwdRun); }
+
+// 16-byte accesses need whole and aligned rows of them
+bool wide_rows(int32_t io, int64_t channels, const void *p, int64_t stride) {
+  const int nv = io == SSM_F32 ? 4 : 8;
+  return channels % nv == 0 && aligned16(p) && stride % nv == 0;
+}
+
+}  // namespace
+}  // namespace ssm
+
+using namespace ssm;
+
+extern "C" int causal_conv1d_varlen_fwd(const causal_conv1d_varlen_args_t *a, void *stream_ptr) {
+  const int st = causal_conv1d_varlen_fwd_validate(a);
+  if (st != SSM_OK) return st;
+  ConvVarParams p = conv_params(a);
+  p.out = a->out; p.os = a->out_stride;
+  p.ring = a->conv_state; p.nslots = a->state_slots; p.ring_len = a->state_len;
+  p.seen = a->cache_seqlens; p.slots = a->slots;
+  const bool wide = wide_rows(a->io_dtype, a->channels, a->x, a->x_stride) &&
+                    wide_rows(a->io_dtype, a->channels, a->out, a->out_stride);
+  const int nv = !wide ? 1 : a->io_dtype == SSM_F32 ? 4 : 8;
+  const int64_t gx = (a->total + kRows * kFwdRun - 1) / (kRows * kFwdRun);
+  const int64_t gy = (a->channels + 64 * nv - 1) / (64 * nv);
+  if (gy > 65535) return SSM_ERR_SHAPE;
+  hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * kRows);
+  auto launch = [&](auto fn) { hipLaunchKernelGGL(fn, grid, block, 0, stream, p); };
+  if (a->io_dtype == SSM_BF16) wide ? launch(conv_var_fwd_kernel<1, 8>) : launch(conv_var_fwd_kernel<1, 1>);
+  else if (a->io_dtype == SSM_F16) wide ? launch(conv_var_fwd_kernel<2, 8>) : launch(conv_var_fwd_kernel<2, 1>);
+  else wide ? launch(conv_var_fwd_kernel<0, 4>) : launch(conv_var_fwd_kernel<0, 1>);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return hip_fail(e);
+  if (a->conv_state) {
+    const int64_t cy = (a->channels + 255) / 256;
+    if (cy > 65535) return SSM_ERR_SHAPE;
+    const dim3 rgrid(static_cast<unsigned>(a->nseq < 65536 ? a->nseq : 65536), static_cast<unsigned>(cy));
+    if (a->io_dtype == SSM_F32) hipLaunchKernelGGL(conv_var_ring_kernel<0>, rgrid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(conv_var_ring_kernel<1>, rgrid, dim3(256), 0, stream, p);
+    e = hipGetLastError();
+    if (e != hipSuccess) return hip_fail(e);
+  }
+  return SSM_OK;
+}
+
+extern "C" int causal_conv1d_varlen_bwd_workspace_size(const causal_conv1d_varlen_args_t *a, size_t *bytes) {
+  const int st = causal_conv1d_varlen_bwd_validate(a);
+  if (st != SSM_OK) return st;
+  if (!bytes) return SSM_ERR_NULL;
+  *bytes = static_cast<size_t>(bwd_blocks(a->total)) * (kW + 1) * a->channels * sizeof(float);
+  return SSM_OK;
+}
+
+extern "C" int causal_conv1d_varlen_bwd(const causal_conv1d_varlen_args_t *a, void *stream_ptr) {
+  size_t need = 0;
+  const int st = causal_conv1d_varlen_bwd_workspace_size(a, &need);
+  if (st != SSM_OK) return st;
+  if (!a->workspace || a->workspace_bytes < need) return SSM_ERR_WORKSPACE;
+  ConvVarParams p = conv_params(a);
+  p.dout = a->dout; p.dos = a->dout_stride;
+  p.dx = a->dx; p.dxs = a->dx_stride;
+  p.part = static_cast<float *>(a->workspace);
+  const bool wide = wide_rows(a->io_dtype, a->channels, a->x, a->x_stride) &&
+                    wide_rows(a->io_dtype, a->channels, a->dout, a->dout_stride) &&
+                    wide_rows(a->io_dtype, a->channels, a->dx, a->dx_stride);
+  const int nv = !wide ? 1 : a->io_dtype == SSM_F32 ? 4 : 8;
+  const int64_t gx = bwd_blocks(a->total), gy = (a->channels + 64 * nv - 1) / (64 * nv);
+  if (gy > 65535) return SSM_ERR_SHAPE;
+  hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * kRows);
+  auto launch = [&](auto fn) { hipLaunchKernelGGL(fn, grid, block, 0, stream, p); };
+  if (a->io_dtype == SSM_BF16) wide ? launch(conv_var_bwd_kernel<1, 8>) : launch(conv_var_bwd_kernel<1, 1>);
+  else if (a->io_dtype == SSM_F16) wide ? launch(conv_var_bwd_kernel<2, 8>) : launch(conv_var_bwd_kernel<2, 1>);
+  else wide ? launch(conv_var_bwd_kernel<0, 4>) : launch(conv_var_bwd_kernel<0, 1>);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return hip_fail(e);
+  const int64_t cols = (kW + 1) * a->channels;
+  hipLaunchKernelGGL(conv_var_reduce_kernel, dim3(static_cast<unsigned>((cols + 63) / 64)), dim3(256), 0, stream, p.part,
+                     a->dweight, a->dbias, gx, a->channels);
+  e = hipGetLastError();
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
+}

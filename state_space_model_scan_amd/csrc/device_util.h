@@ -176,6 +176,14 @@ __device__ __forceinline__ float softplus_f(float v) {
   return v > 20.0f ? v : sp;
 }
 
+// softplus(v) = log(1 + e^v) to a few ulp at every v (no cancellation in 1 + w)
+__device__ __forceinline__ float softplus_acc(float v) {
+  const float w = fast_exp2(-fabsf(v) * kLog2e);
+  const float u = 1.0f + w;
+  const float c = (u - 1.0f) - w;
+  return fmaxf(v, 0.0f) + fmaf(fast_log2(u), kLn2, -c * fast_rcp(u));
+}
+
 // silu(v) = v / (1 + e^-v)
 __device__ __forceinline__ float silu_f(float v) {
   return v * fast_rcp(1.0f + fast_exp2(-v * kLog2e));

@@ -1,0 +1,843 @@
+// ssd_varlen_bwd.hip -- the gradient of the packed chunked scan
+// (ssd_varlen_bwd), on the gfx950 matrix cores.
+//
+// With the steps dt', cs their running sum times A inside a chunk of Q = 64
+// tokens, H the state entering the chunk (from its 8-bit checkpoint), dH the
+// adjoint of the state leaving it, g = dout, e_i = exp(cs_i),
+// w_j = exp(cs_end - cs_j), and for i >= j
+//   L_ij = exp(cs_i - cs_j), S_ij = C_i . B_j, M_ij = g_i . x_j:
+//   dx_j = dt'_j (sum_i S_ij L_ij g_i + w_j dH B_j) + D g_j
+//   dB_j = sum_heads [ sum_i (M_ij L_ij dt'_j) C_i + dt'_j w_j dH^T x_j ]
+//   dC_i = sum_heads [ sum_j (M_ij L_ij dt'_j) B_j + e_i H^T g_i ]
+//   dH  <- exp(cs_end) dH + sum_i e_i g_i C_i^T
+// and, for the steps, with G_ij = S_ij L_ij M_ij, q_i = e_i g_i . (H C_i) and
+// r_j = w_j x_j . (dH B_j):
+//   direct_j = sum_i G_ij + r_j
+//   dcs_i    = sum_j G_ij dt'_j + q_i - dt'_i direct_i,
+//   dcs_end += sum_j dt'_j r_j + exp(cs_end) <dH, H>
+//   da_t = sum_{k >= t} dcs_k,  ddt'_t = direct_t + A da_t,  dA = sum dt' da.
+//
+// Three launches.  (1) adjoint_kernel walks every (sequence, head)'s chunks
+// backwards and leaves each chunk's dH, as a bf16 head and tail (16
+// significant bits), in the workspace; with few (sequence, head) pairs the
+// sequence is cut into segments as in the forward.  (2) chunk_kernel takes one
+// chunk and a block of heads of one group: everything but dH is local to the
+// chunk.  S is formed once for the group.  dB's and dC's pair products are
+// linear in M L dt', so that sum over the heads is kept (64 x 64, in
+// registers) and multiplied with C and B once at the end; their state parts
+// are summed over the heads in registers too.  (3) small kernels add the head
+// blocks' dB and dC and the chunks' dA, dD and ddt_bias, in a fixed order.
+//
+// Precision: x, B, C, g and the dequantised H (seven bits times a power of
+// two) are exact in bf16; dH, S L and the summed M L dt' enter as head and
+// tail, two products each, as the forward's derived operands do: one rounding
+// to bf16 would put 2^-9 into dA and ddt_bias, which are 32-bit sums.
+//
+// Operand layout of the 16x16x32 product as in ssd.hip.  Tiles are kept
+// row-major in LDS, and an operand that runs along the other index is read
+// with the transposing LDS load (ds_read_b64_tr_b16: of four rows by sixteen
+// columns, lane l of sixteen receives column l; checked on the device), so no
+// tile is stored twice.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "host_util.h"
+#include "ssd_util.h"
+#include "ssmscan.h"
+
+namespace ssm {
+namespace {
+
+constexpr int kMaxHeads = 16;   // heads of a chunk_kernel workgroup
+
+struct BwdParams {
+  const uint16_t *x, *dt, *B, *C, *g;
+  const float *A, *D, *dt_bias, *dfin;
+  const int32_t *cu;
+  const int8_t *codes;
+  const float *scales;
+  uint16_t *dx, *ddt, *dB, *dC;
+  float *dinit;
+  uint16_t *ws_dh;               // (entries, heads, 2, p, n): head, tail
+  float *ws_state, *ws_decay;    // adjoint segments
+  float *ws_bc;                  // (2, head blocks of a group, total, groups, n) or NULL (one block: dB, dC directly)
+  float *ws_sum;                 // (entries, heads, 2): dA, ddt_bias
+  float *ws_dd;                  // (entries, heads) or (entries, heads, p): dD
+  int64_t xs, dts, bs, cs, gs, dxs, ddts, dbs, dcs;
+  int64_t total, nseq, max_seqlen, nheads, ngroups, seg_chunks, entries;
+  int nseg, softplus, dt_limit, D_per_channel, hb_heads, hb_per_group;
+  float dt_min, dt_max;
+};
+
+struct Seq {
+  int64_t first, len, chunks, entry;   // entry: its first checkpoint
+};
+
+// A sequence's tokens, kept inside the tensors whatever cu holds.
+__device__ __forceinline__ Seq sequence(const BwdParams &p, int64_t s) {
+  int64_t lo = p.cu[s], hi = p.cu[s + 1];
+  lo = lo < 0 ? 0 : lo > p.total ? p.total : lo;
+  hi = hi < lo ? lo : hi > p.total ? p.total : hi;
+  const int64_t len = hi - lo > p.max_seqlen ? p.max_seqlen : hi - lo;
+  return {lo, len, (len + kQ - 1) / kQ, lo / kQ + s};
+}
+
+// The step of token l of a chunk and its running sum times A over the wave
+// (0 beyond the chunk's end); v: the value before softplus.
+__device__ __forceinline__ float chunk_step(const BwdParams &p, float raw, float bias, bool live, float Ah, float &cs,
+                                            float &v) {
+  v = raw + bias;
+  float d = p.softplus ? softplus_acc(v) : v;
+  if (p.dt_limit) d = fminf(fmaxf(d, p.dt_min), p.dt_max);
+  if (!live) d = 0.0f;
+  cs = d * Ah;
+  const int l = threadIdx.x & 63;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const float o = __shfl_up(cs, off);
+    if (l >= off) cs += o;
+  }
+  return d;
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+// The operand fragment that a row-major tile holds column by column: lane
+// (r, kq) receives tile[row0 + 8 kq + i][col0 + r], i < 8.
+template <int ROW_LEN>
+__device__ __forceinline__ bf16x8 frag_t(uint16_t *tile, int row0, int col0) {
+  typedef __attribute__((address_space(3))) s16x4 *lds;
+  const int l = threadIdx.x & 63, i = l & 15, kq = l >> 4;
+  const int row = row0 + 8 * kq + (i >> 2), col = col0 + 4 * (i & 3);
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + swz<ROW_LEN>(row, col)));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + swz<ROW_LEN>(row + 4, col)));
+  const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
+  return __builtin_bit_cast(bf16x8, make_uint4(ua.x, ua.y, ub.x, ub.y));
+}
+// ... and row by row: lane (r, kq) receives tile[row0 + r][col0 + 8 kq + i].
+template <int ROW_LEN>
+__device__ __forceinline__ bf16x8 frag(const uint16_t *tile, int row0, int col0) {
+  const int l = threadIdx.x & 63;
+  return ld8(tile + swz<ROW_LEN>(row0 + (l & 15), col0 + 8 * (l >> 4)));
+}
+
+// ---------------------------------------------------------------------------
+// (1) the adjoint of the states.  One workgroup of four waves per (sequence,
+// head, segment); wave w holds dH rows p = 16w + r, n = 16 nt + 4 kq + i, as
+// the forward holds the state.  STORE: write every chunk's dH; otherwise find
+// the segment's adjoint from zero and its decay.
+// ---------------------------------------------------------------------------
+template <int N, bool STORE>
+__global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
+  constexpr int NT = N / 16;
+  constexpr int CPIECES = kQ * N / 8, CPER = (CPIECES + 255) / 256;
+  __shared__ __attribute__((aligned(16))) uint16_t sG[kQ * kP], sC[kQ * N];
+  __shared__ __attribute__((aligned(16))) float sE[kQ];
+  __shared__ float sEnd;
+  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r = l & 15, kq = l >> 4;
+  const int64_t sh = blockIdx.x, SH = gridDim.x;
+  const int64_t s = sh / p.nheads, h = sh - s * p.nheads, gr = h / (p.nheads / p.ngroups);
+  const Seq q = sequence(p, s);
+  const int64_t nsegs = q.chunks ? (q.chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
+  // the first launch runs the segments that have one before them
+  const int64_t seg = STORE ? blockIdx.y : blockIdx.y + 1;
+  if (seg >= nsegs) return;
+  const int64_t c_begin = seg * p.seg_chunks;
+  const int64_t c_end = c_begin + p.seg_chunks < q.chunks ? c_begin + p.seg_chunks : q.chunks;
+  const float Ah = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
+  const uint16_t *gb = p.g + q.first * p.gs + h * kP;
+  const uint16_t *Cb = p.C + q.first * p.cs + gr * N;
+  const uint16_t *dtb = p.dt + q.first * p.dts + h;
+  const int srow = (16 * w + r) * N + 4 * kq;
+
+  f32x4 acc[NT];
+  const bool from_end = seg == nsegs - 1 && p.dfin;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const float4 v = from_end ? *reinterpret_cast<const float4 *>(p.dfin + sh * kP * N + srow + 16 * nt)
+                              : make_float4(0, 0, 0, 0);
+    acc[nt] = (f32x4){v.x, v.y, v.z, v.w};
+  }
+  if constexpr (STORE) {
+    // the carry of the later segments, the last one's first
+    for (int64_t j = nsegs - 1; j > seg; --j) {
+      const float P = p.ws_decay[(j - 1) * SH + sh];
+      const float *E = p.ws_state + ((j - 1) * SH + sh) * kP * N + srow;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float4 e = *reinterpret_cast<const float4 *>(E + 16 * nt);
+        acc[nt] = (f32x4){fmaf(P, acc[nt][0], e.x), fmaf(P, acc[nt][1], e.y), fmaf(P, acc[nt][2], e.z),
+                          fmaf(P, acc[nt][3], e.w)};
+      }
+    }
+  }
+  float decay = 1.0f;
+  for (int64_t c = c_end - 1; c >= c_begin; --c) {
+    const int64_t t0 = c * kQ;
+    const int len = static_cast<int>(q.len - t0 < kQ ? q.len - t0 : kQ);
+    uint4 gv[2], cv[CPER];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int piece = tid + 256 * k, t = piece >> 3;
+      gv[k] = t < len ? ld8_raw(gb + (t0 + t) * p.gs + (piece & 7) * 8) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < CPER; ++k) {
+      const int piece = tid + 256 * k, t = piece / (N / 8);
+      cv[k] = (piece < CPIECES && t < len) ? ld8_raw(Cb + (t0 + t) * p.cs + (piece % (N / 8)) * 8) : make_uint4(0, 0, 0, 0);
+    }
+    float raw = 0.0f;
+    if (w == 0 && l < len) raw = bf2f(dtb[(t0 + l) * p.dts]);
+    if constexpr (STORE) {
+      uint16_t *dh = p.ws_dh + ((q.entry + c) * p.nheads + h) * 2 * kP * N + srow;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint2 hi, lo;
+        split_bf2(acc[nt][0], acc[nt][1], hi.x, lo.x);
+        split_bf2(acc[nt][2], acc[nt][3], hi.y, lo.y);
+        *reinterpret_cast<uint2 *>(dh + 16 * nt) = hi;
+        *reinterpret_cast<uint2 *>(dh + kP * N + 16 * nt) = lo;
+      }
+    }
+    __syncthreads();   // the previous chunk's reads are done
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int piece = tid + 256 * k;
+      *reinterpret_cast<uint4 *>(&sG[swz<kP>(piece >> 3, (piece & 7) * 8)]) = gv[k];
+    }
+#pragma unroll
+    for (int k = 0; k < CPER; ++k) {
+      const int piece = tid + 256 * k;
+      if (piece < CPIECES) *reinterpret_cast<uint4 *>(&sC[swz<N>(piece / (N / 8), (piece % (N / 8)) * 8)]) = cv[k];
+    }
+    if (w == 0) {
+      float cs, v;
+      chunk_step(p, raw, bias, l < len, Ah, cs, v);
+      sE[l] = fast_exp2(cs * kLog2e);
+      if (l == 63) sEnd = fast_exp2(cs * kLog2e);
+    }
+    __syncthreads();
+    const float end = sEnd;
+    decay *= end;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[nt] *= end;
+#pragma unroll
+    for (int kk = 0; kk < kQ / 32; ++kk) {
+      const uint4 gt = __builtin_bit_cast(uint4, frag_t<kP>(sG, 32 * kk, 16 * w));
+      uint32_t gh[4], gl[4];
+#pragma unroll
+      for (int i = 0; i < 8; i += 2)
+        split_bf2(bf2f(raw_bits(gt, i)) * sE[32 * kk + 8 * kq + i], bf2f(raw_bits(gt, i + 1)) * sE[32 * kk + 8 * kq + i + 1],
+                  gh[i / 2], gl[i / 2]);
+      const bf16x8 hi = __builtin_bit_cast(bf16x8, make_uint4(gh[0], gh[1], gh[2], gh[3]));
+      const bf16x8 lo = __builtin_bit_cast(bf16x8, make_uint4(gl[0], gl[1], gl[2], gl[3]));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const bf16x8 ct = frag_t<N>(sC, 32 * kk, 16 * nt);
+        acc[nt] = mfma(ct, hi, acc[nt]);
+        acc[nt] = mfma(ct, lo, acc[nt]);
+      }
+    }
+  }
+  float *to = nullptr;
+  if constexpr (STORE) {
+    if (p.dinit && seg == 0) to = p.dinit + sh * kP * N + srow;
+  } else {
+    to = p.ws_state + ((seg - 1) * SH + sh) * kP * N + srow;
+    if (tid == 0) p.ws_decay[(seg - 1) * SH + sh] = decay;
+  }
+  if (to) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      *reinterpret_cast<float4 *>(to + 16 * nt) = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// (2) one chunk and hb_heads heads of a group: eight waves.
+// ---------------------------------------------------------------------------
+
+// sum over the four kq lanes of a column r
+__device__ __forceinline__ float sum_kq(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+// sum over the sixteen r lanes of a row kq
+__device__ __forceinline__ float sum_r(float v) {
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+__device__ __forceinline__ float sum_wave(float v) { return sum_kq(sum_r(v)); }
+
+template <int N>
+struct ChunkLds {
+  uint16_t B[kQ * N], C[kQ * N];          // [t][n]
+  uint16_t x[kQ * kP], g[kQ * kP];        // [t][p]
+  uint16_t H[kP * N];                     // [p][n]
+  uint16_t dh[2][kP * N > kQ * kQ ? kP * N : kQ * kQ];   // [p][n] head, tail; at the end M L dt' [j][i]
+  uint16_t U[2][kQ * kQ];                 // S L [j][i] head, tail
+  float cs[kMaxHeads][kQ], dt[kMaxHeads][kQ], v[kMaxHeads][kQ];
+  float row[2][kQ], col[4][kQ], q[N / 16][kQ], r[4][kQ], hh[8], dd[2][kP];
+};
+
+template <int N>
+__global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
+  constexpr int NT = N / 16;          // n tiles
+  constexpr int KN = N / 32;          // k steps over n
+  constexpr int IT = NT / 2;          // token tiles of a wave in the (n, token) products
+  constexpr int G8 = N / 8;
+  constexpr int BC = (kQ * G8 + 511) / 512;     // 16-byte pieces of a B, C or dH tile per thread
+  constexpr int HPIECES = kP * N / 16;          // 16-code pieces of H
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  ChunkLds<N> &sm = *reinterpret_cast<ChunkLds<N> *>(smem);
+  const int tid = threadIdx.x, l = tid & 63, r = l & 15, kq = l >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  // the entry's sequence: the last s whose first entry is at or before it
+  const int64_t entry = blockIdx.x;
+  int64_t lo = 0, hi = p.nseq;
+  while (hi - lo > 1) {
+    const int64_t mid = (lo + hi) >> 1;
+    int64_t e = p.cu[mid];
+    e = (e < 0 ? 0 : e) / kQ + mid;
+    if (e <= entry) lo = mid;
+    else hi = mid;
+  }
+  const Seq q = sequence(p, lo);
+  const int64_t chunk = entry - q.entry;
+  const int64_t hpg = p.nheads / p.ngroups;
+  const int64_t gr = blockIdx.y / p.hb_per_group, hb = blockIdx.y - gr * p.hb_per_group;
+  const int64_t h0 = gr * hpg + hb * p.hb_heads;
+  const int64_t h1 = h0 + p.hb_heads < (gr + 1) * hpg ? h0 + p.hb_heads : (gr + 1) * hpg;
+  const int nh = static_cast<int>(h1 - h0);
+  if (chunk < 0 || chunk >= q.chunks) {   // an entry of no chunk: nothing to add
+    for (int i = tid; i < nh; i += 512) {
+      p.ws_sum[(entry * p.nheads + h0 + i) * 2] = 0.0f;
+      p.ws_sum[(entry * p.nheads + h0 + i) * 2 + 1] = 0.0f;
+    }
+    if (p.D) {
+      const int64_t per = p.D_per_channel ? kP : 1;
+      for (int64_t i = tid; i < nh * per; i += 512) p.ws_dd[(entry * p.nheads + h0) * per + i] = 0.0f;
+    }
+    return;
+  }
+  const int64_t t0 = q.first + chunk * kQ;      // the chunk's first token
+  const int len = static_cast<int>(q.len - chunk * kQ < kQ ? q.len - chunk * kQ : kQ);
+
+  // ---- B, C, and every head's steps
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int k = 0; k < BC; ++k) {
+    const int piece = tid + 512 * k, t = piece / G8, n0 = (piece % G8) * 8;
+    if (piece < kQ * G8) {
+      *reinterpret_cast<uint4 *>(&sm.B[swz<N>(t, n0)]) = t < len ? ld8_raw(p.B + (t0 + t) * p.bs + gr * N + n0) : zero;
+      *reinterpret_cast<uint4 *>(&sm.C[swz<N>(t, n0)]) = t < len ? ld8_raw(p.C + (t0 + t) * p.cs + gr * N + n0) : zero;
+    }
+  }
+  for (int k = w; k < nh; k += 8) {
+    const int64_t h = h0 + k;
+    const float raw = l < len ? bf2f(p.dt[(t0 + l) * p.dts + h]) : 0.0f;
+    float cs, v;
+    const float d = chunk_step(p, raw, p.dt_bias ? p.dt_bias[h] : 0.0f, l < len, p.A[h], cs, v);
+    sm.cs[k][l] = cs;
+    sm.dt[k][l] = d;
+    sm.v[k][l] = v;
+  }
+  // the pairs above the diagonal stay zero
+  for (int i = tid; i < 2 * kQ * kQ / 8; i += 512) *reinterpret_cast<uint4 *>(&sm.U[0][0] + 8 * i) = zero;
+  if (tid < kQ) {
+    for (int k = 0; k < 4; ++k) sm.col[k][tid] = 0.0f;
+  }
+
+  // ---- this thread's pieces of a head's tiles, loaded one head ahead
+  uint4 xv, gv, hv, dv[2][BC];
+  float sc = 0.0f;
+  auto load_head = [&](int64_t h) {
+    const int t = tid >> 3, p0 = (tid & 7) * 8;
+    xv = t < len ? ld8_raw(p.x + (t0 + t) * p.xs + h * kP + p0) : zero;
+    gv = t < len ? ld8_raw(p.g + (t0 + t) * p.gs + h * kP + p0) : zero;
+    const int64_t eh = entry * p.nheads + h;
+    if (tid < HPIECES) {
+      hv = *reinterpret_cast<const uint4 *>(p.codes + eh * kP * N + 16 * tid);
+      sc = p.scales[eh * kP + 16 * tid / N];
+    }
+    const uint16_t *dh = p.ws_dh + eh * 2 * kP * N;
+#pragma unroll
+    for (int k = 0; k < BC; ++k) {
+      const int piece = tid + 512 * k;
+      if (piece < kP * G8) {
+        dv[0][k] = ld8_raw(dh + 8 * piece);
+        dv[1][k] = ld8_raw(dh + kP * N + 8 * piece);
+      }
+    }
+  };
+  load_head(h0);
+
+  // tiles of this wave: pairs (i tile, two j tiles); (n tile, IT token
+  // tiles); (p tile, two token tiles)
+  const int it = w >> 1, jt0 = 2 * (w & 1);
+  const int nt = w % NT, ti0 = (w / NT) * IT;
+  const int pt = w & 3, jx0 = 2 * (w >> 2);
+  f32x4 S[2], V[2], dBa[IT], dCa[IT];
+  const f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) S[k] = V[k] = zero4;
+#pragma unroll
+  for (int k = 0; k < IT; ++k) dBa[k] = dCa[k] = zero4;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (jt0 + k <= it) {
+#pragma unroll
+      for (int kk = 0; kk < KN; ++kk)
+        S[k] = mfma(frag<N>(sm.C, 16 * it, 32 * kk), frag<N>(sm.B, 16 * (jt0 + k), 32 * kk), S[k]);
+    }
+
+  for (int k = 0; k < nh; ++k) {
+    const int64_t h = h0 + k;
+    const float *cs = sm.cs[k], *dt = sm.dt[k];
+    // ---- stage the head (its tiles' last readers passed the barrier before)
+    {
+      const int t = tid >> 3, p0 = (tid & 7) * 8;
+      *reinterpret_cast<uint4 *>(&sm.x[swz<kP>(t, p0)]) = xv;
+      *reinterpret_cast<uint4 *>(&sm.g[swz<kP>(t, p0)]) = gv;
+    }
+    if (tid < HPIECES) {
+      const int row = 16 * tid / N, n0 = (16 * tid) % N;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t word = raw_word(hv, 2 * half + (i >> 1));
+          const int sh0 = (i & 1) * 16;
+          const float a = static_cast<float>(static_cast<int8_t>(word >> sh0)) * sc;
+          const float b = static_cast<float>(static_cast<int8_t>(word >> (sh0 + 8))) * sc;
+          o[i] = pack_bf2(a, b);
+        }
+        *reinterpret_cast<uint4 *>(&sm.H[swz<N>(row, n0 + 8 * half)]) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < BC; ++b) {
+      const int piece = tid + 512 * b;
+      if (piece < kP * G8) {
+        const int o = swz<N>(piece / G8, (piece % G8) * 8);
+        *reinterpret_cast<uint4 *>(&sm.dh[0][o]) = dv[0][b];
+        *reinterpret_cast<uint4 *>(&sm.dh[1][o]) = dv[1][b];
+      }
+    }
+    __syncthreads();
+    if (k + 1 < nh) load_head(h + 1);
+    const float cse = cs[kQ - 1];
+
+    // ---- the pairs: lane holds (i = 16 it + 4 kq + ii, j = 16 jt + r)
+    float rowsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const float4 ci4 = *reinterpret_cast<const float4 *>(&cs[16 * it + 4 * kq]);
+    const float ci[4] = {ci4.x, ci4.y, ci4.z, ci4.w};
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      const int jt = jt0 + a;
+      if (jt <= it) {
+        f32x4 m = zero4;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) m = mfma(frag<kP>(sm.g, 16 * it, 32 * kk), frag<kP>(sm.x, 16 * jt, 32 * kk), m);
+        const int j = 16 * jt + r;
+        const float cj = cs[j], dj = dt[j];
+        float u[4], col = 0.0f;
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          const bool in = 16 * it + 4 * kq + ii >= j;
+          const float L = in ? fast_exp2((ci[ii] - cj) * kLog2e) : 0.0f;
+          u[ii] = in ? S[a][ii] * L : 0.0f;
+          const float ml = in ? m[ii] * L : 0.0f;
+          V[a][ii] = fmaf(ml, dj, V[a][ii]);
+          const float G = in ? u[ii] * m[ii] : 0.0f;
+          col += G;
+          rowsum[ii] = fmaf(G, dj, rowsum[ii]);
+        }
+        uint2 hi, lo;
+        split_bf2(u[0], u[1], hi.x, lo.x);
+        split_bf2(u[2], u[3], hi.y, lo.y);
+        const int o = swz<kQ>(j, 16 * it + 4 * kq);
+        *reinterpret_cast<uint2 *>(&sm.U[0][o]) = hi;
+        *reinterpret_cast<uint2 *>(&sm.U[1][o]) = lo;
+        col = sum_kq(col);
+        if (kq == 0) sm.col[it][j] = col;
+      }
+    }
+#pragma unroll
+    for (int ii = 0; ii < 4; ++ii) {
+      rowsum[ii] = sum_r(rowsum[ii]);
+      if (r == 0) sm.row[w & 1][16 * it + 4 * kq + ii] = rowsum[ii];
+    }
+
+    // ---- H^T g and dH^T x: lane holds (n = 16 nt + 4 kq + ii, token = 16 ti + r)
+    {
+      bf16x8 hf[2], df[2][2];
+      float hh = 0.0f;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        hf[kk] = frag_t<N>(sm.H, 32 * kk, 16 * nt);
+        df[0][kk] = frag_t<N>(sm.dh[0], 32 * kk, 16 * nt);
+        df[1][kk] = frag_t<N>(sm.dh[1], 32 * kk, 16 * nt);
+        if (ti0 == 0) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            hh = fmaf(static_cast<float>(hf[kk][i]), static_cast<float>(df[0][kk][i]) + static_cast<float>(df[1][kk][i]), hh);
+        }
+      }
+      hh = sum_wave(hh);
+      if (l == 0) sm.hh[w] = hh;
+#pragma unroll
+      for (int a = 0; a < IT; ++a) {
+        const int t = 16 * (ti0 + a) + r;
+        f32x4 c = zero4, b = zero4;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          const bf16x8 gf = frag<kP>(sm.g, 16 * (ti0 + a), 32 * kk), xf = frag<kP>(sm.x, 16 * (ti0 + a), 32 * kk);
+          c = mfma(hf[kk], gf, c);
+          b = mfma(df[0][kk], xf, b);
+          b = mfma(df[1][kk], xf, b);
+        }
+        const float e = fast_exp2(cs[t] * kLog2e), wj = fast_exp2((cse - cs[t]) * kLog2e) * dt[t];
+        c *= e;
+        dCa[a] += c;
+        dBa[a] += b * wj;
+        const uint2 cw = *reinterpret_cast<const uint2 *>(&sm.C[swz<N>(t, 16 * nt + 4 * kq)]);
+        float qs = c[0] * __uint_as_float(cw.x << 16);
+        qs = fmaf(c[1], __uint_as_float(cw.x & 0xffff0000u), qs);
+        qs = fmaf(c[2], __uint_as_float(cw.y << 16), qs);
+        qs = fmaf(c[3], __uint_as_float(cw.y & 0xffff0000u), qs);
+        qs = sum_kq(qs);
+        if (kq == 0) sm.q[nt][t] = qs;
+      }
+    }
+    __syncthreads();
+
+    // ---- dx: lane holds (p = 16 pt + 4 kq + ii, j = 16 jt + r)
+    {
+      float dd4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      const int pc = 16 * pt + 4 * kq;
+      float Dv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (p.D) {
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) Dv[ii] = p.D_per_channel ? p.D[h * kP + pc + ii] : p.D[h];
+      }
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const int jt = jx0 + a, j = 16 * jt + r;
+        f32x4 st = zero4, pr = zero4;
+#pragma unroll
+        for (int kk = 0; kk < KN; ++kk) {
+          const bf16x8 bf = frag<N>(sm.B, 16 * jt, 32 * kk);
+          st = mfma(frag<N>(sm.dh[0], 16 * pt, 32 * kk), bf, st);
+          st = mfma(frag<N>(sm.dh[1], 16 * pt, 32 * kk), bf, st);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+          if (32 * (kk + 1) > 16 * jt) {
+            const bf16x8 gf = frag_t<kP>(sm.g, 32 * kk, 16 * pt);
+            pr = mfma(gf, frag<kQ>(sm.U[0], 16 * jt, 32 * kk), pr);
+            pr = mfma(gf, frag<kQ>(sm.U[1], 16 * jt, 32 * kk), pr);
+          }
+        st *= fast_exp2((cse - cs[j]) * kLog2e);
+        const uint2 xw = *reinterpret_cast<const uint2 *>(&sm.x[swz<kP>(j, pc)]);
+        const uint2 gw = *reinterpret_cast<const uint2 *>(&sm.g[swz<kP>(j, pc)]);
+        const float xf[4] = {__uint_as_float(xw.x << 16), __uint_as_float(xw.x & 0xffff0000u), __uint_as_float(xw.y << 16),
+                             __uint_as_float(xw.y & 0xffff0000u)};
+        const float gf[4] = {__uint_as_float(gw.x << 16), __uint_as_float(gw.x & 0xffff0000u), __uint_as_float(gw.y << 16),
+                             __uint_as_float(gw.y & 0xffff0000u)};
+        float rs = 0.0f, o[4];
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          rs = fmaf(xf[ii], st[ii], rs);
+          dd4[ii] = fmaf(gf[ii], xf[ii], dd4[ii]);
+          o[ii] = fmaf(dt[j], pr[ii] + st[ii], Dv[ii] * gf[ii]);
+        }
+        rs = sum_kq(rs);
+        if (kq == 0) sm.r[pt][j] = rs;
+        if (j < len)
+          *reinterpret_cast<uint2 *>(p.dx + (t0 + j) * p.dxs + h * kP + pc) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+      }
+      if (p.D) {   // this wave's tokens' part of each channel's sum
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          dd4[ii] = sum_r(dd4[ii]);
+          if (r == 0) sm.dd[w >> 2][pc + ii] = dd4[ii];
+        }
+      }
+    }
+    __syncthreads();
+
+    // ---- the steps: wave 0, lane = token
+    if (w == 0) {
+      const float d = dt[l];
+      const float rs = (sm.r[0][l] + sm.r[1][l]) + (sm.r[2][l] + sm.r[3][l]);
+      const float direct = (sm.col[0][l] + sm.col[1][l]) + (sm.col[2][l] + sm.col[3][l]) + rs;
+      float qs = 0.0f;
+#pragma unroll
+      for (int a = 0; a < NT; ++a) qs += sm.q[a][l];
+      float dcs = sm.row[0][l] + sm.row[1][l] + qs - d * direct;
+      float hh = 0.0f;
+#pragma unroll
+      for (int a = 0; a < 8; ++a) hh += sm.hh[a];
+      const float into_end = fmaf(fast_exp2(cse * kLog2e), hh, sum_wave(d * rs));
+      if (l == kQ - 1) dcs += into_end;
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const float o = __shfl_down(dcs, off);
+        if (l + off < 64) dcs += o;
+      }
+      const float Ah = p.A[h], v = sm.v[k][l];
+      float dd = fmaf(Ah, dcs, direct);
+      if (p.dt_limit) {
+        const float sp = p.softplus ? softplus_acc(v) : v;
+        if (!(sp >= p.dt_min && sp <= p.dt_max)) dd = 0.0f;
+      }
+      if (p.softplus) dd *= fast_rcp(1.0f + fast_exp2(-v * kLog2e));
+      if (l >= len) dd = 0.0f;
+      else p.ddt[(t0 + l) * p.ddts + h] = static_cast<uint16_t>(float_to_half_bits<1>(dd));
+      const float dA = sum_wave(d * dcs), db = sum_wave(dd);
+      if (l == 0) {
+        p.ws_sum[(entry * p.nheads + h) * 2] = dA;
+        p.ws_sum[(entry * p.nheads + h) * 2 + 1] = db;
+      }
+      if (p.D) {
+        const float s = sm.dd[0][l] + sm.dd[1][l];
+        if (p.D_per_channel) p.ws_dd[(entry * p.nheads + h) * kP + l] = s;
+        else if (const float all = sum_wave(s); l == 0) p.ws_dd[entry * p.nheads + h] = all;
+      }
+    }
+  }
+
+  // ---- the pair parts of dB and dC, from the heads' summed M L dt'
+  __syncthreads();
+  uint16_t *Vh = sm.dh[0], *Vl = sm.dh[1];
+#pragma unroll
+  for (int a = 0; a < 2; ++a) {
+    uint2 hi, lo;
+    split_bf2(V[a][0], V[a][1], hi.x, lo.x);
+    split_bf2(V[a][2], V[a][3], hi.y, lo.y);
+    const int o = swz<kQ>(16 * (jt0 + a) + r, 16 * it + 4 * kq);
+    *reinterpret_cast<uint2 *>(&Vh[o]) = hi;
+    *reinterpret_cast<uint2 *>(&Vl[o]) = lo;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) {
+    const bf16x8 bt = frag_t<N>(sm.B, 32 * kk, 16 * nt), ct = frag_t<N>(sm.C, 32 * kk, 16 * nt);
+#pragma unroll
+    for (int a = 0; a < IT; ++a) {
+      const int tt = 16 * (ti0 + a);
+      dCa[a] = mfma(bt, frag_t<kQ>(Vh, 32 * kk, tt), dCa[a]);
+      dCa[a] = mfma(bt, frag_t<kQ>(Vl, 32 * kk, tt), dCa[a]);
+      dBa[a] = mfma(ct, frag<kQ>(Vh, tt, 32 * kk), dBa[a]);
+      dBa[a] = mfma(ct, frag<kQ>(Vl, tt, 32 * kk), dBa[a]);
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < IT; ++a) {
+    const int t = 16 * (ti0 + a) + r, n0 = 16 * nt + 4 * kq;
+    if (t < len) {
+      if (p.ws_bc) {
+        const int64_t plane = p.hb_per_group * p.total * p.ngroups * N;
+        float *o = p.ws_bc + ((hb * p.total + t0 + t) * p.ngroups + gr) * N + n0;
+        *reinterpret_cast<float4 *>(o) = make_float4(dBa[a][0], dBa[a][1], dBa[a][2], dBa[a][3]);
+        *reinterpret_cast<float4 *>(o + plane) = make_float4(dCa[a][0], dCa[a][1], dCa[a][2], dCa[a][3]);
+      } else {
+        *reinterpret_cast<uint2 *>(p.dB + (t0 + t) * p.dbs + gr * N + n0) =
+            make_uint2(pack_bf2(dBa[a][0], dBa[a][1]), pack_bf2(dBa[a][2], dBa[a][3]));
+        *reinterpret_cast<uint2 *>(p.dC + (t0 + t) * p.dcs + gr * N + n0) =
+            make_uint2(pack_bf2(dCa[a][0], dCa[a][1]), pack_bf2(dCa[a][2], dCa[a][3]));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// (3) the sums over head blocks and chunks
+// ---------------------------------------------------------------------------
+
+__global__ void __launch_bounds__(256) bc_sum_kernel(const float *ws, uint16_t *dB, uint16_t *dC, int64_t total,
+                                                     int64_t row, int64_t dbs, int64_t dcs, int blocks) {
+  const int64_t plane = total * row;
+  const float *from = ws + (blockIdx.y ? blocks * plane : 0);
+  uint16_t *to = blockIdx.y ? dC : dB;
+  const int64_t stride = blockIdx.y ? dcs : dbs;
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= plane) return;
+  float4 a = *reinterpret_cast<const float4 *>(from + i);
+  for (int k = 1; k < blocks; ++k) {
+    const float4 b = *reinterpret_cast<const float4 *>(from + k * plane + i);
+    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
+  }
+  const int64_t t = i / row, c = i - t * row;
+  *reinterpret_cast<uint2 *>(to + t * stride + c) = make_uint2(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w));
+}
+
+// Column sums of (entries, cols) partials in 64 bits: workgroup = 64 columns,
+// four threads each.  PAIR: columns are (head, {dA, ddt_bias}).
+template <bool PAIR>
+__global__ void __launch_bounds__(256) entry_sum_kernel(const float *part, float *a, float *b, int64_t entries, int64_t cols) {
+  __shared__ double sum[4][64];
+  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  double v = 0.0;
+  if (col < cols)
+    for (int64_t e = entries * q / 4; e < entries * (q + 1) / 4; ++e) v += part[e * cols + col];
+  sum[q][lane] = v;
+  __syncthreads();
+  if (q == 0 && col < cols) {
+    const float s = static_cast<float>((sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]));
+    if constexpr (PAIR) {
+      if (!(col & 1)) a[col >> 1] = s;
+      else if (b) b[col >> 1] = s;
+    } else {
+      a[col] = s;
+    }
+  }
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct BwdPlan {
+  int nseg, hb_heads, hb_per_group;
+  int64_t seg_chunks, entries;
+  size_t off_state, off_decay, off_bc, off_sum, off_dd, bytes;
+};
+
+BwdPlan bwd_plan(const ssd_varlen_args_t *a, int cus) {
+  BwdPlan pl{};
+  pl.entries = ssd_checkpoint_slots(a->total, a->nseq);
+  const int64_t SH = a->nseq * a->nheads, hpg = a->nheads / a->ngroups;
+  // adjoint segments
+  int64_t nchunks = (a->max_seqlen + kQ - 1) / kQ;
+  if (nchunks < 1) nchunks = 1;
+  int64_t G = 1;
+  if (a->seq_segments >= 1) {
+    G = a->seq_segments;
+  } else {
+    const int64_t full_rows = (pl.entries + nchunks - 1) / nchunks;
+    const int64_t busy = (full_rows < a->nseq ? full_rows : a->nseq) * a->nheads;
+    const int64_t want = 3LL * cus;
+    if (busy < want) G = (want + busy - 1) / busy;
+    if (G > nchunks / 2) G = nchunks / 2;
+    if (G < 1) G = 1;
+  }
+  if (G > nchunks) G = nchunks;
+  if (G > 65535) G = 65535;
+  pl.seg_chunks = (nchunks + G - 1) / G;
+  pl.nseg = static_cast<int>((nchunks + pl.seg_chunks - 1) / pl.seg_chunks);
+  // head blocks: enough workgroups for four rounds, as few partial dB and dC
+  // as that allows
+  int64_t per = (4LL * cus + pl.entries * a->ngroups - 1) / (pl.entries * a->ngroups);
+  if (per < (hpg + kMaxHeads - 1) / kMaxHeads) per = (hpg + kMaxHeads - 1) / kMaxHeads;
+  if (per > hpg) per = hpg;
+  pl.hb_heads = static_cast<int>((hpg + per - 1) / per);
+  pl.hb_per_group = static_cast<int>((hpg + pl.hb_heads - 1) / pl.hb_heads);
+  size_t at = up256(static_cast<size_t>(pl.entries) * a->nheads * 2 * kP * a->dstate * sizeof(uint16_t));
+  pl.off_state = at;
+  if (pl.nseg > 1) at += up256(static_cast<size_t>(pl.nseg - 1) * SH * kP * a->dstate * sizeof(float));
+  pl.off_decay = at;
+  if (pl.nseg > 1) at += up256(static_cast<size_t>(pl.nseg - 1) * SH * sizeof(float));
+  pl.off_bc = at;
+  if (pl.hb_per_group > 1)
+    at += up256(2 * static_cast<size_t>(pl.hb_per_group) * a->total * a->ngroups * a->dstate * sizeof(float));
+  pl.off_sum = at;
+  at += up256(static_cast<size_t>(pl.entries) * a->nheads * 2 * sizeof(float));
+  pl.off_dd = at;
+  if (a->D) at += up256(static_cast<size_t>(pl.entries) * a->nheads * (a->D_per_channel ? kP : 1) * sizeof(float));
+  pl.bytes = at;
+  return pl;
+}
+
+template <int N>
+hipError_t launch_bwd(const BwdParams &p, const BwdPlan &pl, hipStream_t stream) {
+  const unsigned sh = static_cast<unsigned>(p.nseq * p.nheads);
+  hipError_t e;
+  if (pl.nseg > 1) {
+    hipLaunchKernelGGL((adjoint_kernel<N, false>), dim3(sh, pl.nseg - 1), dim3(256), 0, stream, p);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((adjoint_kernel<N, true>), dim3(sh, pl.nseg), dim3(256), 0, stream, p);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  const unsigned lds = sizeof(ChunkLds<N>);
+  e = hipFuncSetAttribute(reinterpret_cast<const void *>(&chunk_kernel<N>), hipFuncAttributeMaxDynamicSharedMemorySize,
+                          static_cast<int>(lds));
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(chunk_kernel<N>, dim3(static_cast<unsigned>(pl.entries), static_cast<unsigned>(p.ngroups * pl.hb_per_group)),
+                     dim3(512), lds, stream, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace ssm
+
+using namespace ssm;
+
+extern "C" int ssd_varlen_bwd_workspace_size(const ssd_varlen_bwd_args_t *a, size_t *bytes) {
+  const int st = ssd_varlen_bwd_validate(a);
+  if (st != SSM_OK) return st;
+  if (!bytes) return SSM_ERR_NULL;
+  *bytes = bwd_plan(&a->fwd, cu_count_cached()).bytes;
+  return SSM_OK;
+}
+
+extern "C" int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *a, void *stream_ptr) {
+  const int st = ssd_varlen_bwd_validate(a);
+  if (st != SSM_OK) return st;
+  const ssd_varlen_args_t &f = a->fwd;
+  const BwdPlan pl = bwd_plan(&f, cu_count_cached());
+  if (!a->workspace || a->workspace_bytes < pl.bytes) return SSM_ERR_WORKSPACE;
+  if (!aligned16(a->workspace)) return SSM_ERR_UNSUPPORTED;
+  if (f.nseq * f.nheads > 0x7fffffffLL || pl.entries > 0x7fffffffLL || f.ngroups * pl.hb_per_group > 65535)
+    return SSM_ERR_SHAPE;
+  char *ws = static_cast<char *>(a->workspace);
+  BwdParams p{};
+  p.x = static_cast<const uint16_t *>(f.x); p.xs = f.x_stride;
+  p.dt = static_cast<const uint16_t *>(f.dt); p.dts = f.dt_stride;
+  p.B = static_cast<const uint16_t *>(f.B); p.bs = f.B_stride;
+  p.C = static_cast<const uint16_t *>(f.C); p.cs = f.C_stride;
+  p.g = static_cast<const uint16_t *>(a->dout); p.gs = a->dout_stride;
+  p.A = f.A; p.D = f.D; p.dt_bias = f.dt_bias; p.dfin = a->dfinal_states;
+  p.cu = f.cu_seqlens; p.codes = f.checkpoints; p.scales = f.checkpoint_scales;
+  p.dx = static_cast<uint16_t *>(a->dx); p.dxs = a->dx_stride;
+  p.ddt = static_cast<uint16_t *>(a->ddt); p.ddts = a->ddt_stride;
+  p.dB = static_cast<uint16_t *>(a->dB); p.dbs = a->dB_stride;
+  p.dC = static_cast<uint16_t *>(a->dC); p.dcs = a->dC_stride;
+  p.dinit = a->dinitial_states;
+  p.ws_dh = reinterpret_cast<uint16_t *>(ws);
+  p.ws_state = reinterpret_cast<float *>(ws + pl.off_state);
+  p.ws_decay = reinterpret_cast<float *>(ws + pl.off_decay);
+  p.ws_bc = pl.hb_per_group > 1 ? reinterpret_cast<float *>(ws + pl.off_bc) : nullptr;
+  p.ws_sum = reinterpret_cast<float *>(ws + pl.off_sum);
+  p.ws_dd = reinterpret_cast<float *>(ws + pl.off_dd);
+  p.total = f.total; p.nseq = f.nseq; p.max_seqlen = f.max_seqlen;
+  p.nheads = f.nheads; p.ngroups = f.ngroups;
+  p.seg_chunks = pl.seg_chunks; p.nseg = pl.nseg; p.entries = pl.entries;
+  p.hb_heads = pl.hb_heads; p.hb_per_group = pl.hb_per_group;
+  p.softplus = f.dt_softplus; p.D_per_channel = f.D_per_channel;
+  p.dt_limit = f.dt_limit; p.dt_min = f.dt_min; p.dt_max = f.dt_max;
+  hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
+  hipError_t e = f.dstate == 32 ? launch_bwd<32>(p, pl, stream)
+                 : f.dstate == 64 ? launch_bwd<64>(p, pl, stream) : launch_bwd<128>(p, pl, stream);
+  if (e != hipSuccess) return hip_fail(e);
+  if (p.ws_bc) {
+    const int64_t row = f.ngroups * f.dstate, quads = (f.total * row + 1023) / 1024;
+    hipLaunchKernelGGL(bc_sum_kernel, dim3(static_cast<unsigned>(quads), 2), dim3(256), 0, stream, p.ws_bc, p.dB, p.dC,
+                       f.total, row, a->dB_stride, a->dC_stride, pl.hb_per_group);
+    if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e);
+  }
+  hipLaunchKernelGGL(entry_sum_kernel<true>, dim3(static_cast<unsigned>((2 * f.nheads + 63) / 64)), dim3(256), 0, stream,
+                     p.ws_sum, a->dA, f.dt_bias ? a->ddt_bias : nullptr, pl.entries, 2 * f.nheads);
+  if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e);
+  if (f.D) {
+    const int64_t cols = f.nheads * (f.D_per_channel ? kP : 1);
+    hipLaunchKernelGGL(entry_sum_kernel<false>, dim3(static_cast<unsigned>((cols + 63) / 64)), dim3(256), 0, stream, p.ws_dd,
+                       a->dD, nullptr, pl.entries, cols);
+    if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e);
+  }
+  return SSM_OK;
+}

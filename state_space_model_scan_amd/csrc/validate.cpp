@@ -238,6 +238,142 @@ extern "C" int ssd_state_passing_validate(int64_t nchunks, int64_t batch, int64_
   return SSM_OK;
 }
 
+// Packed tokens: the short conv, the chunked scan and its step.
+namespace {
+
+bool io_ok(int32_t io) { return io == SSM_F32 || io == SSM_BF16 || io == SSM_F16; }
+bool flag_ok(int32_t v) { return v == 0 || v == 1; }
+uintptr_t bits(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
+int conv_varlen_common(const causal_conv1d_varlen_args_t *a) {
+  if (!a) return SSM_ERR_NULL;
+  if (!positive(a->total) || !positive(a->nseq) || !positive(a->channels)) return SSM_ERR_SHAPE;
+  if (a->total > 0x7fffffffLL || a->nseq > 0x7fffffffLL) return SSM_ERR_SHAPE;   // int32 edges
+  if (a->channels > 0x7fffffffLL || a->x_stride < a->channels || !product_fits(a->total, a->x_stride, 1))
+    return SSM_ERR_SHAPE;
+  if (!io_ok(a->io_dtype)) return SSM_ERR_UNSUPPORTED;
+  if (a->width != SSM_CONV_WIDTH) return SSM_ERR_UNSUPPORTED;
+  if (a->act != SSM_ACT_NONE && a->act != SSM_ACT_SILU) return SSM_ERR_UNSUPPORTED;
+  if (!a->x || !a->weight || !a->cu_seqlens) return SSM_ERR_NULL;
+  return SSM_OK;
+}
+
+// what the packed scan's forward and backward share
+int ssd_varlen_common(const ssd_varlen_args_t *a) {
+  if (!a) return SSM_ERR_NULL;
+  if (!positive(a->total) || !positive(a->nseq) || a->max_seqlen < 0 || !positive(a->nheads) ||
+      !positive(a->headdim) || !positive(a->dstate) || !positive(a->ngroups))
+    return SSM_ERR_SHAPE;
+  if (a->total > 0x7fffffffLL || a->nseq > 0x7fffffffLL || a->max_seqlen > a->total) return SSM_ERR_SHAPE;
+  if (a->nheads > 65535 || a->nheads % a->ngroups != 0) return SSM_ERR_SHAPE;
+  if (a->io_dtype != SSM_BF16) return SSM_ERR_UNSUPPORTED;
+  if (a->headdim != SSD_HEADDIM) return SSM_ERR_UNSUPPORTED;
+  if (a->dstate != 32 && a->dstate != 64 && a->dstate != 128) return SSM_ERR_UNSUPPORTED;
+  const int64_t hp = a->nheads * a->headdim, gn = a->ngroups * a->dstate;
+  if (a->x_stride < hp || a->B_stride < gn || a->C_stride < gn || a->dt_stride < a->nheads ||
+      !product_fits(a->total, a->x_stride, 1) || !product_fits(a->total, a->B_stride, 1) ||
+      !product_fits(a->total, a->C_stride, 1) || !product_fits(a->total, a->dt_stride, 1) ||
+      !product_fits(a->total / SSD_CHUNK + a->nseq, hp, a->dstate))
+    return SSM_ERR_SHAPE;
+  if (!flag_ok(a->D_per_channel) || !flag_ok(a->dt_softplus) || !flag_ok(a->dt_limit)) return SSM_ERR_UNSUPPORTED;
+  if (a->dt_limit && !(a->dt_min <= a->dt_max)) return SSM_ERR_SHAPE;
+  if (a->seq_segments < 0) return SSM_ERR_SHAPE;
+  if (!a->x || !a->dt || !a->A || !a->B || !a->C || !a->cu_seqlens) return SSM_ERR_NULL;
+  if ((bits(a->x) | bits(a->B) | bits(a->C)) & 15u) return SSM_ERR_UNSUPPORTED;
+  if ((a->x_stride | a->B_stride | a->C_stride) & 7) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" int causal_conv1d_varlen_fwd_validate(const causal_conv1d_varlen_args_t *a) {
+  const int st = conv_varlen_common(a);
+  if (st != SSM_OK) return st;
+  if (!a->out) return SSM_ERR_NULL;
+  if (a->out_stride < a->channels || !product_fits(a->total, a->out_stride, 1)) return SSM_ERR_SHAPE;
+  if (a->conv_state) {
+    if (!positive(a->state_slots) || a->state_len < a->width) return SSM_ERR_SHAPE;
+    if (a->state_len > SSM_MAX_CONV_STATE) return SSM_ERR_UNSUPPORTED;
+    if (!product_fits(a->state_slots, a->channels, a->state_len)) return SSM_ERR_SHAPE;
+  }
+  return SSM_OK;
+}
+
+extern "C" int causal_conv1d_varlen_bwd_validate(const causal_conv1d_varlen_args_t *a) {
+  const int st = conv_varlen_common(a);
+  if (st != SSM_OK) return st;
+  if (!a->dout || !a->dx || !a->dweight || (a->bias && !a->dbias)) return SSM_ERR_NULL;
+  if (a->dout_stride < a->channels || a->dx_stride < a->channels || !product_fits(a->total, a->dout_stride, 1) ||
+      !product_fits(a->total, a->dx_stride, 1))
+    return SSM_ERR_SHAPE;
+  return SSM_OK;
+}
+
+extern "C" int64_t ssd_checkpoint_slots(int64_t total, int64_t nseq) { return total / SSD_CHUNK + nseq; }
+
+extern "C" int ssd_varlen_fwd_validate(const ssd_varlen_args_t *a) {
+  const int st = ssd_varlen_common(a);
+  if (st != SSM_OK) return st;
+  if (!a->out || (!a->checkpoints) != (!a->checkpoint_scales)) return SSM_ERR_NULL;
+  const int64_t hp = a->nheads * a->headdim;
+  if (a->out_stride < hp || !product_fits(a->total, a->out_stride, 1)) return SSM_ERR_SHAPE;
+  if ((bits(a->out) & 15u) || (a->out_stride & 7)) return SSM_ERR_UNSUPPORTED;
+  if (a->z) {
+    if (a->z_stride < hp || !product_fits(a->total, a->z_stride, 1)) return SSM_ERR_SHAPE;
+    if ((bits(a->z) & 15u) || (a->z_stride & 7)) return SSM_ERR_UNSUPPORTED;
+  }
+  if (a->ssm_state && (!positive(a->state_slots) || !product_fits(a->state_slots, hp, a->dstate))) return SSM_ERR_SHAPE;
+  if (bits(a->ssm_state) & 15u || bits(a->checkpoints) & 15u) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+extern "C" int ssd_varlen_bwd_validate(const ssd_varlen_bwd_args_t *a) {
+  if (!a) return SSM_ERR_NULL;
+  const ssd_varlen_args_t &f = a->fwd;
+  const int st = ssd_varlen_common(&f);
+  if (st != SSM_OK) return st;
+  if (f.z) return SSM_ERR_UNSUPPORTED;
+  if (!f.checkpoints || !f.checkpoint_scales || !a->dout || !a->dx || !a->ddt || !a->dB || !a->dC || !a->dA ||
+      (f.D && !a->dD) || (f.dt_bias && !a->ddt_bias))
+    return SSM_ERR_NULL;
+  const int64_t hp = f.nheads * f.headdim, gn = f.ngroups * f.dstate;
+  if (a->dout_stride < hp || a->dx_stride < hp || a->ddt_stride < f.nheads || a->dB_stride < gn || a->dC_stride < gn ||
+      !product_fits(f.total, a->dout_stride, 1) || !product_fits(f.total, a->dx_stride, 1) ||
+      !product_fits(f.total, a->ddt_stride, 1) || !product_fits(f.total, a->dB_stride, 1) ||
+      !product_fits(f.total, a->dC_stride, 1))
+    return SSM_ERR_SHAPE;
+  if ((bits(a->dout) | bits(a->dx) | bits(a->dB) | bits(a->dC) | bits(f.checkpoints) | bits(a->dfinal_states) |
+       bits(a->dinitial_states)) & 15u)
+    return SSM_ERR_UNSUPPORTED;
+  if ((a->dout_stride | a->dx_stride | a->dB_stride | a->dC_stride) & 7) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+extern "C" int conv1d_ssd_update_validate(const conv1d_ssd_update_args_t *a) {
+  if (!a) return SSM_ERR_NULL;
+  if (!positive(a->batch) || !positive(a->nheads) || !positive(a->headdim) || !positive(a->dstate) ||
+      !positive(a->ngroups) || !positive(a->state_slots))
+    return SSM_ERR_SHAPE;
+  if (a->batch > 65535 || a->nheads > 65535 || a->nheads % a->ngroups != 0) return SSM_ERR_SHAPE;   // the grid
+  if (!io_ok(a->io_dtype) || a->headdim != SSD_HEADDIM) return SSM_ERR_UNSUPPORTED;
+  if (a->dstate != 32 && a->dstate != 64 && a->dstate != 128) return SSM_ERR_UNSUPPORTED;
+  if (a->width != SSM_CONV_WIDTH || a->state_len > SSM_MAX_CONV_STATE) return SSM_ERR_UNSUPPORTED;
+  if (a->act != SSM_ACT_NONE && a->act != SSM_ACT_SILU) return SSM_ERR_UNSUPPORTED;
+  if (!flag_ok(a->D_per_channel) || !flag_ok(a->dt_softplus) || !flag_ok(a->dt_limit)) return SSM_ERR_UNSUPPORTED;
+  if (a->dt_limit && !(a->dt_min <= a->dt_max)) return SSM_ERR_SHAPE;
+  const int64_t hp = a->nheads * a->headdim, c = hp + 2 * a->ngroups * a->dstate;
+  if (a->state_len < a->width || a->xBC_stride < c || a->dt_stride < a->nheads || a->out_stride < hp ||
+      (a->z && a->z_stride < hp))
+    return SSM_ERR_SHAPE;
+  if (!product_fits(a->batch, a->xBC_stride, 1) || !product_fits(a->batch, a->dt_stride, 1) ||
+      !product_fits(a->batch, a->out_stride, 1) || (a->z && !product_fits(a->batch, a->z_stride, 1)) ||
+      !product_fits(a->state_slots, hp, a->dstate) || !product_fits(a->state_slots, c, a->state_len))
+    return SSM_ERR_SHAPE;
+  if (!a->xBC || !a->dt || !a->A || !a->conv_weight || !a->conv_state || !a->ssm_state || !a->out) return SSM_ERR_NULL;
+  if ((bits(a->ssm_state) | bits(a->conv_weight)) & 15u) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
 extern "C" const char *ssm_status_str(int status) {
   switch (status) {
     case SSM_OK: return "ok";
