@@ -677,10 +677,13 @@ int64_t ssd_checkpoint_slots(int64_t total, int64_t nseq);
 /* Arguments of ssd_varlen_bwd: the forward's (fwd.z must be NULL: with the
  * gate outside the scan, as where a gated norm follows, its gradient belongs
  * there; fwd.out, ssm_state, cache_seqlens, slots and workspace are ignored;
- * fwd.checkpoints and scales are those that the forward wrote), and the
- * gradients, caller-allocated and fully overwritten. */
+ * fwd.checkpoints and scales are those that the forward wrote, or the same
+ * values laid out with other strides from entry to entry and head to head),
+ * and the gradients, caller-allocated and fully overwritten. */
 typedef struct ssd_varlen_bwd_args {
   ssd_varlen_args_t fwd;
+  int64_t code_entry_stride, code_head_stride;  /* multiples of 16; as the forward writes: h p n, p n */
+  int64_t scale_entry_stride, scale_head_stride;  /* h p, p */
   const void *dout; int64_t dout_stride;        /* (total, h, p) io */
   const float *dfinal_states;                   /* (nseq, h, p, n) fp32 or NULL (zero) */
   void *dx; int64_t dx_stride;                  /* (total, h, p) io */

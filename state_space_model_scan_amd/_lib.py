@@ -156,6 +156,7 @@ class SsdVarlenArgs(ctypes.Structure):
 class SsdVarlenBwdArgs(ctypes.Structure):
     """Mirror of ssd_varlen_bwd_args_t."""
     _fields_ = [("fwd", SsdVarlenArgs)] + _fields("""
+        q code_entry_stride q code_head_stride q scale_entry_stride q scale_head_stride
         p dout q dout_stride p dfinal_states p dx q dx_stride p ddt q ddt_stride p dB q dB_stride
         p dC q dC_stride p dA p dD p ddt_bias p dinitial_states p workspace z workspace_bytes""")
 

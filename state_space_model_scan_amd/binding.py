@@ -1109,8 +1109,8 @@ def _ssd_varlen_args(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_s
         raise ValueError(f"max_seqlen must be the longest sequence's length, at most {total}, got {max_seqlen}")
     if checkpoints is not None:
         rows = (ssd_checkpoint_slots(total, nseq), nheads, headdim)
-        _out_spec(checkpoints[0], "checkpoints[0]", rows + (dstate,), torch.int8, dev)
-        _out_spec(checkpoints[1], "checkpoints[1]", rows, f32, dev)
+        _spec(checkpoints[0], "checkpoints[0]", rows + (dstate,), torch.int8, dev)
+        _spec(checkpoints[1], "checkpoints[1]", rows, f32, dev)
     a = _lib.SsdVarlenArgs()
     x, B, C, z, dt = _tokens(x, 8), _tokens(B, 8), _tokens(C, 8), _tokens(z, 8), _tokens(dt)
     A, D, dt_bias, cu_seqlens = _dense(A), _dense(D), _dense(dt_bias), _dense(cu_seqlens)
@@ -1153,6 +1153,8 @@ def ssd_varlen_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     a, keep = _ssd_varlen_args(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_softplus, dt_limit,
                                checkpoints, seq_segments)
     dev, nseq = x.device, a.nseq
+    for i, t in enumerate(checkpoints or ()):
+        _out_spec(t, f"checkpoints[{i}]", t.shape, t.dtype, dev)
     _cache_spec(ssm_state, "ssm_state", (a.nheads, a.headdim, a.dstate), torch.float32, dev)
     cache_seqlens, slots = _int32(cache_seqlens, "cache_seqlens", nseq, dev), _int32(slots, "slots", nseq, dev)
     out = _tokens_out(out, "out", x.shape, x.dtype, dev, 8)
@@ -1181,7 +1183,7 @@ def ssd_varlen_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     """Gradients of ssd_varlen_fwd (without z) in a dict.
 
     ``dout``: (total, nheads, headdim) bf16; ``checkpoints``: what the forward
-    wrote.  dx, ddt, dB and dC come in bf16 (into the tensors given, which may
+    wrote, with any strides from entry to entry and head to head.  dx, ddt, dB and dC come in bf16 (into the tensors given, which may
     be parts of one row, or new ones), dA, dD and ddt_bias in float32.
     ``dfinal_states`` (nseq, nheads, headdim, dstate) float32 is the gradient
     of the sequences' last states; with ``want_dinitial_states`` that of their
@@ -1189,6 +1191,14 @@ def ssd_varlen_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     if checkpoints is None:
         raise ValueError("the backward needs the checkpoints that the forward wrote")
     a = _lib.SsdVarlenBwdArgs()
+    codes, scales = checkpoints
+    # any strides from entry to entry and head to head; a channel's states dense
+    if codes.dim() == 4 and not (codes[0, 0].is_contiguous() and codes.data_ptr() % 16 == 0 and codes.stride(0) % 16 == 0
+                                 and codes.stride(1) % 16 == 0 and min(codes.stride()[:2]) >= codes[0, 0].numel()):
+        codes = codes.clone(memory_format=torch.contiguous_format)
+    if scales.dim() == 3 and not (scales[0, 0].is_contiguous() and min(scales.stride()[:2]) >= scales.shape[2]):
+        scales = scales.clone(memory_format=torch.contiguous_format)
+    checkpoints = (codes, scales)
     a.fwd, keep = _ssd_varlen_args(x, dt, A, B, C, cu_seqlens, max_seqlen, D, None, dt_bias, dt_softplus, dt_limit,
                                    checkpoints, seq_segments)
     dev, f32, io = x.device, torch.float32, x.dtype
@@ -1208,6 +1218,8 @@ def ssd_varlen_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
         g["ddt_bias"] = torch.empty(dt_bias.shape, dtype=f32, device=dev)
     if want_dinitial_states:
         g["dinitial_states"] = torch.empty(states, dtype=f32, device=dev)
+    a.code_entry_stride, a.code_head_stride = codes.stride()[:2]
+    a.scale_entry_stride, a.scale_head_stride = scales.stride()[:2]
     a.dout, a.dout_stride, a.dfinal_states = _ptr(dout), _token_stride(dout), _ptr(dfinal_states)
     for k in ("dx", "ddt", "dB", "dC"):
         setattr(a, k, _ptr(g[k]))

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(256, 2) ssd_kernel(const SsdParams p) {
     }
     float dtraw = 0.0f;
     int32_t sid = 0;
-    if (w == 0) {
+    if (w == 0 || (VAR && w == 1)) {
       if (l < len) dtraw = bf2f(dtb[(t0 + l) * dtrow]);
       if constexpr (SEQ) sid = sidb[t0 + (l < len ? l : len - 1)];
     }
@@ -323,8 +323,11 @@ __global__ void __launch_bounds__(256, 2) ssd_kernel(const SsdParams p) {
         *reinterpret_cast<uint2 *>(&sC[swz8<N>(rr, 32 * kk + 8 * kq + 4)]) = make_uint2(cw.z, cw.w);
       }
     }
-    // ---- the steps and their running sum inside the chunk (padding: dt' = 0)
-    if (w == 0) {
+    // ---- the steps and their running sum inside the chunk (padding: dt' = 0).
+    // Packed tokens: wave 1 forms the state-update weights from the sum of the
+    // later steps themselves; the difference of two running sums would carry
+    // the rounding of the larger one.
+    if (w == 0 || (VAR && w == 1)) {
       float dtp = 0.0f;
       if (l < len) {
         const float v = dtraw + bias;
@@ -332,14 +335,25 @@ __global__ void __launch_bounds__(256, 2) ssd_kernel(const SsdParams p) {
         if (p.dt_limit) dtp = fminf(fmaxf(dtp, p.dt_min), p.dt_max);
       }
       float cs = dtp * Ah;
+      if (VAR && w == 1) {
+        cs = __shfl_down(cs, 1);
+        if (l == 63) cs = 0.0f;
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const float o = __shfl_up(cs, off);
-        if (l >= off) cs += o;
+        for (int off = 1; off < 64; off <<= 1) {
+          const float o = __shfl_down(cs, off);
+          if (l + off < 64) cs += o;
+        }
+        sW[l] = fast_exp2(cs * kLog2e) * dtp;
+      } else {
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const float o = __shfl_up(cs, off);
+          if (l >= off) cs += o;
+        }
+        sCs[l] = cs;
+        sDt[l] = dtp;
+        if constexpr (SEQ) sSid[l] = sid;
       }
-      sCs[l] = cs;
-      sDt[l] = dtp;
-      if constexpr (SEQ) sSid[l] = sid;
     }
     __syncthreads();
 
@@ -350,11 +364,11 @@ __global__ void __launch_bounds__(256, 2) ssd_kernel(const SsdParams p) {
     const bool carry = !SEQ || sid_last == sid_prev;
     // the state-update weights w_t = exp(cs_last - cs_t) * dt'_t, for the
     // tokens of the chunk's last sequence
-    if (tid < kQ) {
+    if (!VAR && tid < kQ) {
       const bool mine = !SEQ || sSid[tid] == sid_last;
       sW[tid] = mine ? fast_exp2((csl - sCs[tid]) * kLog2e) * sDt[tid] : 0.0f;
     }
-    if constexpr (!FULL) __syncthreads();
+    if constexpr (!FULL && !VAR) __syncthreads();
 
     if constexpr (FULL) {
       // ---- M, from G^T = B C^T: lane holds G[t = 16w + r][tau = 16 tb + 4kq + i],
@@ -475,20 +489,30 @@ __global__ void __launch_bounds__(256, 2) ssd_kernel(const SsdParams p) {
     for (int nt = 0; nt < NT; ++nt) accs[nt] *= dec;
 #pragma unroll
     for (int kk = 0; kk < kQ / 32; ++kk) {
-      // B operand: (X w) at tokens 32kk + 8kq + i, channel 16w + r, split hi / lo
+      // B operand: (X w) at tokens 32kk + 8kq + i, channel 16w + r, split into
+      // hi and lo; packed tokens: into three parts (all 24 bits), because the
+      // state is a 32-bit output and its 8-bit form is decided by it
       const uint4 xt = ld8_raw(&sXT[swz<kQ>(16 * w + r, 32 * kk + 8 * kq)]);
-      uint32_t xh[4], xl[4];
+      uint32_t xh[4], xl[4], xr2[4];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2)
-        split_bf2(bf2f(raw_bits(xt, i)) * sW[32 * kk + 8 * kq + i],
-                  bf2f(raw_bits(xt, i + 1)) * sW[32 * kk + 8 * kq + i + 1], xh[i / 2], xl[i / 2]);
+      for (int i = 0; i < 8; i += 2) {
+        const float a = bf2f(raw_bits(xt, i)) * sW[32 * kk + 8 * kq + i];
+        const float b = bf2f(raw_bits(xt, i + 1)) * sW[32 * kk + 8 * kq + i + 1];
+        split_bf2(a, b, xh[i / 2], xl[i / 2]);
+        if constexpr (VAR)
+          xr2[i / 2] = pack_bf2(a - __uint_as_float(xh[i / 2] << 16) - __uint_as_float(xl[i / 2] << 16),
+                                b - __uint_as_float(xh[i / 2] & 0xffff0000u) - __uint_as_float(xl[i / 2] & 0xffff0000u));
+      }
       const bf16x8 xhi = __builtin_bit_cast(bf16x8, make_uint4(xh[0], xh[1], xh[2], xh[3]));
       const bf16x8 xlo = __builtin_bit_cast(bf16x8, make_uint4(xl[0], xl[1], xl[2], xl[3]));
+      bf16x8 xrest = zero8;
+      if constexpr (VAR) xrest = __builtin_bit_cast(bf16x8, make_uint4(xr2[0], xr2[1], xr2[2], xr2[3]));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const bf16x8 bop = ld8(&sBT[swz<kQ>(16 * nt + r, 32 * kk + 8 * kq)]);
         accs[nt] = mfma(bop, xhi, accs[nt]);
         accs[nt] = mfma(bop, xlo, accs[nt]);
+        if constexpr (VAR) accs[nt] = mfma(bop, xrest, accs[nt]);
       }
     }
     sid_prev = sid_last;

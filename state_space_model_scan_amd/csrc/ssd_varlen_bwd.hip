@@ -65,6 +65,7 @@ struct BwdParams {
   float *ws_sum;                 // (entries, heads, 2): dA, ddt_bias
   float *ws_dd;                  // (entries, heads) or (entries, heads, p): dD
   int64_t xs, dts, bs, cs, gs, dxs, ddts, dbs, dcs;
+  int64_t code_entry, code_head, scale_entry, scale_head;
   int64_t total, nseq, max_seqlen, nheads, ngroups, seg_chunks, entries;
   int nseg, softplus, dt_limit, D_per_channel, hb_heads, hb_per_group;
   float dt_min, dt_max;
@@ -359,8 +360,8 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     gv = t < len ? ld8_raw(p.g + (t0 + t) * p.gs + h * kP + p0) : zero;
     const int64_t eh = entry * p.nheads + h;
     if (tid < HPIECES) {
-      hv = *reinterpret_cast<const uint4 *>(p.codes + eh * kP * N + 16 * tid);
-      sc = p.scales[eh * kP + 16 * tid / N];
+      hv = *reinterpret_cast<const uint4 *>(p.codes + entry * p.code_entry + h * p.code_head + 16 * tid);
+      sc = p.scales[entry * p.scale_entry + h * p.scale_head + 16 * tid / N];
     }
     const uint16_t *dh = p.ws_dh + eh * 2 * kP * N;
 #pragma unroll
@@ -816,6 +817,8 @@ extern "C" int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *a, void *stream_ptr) 
   p.ws_dd = reinterpret_cast<float *>(ws + pl.off_dd);
   p.total = f.total; p.nseq = f.nseq; p.max_seqlen = f.max_seqlen;
   p.nheads = f.nheads; p.ngroups = f.ngroups;
+  p.code_entry = a->code_entry_stride; p.code_head = a->code_head_stride;
+  p.scale_entry = a->scale_entry_stride; p.scale_head = a->scale_head_stride;
   p.seg_chunks = pl.seg_chunks; p.nseg = pl.nseg; p.entries = pl.entries;
   p.hb_heads = pl.hb_heads; p.hb_per_group = pl.hb_per_group;
   p.softplus = f.dt_softplus; p.D_per_channel = f.D_per_channel;

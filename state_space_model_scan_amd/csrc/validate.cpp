@@ -336,7 +336,17 @@ extern "C" int ssd_varlen_bwd_validate(const ssd_varlen_bwd_args_t *a) {
   if (!f.checkpoints || !f.checkpoint_scales || !a->dout || !a->dx || !a->ddt || !a->dB || !a->dC || !a->dA ||
       (f.D && !a->dD) || (f.dt_bias && !a->ddt_bias))
     return SSM_ERR_NULL;
-  const int64_t hp = f.nheads * f.headdim, gn = f.ngroups * f.dstate;
+  const int64_t hp = f.nheads * f.headdim, gn = f.ngroups * f.dstate, pn = f.headdim * f.dstate;
+  const int64_t entries = ssd_checkpoint_slots(f.total, f.nseq);
+  if ((entries > 1 && (a->code_entry_stride < pn || a->scale_entry_stride < f.headdim)) ||
+      (f.nheads > 1 && (a->code_head_stride < pn || a->scale_head_stride < f.headdim)))
+    return SSM_ERR_SHAPE;
+  if (!product_fits(entries, a->code_entry_stride > 0 ? a->code_entry_stride : 1, 1) ||
+      !product_fits(f.nheads, a->code_head_stride > 0 ? a->code_head_stride : 1, 1) ||
+      !product_fits(entries, a->scale_entry_stride > 0 ? a->scale_entry_stride : 1, 1) ||
+      !product_fits(f.nheads, a->scale_head_stride > 0 ? a->scale_head_stride : 1, 1))
+    return SSM_ERR_SHAPE;
+  if ((a->code_entry_stride | a->code_head_stride) & 15) return SSM_ERR_UNSUPPORTED;
   if (a->dout_stride < hp || a->dx_stride < hp || a->ddt_stride < f.nheads || a->dB_stride < gn || a->dC_stride < gn ||
       !product_fits(f.total, a->dout_stride, 1) || !product_fits(f.total, a->dx_stride, 1) ||
       !product_fits(f.total, a->ddt_stride, 1) || !product_fits(f.total, a->dB_stride, 1) ||

@@ -236,9 +236,13 @@ def _check_bwd(t, cu, what, dlast=None, strided=False, segments=0):
         row = torch.full((T, h * R.P + 2 * G * n), float("nan"), dtype=bf, device="cuda")
         given = dict(dx=row[:, :h * R.P].view(T, h, R.P), dB=row[:, h * R.P:h * R.P + G * n].view(T, G, n),
                      dC=row[:, h * R.P + G * n:].view(T, G, n), ddt=torch.zeros(T, h + 3, dtype=bf, device="cuda")[:, 3:])
+    held_codes, held_scales = codes.cuda(), scales.cuda()
+    if strided:   # laid out head by head
+        held_codes = held_codes.transpose(0, 1).contiguous().transpose(0, 1)
+        held_scales = held_scales.transpose(0, 1).contiguous().transpose(0, 1)
     call = lambda: binding.ssd_varlen_bwd(  # noqa: E731
         d["x"], d["dt"], d["A"], d["B"], d["C"], _ints(cu), max(b - a for a, b in zip(cu, cu[1:])), dout.cuda(),
-        (codes.cuda(), scales.cuda()), D=d["D"], dt_bias=d["dt_bias"], dfinal_states=_dev(dlast),
+        (held_codes, held_scales), D=d["D"], dt_bias=d["dt_bias"], dfinal_states=_dev(dlast),
         want_dinitial_states=True, seq_segments=segments, **given, **kw)
     got = call()
     for k in ("dx", "ddt", "dB", "dC"):

@@ -40,6 +40,7 @@ def _scan_bwd(fwd=None, **kw):
     a.dout = a.dx = a.ddt = a.dB = a.dC = a.dA = FAKE
     a.dout_stride = a.dx_stride = a.dB_stride = a.dC_stride = 256
     a.ddt_stride = 4
+    a.code_entry_stride, a.code_head_stride, a.scale_entry_stride, a.scale_head_stride = 4 * 64 * 128, 64 * 128, 256, 64
     for k, v in kw.items():
         setattr(a, k, v)
     return a
@@ -118,7 +119,9 @@ def test_scan_bwd_refuses_the_forwards_arguments(kw, want):
 
 @pytest.mark.parametrize("kw,want", [(dict(dout=None), N), (dict(dx=None), N), (dict(ddt=None), N), (dict(dA=None), N),
                                      (dict(dB=None), N), (dict(dC=None), N), (dict(dx_stride=8), S),
-                                     (dict(dx=FAKE + 2), U), (dict(dC_stride=260), U), (dict(ddt_stride=1), S)])
+                                     (dict(dx=FAKE + 2), U), (dict(dC_stride=260), U), (dict(ddt_stride=1), S),
+                                     (dict(code_entry_stride=64), S), (dict(code_head_stride=64 * 128 + 8), U),
+                                     (dict(scale_head_stride=32), S)])
 def test_scan_bwd_refusals(kw, want):
     assert _st("ssd_varlen_bwd", _scan_bwd(**kw)) == want
 
