@@ -102,24 +102,35 @@ __device__ __forceinline__ float chunk_step(const BwdParams &p, float raw, float
   return d;
 }
 
+// Element offset of (row, col) in a row-major tile of ROW_LEN bf16.  A row's
+// 16-byte groups are permuted by g = the row's last three bits rotated, so
+// that eight consecutive rows at one column (an operand read row by row) have
+// eight values of g, and four consecutive rows (a transposing read: 32 bytes
+// of each) four values of g / 2: neither meets in a bank.
+template <int ROW_LEN>
+__device__ __forceinline__ int tile_at(int row, int col) {
+  constexpr int GROUPS = ROW_LEN / 8;
+  const int g = (((row & 3) << 1) | ((row >> 2) & 1)) & (GROUPS - 1);
+  return row * ROW_LEN + (col & ~63) + ((col & 63) ^ (g << 3));
+}
+
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 // The operand fragment that a row-major tile holds column by column: lane
 // (r, kq) receives tile[row0 + 8 kq + i][col0 + r], i < 8.
 template <int ROW_LEN>
-__device__ __forceinline__ bf16x8 frag_t(uint16_t *tile, int row0, int col0) {
+__device__ __forceinline__ bf16x8 frag_t(int l, uint16_t *tile, int row0, int col0) {
   typedef __attribute__((address_space(3))) s16x4 *lds;
-  const int l = threadIdx.x & 63, i = l & 15, kq = l >> 4;
+  const int i = l & 15, kq = l >> 4;
   const int row = row0 + 8 * kq + (i >> 2), col = col0 + 4 * (i & 3);
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + swz<ROW_LEN>(row, col)));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + swz<ROW_LEN>(row + 4, col)));
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<ROW_LEN>(row, col)));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<ROW_LEN>(row + 4, col)));
   const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
   return __builtin_bit_cast(bf16x8, make_uint4(ua.x, ua.y, ub.x, ub.y));
 }
 // ... and row by row: lane (r, kq) receives tile[row0 + r][col0 + 8 kq + i].
 template <int ROW_LEN>
-__device__ __forceinline__ bf16x8 frag(const uint16_t *tile, int row0, int col0) {
-  const int l = threadIdx.x & 63;
-  return ld8(tile + swz<ROW_LEN>(row0 + (l & 15), col0 + 8 * (l >> 4)));
+__device__ __forceinline__ bf16x8 frag(int l, const uint16_t *tile, int row0, int col0) {
+  return ld8(tile + tile_at<ROW_LEN>(row0 + (l & 15), col0 + 8 * (l >> 4)));
 }
 
 // ---------------------------------------------------------------------------
@@ -204,12 +215,12 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int piece = tid + 256 * k;
-      *reinterpret_cast<uint4 *>(&sG[swz<kP>(piece >> 3, (piece & 7) * 8)]) = gv[k];
+      *reinterpret_cast<uint4 *>(&sG[tile_at<kP>(piece >> 3, (piece & 7) * 8)]) = gv[k];
     }
 #pragma unroll
     for (int k = 0; k < CPER; ++k) {
       const int piece = tid + 256 * k;
-      if (piece < CPIECES) *reinterpret_cast<uint4 *>(&sC[swz<N>(piece / (N / 8), (piece % (N / 8)) * 8)]) = cv[k];
+      if (piece < CPIECES) *reinterpret_cast<uint4 *>(&sC[tile_at<N>(piece / (N / 8), (piece % (N / 8)) * 8)]) = cv[k];
     }
     if (w == 0) {
       float cs, v;
@@ -224,7 +235,7 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
     for (int nt = 0; nt < NT; ++nt) acc[nt] *= end;
 #pragma unroll
     for (int kk = 0; kk < kQ / 32; ++kk) {
-      const uint4 gt = __builtin_bit_cast(uint4, frag_t<kP>(sG, 32 * kk, 16 * w));
+      const uint4 gt = __builtin_bit_cast(uint4, frag_t<kP>(l, sG, 32 * kk, 16 * w));
       uint32_t gh[4], gl[4];
 #pragma unroll
       for (int i = 0; i < 8; i += 2)
@@ -234,7 +245,7 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
       const bf16x8 lo = __builtin_bit_cast(bf16x8, make_uint4(gl[0], gl[1], gl[2], gl[3]));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const bf16x8 ct = frag_t<N>(sC, 32 * kk, 16 * nt);
+        const bf16x8 ct = frag_t<N>(l, sC, 32 * kk, 16 * nt);
         acc[nt] = mfma(ct, hi, acc[nt]);
         acc[nt] = mfma(ct, lo, acc[nt]);
       }
@@ -292,9 +303,10 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   constexpr int HPIECES = kP * N / 16;          // 16-code pieces of H
   extern __shared__ __attribute__((aligned(16))) char smem[];
   ChunkLds<N> &sm = *reinterpret_cast<ChunkLds<N> *>(smem);
-  const int tid = threadIdx.x, l = tid & 63, r = l & 15, kq = l >> 4;
+  const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
+  int l = lane, r = l & 15, kq = l >> 4;
   // the entry's sequence: the last s whose first entry is at or before it
   const int64_t entry = blockIdx.x;
   int64_t lo = 0, hi = p.nseq;
@@ -332,8 +344,8 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   for (int k = 0; k < BC; ++k) {
     const int piece = tid + 512 * k, t = piece / G8, n0 = (piece % G8) * 8;
     if (piece < kQ * G8) {
-      *reinterpret_cast<uint4 *>(&sm.B[swz<N>(t, n0)]) = t < len ? ld8_raw(p.B + (t0 + t) * p.bs + gr * N + n0) : zero;
-      *reinterpret_cast<uint4 *>(&sm.C[swz<N>(t, n0)]) = t < len ? ld8_raw(p.C + (t0 + t) * p.cs + gr * N + n0) : zero;
+      *reinterpret_cast<uint4 *>(&sm.B[tile_at<N>(t, n0)]) = t < len ? ld8_raw(p.B + (t0 + t) * p.bs + gr * N + n0) : zero;
+      *reinterpret_cast<uint4 *>(&sm.C[tile_at<N>(t, n0)]) = t < len ? ld8_raw(p.C + (t0 + t) * p.cs + gr * N + n0) : zero;
     }
   }
   for (int k = w; k < nh; k += 8) {
@@ -392,17 +404,22 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     if (jt0 + k <= it) {
 #pragma unroll
       for (int kk = 0; kk < KN; ++kk)
-        S[k] = mfma(frag<N>(sm.C, 16 * it, 32 * kk), frag<N>(sm.B, 16 * (jt0 + k), 32 * kk), S[k]);
+        S[k] = mfma(frag<N>(l, sm.C, 16 * it, 32 * kk), frag<N>(l, sm.B, 16 * (jt0 + k), 32 * kk), S[k]);
     }
 
   for (int k = 0; k < nh; ++k) {
     const int64_t h = h0 + k;
+    // the lane anew for every head: the tiles' addresses are then formed where
+    // they are used; kept over the loop they would take the registers
+    asm volatile("" : "+v"(l));
+    r = l & 15;
+    kq = l >> 4;
     const float *cs = sm.cs[k], *dt = sm.dt[k];
     // ---- stage the head (its tiles' last readers passed the barrier before)
     {
       const int t = tid >> 3, p0 = (tid & 7) * 8;
-      *reinterpret_cast<uint4 *>(&sm.x[swz<kP>(t, p0)]) = xv;
-      *reinterpret_cast<uint4 *>(&sm.g[swz<kP>(t, p0)]) = gv;
+      *reinterpret_cast<uint4 *>(&sm.x[tile_at<kP>(t, p0)]) = xv;
+      *reinterpret_cast<uint4 *>(&sm.g[tile_at<kP>(t, p0)]) = gv;
     }
     if (tid < HPIECES) {
       const int row = 16 * tid / N, n0 = (16 * tid) % N;
@@ -417,14 +434,14 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
           const float b = static_cast<float>(static_cast<int8_t>(word >> (sh0 + 8))) * sc;
           o[i] = pack_bf2(a, b);
         }
-        *reinterpret_cast<uint4 *>(&sm.H[swz<N>(row, n0 + 8 * half)]) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(&sm.H[tile_at<N>(row, n0 + 8 * half)]) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
 #pragma unroll
     for (int b = 0; b < BC; ++b) {
       const int piece = tid + 512 * b;
       if (piece < kP * G8) {
-        const int o = swz<N>(piece / G8, (piece % G8) * 8);
+        const int o = tile_at<N>(piece / G8, (piece % G8) * 8);
         *reinterpret_cast<uint4 *>(&sm.dh[0][o]) = dv[0][b];
         *reinterpret_cast<uint4 *>(&sm.dh[1][o]) = dv[1][b];
       }
@@ -443,7 +460,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       if (jt <= it) {
         f32x4 m = zero4;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) m = mfma(frag<kP>(sm.g, 16 * it, 32 * kk), frag<kP>(sm.x, 16 * jt, 32 * kk), m);
+        for (int kk = 0; kk < 2; ++kk) m = mfma(frag<kP>(l, sm.g, 16 * it, 32 * kk), frag<kP>(l, sm.x, 16 * jt, 32 * kk), m);
         const int j = 16 * jt + r;
         const float cj = cs[j], dj = dt[j];
         float u[4], col = 0.0f;
@@ -461,7 +478,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
         uint2 hi, lo;
         split_bf2(u[0], u[1], hi.x, lo.x);
         split_bf2(u[2], u[3], hi.y, lo.y);
-        const int o = swz<kQ>(j, 16 * it + 4 * kq);
+        const int o = tile_at<kQ>(j, 16 * it + 4 * kq);
         *reinterpret_cast<uint2 *>(&sm.U[0][o]) = hi;
         *reinterpret_cast<uint2 *>(&sm.U[1][o]) = lo;
         col = sum_kq(col);
@@ -474,15 +491,16 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       if (r == 0) sm.row[w & 1][16 * it + 4 * kq + ii] = rowsum[ii];
     }
 
+    __builtin_amdgcn_sched_barrier(0);
     // ---- H^T g and dH^T x: lane holds (n = 16 nt + 4 kq + ii, token = 16 ti + r)
     {
       bf16x8 hf[2], df[2][2];
       float hh = 0.0f;
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        hf[kk] = frag_t<N>(sm.H, 32 * kk, 16 * nt);
-        df[0][kk] = frag_t<N>(sm.dh[0], 32 * kk, 16 * nt);
-        df[1][kk] = frag_t<N>(sm.dh[1], 32 * kk, 16 * nt);
+        hf[kk] = frag_t<N>(l, sm.H, 32 * kk, 16 * nt);
+        df[0][kk] = frag_t<N>(l, sm.dh[0], 32 * kk, 16 * nt);
+        df[1][kk] = frag_t<N>(l, sm.dh[1], 32 * kk, 16 * nt);
         if (ti0 == 0) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -493,11 +511,12 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       if (l == 0) sm.hh[w] = hh;
 #pragma unroll
       for (int a = 0; a < IT; ++a) {
+        __builtin_amdgcn_sched_barrier(0);
         const int t = 16 * (ti0 + a) + r;
         f32x4 c = zero4, b = zero4;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
-          const bf16x8 gf = frag<kP>(sm.g, 16 * (ti0 + a), 32 * kk), xf = frag<kP>(sm.x, 16 * (ti0 + a), 32 * kk);
+          const bf16x8 gf = frag<kP>(l, sm.g, 16 * (ti0 + a), 32 * kk), xf = frag<kP>(l, sm.x, 16 * (ti0 + a), 32 * kk);
           c = mfma(hf[kk], gf, c);
           b = mfma(df[0][kk], xf, b);
           b = mfma(df[1][kk], xf, b);
@@ -506,7 +525,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
         c *= e;
         dCa[a] += c;
         dBa[a] += b * wj;
-        const uint2 cw = *reinterpret_cast<const uint2 *>(&sm.C[swz<N>(t, 16 * nt + 4 * kq)]);
+        const uint2 cw = *reinterpret_cast<const uint2 *>(&sm.C[tile_at<N>(t, 16 * nt + 4 * kq)]);
         float qs = c[0] * __uint_as_float(cw.x << 16);
         qs = fmaf(c[1], __uint_as_float(cw.x & 0xffff0000u), qs);
         qs = fmaf(c[2], __uint_as_float(cw.y << 16), qs);
@@ -528,24 +547,25 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       }
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
+        __builtin_amdgcn_sched_barrier(0);
         const int jt = jx0 + a, j = 16 * jt + r;
         f32x4 st = zero4, pr = zero4;
 #pragma unroll
         for (int kk = 0; kk < KN; ++kk) {
-          const bf16x8 bf = frag<N>(sm.B, 16 * jt, 32 * kk);
-          st = mfma(frag<N>(sm.dh[0], 16 * pt, 32 * kk), bf, st);
-          st = mfma(frag<N>(sm.dh[1], 16 * pt, 32 * kk), bf, st);
+          const bf16x8 bf = frag<N>(l, sm.B, 16 * jt, 32 * kk);
+          st = mfma(frag<N>(l, sm.dh[0], 16 * pt, 32 * kk), bf, st);
+          st = mfma(frag<N>(l, sm.dh[1], 16 * pt, 32 * kk), bf, st);
         }
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
           if (32 * (kk + 1) > 16 * jt) {
-            const bf16x8 gf = frag_t<kP>(sm.g, 32 * kk, 16 * pt);
-            pr = mfma(gf, frag<kQ>(sm.U[0], 16 * jt, 32 * kk), pr);
-            pr = mfma(gf, frag<kQ>(sm.U[1], 16 * jt, 32 * kk), pr);
+            const bf16x8 gf = frag_t<kP>(l, sm.g, 32 * kk, 16 * pt);
+            pr = mfma(gf, frag<kQ>(l, sm.U[0], 16 * jt, 32 * kk), pr);
+            pr = mfma(gf, frag<kQ>(l, sm.U[1], 16 * jt, 32 * kk), pr);
           }
         st *= fast_exp2((cse - cs[j]) * kLog2e);
-        const uint2 xw = *reinterpret_cast<const uint2 *>(&sm.x[swz<kP>(j, pc)]);
-        const uint2 gw = *reinterpret_cast<const uint2 *>(&sm.g[swz<kP>(j, pc)]);
+        const uint2 xw = *reinterpret_cast<const uint2 *>(&sm.x[tile_at<kP>(j, pc)]);
+        const uint2 gw = *reinterpret_cast<const uint2 *>(&sm.g[tile_at<kP>(j, pc)]);
         const float xf[4] = {__uint_as_float(xw.x << 16), __uint_as_float(xw.x & 0xffff0000u), __uint_as_float(xw.y << 16),
                              __uint_as_float(xw.y & 0xffff0000u)};
         const float gf[4] = {__uint_as_float(gw.x << 16), __uint_as_float(gw.x & 0xffff0000u), __uint_as_float(gw.y << 16),
@@ -621,21 +641,21 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     uint2 hi, lo;
     split_bf2(V[a][0], V[a][1], hi.x, lo.x);
     split_bf2(V[a][2], V[a][3], hi.y, lo.y);
-    const int o = swz<kQ>(16 * (jt0 + a) + r, 16 * it + 4 * kq);
+    const int o = tile_at<kQ>(16 * (jt0 + a) + r, 16 * it + 4 * kq);
     *reinterpret_cast<uint2 *>(&Vh[o]) = hi;
     *reinterpret_cast<uint2 *>(&Vl[o]) = lo;
   }
   __syncthreads();
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) {
-    const bf16x8 bt = frag_t<N>(sm.B, 32 * kk, 16 * nt), ct = frag_t<N>(sm.C, 32 * kk, 16 * nt);
+    const bf16x8 bt = frag_t<N>(l, sm.B, 32 * kk, 16 * nt), ct = frag_t<N>(l, sm.C, 32 * kk, 16 * nt);
 #pragma unroll
     for (int a = 0; a < IT; ++a) {
       const int tt = 16 * (ti0 + a);
-      dCa[a] = mfma(bt, frag_t<kQ>(Vh, 32 * kk, tt), dCa[a]);
-      dCa[a] = mfma(bt, frag_t<kQ>(Vl, 32 * kk, tt), dCa[a]);
-      dBa[a] = mfma(ct, frag<kQ>(Vh, tt, 32 * kk), dBa[a]);
-      dBa[a] = mfma(ct, frag<kQ>(Vl, tt, 32 * kk), dBa[a]);
+      dCa[a] = mfma(bt, frag_t<kQ>(l, Vh, 32 * kk, tt), dCa[a]);
+      dCa[a] = mfma(bt, frag_t<kQ>(l, Vl, 32 * kk, tt), dCa[a]);
+      dBa[a] = mfma(ct, frag<kQ>(l, Vh, tt, 32 * kk), dBa[a]);
+      dBa[a] = mfma(ct, frag<kQ>(l, Vl, tt, 32 * kk), dBa[a]);
     }
   }
 #pragma unroll
@@ -660,45 +680,57 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
 // ---------------------------------------------------------------------------
 // (3) the sums over head blocks and chunks
 // ---------------------------------------------------------------------------
+// One launch for all of them: workgroups [0, 2 bc_blocks) add the head blocks'
+// dB and dC (1024 elements each), the next ones the chunks' (dA, ddt_bias),
+// the last ones the chunks' dD: 8 columns each, 32 threads a column, every
+// thread its chunks in order and then the 32 in order, in 64 bits.
+struct SumParams {
+  const float *bc, *sum, *dd;
+  uint16_t *dB, *dC;
+  float *dA, *ddt_bias, *dD;
+  int64_t total, row, dbs, dcs, entries, nheads, dd_cols, bc_blocks, sum_blocks;
+  int hb;
+};
 
-__global__ void __launch_bounds__(256) bc_sum_kernel(const float *ws, uint16_t *dB, uint16_t *dC, int64_t total,
-                                                     int64_t row, int64_t dbs, int64_t dcs, int blocks) {
-  const int64_t plane = total * row;
-  const float *from = ws + (blockIdx.y ? blocks * plane : 0);
-  uint16_t *to = blockIdx.y ? dC : dB;
-  const int64_t stride = blockIdx.y ? dcs : dbs;
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i >= plane) return;
-  float4 a = *reinterpret_cast<const float4 *>(from + i);
-  for (int k = 1; k < blocks; ++k) {
-    const float4 b = *reinterpret_cast<const float4 *>(from + k * plane + i);
-    a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
-  }
-  const int64_t t = i / row, c = i - t * row;
-  *reinterpret_cast<uint2 *>(to + t * stride + c) = make_uint2(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w));
-}
-
-// Column sums of (entries, cols) partials in 64 bits: workgroup = 64 columns,
-// four threads each.  PAIR: columns are (head, {dA, ddt_bias}).
-template <bool PAIR>
-__global__ void __launch_bounds__(256) entry_sum_kernel(const float *part, float *a, float *b, int64_t entries, int64_t cols) {
-  __shared__ double sum[4][64];
-  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  double v = 0.0;
-  if (col < cols)
-    for (int64_t e = entries * q / 4; e < entries * (q + 1) / 4; ++e) v += part[e * cols + col];
-  sum[q][lane] = v;
-  __syncthreads();
-  if (q == 0 && col < cols) {
-    const float s = static_cast<float>((sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]));
-    if constexpr (PAIR) {
-      if (!(col & 1)) a[col >> 1] = s;
-      else if (b) b[col >> 1] = s;
-    } else {
-      a[col] = s;
+__global__ void __launch_bounds__(256) sum_kernel(const SumParams p) {
+  __shared__ double part[32][8];
+  const int tid = threadIdx.x;
+  int64_t blk = blockIdx.x;
+  if (blk < 2 * p.bc_blocks) {
+    const bool second = blk >= p.bc_blocks;
+    const int64_t plane = p.total * p.row;
+    const float *from = p.bc + (second ? p.hb * plane : 0);
+    const int64_t i = ((blk - (second ? p.bc_blocks : 0)) * 256 + tid) * 4;
+    if (i >= plane) return;
+    float4 a = *reinterpret_cast<const float4 *>(from + i);
+    for (int k = 1; k < p.hb; ++k) {
+      const float4 b = *reinterpret_cast<const float4 *>(from + k * plane + i);
+      a.x += b.x; a.y += b.y; a.z += b.z; a.w += b.w;
     }
+    const int64_t t = i / p.row, c = i - t * p.row;
+    *reinterpret_cast<uint2 *>((second ? p.dC + t * p.dcs : p.dB + t * p.dbs) + c) =
+        make_uint2(pack_bf2(a.x, a.y), pack_bf2(a.z, a.w));
+    return;
   }
+  blk -= 2 * p.bc_blocks;
+  const bool steps = blk < p.sum_blocks;
+  const float *from = steps ? p.sum : p.dd;
+  const int64_t cols = steps ? 2 * p.nheads : p.dd_cols;
+  const int64_t col = (steps ? blk : blk - p.sum_blocks) * 8 + (tid & 7);
+  double v = 0.0;
+  if (col < cols) {
+#pragma unroll 4
+    for (int64_t e = tid >> 3; e < p.entries; e += 32) v += from[e * cols + col];
+  }
+  part[tid >> 3][tid & 7] = v;
+  __syncthreads();
+  if (tid >= 8 || col >= cols) return;
+  v = 0.0;
+  for (int k = 0; k < 32; ++k) v += part[k][tid];
+  const float out = static_cast<float>(v);
+  if (!steps) p.dD[col] = out;
+  else if (!(col & 1)) p.dA[col >> 1] = out;
+  else if (p.ddt_bias) p.ddt_bias[col >> 1] = out;
 }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
@@ -793,7 +825,8 @@ extern "C" int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *a, void *stream_ptr) 
   const BwdPlan pl = bwd_plan(&f, cu_count_cached());
   if (!a->workspace || a->workspace_bytes < pl.bytes) return SSM_ERR_WORKSPACE;
   if (!aligned16(a->workspace)) return SSM_ERR_UNSUPPORTED;
-  if (f.nseq * f.nheads > 0x7fffffffLL || pl.entries > 0x7fffffffLL || f.ngroups * pl.hb_per_group > 65535)
+  if (f.nseq * f.nheads > 0x7fffffffLL || pl.entries > 0x7fffffffLL || f.ngroups * pl.hb_per_group > 65535 ||
+      f.total * f.ngroups * f.dstate > (0x3fffffffLL << 10))
     return SSM_ERR_SHAPE;
   char *ws = static_cast<char *>(a->workspace);
   BwdParams p{};
@@ -827,20 +860,17 @@ extern "C" int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *a, void *stream_ptr) 
   hipError_t e = f.dstate == 32 ? launch_bwd<32>(p, pl, stream)
                  : f.dstate == 64 ? launch_bwd<64>(p, pl, stream) : launch_bwd<128>(p, pl, stream);
   if (e != hipSuccess) return hip_fail(e);
-  if (p.ws_bc) {
-    const int64_t row = f.ngroups * f.dstate, quads = (f.total * row + 1023) / 1024;
-    hipLaunchKernelGGL(bc_sum_kernel, dim3(static_cast<unsigned>(quads), 2), dim3(256), 0, stream, p.ws_bc, p.dB, p.dC,
-                       f.total, row, a->dB_stride, a->dC_stride, pl.hb_per_group);
-    if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e);
-  }
-  hipLaunchKernelGGL(entry_sum_kernel<true>, dim3(static_cast<unsigned>((2 * f.nheads + 63) / 64)), dim3(256), 0, stream,
-                     p.ws_sum, a->dA, f.dt_bias ? a->ddt_bias : nullptr, pl.entries, 2 * f.nheads);
-  if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e);
-  if (f.D) {
-    const int64_t cols = f.nheads * (f.D_per_channel ? kP : 1);
-    hipLaunchKernelGGL(entry_sum_kernel<false>, dim3(static_cast<unsigned>((cols + 63) / 64)), dim3(256), 0, stream, p.ws_dd,
-                       a->dD, nullptr, pl.entries, cols);
-    if ((e = hipGetLastError()) != hipSuccess) return hip_fail(e);
-  }
-  return SSM_OK;
+  SumParams q{};
+  q.bc = p.ws_bc; q.sum = p.ws_sum; q.dd = p.ws_dd;
+  q.dB = p.dB; q.dC = p.dC; q.dbs = p.dbs; q.dcs = p.dcs;
+  q.dA = a->dA; q.ddt_bias = f.dt_bias ? a->ddt_bias : nullptr; q.dD = a->dD;
+  q.total = f.total; q.row = f.ngroups * f.dstate; q.entries = pl.entries; q.nheads = f.nheads;
+  q.hb = pl.hb_per_group;
+  q.bc_blocks = p.ws_bc ? (f.total * q.row + 1023) / 1024 : 0;
+  q.sum_blocks = (2 * f.nheads + 7) / 8;
+  q.dd_cols = f.D ? f.nheads * (f.D_per_channel ? kP : 1) : 0;
+  const int64_t blocks = 2 * q.bc_blocks + q.sum_blocks + (q.dd_cols + 7) / 8;
+  hipLaunchKernelGGL(sum_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, q);
+  e = hipGetLastError();
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
 }
