@@ -84,22 +84,39 @@ __device__ __forceinline__ Seq sequence(const BwdParams &p, int64_t s) {
   return {lo, len, (len + kQ - 1) / kQ, lo / kQ + s};
 }
 
-// The step of token l of a chunk and its running sum times A over the wave
-// (0 beyond the chunk's end); v: the value before softplus.
-__device__ __forceinline__ float chunk_step(const BwdParams &p, float raw, float bias, bool live, float Ah, float &cs,
-                                            float &v) {
+// The value before softplus of token l's step, and the step (0 beyond the
+// chunk's end).
+__device__ __forceinline__ float chunk_step(const BwdParams &p, float raw, float bias, bool live, float &v) {
   v = raw + bias;
   float d = p.softplus ? softplus_acc(v) : v;
   if (p.dt_limit) d = fminf(fmaxf(d, p.dt_min), p.dt_max);
-  if (!live) d = 0.0f;
-  cs = d * Ah;
-  const int l = threadIdx.x & 63;
+  return live ? d : 0.0f;
+}
+
+// Running sum over the wave's lanes of d A, as an unevaluated sum of two
+// floats: decays are exponentials of its differences, whose error would
+// otherwise be the rounding of a sum that reaches 100 and more.
+struct TwoSum {
+  float hi, lo;
+};
+__device__ __forceinline__ TwoSum running_sum(float d, float A, int l) {
+  TwoSum s;
+  s.hi = d * A;
+  s.lo = fmaf(d, A, -s.hi);
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const float o = __shfl_up(cs, off);
-    if (l >= off) cs += o;
+    const float oh = __shfl_up(s.hi, off), ol = __shfl_up(s.lo, off);
+    if (l >= off) {
+      const float t = s.hi + oh, b = t - s.hi;
+      s.lo += ol + ((s.hi - (t - b)) + (oh - b));
+      s.hi = t;
+    }
   }
-  return d;
+  return s;
+}
+// exp(a - b)
+__device__ __forceinline__ float exp_diff(float ah, float al, float bh, float bl) {
+  return fast_exp2(((ah - bh) + (al - bl)) * kLog2e);
 }
 
 // Element offset of (row, col) in a row-major tile of ROW_LEN bf16.  A row's
@@ -126,6 +143,13 @@ __device__ __forceinline__ bf16x8 frag_t(int l, uint16_t *tile, int row0, int co
   const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<ROW_LEN>(row + 4, col)));
   const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
   return __builtin_bit_cast(bf16x8, make_uint4(ua.x, ua.y, ub.x, ub.y));
+}
+// ... of four rows only: lane (r, kq) receives tile[row0 + 4 kq + i][col0 + r], i < 4.
+template <int ROW_LEN>
+__device__ __forceinline__ s16x4 frag_t4(int l, uint16_t *tile, int row0, int col0) {
+  typedef __attribute__((address_space(3))) s16x4 *lds;
+  const int i = l & 15, kq = l >> 4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<ROW_LEN>(row0 + 4 * kq + (i >> 2), col0 + 4 * (i & 3))));
 }
 // ... and row by row: lane (r, kq) receives tile[row0 + r][col0 + 8 kq + i].
 template <int ROW_LEN>
@@ -201,14 +225,19 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
     float raw = 0.0f;
     if (w == 0 && l < len) raw = bf2f(dtb[(t0 + l) * p.dts]);
     if constexpr (STORE) {
-      uint16_t *dh = p.ws_dh + ((q.entry + c) * p.nheads + h) * 2 * kP * N + srow;
+      // in the order (n / 32, (n / 4) % 4, (n / 16) % 2, n % 4) along a row,
+      // so that a lane's eight states of two tiles are 16 bytes and the four
+      // kq lanes of a row 64
+      uint16_t *dh = p.ws_dh + ((q.entry + c) * p.nheads + h) * 2 * kP * N + (16 * w + r) * N + 8 * kq;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        uint2 hi, lo;
+      for (int nt = 0; nt < NT; nt += 2) {
+        uint4 hi, lo;
         split_bf2(acc[nt][0], acc[nt][1], hi.x, lo.x);
         split_bf2(acc[nt][2], acc[nt][3], hi.y, lo.y);
-        *reinterpret_cast<uint2 *>(dh + 16 * nt) = hi;
-        *reinterpret_cast<uint2 *>(dh + kP * N + 16 * nt) = lo;
+        split_bf2(acc[nt + 1][0], acc[nt + 1][1], hi.z, lo.z);
+        split_bf2(acc[nt + 1][2], acc[nt + 1][3], hi.w, lo.w);
+        *reinterpret_cast<uint4 *>(dh + 16 * nt) = hi;
+        *reinterpret_cast<uint4 *>(dh + kP * N + 16 * nt) = lo;
       }
     }
     __syncthreads();   // the previous chunk's reads are done
@@ -223,10 +252,12 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
       if (piece < CPIECES) *reinterpret_cast<uint4 *>(&sC[tile_at<N>(piece / (N / 8), (piece % (N / 8)) * 8)]) = cv[k];
     }
     if (w == 0) {
-      float cs, v;
-      chunk_step(p, raw, bias, l < len, Ah, cs, v);
-      sE[l] = fast_exp2(cs * kLog2e);
-      if (l == 63) sEnd = fast_exp2(cs * kLog2e);
+      float v;
+      const float d = chunk_step(p, raw, bias, l < len, v);
+      const TwoSum cs = running_sum(d, Ah, l);
+      const float e = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
+      sE[l] = e;
+      if (l == 63) sEnd = e;
     }
     __syncthreads();
     const float end = sEnd;
@@ -269,18 +300,36 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
 // (2) one chunk and hb_heads heads of a group: eight waves.
 // ---------------------------------------------------------------------------
 
-// sum over the four kq lanes of a column r
+// sum over the four kq lanes of a column r: neighbouring rows of 16 lanes swap,
+// then the halves
 __device__ __forceinline__ float sum_kq(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
+  const uint32_t a = __float_as_uint(v);
+  const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t b = __float_as_uint(__uint_as_float(x[0]) + __uint_as_float(x[1]));
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(y[0]) + __uint_as_float(y[1]);
 }
-// sum over the sixteen r lanes of a row kq
+// sum over the sixteen r lanes of a row kq: rotations of the row
+template <int N>
+__device__ __forceinline__ float row_rotate(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xf, 0xf, false));
+}
 __device__ __forceinline__ float sum_r(float v) {
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o);
-  return v;
+  v += row_rotate<8>(v);
+  v += row_rotate<4>(v);
+  v += row_rotate<2>(v);
+  return v + row_rotate<1>(v);
 }
 __device__ __forceinline__ float sum_wave(float v) { return sum_kq(sum_r(v)); }
+
+// four bf16 of one 8-byte piece
+__device__ __forceinline__ void four(const uint16_t *p, float (&v)[4]) {
+  const uint2 w = *reinterpret_cast<const uint2 *>(p);
+  v[0] = __uint_as_float(w.x << 16);
+  v[1] = __uint_as_float(w.x & 0xffff0000u);
+  v[2] = __uint_as_float(w.y << 16);
+  v[3] = __uint_as_float(w.y & 0xffff0000u);
+}
 
 template <int N>
 struct ChunkLds {
@@ -288,11 +337,33 @@ struct ChunkLds {
   uint16_t x[kQ * kP], g[kQ * kP];        // [t][p]
   uint16_t H[kP * N];                     // [p][n]
   uint16_t dh[2][kP * N > kQ * kQ ? kP * N : kQ * kQ];   // [p][n] head, tail; at the end M L dt' [j][i]
-  uint16_t U[2][kQ * kQ];                 // S L [j][i] head, tail
-  float cs[kMaxHeads][kQ], dt[kMaxHeads][kQ], v[kMaxHeads][kQ];
-  float row[2][kQ], col[4][kQ], q[N / 16][kQ], r[4][kQ], hh[8], dd[2][kP];
+  // per head and token: the running sum, the step, exp(cs) to the chunk's
+  // start, to the 16-token block's start, and from the chunk's end
+  float ch[kMaxHeads][kQ], cl[kMaxHeads][kQ], dt[kMaxHeads][kQ], e0[kMaxHeads][kQ], eb[kMaxHeads][kQ], we[kMaxHeads][kQ];
+  // one head's partial sums, and what the heads' steps need of them
+  float row[4][kQ], col[4][kQ], q[N / 16][kQ], r[4][kQ], dd[2][kP], hh[8];
+  float direct[kMaxHeads][kQ], into[kMaxHeads][kQ], rs[kMaxHeads][kQ], ddc[kMaxHeads][kP], hhs[kMaxHeads];
 };
 
+// The ten 16 x 16 tiles of pairs (i block, j block), j <= i, in two halves of
+// five: waves 0-3 take j blocks 0 and 3, waves 4-7 blocks 1 and 2.
+template <int HALF>
+struct Pairs {
+  static constexpr int it(int k) { return HALF == 0 ? (k < 4 ? k : 3) : (k < 3 ? k + 1 : k - 1); }
+  static constexpr int jt(int k) { return HALF == 0 ? (k < 4 ? 0 : 3) : (k < 3 ? 1 : 2); }
+  static constexpr int at(int k) { return HALF == 0 ? (k < 4 ? 0 : 1) : (k < 3 ? 0 : 1); }   // which of the two j blocks
+};
+
+// One workgroup of eight waves.  For a head, between two barriers:
+//   wave w = (pt = w % 4, half = w / 4) forms the pair tiles of its half,
+//     M = g x^T, and multiplies S L straight from its registers (a product's
+//     result lies as the 16x16x16 product's second operand does) with the
+//     channels [16 pt, 16 pt + 16) of g: dx of its two token blocks; the four
+//     waves of a half form the same tiles again, which costs less than an LDS
+//     round trip and a third barrier; tile k's sums are kept by wave pt = k % 4;
+//   and the state products of its n tile, dH^T x and H^T g.
+// The partial sums over tiles meet in LDS; the steps' gradients, chains of
+// lane sums, wait until the end and are then done for all heads at once.
 template <int N>
 __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   constexpr int NT = N / 16;          // n tiles
@@ -306,7 +377,6 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  int l = lane, r = l & 15, kq = l >> 4;
   // the entry's sequence: the last s whose first entry is at or before it
   const int64_t entry = blockIdx.x;
   int64_t lo = 0, hi = p.nseq;
@@ -337,45 +407,21 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   }
   const int64_t t0 = q.first + chunk * kQ;      // the chunk's first token
   const int len = static_cast<int>(q.len - chunk * kQ < kQ ? q.len - chunk * kQ : kQ);
-
-  // ---- B, C, and every head's steps
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int k = 0; k < BC; ++k) {
-    const int piece = tid + 512 * k, t = piece / G8, n0 = (piece % G8) * 8;
-    if (piece < kQ * G8) {
-      *reinterpret_cast<uint4 *>(&sm.B[tile_at<N>(t, n0)]) = t < len ? ld8_raw(p.B + (t0 + t) * p.bs + gr * N + n0) : zero;
-      *reinterpret_cast<uint4 *>(&sm.C[tile_at<N>(t, n0)]) = t < len ? ld8_raw(p.C + (t0 + t) * p.cs + gr * N + n0) : zero;
-    }
-  }
-  for (int k = w; k < nh; k += 8) {
-    const int64_t h = h0 + k;
-    const float raw = l < len ? bf2f(p.dt[(t0 + l) * p.dts + h]) : 0.0f;
-    float cs, v;
-    const float d = chunk_step(p, raw, p.dt_bias ? p.dt_bias[h] : 0.0f, l < len, p.A[h], cs, v);
-    sm.cs[k][l] = cs;
-    sm.dt[k][l] = d;
-    sm.v[k][l] = v;
-  }
-  // the pairs above the diagonal stay zero
-  for (int i = tid; i < 2 * kQ * kQ / 8; i += 512) *reinterpret_cast<uint4 *>(&sm.U[0][0] + 8 * i) = zero;
-  if (tid < kQ) {
-    for (int k = 0; k < 4; ++k) sm.col[k][tid] = 0.0f;
-  }
+  int l = lane, r = l & 15, kq = l >> 4;
 
   // ---- this thread's pieces of a head's tiles, loaded one head ahead
+  const uint4 zero = make_uint4(0, 0, 0, 0);
   uint4 xv, gv, hv, dv[2][BC];
   float sc = 0.0f;
   auto load_head = [&](int64_t h) {
     const int t = tid >> 3, p0 = (tid & 7) * 8;
     xv = t < len ? ld8_raw(p.x + (t0 + t) * p.xs + h * kP + p0) : zero;
     gv = t < len ? ld8_raw(p.g + (t0 + t) * p.gs + h * kP + p0) : zero;
-    const int64_t eh = entry * p.nheads + h;
     if (tid < HPIECES) {
       hv = *reinterpret_cast<const uint4 *>(p.codes + entry * p.code_entry + h * p.code_head + 16 * tid);
       sc = p.scales[entry * p.scale_entry + h * p.scale_head + 16 * tid / N];
     }
-    const uint16_t *dh = p.ws_dh + eh * 2 * kP * N;
+    const uint16_t *dh = p.ws_dh + (entry * p.nheads + h) * 2 * kP * N;
 #pragma unroll
     for (int k = 0; k < BC; ++k) {
       const int piece = tid + 512 * k;
@@ -387,25 +433,52 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   };
   load_head(h0);
 
-  // tiles of this wave: pairs (i tile, two j tiles); (n tile, IT token
-  // tiles); (p tile, two token tiles)
-  const int it = w >> 1, jt0 = 2 * (w & 1);
+  // ---- B, C, and every head's steps
+#pragma unroll
+  for (int k = 0; k < BC; ++k) {
+    const int piece = tid + 512 * k, t = piece / G8, n0 = (piece % G8) * 8;
+    if (piece < kQ * G8) {
+      *reinterpret_cast<uint4 *>(&sm.B[tile_at<N>(t, n0)]) = t < len ? ld8_raw(p.B + (t0 + t) * p.bs + gr * N + n0) : zero;
+      *reinterpret_cast<uint4 *>(&sm.C[tile_at<N>(t, n0)]) = t < len ? ld8_raw(p.C + (t0 + t) * p.cs + gr * N + n0) : zero;
+    }
+  }
+  for (int k = w; k < nh; k += 8) {
+    const int64_t h = h0 + k;
+    const float raw = l < len ? bf2f(p.dt[(t0 + l) * p.dts + h]) : 0.0f;
+    float v;
+    const float d = chunk_step(p, raw, p.dt_bias ? p.dt_bias[h] : 0.0f, l < len, v);
+    const TwoSum cs = running_sum(d, p.A[h], l);
+    sm.ch[k][l] = cs.hi;
+    sm.cl[k][l] = cs.lo;
+    sm.dt[k][l] = d;
+    sm.e0[k][l] = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
+    sm.eb[k][l] = exp_diff(cs.hi, cs.lo, __shfl(cs.hi, l & 48), __shfl(cs.lo, l & 48));
+    sm.we[k][l] = exp_diff(__shfl(cs.hi, 63), __shfl(cs.lo, 63), cs.hi, cs.lo);
+  }
+  if (tid < kQ) {   // no pair tile above the diagonal adds to these
+    for (int k = 0; k < 4; ++k) sm.row[k][tid] = sm.col[k][tid] = 0.0f;
+  }
+
+  const int pt = w & 3, half = w >> 2;
   const int nt = w % NT, ti0 = (w / NT) * IT;
-  const int pt = w & 3, jx0 = 2 * (w >> 2);
-  f32x4 S[2], V[2], dBa[IT], dCa[IT];
+  f32x4 S[5], V[2], dBa[IT], dCa[IT];
   const f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int k = 0; k < 2; ++k) S[k] = V[k] = zero4;
+  for (int k = 0; k < 5; ++k) S[k] = zero4;
+  V[0] = V[1] = zero4;
 #pragma unroll
   for (int k = 0; k < IT; ++k) dBa[k] = dCa[k] = zero4;
   __syncthreads();
+  auto form_S = [&](auto hc) {
+    using PR = Pairs<decltype(hc)::value>;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    if (jt0 + k <= it) {
+    for (int k = 0; k < 5; ++k)
 #pragma unroll
       for (int kk = 0; kk < KN; ++kk)
-        S[k] = mfma(frag<N>(l, sm.C, 16 * it, 32 * kk), frag<N>(l, sm.B, 16 * (jt0 + k), 32 * kk), S[k]);
-    }
+        S[k] = mfma(frag<N>(l, sm.C, 16 * PR::it(k), 32 * kk), frag<N>(l, sm.B, 16 * PR::jt(k), 32 * kk), S[k]);
+  };
+  if (half == 0) form_S(std::integral_constant<int, 0>{});
+  else form_S(std::integral_constant<int, 1>{});
 
   for (int k = 0; k < nh; ++k) {
     const int64_t h = h0 + k;
@@ -414,7 +487,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     asm volatile("" : "+v"(l));
     r = l & 15;
     kq = l >> 4;
-    const float *cs = sm.cs[k], *dt = sm.dt[k];
+    const float *dt = sm.dt[k];
     // ---- stage the head (its tiles' last readers passed the barrier before)
     {
       const int t = tid >> 3, p0 = (tid & 7) * 8;
@@ -422,96 +495,161 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       *reinterpret_cast<uint4 *>(&sm.g[tile_at<kP>(t, p0)]) = gv;
     }
     if (tid < HPIECES) {
+      // codes as unsigned bytes (code + 128), one conversion each
       const int row = 16 * tid / N, n0 = (16 * tid) % N;
+      const float off = -128.0f * sc;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int hf = 0; hf < 2; ++hf) {
         uint32_t o[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t word = raw_word(hv, 2 * half + (i >> 1));
-          const int sh0 = (i & 1) * 16;
-          const float a = static_cast<float>(static_cast<int8_t>(word >> sh0)) * sc;
-          const float b = static_cast<float>(static_cast<int8_t>(word >> (sh0 + 8))) * sc;
-          o[i] = pack_bf2(a, b);
+          const uint32_t word = raw_word(hv, 2 * hf + (i >> 1)) ^ 0x80808080u;
+          const int sh = (i & 1) * 16;
+          o[i] = pack_bf2(fmaf(static_cast<float>((word >> sh) & 0xffu), sc, off),
+                          fmaf(static_cast<float>((word >> (sh + 8)) & 0xffu), sc, off));
         }
-        *reinterpret_cast<uint4 *>(&sm.H[tile_at<N>(row, n0 + 8 * half)]) = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4 *>(&sm.H[tile_at<N>(row, n0 + 8 * hf)]) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
 #pragma unroll
     for (int b = 0; b < BC; ++b) {
       const int piece = tid + 512 * b;
-      if (piece < kP * G8) {
-        const int o = tile_at<N>(piece / G8, (piece % G8) * 8);
-        *reinterpret_cast<uint4 *>(&sm.dh[0][o]) = dv[0][b];
-        *reinterpret_cast<uint4 *>(&sm.dh[1][o]) = dv[1][b];
+      if (piece < kP * G8) {   // out of adjoint_kernel's order
+        const int row = piece / G8, n0 = ((piece % G8) >> 2) * 32 + (piece & 3) * 4;
+        const int o0 = tile_at<N>(row, n0), o1 = tile_at<N>(row, n0 + 16);
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          *reinterpret_cast<uint2 *>(&sm.dh[a][o0]) = make_uint2(dv[a][b].x, dv[a][b].y);
+          *reinterpret_cast<uint2 *>(&sm.dh[a][o1]) = make_uint2(dv[a][b].z, dv[a][b].w);
+        }
       }
     }
     __syncthreads();
     if (k + 1 < nh) load_head(h + 1);
-    const float cse = cs[kQ - 1];
 
-    // ---- the pairs: lane holds (i = 16 it + 4 kq + ii, j = 16 jt + r)
-    float rowsum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    const float4 ci4 = *reinterpret_cast<const float4 *>(&cs[16 * it + 4 * kq]);
-    const float ci[4] = {ci4.x, ci4.y, ci4.z, ci4.w};
+    // ---- the pairs, and dx: pair tiles lie as (i = 16 it + 4 kq + ii,
+    // j = 16 jt + r), dx as (p = 16 pt + 4 kq + ii, j = 16 jt + r)
+    auto pairs_and_dx = [&](auto hc) {
+      using PR = Pairs<decltype(hc)::value>;
+      f32x4 pr[2] = {zero4, zero4}, st[2] = {zero4, zero4};
 #pragma unroll
-    for (int a = 0; a < 2; ++a) {
-      const int jt = jt0 + a;
-      if (jt <= it) {
+      for (int kk = 0; kk < KN; ++kk) {
+        const bf16x8 d0 = frag<N>(l, sm.dh[0], 16 * pt, 32 * kk), d1 = frag<N>(l, sm.dh[1], 16 * pt, 32 * kk);
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          const bf16x8 bf = frag<N>(l, sm.B, 16 * PR::jt(4 * a), 32 * kk);
+          st[a] = mfma(d0, bf, st[a]);
+          st[a] = mfma(d1, bf, st[a]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 5; ++t) {
+        if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);   // bounds the operands in flight
+        const int it = PR::it(t), jt = PR::jt(t), j = 16 * jt + r, i0 = 16 * it + 4 * kq;
         f32x4 m = zero4;
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) m = mfma(frag<kP>(l, sm.g, 16 * it, 32 * kk), frag<kP>(l, sm.x, 16 * jt, 32 * kk), m);
-        const int j = 16 * jt + r;
-        const float cj = cs[j], dj = dt[j];
-        float u[4], col = 0.0f;
+        const float jh = sm.ch[k][j], jl = sm.cl[k][j];
+        float L[4];
+        if (it == jt) {
+          const float4 ih = *reinterpret_cast<const float4 *>(&sm.ch[k][i0]), il = *reinterpret_cast<const float4 *>(&sm.cl[k][i0]);
+          const float ihv[4] = {ih.x, ih.y, ih.z, ih.w}, ilv[4] = {il.x, il.y, il.z, il.w};
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii) L[ii] = exp_diff(ihv[ii], ilv[ii], jh, jl);
+        } else {
+          // the decay from j to block i's start, and from there to i
+          const float f = exp_diff(sm.ch[k][16 * it], sm.cl[k][16 * it], jh, jl);
+          const float4 e = *reinterpret_cast<const float4 *>(&sm.eb[k][i0]);
+          L[0] = e.x * f; L[1] = e.y * f; L[2] = e.z * f; L[3] = e.w * f;
+        }
+        float u[4];
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii) {
-          const bool in = 16 * it + 4 * kq + ii >= j;
-          const float L = in ? fast_exp2((ci[ii] - cj) * kLog2e) : 0.0f;
-          u[ii] = in ? S[a][ii] * L : 0.0f;
-          const float ml = in ? m[ii] * L : 0.0f;
-          V[a][ii] = fmaf(ml, dj, V[a][ii]);
-          const float G = in ? u[ii] * m[ii] : 0.0f;
-          col += G;
-          rowsum[ii] = fmaf(G, dj, rowsum[ii]);
+          u[ii] = S[t][ii] * L[ii];
+          if (it == jt && i0 + ii < j) u[ii] = 0.0f;
         }
-        uint2 hi, lo;
-        split_bf2(u[0], u[1], hi.x, lo.x);
-        split_bf2(u[2], u[3], hi.y, lo.y);
-        const int o = tile_at<kQ>(j, 16 * it + 4 * kq);
-        *reinterpret_cast<uint2 *>(&sm.U[0][o]) = hi;
-        *reinterpret_cast<uint2 *>(&sm.U[1][o]) = lo;
-        col = sum_kq(col);
-        if (kq == 0) sm.col[it][j] = col;
-      }
-    }
+        uint2 uh, ul;
+        split_bf2(u[0], u[1], uh.x, ul.x);
+        split_bf2(u[2], u[3], uh.y, ul.y);
+        const s16x4 gt = frag_t4<kP>(l, sm.g, 16 * it, 16 * pt);
+        f32x4 &acc = pr[PR::at(t)];
+        acc = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(gt, __builtin_bit_cast(s16x4, uh), acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(gt, __builtin_bit_cast(s16x4, ul), acc, 0, 0, 0);
+        if (pt == (t & 3)) {
+          const float dj = dt[j];
+          float col = 0.0f, rows[4];
 #pragma unroll
-    for (int ii = 0; ii < 4; ++ii) {
-      rowsum[ii] = sum_r(rowsum[ii]);
-      if (r == 0) sm.row[w & 1][16 * it + 4 * kq + ii] = rowsum[ii];
-    }
+          for (int ii = 0; ii < 4; ++ii) {
+            const bool out = it == jt && i0 + ii < j;
+            V[t >> 2][ii] = fmaf(out ? 0.0f : m[ii] * L[ii], dj, V[t >> 2][ii]);
+            const float G = out ? 0.0f : u[ii] * m[ii];
+            col += G;
+            rows[ii] = sum_r(G * dj);
+          }
+          col = sum_kq(col);
+          if (kq == 0) sm.col[it][j] = col;
+          if (r == 0) *reinterpret_cast<float4 *>(&sm.row[jt][i0]) = make_float4(rows[0], rows[1], rows[2], rows[3]);
+        }
+      }
+      const int pc = 16 * pt + 4 * kq;
+      float Dv[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dd4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (p.D) {
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) Dv[ii] = p.D_per_channel ? p.D[h * kP + pc + ii] : p.D[h];
+      }
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const int j = 16 * PR::jt(4 * a) + r;
+        const float wj = sm.we[k][j], dj = dt[j];
+        float xf[4], gf[4], o[4], rs = 0.0f;
+        four(&sm.x[tile_at<kP>(j, pc)], xf);
+        four(&sm.g[tile_at<kP>(j, pc)], gf);
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          const float sv = st[a][ii] * wj;
+          rs = fmaf(xf[ii], sv, rs);
+          dd4[ii] = fmaf(gf[ii], xf[ii], dd4[ii]);
+          o[ii] = fmaf(dj, pr[a][ii] + sv, Dv[ii] * gf[ii]);
+        }
+        rs = sum_kq(rs);
+        if (kq == 0) sm.r[pt][j] = rs;
+        if (j < len)
+          *reinterpret_cast<uint2 *>(p.dx + (t0 + j) * p.dxs + h * kP + pc) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+      }
+      if (p.D) {   // these tokens' part of each channel's sum
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) dd4[ii] = sum_r(dd4[ii]);
+        if (r == 0) *reinterpret_cast<float4 *>(&sm.dd[decltype(hc)::value][pc]) = make_float4(dd4[0], dd4[1], dd4[2], dd4[3]);
+      }
+    };
+    if (half == 0) pairs_and_dx(std::integral_constant<int, 0>{});
+    else pairs_and_dx(std::integral_constant<int, 1>{});
 
-    __builtin_amdgcn_sched_barrier(0);
     // ---- H^T g and dH^T x: lane holds (n = 16 nt + 4 kq + ii, token = 16 ti + r)
+    __builtin_amdgcn_sched_barrier(0);
     {
       bf16x8 hf[2], df[2][2];
-      float hh = 0.0f;
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         hf[kk] = frag_t<N>(l, sm.H, 32 * kk, 16 * nt);
         df[0][kk] = frag_t<N>(l, sm.dh[0], 32 * kk, 16 * nt);
         df[1][kk] = frag_t<N>(l, sm.dh[1], 32 * kk, 16 * nt);
-        if (ti0 == 0) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            hh = fmaf(static_cast<float>(hf[kk][i]), static_cast<float>(df[0][kk][i]) + static_cast<float>(df[1][kk][i]), hh);
-        }
       }
-      hh = sum_wave(hh);
-      if (l == 0) sm.hh[w] = hh;
+      if (ti0 == 0) {   // <dH, H> over these n: the diagonal of the tiles' product
+        f32x4 t = zero4;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          t = mfma(hf[kk], df[0][kk], t);
+          t = mfma(hf[kk], df[1][kk], t);
+        }
+        const int ii = r - 4 * kq;
+        const float d = ii == 0 ? t[0] : ii == 1 ? t[1] : ii == 2 ? t[2] : ii == 3 ? t[3] : 0.0f;
+        const float hh = sum_wave(d);
+        if (l == 0) sm.hh[w] = hh;
+      }
 #pragma unroll
       for (int a = 0; a < IT; ++a) {
-        __builtin_amdgcn_sched_barrier(0);
+        if (a % 2 == 0) __builtin_amdgcn_sched_barrier(0);
         const int t = 16 * (ti0 + a) + r;
         f32x4 c = zero4, b = zero4;
 #pragma unroll
@@ -521,130 +659,98 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
           b = mfma(df[0][kk], xf, b);
           b = mfma(df[1][kk], xf, b);
         }
-        const float e = fast_exp2(cs[t] * kLog2e), wj = fast_exp2((cse - cs[t]) * kLog2e) * dt[t];
-        c *= e;
-        dCa[a] += c;
-        dBa[a] += b * wj;
-        const uint2 cw = *reinterpret_cast<const uint2 *>(&sm.C[tile_at<N>(t, 16 * nt + 4 * kq)]);
-        float qs = c[0] * __uint_as_float(cw.x << 16);
-        qs = fmaf(c[1], __uint_as_float(cw.x & 0xffff0000u), qs);
-        qs = fmaf(c[2], __uint_as_float(cw.y << 16), qs);
-        qs = fmaf(c[3], __uint_as_float(cw.y & 0xffff0000u), qs);
+        const float e = sm.e0[k][t], wj = sm.we[k][t] * dt[t];
+        float cf[4], qs = 0.0f;
+        four(&sm.C[tile_at<N>(t, 16 * nt + 4 * kq)], cf);
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          const float ce = c[ii] * e;
+          dCa[a][ii] += ce;
+          dBa[a][ii] = fmaf(b[ii], wj, dBa[a][ii]);
+          qs = fmaf(ce, cf[ii], qs);
+        }
         qs = sum_kq(qs);
         if (kq == 0) sm.q[nt][t] = qs;
       }
     }
     __syncthreads();
-
-    // ---- dx: lane holds (p = 16 pt + 4 kq + ii, j = 16 jt + r)
-    {
-      float dd4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      const int pc = 16 * pt + 4 * kq;
-      float Dv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (p.D) {
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii) Dv[ii] = p.D_per_channel ? p.D[h * kP + pc + ii] : p.D[h];
-      }
-#pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        __builtin_amdgcn_sched_barrier(0);
-        const int jt = jx0 + a, j = 16 * jt + r;
-        f32x4 st = zero4, pr = zero4;
-#pragma unroll
-        for (int kk = 0; kk < KN; ++kk) {
-          const bf16x8 bf = frag<N>(l, sm.B, 16 * jt, 32 * kk);
-          st = mfma(frag<N>(l, sm.dh[0], 16 * pt, 32 * kk), bf, st);
-          st = mfma(frag<N>(l, sm.dh[1], 16 * pt, 32 * kk), bf, st);
-        }
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-          if (32 * (kk + 1) > 16 * jt) {
-            const bf16x8 gf = frag_t<kP>(l, sm.g, 32 * kk, 16 * pt);
-            pr = mfma(gf, frag<kQ>(l, sm.U[0], 16 * jt, 32 * kk), pr);
-            pr = mfma(gf, frag<kQ>(l, sm.U[1], 16 * jt, 32 * kk), pr);
-          }
-        st *= fast_exp2((cse - cs[j]) * kLog2e);
-        const uint2 xw = *reinterpret_cast<const uint2 *>(&sm.x[tile_at<kP>(j, pc)]);
-        const uint2 gw = *reinterpret_cast<const uint2 *>(&sm.g[tile_at<kP>(j, pc)]);
-        const float xf[4] = {__uint_as_float(xw.x << 16), __uint_as_float(xw.x & 0xffff0000u), __uint_as_float(xw.y << 16),
-                             __uint_as_float(xw.y & 0xffff0000u)};
-        const float gf[4] = {__uint_as_float(gw.x << 16), __uint_as_float(gw.x & 0xffff0000u), __uint_as_float(gw.y << 16),
-                             __uint_as_float(gw.y & 0xffff0000u)};
-        float rs = 0.0f, o[4];
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii) {
-          rs = fmaf(xf[ii], st[ii], rs);
-          dd4[ii] = fmaf(gf[ii], xf[ii], dd4[ii]);
-          o[ii] = fmaf(dt[j], pr[ii] + st[ii], Dv[ii] * gf[ii]);
-        }
-        rs = sum_kq(rs);
-        if (kq == 0) sm.r[pt][j] = rs;
-        if (j < len)
-          *reinterpret_cast<uint2 *>(p.dx + (t0 + j) * p.dxs + h * kP + pc) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
-      }
-      if (p.D) {   // this wave's tokens' part of each channel's sum
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii) {
-          dd4[ii] = sum_r(dd4[ii]);
-          if (r == 0) sm.dd[w >> 2][pc + ii] = dd4[ii];
-        }
-      }
-    }
-    __syncthreads();
-
-    // ---- the steps: wave 0, lane = token
-    if (w == 0) {
-      const float d = dt[l];
+    // ---- add up the head's partial sums (read before the next barrier, after
+    // which the next head writes its own)
+    if (w == (k & 7)) {
       const float rs = (sm.r[0][l] + sm.r[1][l]) + (sm.r[2][l] + sm.r[3][l]);
       const float direct = (sm.col[0][l] + sm.col[1][l]) + (sm.col[2][l] + sm.col[3][l]) + rs;
-      float qs = 0.0f;
+      float into = (sm.row[0][l] + sm.row[1][l]) + (sm.row[2][l] + sm.row[3][l]);
 #pragma unroll
-      for (int a = 0; a < NT; ++a) qs += sm.q[a][l];
-      float dcs = sm.row[0][l] + sm.row[1][l] + qs - d * direct;
-      float hh = 0.0f;
-#pragma unroll
-      for (int a = 0; a < 8; ++a) hh += sm.hh[a];
-      const float into_end = fmaf(fast_exp2(cse * kLog2e), hh, sum_wave(d * rs));
-      if (l == kQ - 1) dcs += into_end;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const float o = __shfl_down(dcs, off);
-        if (l + off < 64) dcs += o;
-      }
-      const float Ah = p.A[h], v = sm.v[k][l];
-      float dd = fmaf(Ah, dcs, direct);
-      if (p.dt_limit) {
-        const float sp = p.softplus ? softplus_acc(v) : v;
-        if (!(sp >= p.dt_min && sp <= p.dt_max)) dd = 0.0f;
-      }
-      if (p.softplus) dd *= fast_rcp(1.0f + fast_exp2(-v * kLog2e));
-      if (l >= len) dd = 0.0f;
-      else p.ddt[(t0 + l) * p.ddts + h] = static_cast<uint16_t>(float_to_half_bits<1>(dd));
-      const float dA = sum_wave(d * dcs), db = sum_wave(dd);
+      for (int a = 0; a < NT; ++a) into += sm.q[a][l];
+      sm.rs[k][l] = rs;
+      sm.direct[k][l] = direct;
+      sm.into[k][l] = into;
+      if (p.D) sm.ddc[k][l] = sm.dd[0][l] + sm.dd[1][l];
       if (l == 0) {
-        p.ws_sum[(entry * p.nheads + h) * 2] = dA;
-        p.ws_sum[(entry * p.nheads + h) * 2 + 1] = db;
+        float hh = 0.0f;
+#pragma unroll
+        for (int a = 0; a < NT; ++a) hh += sm.hh[a];
+        sm.hhs[k] = hh;
       }
-      if (p.D) {
-        const float s = sm.dd[0][l] + sm.dd[1][l];
-        if (p.D_per_channel) p.ws_dd[(entry * p.nheads + h) * kP + l] = s;
-        else if (const float all = sum_wave(s); l == 0) p.ws_dd[entry * p.nheads + h] = all;
-      }
+    }
+  }
+  __syncthreads();
+
+  // ---- the heads' steps: lane = token
+  for (int k = w; k < nh; k += 8) {
+    const int64_t h = h0 + k;
+    const float Ah = p.A[h], d = sm.dt[k][l], rs = sm.rs[k][l], direct = sm.direct[k][l];
+    const float raw = l < len ? bf2f(p.dt[(t0 + l) * p.dts + h]) : 0.0f;
+    float dcs = sm.into[k][l] - d * direct;
+    const float into_end = fmaf(sm.e0[k][kQ - 1], sm.hhs[k], sum_wave(d * rs));
+    if (l == kQ - 1) dcs += into_end;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const float o = __shfl_down(dcs, off);
+      if (l + off < 64) dcs += o;
+    }
+    float v, dd = fmaf(Ah, dcs, direct);
+    chunk_step(p, raw, p.dt_bias ? p.dt_bias[h] : 0.0f, true, v);
+    if (p.dt_limit) {
+      const float sp = p.softplus ? softplus_acc(v) : v;
+      if (!(sp >= p.dt_min && sp <= p.dt_max)) dd = 0.0f;
+    }
+    if (p.softplus) dd *= fast_rcp(1.0f + fast_exp2(-v * kLog2e));
+    if (l >= len) dd = 0.0f;
+    else p.ddt[(t0 + l) * p.ddts + h] = static_cast<uint16_t>(float_to_half_bits<1>(dd));
+    const float dA = sum_wave(d * dcs), db = sum_wave(dd);
+    if (l == 0) {
+      p.ws_sum[(entry * p.nheads + h) * 2] = dA;
+      p.ws_sum[(entry * p.nheads + h) * 2 + 1] = db;
+    }
+    if (p.D) {
+      const float s = sm.ddc[k][l];
+      if (p.D_per_channel) p.ws_dd[(entry * p.nheads + h) * kP + l] = s;
+      else if (const float all = sum_wave(s); l == 0) p.ws_dd[entry * p.nheads + h] = all;
     }
   }
 
   // ---- the pair parts of dB and dC, from the heads' summed M L dt'
-  __syncthreads();
   uint16_t *Vh = sm.dh[0], *Vl = sm.dh[1];
+  *reinterpret_cast<uint4 *>(Vh + 8 * tid) = zero;
+  *reinterpret_cast<uint4 *>(Vl + 8 * tid) = zero;
+  __syncthreads();
+  auto put_V = [&](auto hc) {
+    using PR = Pairs<decltype(hc)::value>;
 #pragma unroll
-  for (int a = 0; a < 2; ++a) {
-    uint2 hi, lo;
-    split_bf2(V[a][0], V[a][1], hi.x, lo.x);
-    split_bf2(V[a][2], V[a][3], hi.y, lo.y);
-    const int o = tile_at<kQ>(16 * (jt0 + a) + r, 16 * it + 4 * kq);
-    *reinterpret_cast<uint2 *>(&Vh[o]) = hi;
-    *reinterpret_cast<uint2 *>(&Vl[o]) = lo;
-  }
+    for (int t = 0; t < 5; ++t) {
+      if (pt != (t & 3)) continue;
+      const f32x4 &v = V[t >> 2];
+      uint2 vh, vl;
+      split_bf2(v[0], v[1], vh.x, vl.x);
+      split_bf2(v[2], v[3], vh.y, vl.y);
+      const int o = tile_at<kQ>(16 * PR::jt(t) + r, 16 * PR::it(t) + 4 * kq);
+      *reinterpret_cast<uint2 *>(&Vh[o]) = vh;
+      *reinterpret_cast<uint2 *>(&Vl[o]) = vl;
+    }
+  };
+  if (half == 0) put_V(std::integral_constant<int, 0>{});
+  else put_V(std::integral_constant<int, 1>{});
   __syncthreads();
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) {
