@@ -33,8 +33,9 @@ def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
 
 
 def _stream(device: torch.device, stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:   # torch.cuda.current_stream builds a Stream object around the same handle
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 # Every wrapper checks each tensor against the sizes that delta (or x) and A
@@ -45,7 +46,7 @@ def _stream(device: torch.device, stream=None):
 def _spec(t: Optional[torch.Tensor], name: str, shape, dtype, dev: torch.device) -> None:
     """Raise ValueError unless t (when given) has this shape and dtype and
     lives on dev."""
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype == dtype and t.device == dev):
         return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -935,8 +936,14 @@ def ssd_scan_workspace_size(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
 
 
 # ---------------------------------------------------------------------------
-# Packed tokens: a Mamba-2 mixer's conv, scan and step
+# Packed tokens: a Mamba-2 mixer's conv, scan and step.  The smallest calls
+# take the GPU a few microseconds, so the checks' passing path is kept short
+# and the argument structures are filled by position, in the C order.
 # ---------------------------------------------------------------------------
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
 
 def _tokens(t: Optional[torch.Tensor], vec: int = 0) -> Optional[torch.Tensor]:
     """t as the library takes a packed tensor: whatever a token holds dense,
@@ -945,22 +952,21 @@ def _tokens(t: Optional[torch.Tensor], vec: int = 0) -> Optional[torch.Tensor]:
     not so is copied."""
     if t is None:
         return None
-    want, ok = 1, t.shape[0] <= 1 or t.stride(0) >= 1
-    for d in range(t.dim() - 1, 0, -1):
-        ok = ok and (t.shape[d] == 1 or t.stride(d) == want)
-        want *= t.shape[d]
-    ok = ok and (t.shape[0] <= 1 or t.stride(0) >= want)
-    if ok and vec:
-        ok = t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or t.stride(0) % vec == 0)
+    shape, stride, want, ok = t.shape, t.stride(), 1, True
+    for d in range(len(shape) - 1, 0, -1):
+        if stride[d] != want and shape[d] != 1:
+            ok = False
+        want *= shape[d]
+    if shape[0] > 1:
+        ok = ok and stride[0] >= want and not (vec and stride[0] % vec)
+    if vec:
+        ok = ok and want % vec == 0 and t.data_ptr() % 16 == 0
     return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 def _token_stride(t: torch.Tensor) -> int:
     """Elements from a token to the next."""
-    n = 1
-    for d in t.shape[1:]:
-        n *= d
-    return t.stride(0) if t.shape[0] > 1 else n
+    return t.stride(0) if t.shape[0] > 1 else t.numel()
 
 
 def _tokens_out(t: Optional[torch.Tensor], name: str, shape, dtype, dev: torch.device, vec: int = 0) -> torch.Tensor:
@@ -975,6 +981,8 @@ def _tokens_out(t: Optional[torch.Tensor], name: str, shape, dtype, dev: torch.d
 
 
 def _int32(t: Optional[torch.Tensor], name: str, count: int, dev: torch.device) -> Optional[torch.Tensor]:
+    if t is None:
+        return None
     _spec(t, name, (count,), torch.int32, dev)
     return _dense(t)
 
@@ -983,7 +991,7 @@ def _cu_spec(cu: torch.Tensor, dev: torch.device) -> int:
     """Checks cu_seqlens and returns the number of sequences."""
     if cu.dim() != 1 or cu.shape[0] < 2:
         raise ValueError(f"cu_seqlens must have shape (nseq + 1,) with nseq >= 1, got {tuple(cu.shape)}")
-    _int32(cu, "cu_seqlens", cu.shape[0], dev)
+    _spec(cu, "cu_seqlens", cu.shape, torch.int32, dev)
     return cu.shape[0] - 1
 
 
@@ -995,37 +1003,28 @@ def _cache_spec(t: Optional[torch.Tensor], name: str, tail, dtype, dev: torch.de
     _out_spec(t, name, (t.shape[0],) + tuple(tail), dtype, dev)
 
 
-def _limit(a, dt_limit) -> None:
-    if dt_limit is not None:
-        a.dt_limit, a.dt_min, a.dt_max = 1, float(dt_limit[0]), float(dt_limit[1])
-
-
 def _workspace(size_fn, a, given: Optional[torch.Tensor], dev: torch.device) -> Optional[torch.Tensor]:
     """The caller's scratch, or as much as the call needs; set in a."""
     ws = given
     if ws is None:
         need = ctypes.c_size_t(0)
-        check(size_fn(ctypes.byref(a), ctypes.byref(need)))
+        check(size_fn(a, need))
         if need.value:
             ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
     if ws is not None:
-        _workspace_spec(ws, dev)
-        a.workspace, a.workspace_bytes = _ptr(ws), ws.numel() * ws.element_size()
+        if given is not None:
+            _workspace_spec(ws, dev)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     return ws
 
 
-def _conv_varlen_args(x, weight, cu_seqlens, bias, activation):
-    io = _io_of(x, "x", 2)
-    total, channels = x.shape
-    weight, bias, dev = _dense(weight), _dense(bias), x.device
-    _conv_params_spec(weight, bias, channels, dev)
-    nseq = _cu_spec(cu_seqlens, dev)
-    x, cu_seqlens = _tokens(x), _dense(cu_seqlens)
-    a = _lib.ConvVarlenArgs()
-    a.total, a.nseq, a.channels = total, nseq, channels
-    a.width, a.io_dtype, a.act = weight.shape[1], io, _act_code(activation)
-    a.x, a.x_stride, a.weight, a.bias, a.cu_seqlens = _ptr(x), _token_stride(x), _ptr(weight), _ptr(bias), _ptr(cu_seqlens)
-    return a, (x, weight, bias, cu_seqlens)
+def _conv_varlen(x, weight, cu_seqlens, bias):
+    """The checks that the conv's two directions share: (io, nseq, and the
+    tensors as the library takes them)."""
+    io, dev = _io_of(x, "x", 2), x.device
+    weight, bias = _dense(weight), _dense(bias)
+    _conv_params_spec(weight, bias, x.shape[1], dev)
+    return io, _cu_spec(cu_seqlens, dev), _tokens(x), weight, _dense(cu_seqlens), bias
 
 
 def causal_conv1d_varlen_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -1041,17 +1040,21 @@ def causal_conv1d_varlen_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: 
     continues from entry ``slots[s]`` (s without ``slots``; an entry outside
     the cache is skipped) if ``cache_seqlens[s]`` > 0 tokens went before it,
     and leaves its last inputs there."""
-    a, keep = _conv_varlen_args(x, weight, cu_seqlens, bias, activation)
-    dev, nseq = x.device, a.nseq
+    io, nseq, x, weight, cu_seqlens, bias = _conv_varlen(x, weight, cu_seqlens, bias)
+    dev = x.device
+    total, channels = x.shape
     cache_seqlens, slots = _int32(cache_seqlens, "cache_seqlens", nseq, dev), _int32(slots, "slots", nseq, dev)
+    entries = state_len = 0
     if conv_state is not None:
-        _cache_spec(conv_state, "conv_state", (x.shape[1], conv_state.shape[-1]), x.dtype, dev)
-        a.conv_state, a.state_slots, a.state_len = _ptr(conv_state), conv_state.shape[0], conv_state.shape[2]
-    out = _tokens_out(out, "out", x.shape, x.dtype, dev)
+        _cache_spec(conv_state, "conv_state", (channels, conv_state.shape[-1]), x.dtype, dev)
+        entries, state_len = conv_state.shape[0], conv_state.shape[2]
+    act = _act_code(activation)
     _on_gpu(dev)
-    a.out, a.out_stride = _ptr(out), _token_stride(out)
-    a.cache_seqlens, a.slots = _ptr(cache_seqlens), _ptr(slots)
-    check(_lib.lib().causal_conv1d_varlen_fwd(ctypes.byref(a), _stream(dev, stream)))
+    out = _tokens_out(out, "out", x.shape, x.dtype, dev)
+    a = _lib.ConvVarlenArgs(total, nseq, channels, weight.shape[1], io, act, x.data_ptr(), _token_stride(x),
+                            weight.data_ptr(), _addr(bias), cu_seqlens.data_ptr(), out.data_ptr(), _token_stride(out),
+                            _addr(conv_state), entries, state_len, _addr(cache_seqlens), _addr(slots))
+    check(_lib.lib().causal_conv1d_varlen_fwd(a, _stream(dev, stream)))
     return out
 
 
@@ -1062,21 +1065,23 @@ def causal_conv1d_varlen_bwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: 
     """Gradient of causal_conv1d_varlen_fwd for sequences that start from
     nothing: dx (x's dtype; written into ``dx`` when given), dweight and dbias
     (float32)."""
-    a, keep = _conv_varlen_args(x, weight, cu_seqlens, bias, activation)
+    io, nseq, x, weight, cu_seqlens, bias = _conv_varlen(x, weight, cu_seqlens, bias)
     dev, f32 = x.device, torch.float32
+    total, channels = x.shape
     _spec(dout, "dout", x.shape, x.dtype, dev)
     dout = _tokens(dout)
-    dx = _tokens_out(dx, "dx", x.shape, x.dtype, dev)
-    if workspace is not None:
-        _workspace_spec(workspace, dev)
+    act = _act_code(activation)
     _on_gpu(dev)
+    dx = _tokens_out(dx, "dx", x.shape, x.dtype, dev)
     dweight = torch.empty(weight.shape, dtype=f32, device=dev)
     dbias = None if bias is None else torch.empty(bias.shape, dtype=f32, device=dev)
-    a.dout, a.dout_stride, a.dx, a.dx_stride = _ptr(dout), _token_stride(dout), _ptr(dx), _token_stride(dx)
-    a.dweight, a.dbias = _ptr(dweight), _ptr(dbias)
+    a = _lib.ConvVarlenArgs(total, nseq, channels, weight.shape[1], io, act, x.data_ptr(), _token_stride(x),
+                            weight.data_ptr(), _addr(bias), cu_seqlens.data_ptr(), None, 0, None, 0, 0, None, None,
+                            dout.data_ptr(), _token_stride(dout), dx.data_ptr(), _token_stride(dx), dweight.data_ptr(),
+                            _addr(dbias))
     L = _lib.lib()
     ws = _workspace(L.causal_conv1d_varlen_bwd_workspace_size, a, workspace, dev)
-    check(L.causal_conv1d_varlen_bwd(ctypes.byref(a), _stream(dev, stream)))
+    check(L.causal_conv1d_varlen_bwd(a, _stream(dev, stream)))
     return {"dx": dx, "dweight": dweight, "dbias": dbias}
 
 
@@ -1085,21 +1090,21 @@ def ssd_checkpoint_slots(total: int, nseq: int) -> int:
     return total // _lib.SSD_CHUNK + nseq
 
 
-def _ssd_varlen_args(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_softplus, dt_limit, checkpoints,
-                     seq_segments):
-    """ssd_varlen_args_t without outputs and caches; returns (args, tensors
-    kept alive until the call)."""
+def _ssd_varlen(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_softplus, dt_limit, checkpoints):
+    """The checks that the scan's two directions share.  Returns the fields of
+    ssd_varlen_args_t up to ``cu_seqlens`` and the tensors to keep alive until
+    the call."""
     if x.dtype != torch.bfloat16:
         raise ValueError(f"the packed scan takes bfloat16 io, got {x.dtype}")
     if x.dim() != 3 or B.dim() != 3:
         raise ValueError("x must be (total, nheads, headdim) and B (total, ngroups, dstate)")
     total, nheads, headdim = x.shape
-    ngroups, dstate = B.shape[1], B.shape[2]
-    dev, f32 = x.device, torch.float32
-    _spec(z, "z", x.shape, x.dtype, dev)
-    _spec(dt, "dt", (total, nheads), x.dtype, dev)
-    _spec(B, "B", (total, ngroups, dstate), x.dtype, dev)
-    _spec(C, "C", (total, ngroups, dstate), x.dtype, dev)
+    _, ngroups, dstate = B.shape
+    dev, io, f32 = x.device, x.dtype, torch.float32
+    _spec(z, "z", x.shape, io, dev)
+    _spec(dt, "dt", (total, nheads), io, dev)
+    _spec(B, "B", (total, ngroups, dstate), io, dev)
+    _spec(C, "C", (total, ngroups, dstate), io, dev)
     _spec(A, "A", (nheads,), f32, dev)
     _spec(dt_bias, "dt_bias", (nheads,), f32, dev)
     if D is not None:
@@ -1111,22 +1116,15 @@ def _ssd_varlen_args(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_s
         rows = (ssd_checkpoint_slots(total, nseq), nheads, headdim)
         _spec(checkpoints[0], "checkpoints[0]", rows + (dstate,), torch.int8, dev)
         _spec(checkpoints[1], "checkpoints[1]", rows, f32, dev)
-    a = _lib.SsdVarlenArgs()
     x, B, C, z, dt = _tokens(x, 8), _tokens(B, 8), _tokens(C, 8), _tokens(z, 8), _tokens(dt)
     A, D, dt_bias, cu_seqlens = _dense(A), _dense(D), _dense(dt_bias), _dense(cu_seqlens)
-    a.total, a.nseq, a.max_seqlen = total, nseq, int(max_seqlen)
-    a.nheads, a.headdim, a.dstate, a.ngroups, a.io_dtype = nheads, headdim, dstate, ngroups, _lib.SSM_BF16
-    a.x, a.x_stride, a.dt, a.dt_stride = _ptr(x), _token_stride(x), _ptr(dt), _token_stride(dt)
-    a.A, a.B, a.B_stride, a.C, a.C_stride = _ptr(A), _ptr(B), _token_stride(B), _ptr(C), _token_stride(C)
-    a.D, a.D_per_channel = _ptr(D), int(D is not None and D.dim() == 2)
-    if z is not None:
-        a.z, a.z_stride = _ptr(z), _token_stride(z)
-    a.dt_bias, a.dt_softplus = _ptr(dt_bias), int(bool(dt_softplus))
-    _limit(a, dt_limit)
-    a.cu_seqlens, a.seq_segments = _ptr(cu_seqlens), int(seq_segments)
-    if checkpoints is not None:
-        a.checkpoints, a.checkpoint_scales = _ptr(checkpoints[0]), _ptr(checkpoints[1])
-    return a, (x, dt, A, B, C, D, z, dt_bias, cu_seqlens)
+    lo, hi = (0.0, 0.0) if dt_limit is None else dt_limit
+    fields = (total, nseq, int(max_seqlen), nheads, headdim, dstate, ngroups, _lib.SSM_BF16, x.data_ptr(), _token_stride(x),
+              dt.data_ptr(), _token_stride(dt), A.data_ptr(), B.data_ptr(), _token_stride(B), C.data_ptr(),
+              _token_stride(C), _addr(D), int(D is not None and D.dim() == 2), _addr(z),
+              0 if z is None else _token_stride(z), _addr(dt_bias), int(bool(dt_softplus)), int(dt_limit is not None),
+              float(lo), float(hi), cu_seqlens.data_ptr())
+    return fields, (x, dt, A, B, C, D, z, dt_bias, cu_seqlens)
 
 
 def ssd_varlen_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
@@ -1150,24 +1148,23 @@ def ssd_varlen_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     headdim, dstate), float32 (entries, nheads, headdim)) with
     ``ssd_checkpoint_slots(total, nseq)`` entries receives every chunk's
     entering state in 8 bits for ``ssd_varlen_bwd``."""
-    a, keep = _ssd_varlen_args(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_softplus, dt_limit,
-                               checkpoints, seq_segments)
-    dev, nseq = x.device, a.nseq
-    for i, t in enumerate(checkpoints or ()):
-        _out_spec(t, f"checkpoints[{i}]", t.shape, t.dtype, dev)
-    _cache_spec(ssm_state, "ssm_state", (a.nheads, a.headdim, a.dstate), torch.float32, dev)
+    fields, keep = _ssd_varlen(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_softplus, dt_limit, checkpoints)
+    dev, nseq = x.device, fields[1]
+    _cache_spec(ssm_state, "ssm_state", fields[3:6], torch.float32, dev)
     cache_seqlens, slots = _int32(cache_seqlens, "cache_seqlens", nseq, dev), _int32(slots, "slots", nseq, dev)
-    out = _tokens_out(out, "out", x.shape, x.dtype, dev, 8)
-    if workspace is not None:
-        _workspace_spec(workspace, dev)
+    codes = scales = None
+    if checkpoints is not None:
+        codes, scales = checkpoints
+        for name, t in (("checkpoints[0]", codes), ("checkpoints[1]", scales)):
+            _out_spec(t, name, t.shape, t.dtype, dev)
     _on_gpu(dev)
-    a.out, a.out_stride = _ptr(out), _token_stride(out)
-    if ssm_state is not None:
-        a.ssm_state, a.state_slots = _ptr(ssm_state), ssm_state.shape[0]
-    a.cache_seqlens, a.slots = _ptr(cache_seqlens), _ptr(slots)
+    out = _tokens_out(out, "out", x.shape, x.dtype, dev, 8)
+    a = _lib.SsdVarlenArgs(*fields, out.data_ptr(), _token_stride(out), _addr(ssm_state),
+                           0 if ssm_state is None else ssm_state.shape[0], _addr(cache_seqlens), _addr(slots),
+                           _addr(codes), _addr(scales), None, 0, int(seq_segments))
     L = _lib.lib()
     ws = _workspace(L.ssd_varlen_fwd_workspace_size, a, workspace, dev)
-    check(L.ssd_varlen_fwd(ctypes.byref(a), _stream(dev, stream)))
+    check(L.ssd_varlen_fwd(a, _stream(dev, stream)))
     return out
 
 
@@ -1183,52 +1180,50 @@ def ssd_varlen_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     """Gradients of ssd_varlen_fwd (without z) in a dict.
 
     ``dout``: (total, nheads, headdim) bf16; ``checkpoints``: what the forward
-    wrote, with any strides from entry to entry and head to head.  dx, ddt, dB and dC come in bf16 (into the tensors given, which may
-    be parts of one row, or new ones), dA, dD and ddt_bias in float32.
+    wrote, with any strides from entry to entry and head to head.  dx, ddt, dB
+    and dC come in bf16 (into the tensors given, which may be parts of one row,
+    or new ones), dA, dD and ddt_bias in float32.
     ``dfinal_states`` (nseq, nheads, headdim, dstate) float32 is the gradient
     of the sequences' last states; with ``want_dinitial_states`` that of their
     first ones is returned."""
     if checkpoints is None:
         raise ValueError("the backward needs the checkpoints that the forward wrote")
-    a = _lib.SsdVarlenBwdArgs()
-    codes, scales = checkpoints
-    # any strides from entry to entry and head to head; a channel's states dense
-    if codes.dim() == 4 and not (codes[0, 0].is_contiguous() and codes.data_ptr() % 16 == 0 and codes.stride(0) % 16 == 0
-                                 and codes.stride(1) % 16 == 0 and min(codes.stride()[:2]) >= codes[0, 0].numel()):
-        codes = codes.clone(memory_format=torch.contiguous_format)
-    if scales.dim() == 3 and not (scales[0, 0].is_contiguous() and min(scales.stride()[:2]) >= scales.shape[2]):
-        scales = scales.clone(memory_format=torch.contiguous_format)
-    checkpoints = (codes, scales)
-    a.fwd, keep = _ssd_varlen_args(x, dt, A, B, C, cu_seqlens, max_seqlen, D, None, dt_bias, dt_softplus, dt_limit,
-                                   checkpoints, seq_segments)
+    fields, keep = _ssd_varlen(x, dt, A, B, C, cu_seqlens, max_seqlen, D, None, dt_bias, dt_softplus, dt_limit,
+                               checkpoints)
     dev, f32, io = x.device, torch.float32, x.dtype
-    states = (a.fwd.nseq,) + (a.fwd.nheads, a.fwd.headdim, a.fwd.dstate)
+    nseq, nheads, headdim, dstate = fields[1], fields[3], fields[4], fields[5]
+    # any strides from entry to entry and head to head; a channel's states dense
+    codes, scales = checkpoints
+    c0, c1, c2, c3 = codes.stride()
+    if c3 != 1 or c2 != dstate or c0 % 16 or c1 % 16 or min(c0, c1) < headdim * dstate or codes.data_ptr() % 16:
+        codes = codes.clone(memory_format=torch.contiguous_format)
+    if scales.stride(2) != 1 or min(scales.stride(0), scales.stride(1)) < headdim:
+        scales = scales.clone(memory_format=torch.contiguous_format)
+    states = (nseq, nheads, headdim, dstate)
     _spec(dout, "dout", x.shape, io, dev)
     _spec(dfinal_states, "dfinal_states", states, f32, dev)
     dout, dfinal_states = _tokens(dout, 8), _dense(dfinal_states)
-    g = {"dx": _tokens_out(dx, "dx", x.shape, io, dev, 8), "ddt": _tokens_out(ddt, "ddt", dt.shape, io, dev),
-         "dB": _tokens_out(dB, "dB", B.shape, io, dev, 8), "dC": _tokens_out(dC, "dC", C.shape, io, dev, 8)}
-    if workspace is not None:
-        _workspace_spec(workspace, dev)
     _on_gpu(dev)
-    g["dA"] = torch.empty(A.shape, dtype=f32, device=dev)
+    g = {"dx": _tokens_out(dx, "dx", x.shape, io, dev, 8), "ddt": _tokens_out(ddt, "ddt", dt.shape, io, dev),
+         "dB": _tokens_out(dB, "dB", B.shape, io, dev, 8), "dC": _tokens_out(dC, "dC", C.shape, io, dev, 8),
+         "dA": torch.empty(A.shape, dtype=f32, device=dev)}
     if D is not None:
         g["dD"] = torch.empty(D.shape, dtype=f32, device=dev)
     if dt_bias is not None:
         g["ddt_bias"] = torch.empty(dt_bias.shape, dtype=f32, device=dev)
     if want_dinitial_states:
         g["dinitial_states"] = torch.empty(states, dtype=f32, device=dev)
-    a.code_entry_stride, a.code_head_stride = codes.stride()[:2]
-    a.scale_entry_stride, a.scale_head_stride = scales.stride()[:2]
-    a.dout, a.dout_stride, a.dfinal_states = _ptr(dout), _token_stride(dout), _ptr(dfinal_states)
+    fwd = _lib.SsdVarlenArgs(*fields, None, 0, None, 0, None, None, codes.data_ptr(), scales.data_ptr(), None, 0,
+                             int(seq_segments))
+    out = []
     for k in ("dx", "ddt", "dB", "dC"):
-        setattr(a, k, _ptr(g[k]))
-        setattr(a, k + "_stride", _token_stride(g[k]))
-    for k in ("dA", "dD", "ddt_bias", "dinitial_states"):
-        setattr(a, k, _ptr(g.get(k)))
+        out += (g[k].data_ptr(), _token_stride(g[k]))
+    a = _lib.SsdVarlenBwdArgs(fwd, codes.stride(0), codes.stride(1), scales.stride(0), scales.stride(1), dout.data_ptr(),
+                              _token_stride(dout), _addr(dfinal_states), *out, g["dA"].data_ptr(), _addr(g.get("dD")),
+                              _addr(g.get("ddt_bias")), _addr(g.get("dinitial_states")))
     L = _lib.lib()
     ws = _workspace(L.ssd_varlen_bwd_workspace_size, a, workspace, dev)
-    check(L.ssd_varlen_bwd(ctypes.byref(a), _stream(dev, stream)))
+    check(L.ssd_varlen_bwd(a, _stream(dev, stream)))
     return g
 
 
@@ -1255,40 +1250,36 @@ def conv1d_ssd_update(xBC: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, conv
         raise ValueError(f"ssm_state must be (entries, nheads, headdim, dstate), got shape {tuple(ssm_state.shape)}")
     entries, nheads, headdim, dstate = ssm_state.shape
     batch, channels = xBC.shape
-    dev, f32, hp = xBC.device, torch.float32, nheads * headdim
+    dev, f32, dtype, hp = xBC.device, torch.float32, xBC.dtype, nheads * headdim
     ngroups = (channels - hp) // (2 * dstate)
     if channels <= hp or (channels - hp) % (2 * dstate) != 0:
         raise ValueError(f"xBC must have nheads * headdim + 2 * ngroups * dstate columns, got {channels} "
                          f"for {nheads} heads of {headdim} and dstate {dstate}")
-    _cache_spec(ssm_state, "ssm_state", (nheads, headdim, dstate), f32, dev)
+    _out_spec(ssm_state, "ssm_state", ssm_state.shape, f32, dev)
     if conv_state.dim() != 3:
         raise ValueError(f"conv_state must be (entries, channels, state_len), got shape {tuple(conv_state.shape)}")
-    _out_spec(conv_state, "conv_state", (entries, channels, conv_state.shape[2]), xBC.dtype, dev)
-    conv_weight, conv_bias, A, D, dt_bias = (_dense(t) for t in (conv_weight, conv_bias, A, D, dt_bias))
+    _out_spec(conv_state, "conv_state", (entries, channels, conv_state.shape[2]), dtype, dev)
+    conv_weight, conv_bias, A, D, dt_bias = _dense(conv_weight), _dense(conv_bias), _dense(A), _dense(D), _dense(dt_bias)
     _conv_params_spec(conv_weight, conv_bias, channels, dev)
-    _spec(dt, "dt", (batch, nheads), xBC.dtype, dev)
-    _spec(z, "z", (batch, hp), xBC.dtype, dev)
+    _spec(dt, "dt", (batch, nheads), dtype, dev)
+    _spec(z, "z", (batch, hp), dtype, dev)
     _spec(A, "A", (nheads,), f32, dev)
     _spec(dt_bias, "dt_bias", (nheads,), f32, dev)
+    per_channel = 0
     if D is not None:
-        _spec(D, "D", (nheads,) if D.dim() == 1 else (nheads, headdim), f32, dev)
+        per_channel = int(D.dim() == 2)
+        _spec(D, "D", (nheads, headdim) if per_channel else (nheads,), f32, dev)
     cache_seqlens, slots = _int32(cache_seqlens, "cache_seqlens", batch, dev), _int32(slots, "slots", batch, dev)
-    out = _tokens_out(out, "out", (batch, hp), xBC.dtype, dev)
     act = _act_code(activation)
     _on_gpu(dev)
+    out = _tokens_out(out, "out", (batch, hp), dtype, dev)
     xBC, dt, z = _tokens(xBC), _tokens(dt), _tokens(z)
-    a = _lib.ConvSsdUpdateArgs()
-    a.batch, a.nheads, a.headdim, a.dstate, a.ngroups = batch, nheads, headdim, dstate, ngroups
-    a.io_dtype, a.act, a.width = io, act, conv_weight.shape[1]
-    a.xBC, a.xBC_stride, a.dt, a.dt_stride = _ptr(xBC), _token_stride(xBC), _ptr(dt), _token_stride(dt)
-    a.A, a.conv_weight, a.conv_bias = _ptr(A), _ptr(conv_weight), _ptr(conv_bias)
-    a.D, a.D_per_channel, a.dt_bias = _ptr(D), int(D is not None and D.dim() == 2), _ptr(dt_bias)
-    if z is not None:
-        a.z, a.z_stride = _ptr(z), _token_stride(z)
-    a.dt_softplus = int(bool(dt_softplus))
-    _limit(a, dt_limit)
-    a.conv_state, a.state_len, a.ssm_state, a.state_slots = _ptr(conv_state), conv_state.shape[2], _ptr(ssm_state), entries
-    a.cache_seqlens, a.slots = _ptr(cache_seqlens), _ptr(slots)
-    a.out, a.out_stride = _ptr(out), _token_stride(out)
-    check(_lib.lib().conv1d_ssd_update(ctypes.byref(a), _stream(dev, stream)))
+    lo, hi = (0.0, 0.0) if dt_limit is None else dt_limit
+    a = _lib.ConvSsdUpdateArgs(
+        batch, nheads, headdim, dstate, ngroups, io, act, conv_weight.shape[1], xBC.data_ptr(), _token_stride(xBC),
+        dt.data_ptr(), _token_stride(dt), A.data_ptr(), conv_weight.data_ptr(), _addr(conv_bias), _addr(D), per_channel,
+        _addr(z), 0 if z is None else _token_stride(z), _addr(dt_bias), int(bool(dt_softplus)),
+        int(dt_limit is not None), float(lo), float(hi), conv_state.data_ptr(), conv_state.shape[2],
+        ssm_state.data_ptr(), entries, _addr(cache_seqlens), _addr(slots), out.data_ptr(), _token_stride(out))
+    check(_lib.lib().conv1d_ssd_update(a, _stream(dev, stream)))
     return out

@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "device_util.h"
 #include "host_util.h"
@@ -21,9 +22,10 @@ namespace ssm {
 namespace {
 
 constexpr int kW = SSM_CONV_WIDTH;
-constexpr int kFwdRun = 16;        // tokens of a wave's run, forward
+constexpr int kFwdRun = 12;        // tokens of a wave's run, forward
 constexpr int kBwdRun = 32;        // tokens of a wave's run, backward
-constexpr int kStep = 8;           // tokens whose loads are in flight together, backward
+constexpr int kBwdVec = 4;        // channels of a lane, backward, 16 bits
+constexpr int kStep = 4;           // tokens whose loads are in flight together, backward
 constexpr int kRows = 4;           // waves (runs) of a workgroup
 
 // NV neighbouring io elements (NV = 1: any alignment)
@@ -68,15 +70,15 @@ __device__ __forceinline__ int64_t find_seq(const int32_t *cu, int64_t nseq, int
   return lo;
 }
 
-// The input j + 1 tokens before a sequence's first one, from its ring.
+// The input `back` tokens before a sequence's first one, from its ring.
 template <int IO, int NV>
 __device__ __forceinline__ void ring_input(const ConvVarParams &p, int64_t s, int back, int64_t c0, float (&v)[NV]) {
-  const int64_t pos = (p.seen ? p.seen[s] : 0) - back;
+  const int pos = (p.ring && p.seen ? p.seen[s] : 0) - back;
   const int64_t slot = p.slots ? p.slots[s] : s;
-  const bool there = p.ring && pos >= 0 && slot >= 0 && slot < p.nslots;
+  const bool there = pos >= 0 && slot >= 0 && slot < p.nslots;
+  const int64_t at = there ? (slot * p.channels + c0) * p.ring_len + static_cast<uint32_t>(pos) % static_cast<uint32_t>(p.ring_len) : 0;
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-    v[k] = there ? load_io<IO>(p.ring, (slot * p.channels + c0 + k) * p.ring_len + pos % p.ring_len) : 0.0f;
+  for (int k = 0; k < NV; ++k) v[k] = there ? load_io<IO>(p.ring, at + k * p.ring_len) : 0.0f;
 }
 
 template <int NV>
@@ -111,35 +113,77 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_fwd_kernel(const ConvVarP
   int64_t s = find_seq(p.cu, p.nseq, t0);
   int64_t end = p.cu[s + 1];
   int64_t pos = t0 - p.cu[s];
+  if (n == kFwdRun && pos >= kW - 1 && t0 + kFwdRun <= end) {
+    // the whole run and what it sees are inside one sequence: no branch
+    // between the loads and their use (with the edge tests of every token in
+    // between the compiler kept few loads in flight: 216 us where this takes
+    // MEASURED at 16384 x 5376 bf16)
 #pragma unroll
-  for (int i = 0; i < kFwdRun; ++i) {
-    if (i >= n) break;
-    while (t0 + i >= end && s + 1 < p.nseq) {
+    for (int i = 0; i < kFwdRun; ++i) {
+      float acc[NV];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        acc[k] = bias[k];
+#pragma unroll
+        for (int j = kW - 1; j >= 0; --j) acc[k] = fmaf(w[j][k], in[i + j].get(k), acc[k]);
+        if (p.silu) acc[k] = silu_f(acc[k]);
+      }
+      put<IO, NV>(p.out, (t0 + i) * p.os + c0, acc);
+    }
+    return;
+  }
+  // A run with an edge in it, sequence by sequence: what lies before the
+  // piece's first token once, then its tokens with the last inputs rolling.
+  int from = 0;
+  while (true) {
+    while (t0 + from >= end && s + 1 < p.nseq) {
       ++s;
       end = p.cu[s + 1];
-      pos = t0 + i - p.cu[s];
+      pos = t0 + from - p.cu[s];
     }
-    float acc[NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) acc[k] = fmaf(w[kW - 1][k], in[i + kW - 1].get(k), bias[k]);
+    const int to = (s + 1 < p.nseq && end - t0 < n) ? static_cast<int>(end - t0) : n;
+    float win[kW - 1][NV];   // the last inputs, oldest first
 #pragma unroll
     for (int back = 1; back < kW; ++back) {
+      float (&h)[NV] = win[kW - 1 - back];
       if (pos >= back) {
+        Vec<IO, NV> v;
+        v.load(p.x, (t0 + from - back) * p.xs + c0);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) acc[k] = fmaf(w[kW - 1 - back][k], in[i + kW - 1 - back].get(k), acc[k]);
-      } else if (p.ring) {
-        float h[NV];
+        for (int k = 0; k < NV; ++k) h[k] = v.get(k);
+      } else {
         ring_input<IO, NV>(p, s, back - static_cast<int>(pos), c0, h);
-#pragma unroll
-        for (int k = 0; k < NV; ++k) acc[k] = fmaf(w[kW - 1 - back][k], h[k], acc[k]);
       }
     }
-    if (p.silu) {
+    // (the run's inputs once more, four tokens at a time: sharing the
+    // registers above with this path doubled the kernel's)
+#pragma unroll 1
+    for (int i = from; i < to; i += 4) {
+      Vec<IO, NV> now[4];
 #pragma unroll
-      for (int k = 0; k < NV; ++k) acc[k] = silu_f(acc[k]);
+      for (int q = 0; q < 4; ++q)
+        if (i + q < to) now[q].load(p.x, (t0 + i + q) * p.xs + c0);
+        else now[q].zero();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (i + q >= to) break;
+        float acc[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          const float v = now[q].get(k);
+          acc[k] = fmaf(w[kW - 1][k], v, bias[k]);
+#pragma unroll
+          for (int j = kW - 2; j >= 0; --j) acc[k] = fmaf(w[j][k], win[j][k], acc[k]);
+          if (p.silu) acc[k] = silu_f(acc[k]);
+#pragma unroll
+          for (int j = 0; j < kW - 2; ++j) win[j][k] = win[j + 1][k];
+          win[kW - 2][k] = v;
+        }
+        put<IO, NV>(p.out, (t0 + i + q) * p.os + c0, acc);
+      }
     }
-    put<IO, NV>(p.out, (t0 + i) * p.os + c0, acc);
-    ++pos;
+    if (to >= n) break;
+    from = to;
   }
 }
 
@@ -158,12 +202,16 @@ __global__ void __launch_bounds__(256) conv_var_ring_kernel(const ConvVarParams 
     int64_t seen = p.seen ? p.seen[s] : 0;
     if (seen < 0) seen = 0;
     const int64_t from = hi - lo > p.ring_len ? hi - p.ring_len : lo;
-    for (int64_t t = from; t < hi; ++t) {
-      const int64_t at = (slot * p.channels + c) * p.ring_len + (seen + t - lo) % p.ring_len;
-      if constexpr (IO != 0)
-        static_cast<uint16_t *>(p.ring)[at] = static_cast<const uint16_t *>(p.x)[t * p.xs + c];
-      else
-        static_cast<uint32_t *>(p.ring)[at] = static_cast<const uint32_t *>(p.x)[t * p.xs + c];
+    using Raw = typename std::conditional<IO != 0, uint16_t, uint32_t>::type;
+    const Raw *x = static_cast<const Raw *>(p.x) + c;
+    Raw *ring = static_cast<Raw *>(p.ring) + (slot * p.channels + c) * p.ring_len;
+    for (int64_t t = from; t < hi; t += 4) {   // four loads in flight
+      Raw v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = t + i < hi ? x[(t + i) * p.xs] : Raw(0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t + i < hi) ring[static_cast<uint64_t>(seen + t + i - lo) % static_cast<uint32_t>(p.ring_len)] = v[i];
     }
   }
 }
@@ -400,14 +448,14 @@ extern "C" int causal_conv1d_varlen_bwd(const causal_conv1d_varlen_args_t *a, vo
   const bool wide = wide_rows(a->io_dtype, a->channels, a->x, a->x_stride) &&
                     wide_rows(a->io_dtype, a->channels, a->dout, a->dout_stride) &&
                     wide_rows(a->io_dtype, a->channels, a->dx, a->dx_stride);
-  const int nv = !wide ? 1 : a->io_dtype == SSM_F32 ? 4 : 8;
+  const int nv = !wide ? 1 : a->io_dtype == SSM_F32 ? 4 : kBwdVec;
   const int64_t gx = bwd_blocks(a->total), gy = (a->channels + 64 * nv - 1) / (64 * nv);
   if (gy > 65535) return SSM_ERR_SHAPE;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * kRows);
   auto launch = [&](auto fn) { hipLaunchKernelGGL(fn, grid, block, 0, stream, p); };
-  if (a->io_dtype == SSM_BF16) wide ? launch(conv_var_bwd_kernel<1, 8>) : launch(conv_var_bwd_kernel<1, 1>);
-  else if (a->io_dtype == SSM_F16) wide ? launch(conv_var_bwd_kernel<2, 8>) : launch(conv_var_bwd_kernel<2, 1>);
+  if (a->io_dtype == SSM_BF16) wide ? launch(conv_var_bwd_kernel<1, kBwdVec>) : launch(conv_var_bwd_kernel<1, 1>);
+  else if (a->io_dtype == SSM_F16) wide ? launch(conv_var_bwd_kernel<2, kBwdVec>) : launch(conv_var_bwd_kernel<2, 1>);
   else wide ? launch(conv_var_bwd_kernel<0, 4>) : launch(conv_var_bwd_kernel<0, 1>);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return hip_fail(e);
