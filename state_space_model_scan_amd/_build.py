@@ -50,6 +50,10 @@ SOURCES = [
     ("validate.cpp", False),
 ]
 MICRO_SOURCES = [("microbench.hip", True)]
+# the torch binding of the packed-token operators: host code only, linked
+# against the operators' library beside it
+PACKED_SOURCE = "packed_binding.cpp"
+PACKED_LIB = os.path.join(PKG, "_packed.so")
 
 
 def _compile(src: str, is_hip: bool) -> str:
@@ -73,16 +77,35 @@ def _link(objs, lib):
     os.replace(tmp, lib)
 
 
+def _build_packed() -> None:
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    lib_dir = os.path.join(base, "lib")
+    include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               "/opt/rocm/include", sysconfig.get_paths()["include"]]
+    tmp = PACKED_LIB + ".tmp"
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", f"-I{INCLUDE}"]
+           + [f"-isystem{d}" for d in include] + [os.path.join(CSRC, PACKED_SOURCE), "-o", tmp, f"-L{PKG}", "-l:libssmscan.so",
+              "-Wl,-rpath,$ORIGIN", f"-L{lib_dir}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"])
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError(f"building {os.path.basename(PACKED_LIB)} failed")
+    os.replace(tmp, PACKED_LIB)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libssmscan.so and libssmmicro.so (always
-    rebuilds)."""
+    """Compile every source and link libssmscan.so, libssmmicro.so and
+    _packed.so (always rebuilds)."""
     srcs = SOURCES + MICRO_SOURCES
     with ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         objs = list(ex.map(lambda s: _compile(*s), srcs))
     _link(objs[:len(SOURCES)], LIB)
     _link(objs[len(SOURCES):], MICRO_LIB)
+    _build_packed()
     if verbose:
-        print(f"built {LIB} and {MICRO_LIB}")
+        print(f"built {LIB}, {MICRO_LIB} and {PACKED_LIB}")
     return LIB
 
 

@@ -276,6 +276,24 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_packed = None
+
+
+def packed():
+    """The torch binding of the packed-token operators (csrc/packed_binding.cpp);
+    raises with a clear message when it is not built."""
+    global _packed
+    if _packed is None:
+        lib()   # the same library serves both bindings
+        try:
+            from . import _packed as module
+        except ImportError as e:
+            raise RuntimeError(f"state_space_model_scan_amd/_packed.so is not built or does not load ({e}): run "
+                               "`python -m state_space_model_scan_amd._build`") from e
+        _packed = module
+    return _packed
+
+
 def check(status: int) -> None:
     if status != SSM_OK:
         text = lib().ssm_status_str(status).decode()

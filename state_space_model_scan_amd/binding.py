@@ -33,9 +33,8 @@ def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
 
 
 def _stream(device: torch.device, stream=None):
-    if stream is None:   # torch.cuda.current_stream builds a Stream object around the same handle
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
-    return ctypes.c_void_p(stream.cuda_stream)
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    return ctypes.c_void_p(s.cuda_stream)
 
 
 # Every wrapper checks each tensor against the sizes that delta (or x) and A
@@ -46,7 +45,7 @@ def _stream(device: torch.device, stream=None):
 def _spec(t: Optional[torch.Tensor], name: str, shape, dtype, dev: torch.device) -> None:
     """Raise ValueError unless t (when given) has this shape and dtype and
     lives on dev."""
-    if t is None or (t.shape == shape and t.dtype == dtype and t.device == dev):
+    if t is None:
         return
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -936,95 +935,13 @@ def ssd_scan_workspace_size(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
 
 
 # ---------------------------------------------------------------------------
-# Packed tokens: a Mamba-2 mixer's conv, scan and step.  The smallest calls
-# take the GPU a few microseconds, so the checks' passing path is kept short
-# and the argument structures are filled by position, in the C order.
+# Packed tokens: a Mamba-2 mixer's conv, scan and step.  Their smallest calls
+# take the GPU a few microseconds, so the checks and the marshalling are in
+# C++ (csrc/packed_binding.cpp); each function there returns a status first.
 # ---------------------------------------------------------------------------
 
-def _addr(t: Optional[torch.Tensor]):
-    return None if t is None else t.data_ptr()
-
-
-def _tokens(t: Optional[torch.Tensor], vec: int = 0) -> Optional[torch.Tensor]:
-    """t as the library takes a packed tensor: whatever a token holds dense,
-    any stride from token to token; with ``vec``, the first element 16-byte
-    aligned and the stride a multiple of ``vec`` elements.  A tensor that is
-    not so is copied."""
-    if t is None:
-        return None
-    shape, stride, want, ok = t.shape, t.stride(), 1, True
-    for d in range(len(shape) - 1, 0, -1):
-        if stride[d] != want and shape[d] != 1:
-            ok = False
-        want *= shape[d]
-    if shape[0] > 1:
-        ok = ok and stride[0] >= want and not (vec and stride[0] % vec)
-    if vec:
-        ok = ok and want % vec == 0 and t.data_ptr() % 16 == 0
-    return t if ok else t.clone(memory_format=torch.contiguous_format)
-
-
-def _token_stride(t: torch.Tensor) -> int:
-    """Elements from a token to the next."""
-    return t.stride(0) if t.shape[0] > 1 else t.numel()
-
-
-def _tokens_out(t: Optional[torch.Tensor], name: str, shape, dtype, dev: torch.device, vec: int = 0) -> torch.Tensor:
-    """An output given by the caller (checked) or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _spec(t, name, shape, dtype, dev)
-    if dev.type == "cuda" and _tokens(t, vec) is not t:
-        raise ValueError(f"{name} is written in place: what a token holds must be dense"
-                         + (f", its start 16-byte aligned and its token stride a multiple of {vec}" if vec else ""))
-    return t
-
-
-def _int32(t: Optional[torch.Tensor], name: str, count: int, dev: torch.device) -> Optional[torch.Tensor]:
-    if t is None:
-        return None
-    _spec(t, name, (count,), torch.int32, dev)
-    return _dense(t)
-
-
-def _cu_spec(cu: torch.Tensor, dev: torch.device) -> int:
-    """Checks cu_seqlens and returns the number of sequences."""
-    if cu.dim() != 1 or cu.shape[0] < 2:
-        raise ValueError(f"cu_seqlens must have shape (nseq + 1,) with nseq >= 1, got {tuple(cu.shape)}")
-    _spec(cu, "cu_seqlens", cu.shape, torch.int32, dev)
-    return cu.shape[0] - 1
-
-
-def _cache_spec(t: Optional[torch.Tensor], name: str, tail, dtype, dev: torch.device) -> None:
-    if t is None:
-        return
-    if t.dim() != len(tail) + 1:
-        raise ValueError(f"{name} must have shape (entries,) + {tuple(tail)}, got {tuple(t.shape)}")
-    _out_spec(t, name, (t.shape[0],) + tuple(tail), dtype, dev)
-
-
-def _workspace(size_fn, a, given: Optional[torch.Tensor], dev: torch.device) -> Optional[torch.Tensor]:
-    """The caller's scratch, or as much as the call needs; set in a."""
-    ws = given
-    if ws is None:
-        need = ctypes.c_size_t(0)
-        check(size_fn(a, need))
-        if need.value:
-            ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-    if ws is not None:
-        if given is not None:
-            _workspace_spec(ws, dev)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
-    return ws
-
-
-def _conv_varlen(x, weight, cu_seqlens, bias):
-    """The checks that the conv's two directions share: (io, nseq, and the
-    tensors as the library takes them)."""
-    io, dev = _io_of(x, "x", 2), x.device
-    weight, bias = _dense(weight), _dense(bias)
-    _conv_params_spec(weight, bias, x.shape[1], dev)
-    return io, _cu_spec(cu_seqlens, dev), _tokens(x), weight, _dense(cu_seqlens), bias
+def _handle(stream) -> Optional[int]:
+    return None if stream is None else stream.cuda_stream
 
 
 def causal_conv1d_varlen_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor,
@@ -1040,21 +957,10 @@ def causal_conv1d_varlen_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: 
     continues from entry ``slots[s]`` (s without ``slots``; an entry outside
     the cache is skipped) if ``cache_seqlens[s]`` > 0 tokens went before it,
     and leaves its last inputs there."""
-    io, nseq, x, weight, cu_seqlens, bias = _conv_varlen(x, weight, cu_seqlens, bias)
-    dev = x.device
-    total, channels = x.shape
-    cache_seqlens, slots = _int32(cache_seqlens, "cache_seqlens", nseq, dev), _int32(slots, "slots", nseq, dev)
-    entries = state_len = 0
-    if conv_state is not None:
-        _cache_spec(conv_state, "conv_state", (channels, conv_state.shape[-1]), x.dtype, dev)
-        entries, state_len = conv_state.shape[0], conv_state.shape[2]
-    act = _act_code(activation)
-    _on_gpu(dev)
-    out = _tokens_out(out, "out", x.shape, x.dtype, dev)
-    a = _lib.ConvVarlenArgs(total, nseq, channels, weight.shape[1], io, act, x.data_ptr(), _token_stride(x),
-                            weight.data_ptr(), _addr(bias), cu_seqlens.data_ptr(), out.data_ptr(), _token_stride(out),
-                            _addr(conv_state), entries, state_len, _addr(cache_seqlens), _addr(slots))
-    check(_lib.lib().causal_conv1d_varlen_fwd(a, _stream(dev, stream)))
+    status, out = _lib.packed().conv_fwd(x, weight, cu_seqlens, bias, _act_code(activation), conv_state, cache_seqlens, slots,
+                                         out, _handle(stream))
+    if status:
+        check(status)
     return out
 
 
@@ -1065,66 +971,16 @@ def causal_conv1d_varlen_bwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: 
     """Gradient of causal_conv1d_varlen_fwd for sequences that start from
     nothing: dx (x's dtype; written into ``dx`` when given), dweight and dbias
     (float32)."""
-    io, nseq, x, weight, cu_seqlens, bias = _conv_varlen(x, weight, cu_seqlens, bias)
-    dev, f32 = x.device, torch.float32
-    total, channels = x.shape
-    _spec(dout, "dout", x.shape, x.dtype, dev)
-    dout = _tokens(dout)
-    act = _act_code(activation)
-    _on_gpu(dev)
-    dx = _tokens_out(dx, "dx", x.shape, x.dtype, dev)
-    dweight = torch.empty(weight.shape, dtype=f32, device=dev)
-    dbias = None if bias is None else torch.empty(bias.shape, dtype=f32, device=dev)
-    a = _lib.ConvVarlenArgs(total, nseq, channels, weight.shape[1], io, act, x.data_ptr(), _token_stride(x),
-                            weight.data_ptr(), _addr(bias), cu_seqlens.data_ptr(), None, 0, None, 0, 0, None, None,
-                            dout.data_ptr(), _token_stride(dout), dx.data_ptr(), _token_stride(dx), dweight.data_ptr(),
-                            _addr(dbias))
-    L = _lib.lib()
-    ws = _workspace(L.causal_conv1d_varlen_bwd_workspace_size, a, workspace, dev)
-    check(L.causal_conv1d_varlen_bwd(a, _stream(dev, stream)))
+    status, dx, dweight, dbias = _lib.packed().conv_bwd(x, weight, cu_seqlens, dout, bias, _act_code(activation), dx,
+                                                        workspace, _handle(stream))
+    if status:
+        check(status)
     return {"dx": dx, "dweight": dweight, "dbias": dbias}
 
 
 def ssd_checkpoint_slots(total: int, nseq: int) -> int:
     """Checkpoint entries of ``total`` packed tokens in ``nseq`` sequences."""
     return total // _lib.SSD_CHUNK + nseq
-
-
-def _ssd_varlen(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_softplus, dt_limit, checkpoints):
-    """The checks that the scan's two directions share.  Returns the fields of
-    ssd_varlen_args_t up to ``cu_seqlens`` and the tensors to keep alive until
-    the call."""
-    if x.dtype != torch.bfloat16:
-        raise ValueError(f"the packed scan takes bfloat16 io, got {x.dtype}")
-    if x.dim() != 3 or B.dim() != 3:
-        raise ValueError("x must be (total, nheads, headdim) and B (total, ngroups, dstate)")
-    total, nheads, headdim = x.shape
-    _, ngroups, dstate = B.shape
-    dev, io, f32 = x.device, x.dtype, torch.float32
-    _spec(z, "z", x.shape, io, dev)
-    _spec(dt, "dt", (total, nheads), io, dev)
-    _spec(B, "B", (total, ngroups, dstate), io, dev)
-    _spec(C, "C", (total, ngroups, dstate), io, dev)
-    _spec(A, "A", (nheads,), f32, dev)
-    _spec(dt_bias, "dt_bias", (nheads,), f32, dev)
-    if D is not None:
-        _spec(D, "D", (nheads,) if D.dim() == 1 else (nheads, headdim), f32, dev)
-    nseq = _cu_spec(cu_seqlens, dev)
-    if not 0 <= int(max_seqlen) <= total:
-        raise ValueError(f"max_seqlen must be the longest sequence's length, at most {total}, got {max_seqlen}")
-    if checkpoints is not None:
-        rows = (ssd_checkpoint_slots(total, nseq), nheads, headdim)
-        _spec(checkpoints[0], "checkpoints[0]", rows + (dstate,), torch.int8, dev)
-        _spec(checkpoints[1], "checkpoints[1]", rows, f32, dev)
-    x, B, C, z, dt = _tokens(x, 8), _tokens(B, 8), _tokens(C, 8), _tokens(z, 8), _tokens(dt)
-    A, D, dt_bias, cu_seqlens = _dense(A), _dense(D), _dense(dt_bias), _dense(cu_seqlens)
-    lo, hi = (0.0, 0.0) if dt_limit is None else dt_limit
-    fields = (total, nseq, int(max_seqlen), nheads, headdim, dstate, ngroups, _lib.SSM_BF16, x.data_ptr(), _token_stride(x),
-              dt.data_ptr(), _token_stride(dt), A.data_ptr(), B.data_ptr(), _token_stride(B), C.data_ptr(),
-              _token_stride(C), _addr(D), int(D is not None and D.dim() == 2), _addr(z),
-              0 if z is None else _token_stride(z), _addr(dt_bias), int(bool(dt_softplus)), int(dt_limit is not None),
-              float(lo), float(hi), cu_seqlens.data_ptr())
-    return fields, (x, dt, A, B, C, D, z, dt_bias, cu_seqlens)
 
 
 def ssd_varlen_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
@@ -1148,23 +1004,12 @@ def ssd_varlen_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     headdim, dstate), float32 (entries, nheads, headdim)) with
     ``ssd_checkpoint_slots(total, nseq)`` entries receives every chunk's
     entering state in 8 bits for ``ssd_varlen_bwd``."""
-    fields, keep = _ssd_varlen(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_softplus, dt_limit, checkpoints)
-    dev, nseq = x.device, fields[1]
-    _cache_spec(ssm_state, "ssm_state", fields[3:6], torch.float32, dev)
-    cache_seqlens, slots = _int32(cache_seqlens, "cache_seqlens", nseq, dev), _int32(slots, "slots", nseq, dev)
-    codes = scales = None
-    if checkpoints is not None:
-        codes, scales = checkpoints
-        for name, t in (("checkpoints[0]", codes), ("checkpoints[1]", scales)):
-            _out_spec(t, name, t.shape, t.dtype, dev)
-    _on_gpu(dev)
-    out = _tokens_out(out, "out", x.shape, x.dtype, dev, 8)
-    a = _lib.SsdVarlenArgs(*fields, out.data_ptr(), _token_stride(out), _addr(ssm_state),
-                           0 if ssm_state is None else ssm_state.shape[0], _addr(cache_seqlens), _addr(slots),
-                           _addr(codes), _addr(scales), None, 0, int(seq_segments))
-    L = _lib.lib()
-    ws = _workspace(L.ssd_varlen_fwd_workspace_size, a, workspace, dev)
-    check(L.ssd_varlen_fwd(a, _stream(dev, stream)))
+    codes, scales = (None, None) if checkpoints is None else checkpoints
+    status, out = _lib.packed().scan_fwd(x, dt, A, B, C, cu_seqlens, max_seqlen, D, z, dt_bias, dt_softplus, dt_limit,
+                                         ssm_state, cache_seqlens, slots, codes, scales, out, workspace, seq_segments,
+                                         _handle(stream))
+    if status:
+        check(status)
     return out
 
 
@@ -1188,43 +1033,13 @@ def ssd_varlen_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     first ones is returned."""
     if checkpoints is None:
         raise ValueError("the backward needs the checkpoints that the forward wrote")
-    fields, keep = _ssd_varlen(x, dt, A, B, C, cu_seqlens, max_seqlen, D, None, dt_bias, dt_softplus, dt_limit,
-                               checkpoints)
-    dev, f32, io = x.device, torch.float32, x.dtype
-    nseq, nheads, headdim, dstate = fields[1], fields[3], fields[4], fields[5]
-    # any strides from entry to entry and head to head; a channel's states dense
-    codes, scales = checkpoints
-    c0, c1, c2, c3 = codes.stride()
-    if c3 != 1 or c2 != dstate or c0 % 16 or c1 % 16 or min(c0, c1) < headdim * dstate or codes.data_ptr() % 16:
-        codes = codes.clone(memory_format=torch.contiguous_format)
-    if scales.stride(2) != 1 or min(scales.stride(0), scales.stride(1)) < headdim:
-        scales = scales.clone(memory_format=torch.contiguous_format)
-    states = (nseq, nheads, headdim, dstate)
-    _spec(dout, "dout", x.shape, io, dev)
-    _spec(dfinal_states, "dfinal_states", states, f32, dev)
-    dout, dfinal_states = _tokens(dout, 8), _dense(dfinal_states)
-    _on_gpu(dev)
-    g = {"dx": _tokens_out(dx, "dx", x.shape, io, dev, 8), "ddt": _tokens_out(ddt, "ddt", dt.shape, io, dev),
-         "dB": _tokens_out(dB, "dB", B.shape, io, dev, 8), "dC": _tokens_out(dC, "dC", C.shape, io, dev, 8),
-         "dA": torch.empty(A.shape, dtype=f32, device=dev)}
-    if D is not None:
-        g["dD"] = torch.empty(D.shape, dtype=f32, device=dev)
-    if dt_bias is not None:
-        g["ddt_bias"] = torch.empty(dt_bias.shape, dtype=f32, device=dev)
-    if want_dinitial_states:
-        g["dinitial_states"] = torch.empty(states, dtype=f32, device=dev)
-    fwd = _lib.SsdVarlenArgs(*fields, None, 0, None, 0, None, None, codes.data_ptr(), scales.data_ptr(), None, 0,
-                             int(seq_segments))
-    out = []
-    for k in ("dx", "ddt", "dB", "dC"):
-        out += (g[k].data_ptr(), _token_stride(g[k]))
-    a = _lib.SsdVarlenBwdArgs(fwd, codes.stride(0), codes.stride(1), scales.stride(0), scales.stride(1), dout.data_ptr(),
-                              _token_stride(dout), _addr(dfinal_states), *out, g["dA"].data_ptr(), _addr(g.get("dD")),
-                              _addr(g.get("ddt_bias")), _addr(g.get("dinitial_states")))
-    L = _lib.lib()
-    ws = _workspace(L.ssd_varlen_bwd_workspace_size, a, workspace, dev)
-    check(L.ssd_varlen_bwd(a, _stream(dev, stream)))
-    return g
+    status, *grads = _lib.packed().scan_bwd(x, dt, A, B, C, cu_seqlens, max_seqlen, dout, checkpoints[0], checkpoints[1], D,
+                                            dt_bias, dt_softplus, dt_limit, dfinal_states, want_dinitial_states, dx, dB, dC,
+                                            ddt, workspace, seq_segments, _handle(stream))
+    if status:
+        check(status)
+    names = ("dx", "ddt", "dB", "dC", "dA", "dD", "ddt_bias", "dinitial_states")
+    return {k: v for k, v in zip(names, grads) if v is not None}
 
 
 def conv1d_ssd_update(xBC: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, conv_weight: torch.Tensor,
@@ -1245,41 +1060,8 @@ def conv1d_ssd_update(xBC: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, conv
     ssd_varlen_fwd fill; request b uses entry ``slots[b]`` and has seen
     ``cache_seqlens[b]`` tokens (None: every request is new).  A row whose entry is outside the cache
     is padding."""
-    io = _io_of(xBC, "xBC", 2)
-    if ssm_state.dim() != 4:
-        raise ValueError(f"ssm_state must be (entries, nheads, headdim, dstate), got shape {tuple(ssm_state.shape)}")
-    entries, nheads, headdim, dstate = ssm_state.shape
-    batch, channels = xBC.shape
-    dev, f32, dtype, hp = xBC.device, torch.float32, xBC.dtype, nheads * headdim
-    ngroups = (channels - hp) // (2 * dstate)
-    if channels <= hp or (channels - hp) % (2 * dstate) != 0:
-        raise ValueError(f"xBC must have nheads * headdim + 2 * ngroups * dstate columns, got {channels} "
-                         f"for {nheads} heads of {headdim} and dstate {dstate}")
-    _out_spec(ssm_state, "ssm_state", ssm_state.shape, f32, dev)
-    if conv_state.dim() != 3:
-        raise ValueError(f"conv_state must be (entries, channels, state_len), got shape {tuple(conv_state.shape)}")
-    _out_spec(conv_state, "conv_state", (entries, channels, conv_state.shape[2]), dtype, dev)
-    conv_weight, conv_bias, A, D, dt_bias = _dense(conv_weight), _dense(conv_bias), _dense(A), _dense(D), _dense(dt_bias)
-    _conv_params_spec(conv_weight, conv_bias, channels, dev)
-    _spec(dt, "dt", (batch, nheads), dtype, dev)
-    _spec(z, "z", (batch, hp), dtype, dev)
-    _spec(A, "A", (nheads,), f32, dev)
-    _spec(dt_bias, "dt_bias", (nheads,), f32, dev)
-    per_channel = 0
-    if D is not None:
-        per_channel = int(D.dim() == 2)
-        _spec(D, "D", (nheads, headdim) if per_channel else (nheads,), f32, dev)
-    cache_seqlens, slots = _int32(cache_seqlens, "cache_seqlens", batch, dev), _int32(slots, "slots", batch, dev)
-    act = _act_code(activation)
-    _on_gpu(dev)
-    out = _tokens_out(out, "out", (batch, hp), dtype, dev)
-    xBC, dt, z = _tokens(xBC), _tokens(dt), _tokens(z)
-    lo, hi = (0.0, 0.0) if dt_limit is None else dt_limit
-    a = _lib.ConvSsdUpdateArgs(
-        batch, nheads, headdim, dstate, ngroups, io, act, conv_weight.shape[1], xBC.data_ptr(), _token_stride(xBC),
-        dt.data_ptr(), _token_stride(dt), A.data_ptr(), conv_weight.data_ptr(), _addr(conv_bias), _addr(D), per_channel,
-        _addr(z), 0 if z is None else _token_stride(z), _addr(dt_bias), int(bool(dt_softplus)),
-        int(dt_limit is not None), float(lo), float(hi), conv_state.data_ptr(), conv_state.shape[2],
-        ssm_state.data_ptr(), entries, _addr(cache_seqlens), _addr(slots), out.data_ptr(), _token_stride(out))
-    check(_lib.lib().conv1d_ssd_update(a, _stream(dev, stream)))
+    status, out = _lib.packed().step(xBC, dt, A, conv_weight, conv_state, ssm_state, cache_seqlens, conv_bias, D, z, dt_bias,
+                                     dt_softplus, dt_limit, slots, _act_code(activation), out, _handle(stream))
+    if status:
+        check(status)
     return out
