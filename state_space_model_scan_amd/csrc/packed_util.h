@@ -1,0 +1,157 @@
+// packed_util.h -- what the packed-token scan's forward and backward share
+// (gfx950): sequences, steps, LDS tiles and their operand fragments, lane sums.
+#pragma once
+
+#include "ssd_util.h"
+
+namespace ssm {
+
+struct Seq {
+  int64_t first, len, chunks, entry;   // entry: its first checkpoint
+};
+// A sequence's tokens, kept inside the tensors whatever cu holds.
+__device__ __forceinline__ Seq sequence(const int32_t *cu, int64_t total, int64_t max_seqlen, int64_t s) {
+  int64_t lo = cu[s], hi = cu[s + 1];
+  lo = lo < 0 ? 0 : lo > total ? total : lo;
+  hi = hi < lo ? lo : hi > total ? total : hi;
+  const int64_t len = hi - lo > max_seqlen ? max_seqlen : hi - lo;
+  return {lo, len, (len + kQ - 1) / kQ, lo / kQ + s};
+}
+
+// How a step comes from dt.
+struct StepRule {
+  int softplus, limit;
+  float lo, hi;
+};
+// The value before softplus of a token's step, and the step (0 beyond the
+// chunk's end).
+__device__ __forceinline__ float chunk_step(const StepRule &s, float raw, float bias, bool live, float &v) {
+  v = raw + bias;
+  float d = s.softplus ? softplus_acc(v) : v;
+  if (s.limit) d = fminf(fmaxf(d, s.lo), s.hi);
+  return live ? d : 0.0f;
+}
+
+// Running sum over the wave's lanes of d A, as an unevaluated sum of two
+// floats: decays are exponentials of its differences, whose error would
+// otherwise be the rounding of a sum that reaches 100 and more.
+struct TwoSum {
+  float hi, lo;
+};
+// lane n's value from the lane that CTRL names, 0 where there is none
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ float from_lane(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROW_MASK, 0xf, false));
+}
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ void add_lane(TwoSum &s) {
+  const float oh = from_lane<CTRL, ROW_MASK>(s.hi), ol = from_lane<CTRL, ROW_MASK>(s.lo);
+  const float t = s.hi + oh, b = t - s.hi;
+  s.lo += ol + ((s.hi - (t - b)) + (oh - b));
+  s.hi = t;
+}
+__device__ __forceinline__ TwoSum running_sum(float d, float A) {
+  TwoSum s;
+  s.hi = d * A;
+  s.lo = fmaf(d, A, -s.hi);
+  add_lane<0x111, 0xf>(s);   // the lanes 1, 2, 4 and 8 before, inside a row of 16
+  add_lane<0x112, 0xf>(s);
+  add_lane<0x114, 0xf>(s);
+  add_lane<0x118, 0xf>(s);
+  add_lane<0x142, 0xa>(s);   // row 0's sum to row 1, row 2's to row 3
+  add_lane<0x143, 0xc>(s);   // the first half's to the second
+  return s;
+}
+// exp(a - b)
+__device__ __forceinline__ float exp_diff(float ah, float al, float bh, float bl) {
+  return fast_exp2(((ah - bh) + (al - bl)) * kLog2e);
+}
+
+// A state row in 8 bits: v ~ code * 2^e with the smallest e for which every
+// |v| <= 127 * 2^e.  The scale is a power of two so that a code's value is
+// exact in bf16 (seven bits times a power of two) and can enter a matrix
+// product as it is.  Against the scale amax / 127 it costs half a bit on
+// average.  e >= -100 keeps the values normal numbers.  A row with an
+// infinity or a NaN gets a NaN scale.
+__device__ __forceinline__ float row_scale(uint32_t amax_bits, float &inv) {
+  if (amax_bits >= 0x7f800000u) {
+    inv = 0.0f;
+    return __uint_as_float(0x7fc00000u);
+  }
+  // 127 = 1.984375 * 2^6, and 1.984375 has the fraction bits 0x7e0000
+  int e = static_cast<int>(amax_bits >> 23) - 127 - 6 + ((amax_bits & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  e = e < -100 ? -100 : e;
+  inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
+// Element offset of (row, col) in a row-major tile of ROW_LEN bf16.  A row's
+// 16-byte groups are permuted by g = the row's last three bits rotated, so
+// that eight consecutive rows at one column (an operand read row by row) have
+// eight values of g, and four consecutive rows (a transposing read: 32 bytes
+// of each) four values of g / 2: neither meets in a bank.
+template <int ROW_LEN>
+__device__ __forceinline__ int tile_at(int row, int col) {
+  constexpr int GROUPS = ROW_LEN / 8;
+  const int g = (((row & 3) << 1) | ((row >> 2) & 1)) & (GROUPS - 1);
+  return row * ROW_LEN + (col & ~63) + ((col & 63) ^ (g << 3));
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+// The operand fragment that a row-major tile holds column by column: lane
+// (r, kq) receives tile[row0 + 8 kq + i][col0 + r], i < 8.
+template <int ROW_LEN>
+__device__ __forceinline__ bf16x8 frag_t(int l, uint16_t *tile, int row0, int col0) {
+  typedef __attribute__((address_space(3))) s16x4 *lds;
+  const int i = l & 15, kq = l >> 4;
+  const int row = row0 + 8 * kq + (i >> 2), col = col0 + 4 * (i & 3);
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<ROW_LEN>(row, col)));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<ROW_LEN>(row + 4, col)));
+  const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
+  return __builtin_bit_cast(bf16x8, make_uint4(ua.x, ua.y, ub.x, ub.y));
+}
+// ... of four rows only: lane (r, kq) receives tile[row0 + 4 kq + i][col0 + r], i < 4.
+template <int ROW_LEN>
+__device__ __forceinline__ s16x4 frag_t4(int l, uint16_t *tile, int row0, int col0) {
+  typedef __attribute__((address_space(3))) s16x4 *lds;
+  const int i = l & 15, kq = l >> 4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<ROW_LEN>(row0 + 4 * kq + (i >> 2), col0 + 4 * (i & 3))));
+}
+// ... and row by row: lane (r, kq) receives tile[row0 + r][col0 + 8 kq + i].
+template <int ROW_LEN>
+__device__ __forceinline__ bf16x8 frag(int l, const uint16_t *tile, int row0, int col0) {
+  return ld8(tile + tile_at<ROW_LEN>(row0 + (l & 15), col0 + 8 * (l >> 4)));
+}
+
+// sum over the four kq lanes of a column r: neighbouring rows of 16 lanes swap,
+// then the halves
+__device__ __forceinline__ float sum_kq(float v) {
+  const uint32_t a = __float_as_uint(v);
+  const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const uint32_t b = __float_as_uint(__uint_as_float(x[0]) + __uint_as_float(x[1]));
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(y[0]) + __uint_as_float(y[1]);
+}
+// sum over the sixteen r lanes of a row kq: rotations of the row
+template <int N>
+__device__ __forceinline__ float row_rotate(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum_r(float v) {
+  v += row_rotate<8>(v);
+  v += row_rotate<4>(v);
+  v += row_rotate<2>(v);
+  return v + row_rotate<1>(v);
+}
+__device__ __forceinline__ float sum_wave(float v) { return sum_kq(sum_r(v)); }
+
+// four bf16 of one 8-byte piece
+__device__ __forceinline__ void four(const uint16_t *p, float (&v)[4]) {
+  const uint2 w = *reinterpret_cast<const uint2 *>(p);
+  v[0] = __uint_as_float(w.x << 16);
+  v[1] = __uint_as_float(w.x & 0xffff0000u);
+  v[2] = __uint_as_float(w.y << 16);
+  v[3] = __uint_as_float(w.y & 0xffff0000u);
+}
+
+}  // namespace ssm

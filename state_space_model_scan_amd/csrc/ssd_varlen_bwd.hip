@@ -43,7 +43,7 @@
 #include <cstdint>
 
 #include "host_util.h"
-#include "ssd_util.h"
+#include "packed_util.h"
 #include "ssmscan.h"
 
 namespace ssm {
@@ -67,95 +67,9 @@ struct BwdParams {
   int64_t xs, dts, bs, cs, gs, dxs, ddts, dbs, dcs;
   int64_t code_entry, code_head, scale_entry, scale_head;
   int64_t total, nseq, max_seqlen, nheads, ngroups, seg_chunks, entries;
-  int nseg, softplus, dt_limit, D_per_channel, hb_heads, hb_per_group;
-  float dt_min, dt_max;
+  int nseg, D_per_channel, hb_heads, hb_per_group;
+  StepRule step;
 };
-
-struct Seq {
-  int64_t first, len, chunks, entry;   // entry: its first checkpoint
-};
-
-// A sequence's tokens, kept inside the tensors whatever cu holds.
-__device__ __forceinline__ Seq sequence(const BwdParams &p, int64_t s) {
-  int64_t lo = p.cu[s], hi = p.cu[s + 1];
-  lo = lo < 0 ? 0 : lo > p.total ? p.total : lo;
-  hi = hi < lo ? lo : hi > p.total ? p.total : hi;
-  const int64_t len = hi - lo > p.max_seqlen ? p.max_seqlen : hi - lo;
-  return {lo, len, (len + kQ - 1) / kQ, lo / kQ + s};
-}
-
-// The value before softplus of token l's step, and the step (0 beyond the
-// chunk's end).
-__device__ __forceinline__ float chunk_step(const BwdParams &p, float raw, float bias, bool live, float &v) {
-  v = raw + bias;
-  float d = p.softplus ? softplus_acc(v) : v;
-  if (p.dt_limit) d = fminf(fmaxf(d, p.dt_min), p.dt_max);
-  return live ? d : 0.0f;
-}
-
-// Running sum over the wave's lanes of d A, as an unevaluated sum of two
-// floats: decays are exponentials of its differences, whose error would
-// otherwise be the rounding of a sum that reaches 100 and more.
-struct TwoSum {
-  float hi, lo;
-};
-__device__ __forceinline__ TwoSum running_sum(float d, float A, int l) {
-  TwoSum s;
-  s.hi = d * A;
-  s.lo = fmaf(d, A, -s.hi);
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const float oh = __shfl_up(s.hi, off), ol = __shfl_up(s.lo, off);
-    if (l >= off) {
-      const float t = s.hi + oh, b = t - s.hi;
-      s.lo += ol + ((s.hi - (t - b)) + (oh - b));
-      s.hi = t;
-    }
-  }
-  return s;
-}
-// exp(a - b)
-__device__ __forceinline__ float exp_diff(float ah, float al, float bh, float bl) {
-  return fast_exp2(((ah - bh) + (al - bl)) * kLog2e);
-}
-
-// Element offset of (row, col) in a row-major tile of ROW_LEN bf16.  A row's
-// 16-byte groups are permuted by g = the row's last three bits rotated, so
-// that eight consecutive rows at one column (an operand read row by row) have
-// eight values of g, and four consecutive rows (a transposing read: 32 bytes
-// of each) four values of g / 2: neither meets in a bank.
-template <int ROW_LEN>
-__device__ __forceinline__ int tile_at(int row, int col) {
-  constexpr int GROUPS = ROW_LEN / 8;
-  const int g = (((row & 3) << 1) | ((row >> 2) & 1)) & (GROUPS - 1);
-  return row * ROW_LEN + (col & ~63) + ((col & 63) ^ (g << 3));
-}
-
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-// The operand fragment that a row-major tile holds column by column: lane
-// (r, kq) receives tile[row0 + 8 kq + i][col0 + r], i < 8.
-template <int ROW_LEN>
-__device__ __forceinline__ bf16x8 frag_t(int l, uint16_t *tile, int row0, int col0) {
-  typedef __attribute__((address_space(3))) s16x4 *lds;
-  const int i = l & 15, kq = l >> 4;
-  const int row = row0 + 8 * kq + (i >> 2), col = col0 + 4 * (i & 3);
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<ROW_LEN>(row, col)));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<ROW_LEN>(row + 4, col)));
-  const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
-  return __builtin_bit_cast(bf16x8, make_uint4(ua.x, ua.y, ub.x, ub.y));
-}
-// ... of four rows only: lane (r, kq) receives tile[row0 + 4 kq + i][col0 + r], i < 4.
-template <int ROW_LEN>
-__device__ __forceinline__ s16x4 frag_t4(int l, uint16_t *tile, int row0, int col0) {
-  typedef __attribute__((address_space(3))) s16x4 *lds;
-  const int i = l & 15, kq = l >> 4;
-  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<ROW_LEN>(row0 + 4 * kq + (i >> 2), col0 + 4 * (i & 3))));
-}
-// ... and row by row: lane (r, kq) receives tile[row0 + r][col0 + 8 kq + i].
-template <int ROW_LEN>
-__device__ __forceinline__ bf16x8 frag(int l, const uint16_t *tile, int row0, int col0) {
-  return ld8(tile + tile_at<ROW_LEN>(row0 + (l & 15), col0 + 8 * (l >> 4)));
-}
 
 // ---------------------------------------------------------------------------
 // (1) the adjoint of the states.  One workgroup of four waves per (sequence,
@@ -173,7 +87,7 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
   const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r = l & 15, kq = l >> 4;
   const int64_t sh = blockIdx.x, SH = gridDim.x;
   const int64_t s = sh / p.nheads, h = sh - s * p.nheads, gr = h / (p.nheads / p.ngroups);
-  const Seq q = sequence(p, s);
+  const Seq q = sequence(p.cu, p.total, p.max_seqlen, s);
   const int64_t nsegs = q.chunks ? (q.chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
   // the first launch runs the segments that have one before them
   const int64_t seg = STORE ? blockIdx.y : blockIdx.y + 1;
@@ -253,8 +167,8 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
     }
     if (w == 0) {
       float v;
-      const float d = chunk_step(p, raw, bias, l < len, v);
-      const TwoSum cs = running_sum(d, Ah, l);
+      const float d = chunk_step(p.step, raw, bias, l < len, v);
+      const TwoSum cs = running_sum(d, Ah);
       const float e = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
       sE[l] = e;
       if (l == 63) sEnd = e;
@@ -299,37 +213,6 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
 // ---------------------------------------------------------------------------
 // (2) one chunk and hb_heads heads of a group: eight waves.
 // ---------------------------------------------------------------------------
-
-// sum over the four kq lanes of a column r: neighbouring rows of 16 lanes swap,
-// then the halves
-__device__ __forceinline__ float sum_kq(float v) {
-  const uint32_t a = __float_as_uint(v);
-  const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-  const uint32_t b = __float_as_uint(__uint_as_float(x[0]) + __uint_as_float(x[1]));
-  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-  return __uint_as_float(y[0]) + __uint_as_float(y[1]);
-}
-// sum over the sixteen r lanes of a row kq: rotations of the row
-template <int N>
-__device__ __forceinline__ float row_rotate(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xf, 0xf, false));
-}
-__device__ __forceinline__ float sum_r(float v) {
-  v += row_rotate<8>(v);
-  v += row_rotate<4>(v);
-  v += row_rotate<2>(v);
-  return v + row_rotate<1>(v);
-}
-__device__ __forceinline__ float sum_wave(float v) { return sum_kq(sum_r(v)); }
-
-// four bf16 of one 8-byte piece
-__device__ __forceinline__ void four(const uint16_t *p, float (&v)[4]) {
-  const uint2 w = *reinterpret_cast<const uint2 *>(p);
-  v[0] = __uint_as_float(w.x << 16);
-  v[1] = __uint_as_float(w.x & 0xffff0000u);
-  v[2] = __uint_as_float(w.y << 16);
-  v[3] = __uint_as_float(w.y & 0xffff0000u);
-}
 
 template <int N>
 struct ChunkLds {
@@ -387,7 +270,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     if (e <= entry) lo = mid;
     else hi = mid;
   }
-  const Seq q = sequence(p, lo);
+  const Seq q = sequence(p.cu, p.total, p.max_seqlen, lo);
   const int64_t chunk = entry - q.entry;
   const int64_t hpg = p.nheads / p.ngroups;
   const int64_t gr = blockIdx.y / p.hb_per_group, hb = blockIdx.y - gr * p.hb_per_group;
@@ -446,8 +329,8 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     const int64_t h = h0 + k;
     const float raw = l < len ? bf2f(p.dt[(t0 + l) * p.dts + h]) : 0.0f;
     float v;
-    const float d = chunk_step(p, raw, p.dt_bias ? p.dt_bias[h] : 0.0f, l < len, v);
-    const TwoSum cs = running_sum(d, p.A[h], l);
+    const float d = chunk_step(p.step, raw, p.dt_bias ? p.dt_bias[h] : 0.0f, l < len, v);
+    const TwoSum cs = running_sum(d, p.A[h]);
     sm.ch[k][l] = cs.hi;
     sm.cl[k][l] = cs.lo;
     sm.dt[k][l] = d;
@@ -710,12 +593,12 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       if (l + off < 64) dcs += o;
     }
     float v, dd = fmaf(Ah, dcs, direct);
-    chunk_step(p, raw, p.dt_bias ? p.dt_bias[h] : 0.0f, true, v);
-    if (p.dt_limit) {
-      const float sp = p.softplus ? softplus_acc(v) : v;
-      if (!(sp >= p.dt_min && sp <= p.dt_max)) dd = 0.0f;
+    chunk_step(p.step, raw, p.dt_bias ? p.dt_bias[h] : 0.0f, true, v);
+    if (p.step.limit) {
+      const float sp = p.step.softplus ? softplus_acc(v) : v;
+      if (!(sp >= p.step.lo && sp <= p.step.hi)) dd = 0.0f;
     }
-    if (p.softplus) dd *= fast_rcp(1.0f + fast_exp2(-v * kLog2e));
+    if (p.step.softplus) dd *= fast_rcp(1.0f + fast_exp2(-v * kLog2e));
     if (l >= len) dd = 0.0f;
     else p.ddt[(t0 + l) * p.ddts + h] = static_cast<uint16_t>(float_to_half_bits<1>(dd));
     const float dA = sum_wave(d * dcs), db = sum_wave(dd);
@@ -960,8 +843,8 @@ extern "C" int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *a, void *stream_ptr) 
   p.scale_entry = a->scale_entry_stride; p.scale_head = a->scale_head_stride;
   p.seg_chunks = pl.seg_chunks; p.nseg = pl.nseg; p.entries = pl.entries;
   p.hb_heads = pl.hb_heads; p.hb_per_group = pl.hb_per_group;
-  p.softplus = f.dt_softplus; p.D_per_channel = f.D_per_channel;
-  p.dt_limit = f.dt_limit; p.dt_min = f.dt_min; p.dt_max = f.dt_max;
+  p.step = {f.dt_softplus, f.dt_limit, f.dt_min, f.dt_max};
+  p.D_per_channel = f.D_per_channel;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   hipError_t e = f.dstate == 32 ? launch_bwd<32>(p, pl, stream)
                  : f.dstate == 64 ? launch_bwd<64>(p, pl, stream) : launch_bwd<128>(p, pl, stream);
