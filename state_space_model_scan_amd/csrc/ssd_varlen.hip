@@ -15,14 +15,18 @@
 //
 // What bounds it is the chain of a chunk's dependent steps, not HBM: the chunks
 // of a (sequence, head) follow each other.  So:
-// - a workgroup of eight waves runs two heads of a group, which share B and C;
-// - the next chunk's x, B and C go from global memory straight into the other
-//   half of a double buffer in LDS while this chunk is computed (no registers,
-//   and the latency, about a third of a chunk's time before, is hidden), and
-//   its steps are summed at this chunk's end;
+// - a workgroup of four waves walks a head's chunks, and 79 KB of LDS let two
+//   run on a compute unit, each in its own phase (one workgroup of eight
+//   waves for two heads, which shares B and C, took 707 us where this takes
+//   650: 32768 tokens, 80 heads);
+// - the next chunk's x and B go from global memory straight into the other
+//   half of a double buffer in LDS while this chunk is computed, its C as soon
+//   as this chunk's outputs are done (no registers, and the latency, about a
+//   third of a chunk's time before, is hidden), and its steps are summed at
+//   this chunk's end;
 // - tiles stay as they lie in memory, token by token, and are read across by
 //   the transposing LDS load, so nothing is rearranged on the way;
-// - two barriers a chunk: data there, M there.
+// - three barriers a chunk: data there, M there, C done with.
 // With few (sequence, head) pairs the sequence is cut into segments; a first
 // launch finds their end states from zero (packed_scan_kernel<N, false>), and
 // the second starts every segment from the states carried over.
@@ -37,8 +41,6 @@
 namespace ssm {
 namespace {
 
-constexpr int kPair = 2;   // heads of a workgroup
-
 struct ScanParams {
   const uint16_t *x, *dt, *B, *C, *z;
   const float *A, *D, *dt_bias;
@@ -49,37 +51,55 @@ struct ScanParams {
   int8_t *codes;
   float *scales;
   int64_t xs, dts, bs, cs, zs, os;
-  int64_t total, max_seqlen, cache_slots, nheads, ngroups, pairs, seg_chunks;
+  int64_t total, max_seqlen, cache_slots, nheads, ngroups, seg_chunks;
   int D_per_channel, nseg;
   StepRule step;
 };
 
+// M keeps its ten 16 x 16 tiles on and below the diagonal, and a zero one for
+// the half of an operand that reaches above it.
+constexpr int kTile = 256, kZeroTile = 10;
+// tile of the (token block, tau block), element of (token, tau) inside a tile
+__device__ __forceinline__ constexpr int m_tile(int tb, int ub) { return ub <= tb ? tb * (tb + 1) / 2 + ub : kZeroTile; }
+__device__ __forceinline__ int m_at(int t, int tau) { return t * 16 + (tau ^ (((t >> 2) & 1) << 3)); }
+
 template <int N, bool FULL>
 struct ScanLds {
-  uint16_t B[2][kQ * N];                       // [t][n]
-  uint16_t x[2][kPair][kQ * kP];               // [t][p]
-  uint16_t C[FULL ? 2 : 1][FULL ? kQ * N : 8];       // [t][n]
-  uint16_t M[FULL ? kPair : 1][2][FULL ? kQ * kQ : 8];   // [t][tau] head, tail
-  // running sum, step, exp(cs), and the state update's weight, per token
-  float cs[2][kPair][kQ], dt[2][kPair][kQ], e[2][kPair][kQ], w[2][kPair][kQ];
+  uint16_t B[2][kQ * N];                              // [t][n]
+  uint16_t x[2][kQ * kP];                             // [t][p]
+  uint16_t C[FULL ? kQ * N : 8];                      // [t][n]
+  uint16_t M[2][FULL ? (kZeroTile + 1) * kTile : 8];    // head, tail
+  // running sum (times log2 e), step, exp(cs), and the state update's weight, per token
+  float cs[2][kQ], dt[2][kQ], e[2][kQ], w[2][kQ];
 };
 
-// 16-byte pieces of a row-major tile of `rows` tokens straight into LDS, the
-// pieces of wave w.  A wave writes one KiB in order, so the tile's permutation
-// (tile_at, its own inverse) is applied to where each lane reads.  Tokens at
-// and after `len` repeat the last one: their steps are 0, and what they give
+// A row-major tile's 16-byte pieces straight into LDS.  A wave writes one KiB
+// in order, so the tile's permutation (tile_at, its own inverse) is applied to
+// where each lane reads: `at` holds a lane's byte offsets from the tile's
+// first token, which only a sequence's last chunk changes.  Tokens at and
+// after `len` repeat the last one: their steps are 0, and what they give
 // reaches no output.
 template <int ROW_LEN>
-__device__ __forceinline__ void tile_to_lds(uint16_t *tile, const uint16_t *from, int64_t stride, int len, int w, int nw,
-                                            int lane) {
-  constexpr int G = ROW_LEN / 8;
-  for (int i = w; i < kQ * G / 64; i += nw) {
-    const int piece = i * 64 + lane, row = piece / G, t = row < len ? row : len - 1;
-    const uint16_t *src = from + t * stride + (tile_at<ROW_LEN>(row, (piece % G) * 8) - row * ROW_LEN);
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
-                                     (__attribute__((address_space(3))) void *)(tile + i * 512), 16, 0, 0);
+struct TileLoad {
+  static constexpr int G = ROW_LEN / 8, ALL = kQ * G / 64, PER = (ALL + 3) / 4;
+  uint32_t at[PER];
+  __device__ __forceinline__ void place(int64_t stride, int len, int w, int lane) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int piece = (w + 4 * i) * 64 + lane, row = piece / G, t = row < len ? row : len - 1;
+      at[i] = 2u * (static_cast<uint32_t>(t) * static_cast<uint32_t>(stride) +
+                    static_cast<uint32_t>(tile_at<ROW_LEN>(row, (piece % G) * 8) - row * ROW_LEN));
+    }
   }
-}
+  __device__ __forceinline__ void fetch(uint16_t *tile, const uint16_t *from, int w) const {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (w + 4 * i < ALL)
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void *)(reinterpret_cast<const char *>(from) + at[i]),
+            (__attribute__((address_space(3))) void *)(tile + (w + 4 * i) * 512), 16, 0, 0);
+  }
+};
 
 // A barrier for LDS alone: what is on its way from global memory stays so.
 __device__ __forceinline__ void lds_barrier() {
@@ -88,22 +108,30 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// The transposed operand of B for state tile a of the k step kk: lane m's row
+// is the state n = 32kk + 8 (m / 4) + 4a + m % 4, so that a lane's accumulators
+// of tiles a = 0 and 1 are eight neighbouring states, 32kk + 8kq + 0..7.
+template <int N>
+__device__ __forceinline__ bf16x8 frag_states(int l, uint16_t *tile, int row0, int kk, int a) {
+  typedef __attribute__((address_space(3))) s16x4 *lds;
+  const int i = l & 15, kq = l >> 4;
+  const int row = row0 + 8 * kq + (i >> 2), col = 32 * kk + 8 * (i & 3) + 4 * a;
+  const s16x4 u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<N>(row, col)));
+  const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(tile + tile_at<N>(row + 4, col)));
+  const uint2 uu = __builtin_bit_cast(uint2, u), uv = __builtin_bit_cast(uint2, v);
+  return __builtin_bit_cast(bf16x8, make_uint4(uu.x, uu.y, uv.x, uv.y));
+}
+
 template <int N, bool FULL>
-__global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const ScanParams p) {
+__global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const ScanParams p) {
   constexpr int KN = N / 32;   // K steps over dstate
   constexpr int NT = N / 16;   // state tiles along dstate
   extern __shared__ __attribute__((aligned(16))) char smem[];
   ScanLds<N, FULL> &sm = *reinterpret_cast<ScanLds<N, FULL> *>(smem);
   const int tid = threadIdx.x, l = tid & 63, r = l & 15, kq = l >> 4;
-  const int w8 = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int hw = w8 >> 2, w = w8 & 3;   // which head of the pair; its channels 16w..16w+15
-  // the pair: heads h0 and h0 + 1 of group g
-  const int64_t s = blockIdx.x / p.pairs, pr = blockIdx.x - s * p.pairs;
-  const int64_t hpg = p.nheads / p.ngroups, per = (hpg + kPair - 1) / kPair;
-  const int64_t g = pr / per, in_group = (pr - g * per) * kPair + hw;
-  const bool alive = in_group < hpg;   // an odd group's last pair: the second head runs along and writes nothing
-  const int64_t h = g * hpg + (alive ? in_group : in_group - 1);
-  const int64_t SH = static_cast<int64_t>(gridDim.x) / p.pairs * p.nheads, sh = s * p.nheads + h;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);   // channels 16w..16w+15
+  const int64_t sh = blockIdx.x, SH = gridDim.x;
+  const int64_t s = sh / p.nheads, h = sh - s * p.nheads, g = h / (p.nheads / p.ngroups);
   const Seq q = sequence(p.cu, p.total, p.max_seqlen, s);
   // the full pass dispatches its last segments first: those of the longest sequences
   const int64_t seg = FULL ? static_cast<int64_t>(gridDim.y) - 1 - blockIdx.y : blockIdx.y;
@@ -123,17 +151,28 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
   uint16_t *ob = p.out + q.first * p.os + h * kP;
   const float Ah = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
   float *state_ws = p.ws_state + sh * kP * N;   // segment k's at k * SH * kP * N
-  const int srow = (16 * w + r) * N + 4 * kq;   // this lane's first state element in a (p, n) block
+  const int srow = (16 * w + r) * N + (FULL ? 8 : 4) * kq;   // this lane's first state element in a (p, n) block
 
   auto chunk_len = [&](int64_t c) { return static_cast<int>(q.len - c * kQ < kQ ? q.len - c * kQ : kQ); };
+  TileLoad<kP> lx;
+  TileLoad<N> lb, lc;
+  lx.place(p.xs, chunk_len(c_begin), w, l);
+  lb.place(p.bs, chunk_len(c_begin), w, l);
+  if constexpr (FULL) lc.place(p.cs, chunk_len(c_begin), w, l);
   auto fetch = [&](int64_t c, int b) {
-    const int64_t t0 = c * kQ;
     const int len = chunk_len(c);
-    tile_to_lds<kP>(sm.x[b][hw], xb + t0 * p.xs, p.xs, len, w, 4, l);
-    tile_to_lds<N>(sm.B[b], Bb + t0 * p.bs, p.bs, len, w8, 8, l);
-    if constexpr (FULL) tile_to_lds<N>(sm.C[b], Cb + t0 * p.cs, p.cs, len, w8, 8, l);
+    if (len < kQ && c > c_begin) {   // the sequence's end
+      lx.place(p.xs, len, w, l);
+      lb.place(p.bs, len, w, l);
+      if constexpr (FULL) lc.place(p.cs, len, w, l);
+    }
+    lx.fetch(sm.x[b], xb + c * kQ * p.xs, w);
+    lb.fetch(sm.B[b], Bb + c * kQ * p.bs, w);
   };
-  // a chunk's raw steps, and what the chunk needs of them (wave 0 of each head)
+  auto fetch_C = [&](int64_t c) {
+    if constexpr (FULL) lc.fetch(sm.C, Cb + c * kQ * p.cs, w);
+  };
+  // a chunk's raw steps, and what the chunk needs of them (wave 0)
   auto raw_steps = [&](int64_t c) { return l < chunk_len(c) ? bf2f(dtb[(c * kQ + l) * p.dts]) : 0.0f; };
   auto put_steps = [&](int64_t c, int b, float raw) {
     float v;
@@ -141,19 +180,22 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
     const TwoSum cs = running_sum(d, Ah);
     const float eh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cs.hi), 63));
     const float el = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cs.lo), 63));
-    sm.cs[b][hw][l] = cs.hi;
-    sm.dt[b][hw][l] = d;
-    sm.e[b][hw][l] = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
-    sm.w[b][hw][l] = exp_diff(eh, el, cs.hi, cs.lo) * d;
+    sm.cs[b][l] = cs.hi * kLog2e;
+    sm.dt[b][l] = d;
+    sm.e[b][l] = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
+    sm.w[b][l] = exp_diff(eh, el, cs.hi, cs.lo) * d;
   };
 
-  // ---- state, transposed: wave w holds S[p = 16w + r][n = 16 nt + 4kq + i].
+  // ---- state, transposed: wave w holds S[p = 16w + r][n = 32 kk + 8kq + 4a + i]
+  // in accs[2 kk + a][i]; the state pass, which feeds no product from it, holds
+  // n = 16 nt + 4kq + i in accs[nt][i], whose operands meet in no LDS bank.
   // The state pass starts segment 0 from the cached state and the others from
   // zero; the full pass starts segment k from E_{k-1} + P_{k-1} (E_{k-2} + ...).
   // The last segment's workgroup writes the cache while others may still be
   // starting, so a sequence of several segments reads it in the state pass
   // alone: segment 0's start is a copy that the state pass leaves behind the
   // E's.
+  auto state_at = [](int nt) { return FULL ? 32 * (nt >> 1) + 4 * (nt & 1) : 16 * nt; };
   f32x4 accs[NT];
   {
     const float *start = nullptr;
@@ -161,10 +203,10 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
       start = (!FULL || last_seg) ? p.cache + (slot * p.nheads + h) * kP * N : state_ws + (p.nseg - 1) * SH * kP * N;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float4 v = start ? *reinterpret_cast<const float4 *>(start + srow + 16 * nt) : make_float4(0, 0, 0, 0);
+      const float4 v = start ? *reinterpret_cast<const float4 *>(start + srow + state_at(nt)) : make_float4(0, 0, 0, 0);
       accs[nt] = (f32x4){v.x, v.y, v.z, v.w};
-      if (!FULL && start && alive)
-        *reinterpret_cast<float4 *>(state_ws + (p.nseg - 1) * SH * kP * N + srow + 16 * nt) = v;
+      if (!FULL && start)
+        *reinterpret_cast<float4 *>(state_ws + (p.nseg - 1) * SH * kP * N + srow + state_at(nt)) = v;
     }
   }
   if (FULL) {
@@ -173,14 +215,14 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
       const float *E = state_ws + j * SH * kP * N + srow;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float4 e = *reinterpret_cast<const float4 *>(E + 16 * nt);
+        const float4 e = *reinterpret_cast<const float4 *>(E + state_at(nt));
         accs[nt] = (f32x4){fmaf(P, accs[nt][0], e.x), fmaf(P, accs[nt][1], e.y), fmaf(P, accs[nt][2], e.z),
                            fmaf(P, accs[nt][3], e.w)};
       }
     }
   }
-  if constexpr (FULL) {   // M's blocks above the diagonal stay zero
-    for (int i = tid; i < kPair * 2 * kQ * kQ / 8; i += 512) reinterpret_cast<uint4 *>(&sm.M[0][0][0])[i] = make_uint4(0, 0, 0, 0);
+  if constexpr (FULL) {   // M's zero tile
+    if (tid < 2 * kTile / 8) *reinterpret_cast<uint4 *>(&sm.M[tid / (kTile / 8)][kZeroTile * kTile + tid % (kTile / 8) * 8]) = make_uint4(0, 0, 0, 0);
   }
   float Dv[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   const int pc = 16 * w + 4 * kq;   // this lane's channels of Y
@@ -192,6 +234,7 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
 
   if (c_begin < c_end) {
     fetch(c_begin, 0);
+    fetch_C(c_begin);
     if (w == 0) put_steps(c_begin, 0, raw_steps(c_begin));
   }
   for (int64_t c = c_begin; c < c_end; ++c) {
@@ -212,8 +255,8 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
         if (16 * tb + r < len) zv[tb] = *reinterpret_cast<const uint2 *>(zb + (t0 + 16 * tb + r) * p.zs + pc);
     }
     if (more) fetch(c + 1, b ^ 1);
-    const float *cs = sm.cs[b][hw], *dt = sm.dt[b][hw], *e0 = sm.e[b][hw], *we = sm.w[b][hw];
-    uint16_t *X = sm.x[b][hw], *B = sm.B[b], *C = sm.C[FULL ? b : 0];
+    const float *cs = sm.cs[b], *dt = sm.dt[b], *e0 = sm.e[b], *we = sm.w[b];
+    uint16_t *X = sm.x[b], *B = sm.B[b];
 
     if constexpr (FULL) {
       if (p.codes) {
@@ -234,48 +277,60 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
         float inv;
         const float scale = row_scale(top, inv);
         const int64_t row = ((q.entry + c) * p.nheads + h) * kP + 16 * w + r;
-        if (alive) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            uint32_t word = 0;
+        for (int kk = 0; kk < KN; ++kk) {
+          uint32_t word[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              word |= (static_cast<uint32_t>(static_cast<int>(rintf(accs[nt][i] * inv))) & 0xffu) << (8 * i);
-            *reinterpret_cast<uint32_t *>(p.codes + row * N + 16 * nt + 4 * kq) = word;
-          }
-          if (kq == 0) p.scales[row] = scale;
+          for (int i = 0; i < 8; ++i)
+            word[i >> 2] |= (static_cast<uint32_t>(static_cast<int>(rintf(accs[2 * kk + (i >> 2)][i & 3] * inv))) & 0xffu) << (8 * (i & 3));
+          *reinterpret_cast<uint2 *>(p.codes + row * N + 32 * kk + 8 * kq) = make_uint2(word[0], word[1]);
         }
+        if (kq == 0) p.scales[row] = scale;
       }
 
       // ---- M, from G^T = B C^T: lane holds (t = 16 wt + r, tau = 16 tb + 4kq + i),
-      // tau <= t.  The second head's waves take the token blocks in the other
-      // order, so that the two waves of a SIMD share the triangle's work.
-      const int wt = hw ? 3 - w : w, t = 16 * wt + r;
-      const float cst = cs[t];
-      bf16x8 cop[KN];
+      // tau <= t.  Every second head's waves take the token blocks in the other
+      // order, so that the waves of a SIMD share the triangle's work.
+      // (One copy of the code for each block: with the block a variable, a
+      // branch stood between any two products.)
+      auto form_M = [&](auto block) {
+        constexpr int WT = decltype(block)::value;
+        const int t = 16 * WT + r;
+        bf16x8 cop[KN];
 #pragma unroll
-      for (int kk = 0; kk < KN; ++kk) cop[kk] = frag<N>(l, C, 16 * wt, 32 * kk);
+        for (int kk = 0; kk < KN; ++kk) cop[kk] = frag<N>(l, sm.C, 16 * WT, 32 * kk);
+        f32x4 acc[WT + 1];
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        if (tb > wt) break;
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int tb = 0; tb <= WT; ++tb) acc[tb] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int kk = 0; kk < KN; ++kk) acc = mfma(frag<N>(l, B, 16 * tb, 32 * kk), cop[kk], acc);
-        const float4 cs4 = *reinterpret_cast<const float4 *>(&cs[16 * tb + 4 * kq]);
-        const float4 dt4 = *reinterpret_cast<const float4 *>(&dt[16 * tb + 4 * kq]);
-        const float csv[4] = {cs4.x, cs4.y, cs4.z, cs4.w}, dtv[4] = {dt4.x, dt4.y, dt4.z, dt4.w};
-        float m[4];
+        for (int kk = 0; kk < KN; ++kk)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = acc[i] * fast_exp2((cst - csv[i]) * kLog2e) * dtv[i];
-          m[i] = 16 * tb + 4 * kq + i <= t ? v : 0.0f;
+          for (int tb = 0; tb <= WT; ++tb) acc[tb] = mfma(frag<N>(l, B, 16 * tb, 32 * kk), cop[kk], acc[tb]);
+        const float cst = cs[t];
+#pragma unroll
+        for (int tb = 0; tb <= WT; ++tb) {
+          const float4 cs4 = *reinterpret_cast<const float4 *>(&cs[16 * tb + 4 * kq]);
+          const float4 dt4 = *reinterpret_cast<const float4 *>(&dt[16 * tb + 4 * kq]);
+          const float csv[4] = {cs4.x, cs4.y, cs4.z, cs4.w}, dtv[4] = {dt4.x, dt4.y, dt4.z, dt4.w};
+          float m[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v = acc[tb][i] * fast_exp2(cst - csv[i]) * dtv[i];
+            m[i] = (tb < WT || 4 * kq + i <= r) ? v : 0.0f;
+          }
+          uint2 hi, lo;
+          split_bf2(m[0], m[1], hi.x, lo.x);
+          split_bf2(m[2], m[3], hi.y, lo.y);
+          const int o = m_tile(WT, tb) * kTile + m_at(r, 4 * kq);
+          *reinterpret_cast<uint2 *>(&sm.M[0][o]) = hi;
+          *reinterpret_cast<uint2 *>(&sm.M[1][o]) = lo;
         }
-        uint2 hi, lo;
-        split_bf2(m[0], m[1], hi.x, lo.x);
-        split_bf2(m[2], m[3], hi.y, lo.y);
-        const int o = tile_at<kQ>(t, 16 * tb + 4 * kq);
-        *reinterpret_cast<uint2 *>(&sm.M[hw][0][o]) = hi;
-        *reinterpret_cast<uint2 *>(&sm.M[hw][1][o]) = lo;
+      };
+      switch ((h & 1) ? 3 - w : w) {
+        case 0: form_M(std::integral_constant<int, 0>{}); break;
+        case 1: form_M(std::integral_constant<int, 1>{}); break;
+        case 2: form_M(std::integral_constant<int, 2>{}); break;
+        default: form_M(std::integral_constant<int, 3>{}); break;
       }
       lds_barrier();
     }
@@ -288,9 +343,7 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
     if constexpr (FULL) {
       // ---- Y^T = S C^T diag(exp(cs)) + X^T M^T for this wave's channels and
       // every token: lane holds Y[t = 16 tb + r][p = 16w + 4kq + i].  The state
-      // operand is this lane's own accumulators: the k index runs over the
-      // states 32kk + 16a + 4kq + j (a < 2, j < 4) in that order for both
-      // operands, and C's are the matching 8-byte pieces of its rows.
+      // operand is this lane's own accumulators.
       f32x4 acc[4];
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) acc[tb] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
@@ -302,36 +355,39 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
           split_bf2(accs[2 * kk + i / 4][i % 4], accs[2 * kk + i / 4][i % 4 + 1], sh_[i / 2], sl_[i / 2]);
         const bf16x8 shi = __builtin_bit_cast(bf16x8, make_uint4(sh_[0], sh_[1], sh_[2], sh_[3]));
         const bf16x8 slo = __builtin_bit_cast(bf16x8, make_uint4(sl_[0], sl_[1], sl_[2], sl_[3]));
+        bf16x8 cf[4];
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
-          const uint2 c0 = *reinterpret_cast<const uint2 *>(&C[tile_at<N>(16 * tb + r, 32 * kk + 4 * kq)]);
-          const uint2 c1 = *reinterpret_cast<const uint2 *>(&C[tile_at<N>(16 * tb + r, 32 * kk + 16 + 4 * kq)]);
-          const bf16x8 cf = __builtin_bit_cast(bf16x8, make_uint4(c0.x, c0.y, c1.x, c1.y));
-          acc[tb] = mfma(shi, cf, acc[tb]);
-          acc[tb] = mfma(slo, cf, acc[tb]);
+          cf[tb] = frag<N>(l, sm.C, 16 * tb, 32 * kk);
+          acc[tb] = mfma(shi, cf[tb], acc[tb]);
         }
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) acc[tb] = mfma(slo, cf[tb], acc[tb]);
       }
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) acc[tb] *= e0[16 * tb + r];
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk)
+      for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb)
-          if (32 * kk < 16 * (tb + 1)) {   // tau blocks at or before the token block
-            acc[tb] = mfma(xt[kk], frag<kQ>(l, sm.M[hw][0], 16 * tb, 32 * kk), acc[tb]);
-            acc[tb] = mfma(xt[kk], frag<kQ>(l, sm.M[hw][1], 16 * tb, 32 * kk), acc[tb]);
-          }
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int tb = 0; tb < 4; ++tb)
+            if (32 * kk < 16 * (tb + 1)) {   // tau blocks at or before the token block
+              const int o = (kq < 2 ? m_tile(tb, 2 * kk) : m_tile(tb, 2 * kk + 1)) * kTile + m_at(r, 8 * (kq & 1));
+              acc[tb] = mfma(xt[kk], ld8(&sm.M[part][o]), acc[tb]);
+            }
       // ---- out = (Y + D x) * silu(z), four channels of a token
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
         const int t = 16 * tb + r;
-        float xv[4], y[4];
-        four(&X[tile_at<kP>(t, pc)], xv);
+        float y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = fmaf(Dv[i], xv[i], acc[tb][i]);
-        if (!p.D) {   // an infinite x times no D is not a NaN
+        for (int i = 0; i < 4; ++i) y[i] = acc[tb][i];
+        if (p.D) {
+          float xv[4];
+          four(&X[tile_at<kP>(t, pc)], xv);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = acc[tb][i];
+          for (int i = 0; i < 4; ++i) y[i] = fmaf(Dv[i], xv[i], y[i]);
         }
         if (zb) {
           const float zf[4] = {__uint_as_float(zv[tb].x << 16), __uint_as_float(zv[tb].x & 0xffff0000u),
@@ -339,11 +395,15 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[i] *= silu_f(zf[i]);
         }
-        if (t < len && alive)
+        if (t < len)
           *reinterpret_cast<uint2 *>(ob + (t0 + t) * p.os + pc) = make_uint2(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]));
       }
     }
 
+    if (FULL && more) {
+      lds_barrier();   // C's readers are done
+      fetch_C(c + 1);
+    }
     // ---- S^T <- exp(cs_end) S^T + B^T (X w), X w in three bf16 parts
     const float dec = e0[kQ - 1];
     if constexpr (!FULL) seg_decay *= dec;
@@ -364,18 +424,21 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
       const bf16x8 f0 = __builtin_bit_cast(bf16x8, make_uint4(x0[0], x0[1], x0[2], x0[3]));
       const bf16x8 f1 = __builtin_bit_cast(bf16x8, make_uint4(x1[0], x1[1], x1[2], x1[3]));
       const bf16x8 f2 = __builtin_bit_cast(bf16x8, make_uint4(x2[0], x2[1], x2[2], x2[3]));
+      // part by part over all tiles: a product never waits for the one before
+      bf16x8 bt[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const bf16x8 bt = frag_t<N>(l, B, 32 * kk, 16 * nt);
-        accs[nt] = mfma(bt, f0, accs[nt]);
-        accs[nt] = mfma(bt, f1, accs[nt]);
-        accs[nt] = mfma(bt, f2, accs[nt]);
+        bt[nt] = FULL ? frag_states<N>(l, B, 32 * kk, nt >> 1, nt & 1) : frag_t<N>(l, B, 32 * kk, 16 * nt);
+        accs[nt] = mfma(bt[nt], f0, accs[nt]);
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) accs[nt] = mfma(bt[nt], f1, accs[nt]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) accs[nt] = mfma(bt[nt], f2, accs[nt]);
     }
     if (w == 0 && more) put_steps(c + 1, b ^ 1, raw);
   }
 
-  if (!alive) return;
   float *end = nullptr;
   if constexpr (FULL) {
     if (p.cache && slot >= 0 && last_seg) end = p.cache + (slot * p.nheads + h) * kP * N + srow;
@@ -386,7 +449,7 @@ __global__ void __launch_bounds__(512, FULL ? 2 : 4) packed_scan_kernel(const Sc
   if (end) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-      *reinterpret_cast<float4 *>(end + 16 * nt) = make_float4(accs[nt][0], accs[nt][1], accs[nt][2], accs[nt][3]);
+      *reinterpret_cast<float4 *>(end + state_at(nt)) = make_float4(accs[nt][0], accs[nt][1], accs[nt][2], accs[nt][3]);
   }
 }
 
@@ -414,28 +477,53 @@ hipError_t launch_var(int64_t dstate, bool full, dim3 grid, hipStream_t stream, 
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(lds));
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fn, grid, dim3(512), lds, stream, p);
+  hipLaunchKernelGGL(fn, grid, dim3(256), lds, stream, p);
   return hipGetLastError();
 }
 
 struct VarPlan {
   int nseg;
-  int64_t pairs, seg_chunks;
+  int64_t seg_chunks;
   size_t off_decay, ws_bytes;
 };
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Segments of the longest sequence; a shorter one has fewer.  One workgroup
-// fills a compute unit's LDS at dstate 128.  The segment count is the one that
-// the model of host_util.h finds fastest, the state pass costing about a
-// quarter of a chunk's time for every chunk but the last segment's.
+// Time in us of `blocks` workgroups of `chunks` chunks: a chunk takes t1 with
+// one workgroup on a compute unit and tn with `per` of them.
+double rounds_us(int64_t blocks, double chunks, double t1, double tn, int64_t per, int64_t cus) {
+  const int64_t slots = per * cus, rest = blocks % slots;
+  double t = static_cast<double>(blocks / slots) * chunks * tn;
+  if (rest > 0) t += chunks * (rest <= cus ? t1 : t1 + (tn - t1) * static_cast<double>(rest - cus) / (slots - cus));
+  return t;
+}
+
+// The whole call with segments of seg chunks.  The chunk times (full pass 4.5
+// and 5.6 us, state pass 1.5 and 2.7) are those measured at dstate 128; a
+// smaller one changes their ratios little.  Each segment costs about 0.8
+// chunks to start, segment k reads the k end states before it (32 KB each, from
+// the caches mostly), and a second launch about 5 us.
+double split_us(int64_t blocks, int64_t nchunks, int64_t seg, int64_t dstate, int64_t cus) {
+  const int64_t G = (nchunks + seg - 1) / seg;
+  const double len = static_cast<double>(seg) + 0.8;
+  double t = rounds_us(blocks * G, len, 4.5, 5.6, 2, cus);
+  if (G > 1) {
+    const double block_bytes = static_cast<double>(blocks) * kP * dstate * sizeof(float);
+    t += rounds_us(blocks * (G - 1), len, 1.5, 2.7, 3, cus) + 5.0 +
+         block_bytes * (static_cast<double>(G) * (G - 1) / 2 / 8e6 + (G - 1) / 5e6);
+  }
+  return t;
+}
+
+// Segments of the longest sequence; a shorter one has fewer.  The library's own
+// count is the one that split_us finds fastest.  Measured at dstate 128 (us,
+// chosen / best of a sweep): 1 x 32768 tokens x 80 heads 684 (6) / 644 (19);
+// 4 x 2048 x 80 178 (1) / 164 (3); 8 x 2048 x 80 316 (2) / 316; 1 x 2048 x 80
+// 71 (4) / 60 (6); 1 x 16384 x 16 109 (26) / 109.
 VarPlan var_plan(const ssd_varlen_args_t *a, int cus) {
   VarPlan pl{};
   int64_t nchunks = (a->max_seqlen + kQ - 1) / kQ;
   if (nchunks < 1) nchunks = 1;
-  const int64_t hpg = a->nheads / a->ngroups;
-  pl.pairs = a->ngroups * ((hpg + kPair - 1) / kPair);
   const int64_t SH = a->nseq * a->nheads;
   int64_t G = 1;
   if (a->seq_segments >= 1) {
@@ -443,8 +531,15 @@ VarPlan var_plan(const ssd_varlen_args_t *a, int cus) {
   } else {
     // sequences of the longest one's length that hold all tokens
     const int64_t rows = (a->total / kQ + a->nseq + nchunks - 1) / nchunks;
-    const int64_t blocks = (rows < a->nseq ? rows : a->nseq) * pl.pairs;
-    G = split_segments(blocks, nchunks, cus, 0.25, 64, 2);
+    const int64_t blocks = (rows < a->nseq ? rows : a->nseq) * a->nheads;
+    double best = 1e300;
+    for (int64_t k = 1; k <= 64 && (k == 1 || 2 * k <= nchunks); ++k) {
+      const double t = split_us(blocks, nchunks, (nchunks + k - 1) / k, a->dstate, cus);
+      if (t < best) {
+        best = t;
+        G = k;
+      }
+    }
   }
   if (G > nchunks) G = nchunks;
   if (G > 65535) G = 65535;
@@ -477,7 +572,7 @@ extern "C" int ssd_varlen_fwd(const ssd_varlen_args_t *a, void *stream_ptr) {
   const VarPlan pl = var_plan(a, cu_count_cached());
   if (pl.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < pl.ws_bytes)) return SSM_ERR_WORKSPACE;
   if (pl.ws_bytes > 0 && !aligned16(a->workspace)) return SSM_ERR_UNSUPPORTED;
-  const int64_t blocks = a->nseq * pl.pairs;
+  const int64_t blocks = a->nseq * a->nheads;
   if (blocks > 0x7fffffffLL) return SSM_ERR_SHAPE;
   ScanParams p{};
   p.x = static_cast<const uint16_t *>(a->x); p.xs = a->x_stride;
@@ -489,7 +584,7 @@ extern "C" int ssd_varlen_fwd(const ssd_varlen_args_t *a, void *stream_ptr) {
   p.A = a->A; p.D = a->D; p.dt_bias = a->dt_bias;
   p.D_per_channel = a->D_per_channel;
   p.step = {a->dt_softplus, a->dt_limit, a->dt_min, a->dt_max};
-  p.nheads = a->nheads; p.ngroups = a->ngroups; p.pairs = pl.pairs;
+  p.nheads = a->nheads; p.ngroups = a->ngroups;
   p.cu = a->cu_seqlens; p.total = a->total; p.max_seqlen = a->max_seqlen;
   p.cache = a->ssm_state; p.cache_slots = a->state_slots; p.seen = a->cache_seqlens; p.slots = a->slots;
   p.codes = a->checkpoints; p.scales = a->checkpoint_scales;

@@ -275,6 +275,9 @@ int ssd_varlen_common(const ssd_varlen_args_t *a) {
       !product_fits(a->total, a->C_stride, 1) || !product_fits(a->total, a->dt_stride, 1) ||
       !product_fits(a->total / SSD_CHUNK + a->nseq, hp, a->dstate))
     return SSM_ERR_SHAPE;
+  // a chunk's tokens are reached by 32-bit byte offsets
+  const int64_t far = (int64_t{1} << 31) / (2 * SSD_CHUNK);
+  if (a->x_stride > far || a->B_stride > far || a->C_stride > far) return SSM_ERR_SHAPE;
   if (!flag_ok(a->D_per_channel) || !flag_ok(a->dt_softplus) || !flag_ok(a->dt_limit)) return SSM_ERR_UNSUPPORTED;
   if (a->dt_limit && !(a->dt_min <= a->dt_max)) return SSM_ERR_SHAPE;
   if (a->seq_segments < 0) return SSM_ERR_SHAPE;
