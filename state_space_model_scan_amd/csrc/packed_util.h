@@ -154,4 +154,39 @@ __device__ __forceinline__ void four(const uint16_t *p, float (&v)[4]) {
   v[3] = __uint_as_float(w.y & 0xffff0000u);
 }
 
+// A row-major tile's 16-byte pieces straight into LDS.  A wave writes one KiB
+// in order, so the tile's permutation (tile_at, its own inverse) is applied to
+// where each lane reads: `at` holds a lane's byte offsets from the tile's
+// first token, which only a sequence's last chunk changes.  Tokens at and
+// after `len` repeat the last one: their steps are 0, and what they give
+// reaches no output.
+template <int ROW_LEN>
+struct TileLoad {
+  static constexpr int G = ROW_LEN / 8, ALL = kQ * G / 64, PER = (ALL + 3) / 4;
+  uint32_t at[PER];
+  __device__ __forceinline__ void place(int64_t stride, int len, int w, int lane) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int piece = (w + 4 * i) * 64 + lane, row = piece / G, t = row < len ? row : len - 1;
+      at[i] = 2u * (static_cast<uint32_t>(t) * static_cast<uint32_t>(stride) +
+                    static_cast<uint32_t>(tile_at<ROW_LEN>(row, (piece % G) * 8) - row * ROW_LEN));
+    }
+  }
+  __device__ __forceinline__ void fetch(uint16_t *tile, const uint16_t *from, int w) const {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (w + 4 * i < ALL)
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void *)(reinterpret_cast<const char *>(from) + at[i]),
+            (__attribute__((address_space(3))) void *)(tile + (w + 4 * i) * 512), 16, 0, 0);
+  }
+};
+
+// A barrier for LDS alone: what is on its way from global memory stays so.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 }  // namespace ssm

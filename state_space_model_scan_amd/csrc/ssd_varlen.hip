@@ -51,7 +51,8 @@ struct ScanParams {
   int8_t *codes;
   float *scales;
   int64_t xs, dts, bs, cs, zs, os;
-  int64_t total, max_seqlen, cache_slots, nheads, ngroups, seg_chunks;
+  int64_t total, max_seqlen, cache_slots, nheads, seg_chunks;
+  uint32_t heads, per_group;   // nheads, heads of a group
   int D_per_channel, nseg;
   StepRule step;
 };
@@ -72,41 +73,6 @@ struct ScanLds {
   // running sum (times log2 e), step, exp(cs), and the state update's weight, per token
   float cs[2][kQ], dt[2][kQ], e[2][kQ], w[2][kQ];
 };
-
-// A row-major tile's 16-byte pieces straight into LDS.  A wave writes one KiB
-// in order, so the tile's permutation (tile_at, its own inverse) is applied to
-// where each lane reads: `at` holds a lane's byte offsets from the tile's
-// first token, which only a sequence's last chunk changes.  Tokens at and
-// after `len` repeat the last one: their steps are 0, and what they give
-// reaches no output.
-template <int ROW_LEN>
-struct TileLoad {
-  static constexpr int G = ROW_LEN / 8, ALL = kQ * G / 64, PER = (ALL + 3) / 4;
-  uint32_t at[PER];
-  __device__ __forceinline__ void place(int64_t stride, int len, int w, int lane) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int piece = (w + 4 * i) * 64 + lane, row = piece / G, t = row < len ? row : len - 1;
-      at[i] = 2u * (static_cast<uint32_t>(t) * static_cast<uint32_t>(stride) +
-                    static_cast<uint32_t>(tile_at<ROW_LEN>(row, (piece % G) * 8) - row * ROW_LEN));
-    }
-  }
-  __device__ __forceinline__ void fetch(uint16_t *tile, const uint16_t *from, int w) const {
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (w + 4 * i < ALL)
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void *)(reinterpret_cast<const char *>(from) + at[i]),
-            (__attribute__((address_space(3))) void *)(tile + (w + 4 * i) * 512), 16, 0, 0);
-  }
-};
-
-// A barrier for LDS alone: what is on its way from global memory stays so.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
 
 // The transposed operand of B for state tile a of the k step kk: lane m's row
 // is the state n = 32kk + 8 (m / 4) + 4a + m % 4, so that a lane's accumulators
@@ -130,8 +96,8 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
   ScanLds<N, FULL> &sm = *reinterpret_cast<ScanLds<N, FULL> *>(smem);
   const int tid = threadIdx.x, l = tid & 63, r = l & 15, kq = l >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);   // channels 16w..16w+15
-  const int64_t sh = blockIdx.x, SH = gridDim.x;
-  const int64_t s = sh / p.nheads, h = sh - s * p.nheads, g = h / (p.nheads / p.ngroups);
+  const int64_t SH = gridDim.x;
+  const uint32_t sh = blockIdx.x, s = sh / p.heads, h = sh - s * p.heads, g = h / p.per_group;
   const Seq q = sequence(p.cu, p.total, p.max_seqlen, s);
   // the full pass dispatches its last segments first: those of the longest sequences
   const int64_t seg = FULL ? static_cast<int64_t>(gridDim.y) - 1 - blockIdx.y : blockIdx.y;
@@ -150,7 +116,7 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
   const uint16_t *dtb = p.dt + q.first * p.dts + h;
   uint16_t *ob = p.out + q.first * p.os + h * kP;
   const float Ah = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
-  float *state_ws = p.ws_state + sh * kP * N;   // segment k's at k * SH * kP * N
+  float *state_ws = p.ws_state + static_cast<int64_t>(sh) * kP * N;   // segment k's at k * SH * kP * N
   const int srow = (16 * w + r) * N + (FULL ? 8 : 4) * kq;   // this lane's first state element in a (p, n) block
 
   auto chunk_len = [&](int64_t c) { return static_cast<int>(q.len - c * kQ < kQ ? q.len - c * kQ : kQ); };
@@ -489,15 +455,6 @@ struct VarPlan {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Time in us of `blocks` workgroups of `chunks` chunks: a chunk takes t1 with
-// one workgroup on a compute unit and tn with `per` of them.
-double rounds_us(int64_t blocks, double chunks, double t1, double tn, int64_t per, int64_t cus) {
-  const int64_t slots = per * cus, rest = blocks % slots;
-  double t = static_cast<double>(blocks / slots) * chunks * tn;
-  if (rest > 0) t += chunks * (rest <= cus ? t1 : t1 + (tn - t1) * static_cast<double>(rest - cus) / (slots - cus));
-  return t;
-}
-
 // The whole call with segments of seg chunks.  The chunk times (full pass 4.5
 // and 5.6 us, state pass 1.5 and 2.7) are those measured at dstate 128; a
 // smaller one changes their ratios little.  Each segment costs about 0.8
@@ -510,16 +467,16 @@ double split_us(int64_t blocks, int64_t nchunks, int64_t seg, int64_t dstate, in
   if (G > 1) {
     const double block_bytes = static_cast<double>(blocks) * kP * dstate * sizeof(float);
     t += rounds_us(blocks * (G - 1), len, 1.5, 2.7, 3, cus) + 5.0 +
-         block_bytes * (static_cast<double>(G) * (G - 1) / 2 / 8e6 + (G - 1) / 5e6);
+         block_bytes * (static_cast<double>(G) * (G - 1) / 2 / 1e7 + (G - 1) / 5e6);
   }
   return t;
 }
 
 // Segments of the longest sequence; a shorter one has fewer.  The library's own
 // count is the one that split_us finds fastest.  Measured at dstate 128 (us,
-// chosen / best of a sweep): 1 x 32768 tokens x 80 heads 684 (6) / 644 (19);
+// chosen / best of a sweep): 1 x 32768 tokens x 80 heads 644 (19) / 644;
 // 4 x 2048 x 80 178 (1) / 164 (3); 8 x 2048 x 80 316 (2) / 316; 1 x 2048 x 80
-// 71 (4) / 60 (6); 1 x 16384 x 16 109 (26) / 109.
+// 60 (6) / 60; 1 x 16384 x 16 109 (26) / 109.
 VarPlan var_plan(const ssd_varlen_args_t *a, int cus) {
   VarPlan pl{};
   int64_t nchunks = (a->max_seqlen + kQ - 1) / kQ;
@@ -584,7 +541,9 @@ extern "C" int ssd_varlen_fwd(const ssd_varlen_args_t *a, void *stream_ptr) {
   p.A = a->A; p.D = a->D; p.dt_bias = a->dt_bias;
   p.D_per_channel = a->D_per_channel;
   p.step = {a->dt_softplus, a->dt_limit, a->dt_min, a->dt_max};
-  p.nheads = a->nheads; p.ngroups = a->ngroups;
+  p.nheads = a->nheads;
+  p.heads = static_cast<uint32_t>(a->nheads);
+  p.per_group = static_cast<uint32_t>(a->nheads / a->ngroups);
   p.cu = a->cu_seqlens; p.total = a->total; p.max_seqlen = a->max_seqlen;
   p.cache = a->ssm_state; p.cache_slots = a->state_slots; p.seen = a->cache_seqlens; p.slots = a->slots;
   p.codes = a->checkpoints; p.scales = a->checkpoint_scales;

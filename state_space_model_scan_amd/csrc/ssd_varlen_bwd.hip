@@ -67,6 +67,7 @@ struct BwdParams {
   int64_t xs, dts, bs, cs, gs, dxs, ddts, dbs, dcs;
   int64_t code_entry, code_head, scale_entry, scale_head;
   int64_t total, nseq, max_seqlen, nheads, ngroups, seg_chunks, entries;
+  uint32_t heads, per_group;   // nheads, heads of a group
   int nseg, D_per_channel, hb_heads, hb_per_group;
   StepRule step;
 };
@@ -77,22 +78,25 @@ struct BwdParams {
 // the forward holds the state.  STORE: write every chunk's dH; otherwise find
 // the segment's adjoint from zero and its decay.
 // ---------------------------------------------------------------------------
+template <int N>
+struct AdjointLds {
+  uint16_t C[2][kQ * N], g[2][kQ * kP];   // [t][n], [t][p]; the next chunk's are on their way into the other half
+  float e[2][kQ], end[2];                 // exp(cs), and at the chunk's end
+};
+
 template <int N, bool STORE>
-__global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
+__global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
   constexpr int NT = N / 16;
-  constexpr int CPIECES = kQ * N / 8, CPER = (CPIECES + 255) / 256;
-  __shared__ __attribute__((aligned(16))) uint16_t sG[kQ * kP], sC[kQ * N];
-  __shared__ __attribute__((aligned(16))) float sE[kQ];
-  __shared__ float sEnd;
-  const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r = l & 15, kq = l >> 4;
-  const int64_t sh = blockIdx.x, SH = gridDim.x;
-  const int64_t s = sh / p.nheads, h = sh - s * p.nheads, gr = h / (p.nheads / p.ngroups);
+  __shared__ __attribute__((aligned(16))) AdjointLds<N> sm;
+  const int tid = threadIdx.x, l = tid & 63, r = l & 15, kq = l >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t SH = gridDim.x;
+  const uint32_t sh = blockIdx.x, s = sh / p.heads, h = sh - s * p.heads, gr = h / p.per_group;
   const Seq q = sequence(p.cu, p.total, p.max_seqlen, s);
-  const int64_t nsegs = q.chunks ? (q.chunks + p.seg_chunks - 1) / p.seg_chunks : 1;
   // the first launch runs the segments that have one before them
   const int64_t seg = STORE ? blockIdx.y : blockIdx.y + 1;
-  if (seg >= nsegs) return;
   const int64_t c_begin = seg * p.seg_chunks;
+  if (seg > 0 && c_begin >= q.chunks) return;
   const int64_t c_end = c_begin + p.seg_chunks < q.chunks ? c_begin + p.seg_chunks : q.chunks;
   const float Ah = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
   const uint16_t *gb = p.g + q.first * p.gs + h * kP;
@@ -100,17 +104,47 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
   const uint16_t *dtb = p.dt + q.first * p.dts + h;
   const int srow = (16 * w + r) * N + 4 * kq;
 
+  auto chunk_len = [&](int64_t c) { return static_cast<int>(q.len - c * kQ < kQ ? q.len - c * kQ : kQ); };
+  TileLoad<kP> lg;
+  TileLoad<N> lc;
+  auto fetch = [&](int64_t c, int b) {   // from the last chunk down: only the first one fetched can be short
+    lg.fetch(sm.g[b], gb + c * kQ * p.gs, w);
+    lc.fetch(sm.C[b], Cb + c * kQ * p.cs, w);
+  };
+  auto raw_steps = [&](int64_t c) { return l < chunk_len(c) ? bf2f(dtb[(c * kQ + l) * p.dts]) : 0.0f; };
+  // tokens beyond the chunk's end repeat its last one and weigh nothing
+  auto put_steps = [&](int64_t c, int b, float raw) {
+    float v;
+    const TwoSum cs = running_sum(chunk_step(p.step, raw, bias, l < chunk_len(c), v), Ah);
+    const float e = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
+    sm.e[b][l] = l < chunk_len(c) ? e : 0.0f;
+    if (l == 63) sm.end[b] = e;
+  };
+  if (c_begin < c_end) {
+    const int len = chunk_len(c_end - 1);
+    lg.place(p.gs, len, w, l);
+    lc.place(p.cs, len, w, l);
+    fetch(c_end - 1, 0);
+    if (len < kQ) {
+      lg.place(p.gs, kQ, w, l);
+      lc.place(p.cs, kQ, w, l);
+    }
+    if (w == 0) put_steps(c_end - 1, 0, raw_steps(c_end - 1));
+  }
+
   f32x4 acc[NT];
-  const bool from_end = seg == nsegs - 1 && p.dfin;
+  const bool from_end = c_end >= q.chunks && p.dfin;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const float4 v = from_end ? *reinterpret_cast<const float4 *>(p.dfin + sh * kP * N + srow + 16 * nt)
+    const float4 v = from_end ? *reinterpret_cast<const float4 *>(p.dfin + static_cast<int64_t>(sh) * kP * N + srow + 16 * nt)
                               : make_float4(0, 0, 0, 0);
     acc[nt] = (f32x4){v.x, v.y, v.z, v.w};
   }
   if constexpr (STORE) {
     // the carry of the later segments, the last one's first
-    for (int64_t j = nsegs - 1; j > seg; --j) {
+    int64_t j = p.nseg - 1;
+    while (j > seg && j * p.seg_chunks >= q.chunks) --j;
+    for (; j > seg; --j) {
       const float P = p.ws_decay[(j - 1) * SH + sh];
       const float *E = p.ws_state + ((j - 1) * SH + sh) * kP * N + srow;
 #pragma unroll
@@ -123,21 +157,13 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
   }
   float decay = 1.0f;
   for (int64_t c = c_end - 1; c >= c_begin; --c) {
-    const int64_t t0 = c * kQ;
-    const int len = static_cast<int>(q.len - t0 < kQ ? q.len - t0 : kQ);
-    uint4 gv[2], cv[CPER];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int piece = tid + 256 * k, t = piece >> 3;
-      gv[k] = t < len ? ld8_raw(gb + (t0 + t) * p.gs + (piece & 7) * 8) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int k = 0; k < CPER; ++k) {
-      const int piece = tid + 256 * k, t = piece / (N / 8);
-      cv[k] = (piece < CPIECES && t < len) ? ld8_raw(Cb + (t0 + t) * p.cs + (piece % (N / 8)) * 8) : make_uint4(0, 0, 0, 0);
-    }
+    const int b = static_cast<int>((c_end - 1 - c) & 1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();   // the chunk's tiles are there; the other half's readers are done
+    const bool more = c > c_begin;
     float raw = 0.0f;
-    if (w == 0 && l < len) raw = bf2f(dtb[(t0 + l) * p.dts]);
+    if (w == 0 && more) raw = raw_steps(c - 1);
+    if (more) fetch(c - 1, b ^ 1);
     if constexpr (STORE) {
       // in the order (n / 32, (n / 4) % 4, (n / 16) % 2, n % 4) along a row,
       // so that a lane's eight states of two tiles are 16 bytes and the four
@@ -154,51 +180,41 @@ __global__ void __launch_bounds__(256, 2) adjoint_kernel(const BwdParams p) {
         *reinterpret_cast<uint4 *>(dh + kP * N + 16 * nt) = lo;
       }
     }
-    __syncthreads();   // the previous chunk's reads are done
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int piece = tid + 256 * k;
-      *reinterpret_cast<uint4 *>(&sG[tile_at<kP>(piece >> 3, (piece & 7) * 8)]) = gv[k];
-    }
-#pragma unroll
-    for (int k = 0; k < CPER; ++k) {
-      const int piece = tid + 256 * k;
-      if (piece < CPIECES) *reinterpret_cast<uint4 *>(&sC[tile_at<N>(piece / (N / 8), (piece % (N / 8)) * 8)]) = cv[k];
-    }
-    if (w == 0) {
-      float v;
-      const float d = chunk_step(p.step, raw, bias, l < len, v);
-      const TwoSum cs = running_sum(d, Ah);
-      const float e = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
-      sE[l] = e;
-      if (l == 63) sEnd = e;
-    }
-    __syncthreads();
-    const float end = sEnd;
+    const float end = sm.end[b];
     decay *= end;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) acc[nt] *= end;
 #pragma unroll
     for (int kk = 0; kk < kQ / 32; ++kk) {
-      const uint4 gt = __builtin_bit_cast(uint4, frag_t<kP>(l, sG, 32 * kk, 16 * w));
-      uint32_t gh[4], gl[4];
+      const uint4 gt = __builtin_bit_cast(uint4, frag_t<kP>(l, sm.g[b], 32 * kk, 16 * w));
+      const float *e = &sm.e[b][32 * kk + 8 * kq];
+      uint32_t g0[4], g1[4], g2[4];
 #pragma unroll
-      for (int i = 0; i < 8; i += 2)
-        split_bf2(bf2f(raw_bits(gt, i)) * sE[32 * kk + 8 * kq + i], bf2f(raw_bits(gt, i + 1)) * sE[32 * kk + 8 * kq + i + 1],
-                  gh[i / 2], gl[i / 2]);
-      const bf16x8 hi = __builtin_bit_cast(bf16x8, make_uint4(gh[0], gh[1], gh[2], gh[3]));
-      const bf16x8 lo = __builtin_bit_cast(bf16x8, make_uint4(gl[0], gl[1], gl[2], gl[3]));
+      for (int i = 0; i < 8; i += 2) {   // in three parts: all 24 bits
+        const float x = bf2f(raw_bits(gt, i)) * e[i], y = bf2f(raw_bits(gt, i + 1)) * e[i + 1];
+        split_bf2(x, y, g0[i / 2], g1[i / 2]);
+        g2[i / 2] = pack_bf2(x - __uint_as_float(g0[i / 2] << 16) - __uint_as_float(g1[i / 2] << 16),
+                             y - __uint_as_float(g0[i / 2] & 0xffff0000u) - __uint_as_float(g1[i / 2] & 0xffff0000u));
+      }
+      const bf16x8 f0 = __builtin_bit_cast(bf16x8, make_uint4(g0[0], g0[1], g0[2], g0[3]));
+      const bf16x8 f1 = __builtin_bit_cast(bf16x8, make_uint4(g1[0], g1[1], g1[2], g1[3]));
+      const bf16x8 f2 = __builtin_bit_cast(bf16x8, make_uint4(g2[0], g2[1], g2[2], g2[3]));
+      bf16x8 ct[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const bf16x8 ct = frag_t<N>(l, sC, 32 * kk, 16 * nt);
-        acc[nt] = mfma(ct, hi, acc[nt]);
-        acc[nt] = mfma(ct, lo, acc[nt]);
+        ct[nt] = frag_t<N>(l, sm.C[b], 32 * kk, 16 * nt);
+        acc[nt] = mfma(ct[nt], f0, acc[nt]);
       }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[nt] = mfma(ct[nt], f1, acc[nt]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) acc[nt] = mfma(ct[nt], f2, acc[nt]);
     }
+    if (w == 0 && more) put_steps(c - 1, b ^ 1, raw);
   }
   float *to = nullptr;
   if constexpr (STORE) {
-    if (p.dinit && seg == 0) to = p.dinit + sh * kP * N + srow;
+    if (p.dinit && seg == 0) to = p.dinit + static_cast<int64_t>(sh) * kP * N + srow;
   } else {
     to = p.ws_state + ((seg - 1) * SH + sh) * kP * N + srow;
     if (tid == 0) p.ws_decay[(seg - 1) * SH + sh] = decay;
@@ -262,19 +278,17 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
 
   // the entry's sequence: the last s whose first entry is at or before it
   const int64_t entry = blockIdx.x;
-  int64_t lo = 0, hi = p.nseq;
+  int lo = 0, hi = static_cast<int>(p.nseq);
   while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    int64_t e = p.cu[mid];
-    e = (e < 0 ? 0 : e) / kQ + mid;
-    if (e <= entry) lo = mid;
+    const int mid = lo + ((hi - lo) >> 1), at = p.cu[mid];
+    if (static_cast<int64_t>((at < 0 ? 0 : at) / kQ) + mid <= entry) lo = mid;
     else hi = mid;
   }
   const Seq q = sequence(p.cu, p.total, p.max_seqlen, lo);
   const int64_t chunk = entry - q.entry;
-  const int64_t hpg = p.nheads / p.ngroups;
-  const int64_t gr = blockIdx.y / p.hb_per_group, hb = blockIdx.y - gr * p.hb_per_group;
-  const int64_t h0 = gr * hpg + hb * p.hb_heads;
+  const int64_t hpg = p.per_group;
+  const uint32_t gr = blockIdx.y / static_cast<uint32_t>(p.hb_per_group), hb = blockIdx.y - gr * p.hb_per_group;
+  const int64_t h0 = gr * hpg + static_cast<int64_t>(hb) * p.hb_heads;
   const int64_t h1 = h0 + p.hb_heads < (gr + 1) * hpg ? h0 + p.hb_heads : (gr + 1) * hpg;
   const int nh = static_cast<int>(h1 - h0);
   if (chunk < 0 || chunk >= q.chunks) {   // an entry of no chunk: nothing to add
@@ -418,12 +432,14 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
 #pragma unroll
       for (int kk = 0; kk < KN; ++kk) {
         const bf16x8 d0 = frag<N>(l, sm.dh[0], 16 * pt, 32 * kk), d1 = frag<N>(l, sm.dh[1], 16 * pt, 32 * kk);
+        bf16x8 bf[2];
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-          const bf16x8 bf = frag<N>(l, sm.B, 16 * PR::jt(4 * a), 32 * kk);
-          st[a] = mfma(d0, bf, st[a]);
-          st[a] = mfma(d1, bf, st[a]);
+          bf[a] = frag<N>(l, sm.B, 16 * PR::jt(4 * a), 32 * kk);
+          st[a] = mfma(d0, bf[a], st[a]);
         }
+#pragma unroll
+        for (int a = 0; a < 2; ++a) st[a] = mfma(d1, bf[a], st[a]);
       }
 #pragma unroll
       for (int t = 0; t < 5; ++t) {
@@ -653,7 +669,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     if (t < len) {
       if (p.ws_bc) {
         const int64_t plane = p.hb_per_group * p.total * p.ngroups * N;
-        float *o = p.ws_bc + ((hb * p.total + t0 + t) * p.ngroups + gr) * N + n0;
+        float *o = p.ws_bc + ((static_cast<int64_t>(hb) * p.total + t0 + t) * p.ngroups + gr) * N + n0;
         *reinterpret_cast<float4 *>(o) = make_float4(dBa[a][0], dBa[a][1], dBa[a][2], dBa[a][3]);
         *reinterpret_cast<float4 *>(o + plane) = make_float4(dCa[a][0], dCa[a][1], dCa[a][2], dCa[a][3]);
       } else {
@@ -839,6 +855,8 @@ extern "C" int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *a, void *stream_ptr) 
   p.ws_dd = reinterpret_cast<float *>(ws + pl.off_dd);
   p.total = f.total; p.nseq = f.nseq; p.max_seqlen = f.max_seqlen;
   p.nheads = f.nheads; p.ngroups = f.ngroups;
+  p.heads = static_cast<uint32_t>(f.nheads);
+  p.per_group = static_cast<uint32_t>(f.nheads / f.ngroups);
   p.code_entry = a->code_entry_stride; p.code_head = a->code_head_stride;
   p.scale_entry = a->scale_entry_stride; p.scale_head = a->scale_head_stride;
   p.seg_chunks = pl.seg_chunks; p.nseg = pl.nseg; p.entries = pl.entries;

@@ -34,7 +34,8 @@ struct StepParams {
   float *state;
   const int32_t *seen, *slots;
   int64_t nheads, ngroups, xs, dts, zs, os, nslots;
-  int ring_len, silu, softplus, dt_limit, D_per_channel;
+  uint32_t per_group, ring_len;
+  int silu, softplus, dt_limit, D_per_channel;
   float dt_min, dt_max;
 };
 
@@ -56,10 +57,10 @@ __global__ void __launch_bounds__(256) step_kernel(const StepParams p) {
   const int tid = threadIdx.x;
   const int h = blockIdx.x, row0 = blockIdx.y * ROWS;
   const int64_t b = blockIdx.z;
-  const int64_t hpg = p.nheads / p.ngroups, g = h / hpg;
+  const uint32_t g = static_cast<uint32_t>(h) / p.per_group;
   int64_t slot = p.slots ? p.slots[b] : b;
   if (slot < 0 || slot >= p.nslots) slot = -1;
-  int64_t seen = p.seen ? p.seen[b] : 0;
+  int32_t seen = p.seen ? p.seen[b] : 0;
   if (seen < 0 || slot < 0) seen = 0;
 
   // ---- this workgroup's part of the state
@@ -79,7 +80,7 @@ __global__ void __launch_bounds__(256) step_kernel(const StepParams p) {
   for (int i = tid; i < ROWS + 2 * N; i += 256) {
     const bool isx = i < ROWS;
     const int64_t c = isx ? static_cast<int64_t>(h) * kP + row0 + i
-                          : hp + (i - ROWS < N ? g * N + (i - ROWS) : (p.ngroups + g) * N + (i - ROWS - N));
+                          : hp + (i - ROWS < N ? static_cast<int64_t>(g) * N + (i - ROWS) : (p.ngroups + g) * N + (i - ROWS - N));
     const float4 w = *reinterpret_cast<const float4 *>(p.w + c * kW);
     const float wk[kW] = {w.x, w.y, w.z, w.w};
     const int64_t rbase = ((slot < 0 ? 0 : slot) * channels + c) * p.ring_len;
@@ -88,11 +89,11 @@ __global__ void __launch_bounds__(256) step_kernel(const StepParams p) {
     v = fmaf(wk[kW - 1], now, v);
 #pragma unroll
     for (int back = 1; back < kW; ++back)
-      if (seen >= back) v = fmaf(wk[kW - 1 - back], load_io<IO>(p.ring, rbase + (seen - back) % p.ring_len), v);
+      if (seen >= back) v = fmaf(wk[kW - 1 - back], load_io<IO>(p.ring, rbase + static_cast<uint32_t>(seen - back) % p.ring_len), v);
     if (p.silu) v = silu_f(v);
     su[i] = v;
-    if (slot >= 0 && (isx || (h == g * hpg && row0 == 0))) {
-      const int64_t at = rbase + seen % p.ring_len, from = b * p.xs + c;   // the input as it is
+    if (slot >= 0 && (isx || (static_cast<uint32_t>(h) == g * p.per_group && row0 == 0))) {
+      const int64_t at = rbase + static_cast<uint32_t>(seen) % p.ring_len, from = b * p.xs + c;   // the input as it is
       if constexpr (IO != 0) static_cast<uint16_t *>(p.ring)[at] = static_cast<const uint16_t *>(p.xBC)[from];
       else static_cast<uint32_t *>(p.ring)[at] = static_cast<const uint32_t *>(p.xBC)[from];
     }
@@ -154,10 +155,11 @@ extern "C" int conv1d_ssd_update(const conv1d_ssd_update_args_t *a, void *stream
   p.out = a->out; p.os = a->out_stride;
   p.A = a->A; p.w = a->conv_weight; p.wb = a->conv_bias; p.D = a->D; p.dt_bias = a->dt_bias;
   p.D_per_channel = a->D_per_channel;
-  p.ring = a->conv_state; p.ring_len = static_cast<int>(a->state_len);
+  p.ring = a->conv_state; p.ring_len = static_cast<uint32_t>(a->state_len);
   p.state = a->ssm_state; p.nslots = a->state_slots;
   p.seen = a->cache_seqlens; p.slots = a->slots;
   p.nheads = a->nheads; p.ngroups = a->ngroups;
+  p.per_group = static_cast<uint32_t>(a->nheads / a->ngroups);
   p.silu = a->act == SSM_ACT_SILU;
   p.softplus = a->dt_softplus;
   p.dt_limit = a->dt_limit; p.dt_min = a->dt_min; p.dt_max = a->dt_max;
