@@ -240,26 +240,20 @@ struct ChunkLds {
   // start, to the 16-token block's start, and from the chunk's end
   float ch[kMaxHeads][kQ], cl[kMaxHeads][kQ], dt[kMaxHeads][kQ], e0[kMaxHeads][kQ], eb[kMaxHeads][kQ], we[kMaxHeads][kQ];
   // one head's partial sums, and what the heads' steps need of them
-  float row[4][kQ], col[4][kQ], q[N / 16][kQ], r[4][kQ], dd[2][kP], hh[8];
+  float row[4][kQ], col[4][kQ], q[N / 16][kQ], r[2][kQ], dd[4][kP], hh[8];
   float direct[kMaxHeads][kQ], into[kMaxHeads][kQ], rs[kMaxHeads][kQ], ddc[kMaxHeads][kP], hhs[kMaxHeads];
 };
 
-// The ten 16 x 16 tiles of pairs (i block, j block), j <= i, in two halves of
-// five: waves 0-3 take j blocks 0 and 3, waves 4-7 blocks 1 and 2.
-template <int HALF>
-struct Pairs {
-  static constexpr int it(int k) { return HALF == 0 ? (k < 4 ? k : 3) : (k < 3 ? k + 1 : k - 1); }
-  static constexpr int jt(int k) { return HALF == 0 ? (k < 4 ? 0 : 3) : (k < 3 ? 1 : 2); }
-  static constexpr int at(int k) { return HALF == 0 ? (k < 4 ? 0 : 1) : (k < 3 ? 0 : 1); }   // which of the two j blocks
-};
-
 // One workgroup of eight waves.  For a head, between two barriers:
-//   wave w = (pt = w % 4, half = w / 4) forms the pair tiles of its half,
-//     M = g x^T, and multiplies S L straight from its registers (a product's
-//     result lies as the 16x16x16 product's second operand does) with the
-//     channels [16 pt, 16 pt + 16) of g: dx of its two token blocks; the four
-//     waves of a half form the same tiles again, which costs less than an LDS
-//     round trip and a third barrier; tile k's sums are kept by wave pt = k % 4;
+//   a wave forms the pair tiles (i block >= j block) of one j block, M = g x^T,
+//     and multiplies S L straight from its registers (a product's result lies
+//     as the 16x16x16 product's second operand does) with one half of the
+//     channels of g: dx of its j block and half.  Two waves form each tile,
+//     which costs less than an LDS round trip and a third barrier; each keeps
+//     every second tile's sums.  Wave w takes block w of the first half, wave
+//     4 + w block 3 - w of the second, so that the two waves of a SIMD have
+//     five tiles together (four waves to a tile, ten to a SIMD, took 659 us
+//     where this takes MEASURED at 8 x 2048 tokens, 80 heads);
 //   and the state products of its n tile, dH^T x and H^T g.
 // The partial sums over tiles meet in LDS; the steps' gradients, chains of
 // lane sums, wait until the end and are then done for all heads at once.
@@ -356,26 +350,32 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     for (int k = 0; k < 4; ++k) sm.row[k][tid] = sm.col[k][tid] = 0.0f;
   }
 
-  const int pt = w & 3, half = w >> 2;
+  const int ph = w >> 2, jb = ph ? 7 - w : w;   // channel half, j block
   const int nt = w % NT, ti0 = (w / NT) * IT;
-  f32x4 S[5], V[2], dBa[IT], dCa[IT];
+  f32x4 S[4], V[2], dBa[IT], dCa[IT];
   const f32x4 zero4 = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int k = 0; k < 5; ++k) S[k] = zero4;
+  for (int k = 0; k < 4; ++k) S[k] = zero4;
   V[0] = V[1] = zero4;
 #pragma unroll
   for (int k = 0; k < IT; ++k) dBa[k] = dCa[k] = zero4;
   __syncthreads();
-  auto form_S = [&](auto hc) {
-    using PR = Pairs<decltype(hc)::value>;
-#pragma unroll
-    for (int k = 0; k < 5; ++k)
-#pragma unroll
-      for (int kk = 0; kk < KN; ++kk)
-        S[k] = mfma(frag<N>(l, sm.C, 16 * PR::it(k), 32 * kk), frag<N>(l, sm.B, 16 * PR::jt(k), 32 * kk), S[k]);
+  // one copy of the code for each j block
+  auto for_block = [&](auto &&f) {
+    if (jb == 0) f(std::integral_constant<int, 0>{});
+    else if (jb == 1) f(std::integral_constant<int, 1>{});
+    else if (jb == 2) f(std::integral_constant<int, 2>{});
+    else f(std::integral_constant<int, 3>{});
   };
-  if (half == 0) form_S(std::integral_constant<int, 0>{});
-  else form_S(std::integral_constant<int, 1>{});
+  for_block([&](auto block) {
+    constexpr int JB = decltype(block)::value;
+#pragma unroll
+    for (int kk = 0; kk < KN; ++kk) {
+      const bf16x8 bf = frag<N>(l, sm.B, 16 * JB, 32 * kk);
+#pragma unroll
+      for (int it = JB; it < 4; ++it) S[it - JB] = mfma(frag<N>(l, sm.C, 16 * it, 32 * kk), bf, S[it - JB]);
+    }
+  });
 
   for (int k = 0; k < nh; ++k) {
     const int64_t h = h0 + k;
@@ -425,32 +425,32 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     if (k + 1 < nh) load_head(h + 1);
 
     // ---- the pairs, and dx: pair tiles lie as (i = 16 it + 4 kq + ii,
-    // j = 16 jt + r), dx as (p = 16 pt + 4 kq + ii, j = 16 jt + r)
-    auto pairs_and_dx = [&](auto hc) {
-      using PR = Pairs<decltype(hc)::value>;
+    // j = 16 JB + r), dx as (p = 16 (2 ph + a) + 4 kq + ii, j = 16 JB + r)
+    for_block([&](auto block) {
+      constexpr int JB = decltype(block)::value;
+      const int j = 16 * JB + r;
+      const float jh = sm.ch[k][j], jl = sm.cl[k][j], dj = dt[j];
       f32x4 pr[2] = {zero4, zero4}, st[2] = {zero4, zero4};
 #pragma unroll
       for (int kk = 0; kk < KN; ++kk) {
-        const bf16x8 d0 = frag<N>(l, sm.dh[0], 16 * pt, 32 * kk), d1 = frag<N>(l, sm.dh[1], 16 * pt, 32 * kk);
-        bf16x8 bf[2];
+        const bf16x8 bf = frag<N>(l, sm.B, 16 * JB, 32 * kk);
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          bf[a] = frag<N>(l, sm.B, 16 * PR::jt(4 * a), 32 * kk);
-          st[a] = mfma(d0, bf[a], st[a]);
-        }
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int a = 0; a < 2; ++a) st[a] = mfma(d1, bf[a], st[a]);
+          for (int a = 0; a < 2; ++a) st[a] = mfma(frag<N>(l, sm.dh[part], 32 * ph + 16 * a, 32 * kk), bf, st[a]);
       }
+      bf16x8 xf[2];
 #pragma unroll
-      for (int t = 0; t < 5; ++t) {
-        if (t % 2 == 0) __builtin_amdgcn_sched_barrier(0);   // bounds the operands in flight
-        const int it = PR::it(t), jt = PR::jt(t), j = 16 * jt + r, i0 = 16 * it + 4 * kq;
+      for (int kk = 0; kk < 2; ++kk) xf[kk] = frag<kP>(l, sm.x, 16 * JB, 32 * kk);
+#pragma unroll
+      for (int it = JB; it < 4; ++it) {
+        if ((it - JB) % 2 == 0) __builtin_amdgcn_sched_barrier(0);   // bounds the operands in flight
+        const int t = it - JB, i0 = 16 * it + 4 * kq;
         f32x4 m = zero4;
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) m = mfma(frag<kP>(l, sm.g, 16 * it, 32 * kk), frag<kP>(l, sm.x, 16 * jt, 32 * kk), m);
-        const float jh = sm.ch[k][j], jl = sm.cl[k][j];
+        for (int kk = 0; kk < 2; ++kk) m = mfma(frag<kP>(l, sm.g, 16 * it, 32 * kk), xf[kk], m);
         float L[4];
-        if (it == jt) {
+        if (it == JB) {
           const float4 ih = *reinterpret_cast<const float4 *>(&sm.ch[k][i0]), il = *reinterpret_cast<const float4 *>(&sm.cl[k][i0]);
           const float ihv[4] = {ih.x, ih.y, ih.z, ih.w}, ilv[4] = {il.x, il.y, il.z, il.w};
 #pragma unroll
@@ -465,64 +465,63 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii) {
           u[ii] = S[t][ii] * L[ii];
-          if (it == jt && i0 + ii < j) u[ii] = 0.0f;
+          if (it == JB && 4 * kq + ii < r) u[ii] = 0.0f;
         }
         uint2 uh, ul;
         split_bf2(u[0], u[1], uh.x, ul.x);
         split_bf2(u[2], u[3], uh.y, ul.y);
-        const s16x4 gt = frag_t4<kP>(l, sm.g, 16 * it, 16 * pt);
-        f32x4 &acc = pr[PR::at(t)];
-        acc = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(gt, __builtin_bit_cast(s16x4, uh), acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(gt, __builtin_bit_cast(s16x4, ul), acc, 0, 0, 0);
-        if (pt == (t & 3)) {
-          const float dj = dt[j];
+        s16x4 gt[2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+          gt[a] = frag_t4<kP>(l, sm.g, 16 * it, 32 * ph + 16 * a);
+          pr[a] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(gt[a], __builtin_bit_cast(s16x4, uh), pr[a], 0, 0, 0);
+        }
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+          pr[a] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(gt[a], __builtin_bit_cast(s16x4, ul), pr[a], 0, 0, 0);
+        if (ph == ((it + JB) & 1)) {
           float col = 0.0f, rows[4];
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii) {
-            const bool out = it == jt && i0 + ii < j;
-            V[t >> 2][ii] = fmaf(out ? 0.0f : m[ii] * L[ii], dj, V[t >> 2][ii]);
+            const bool out = it == JB && 4 * kq + ii < r;
+            V[t >> 1][ii] = fmaf(out ? 0.0f : m[ii] * L[ii], dj, V[t >> 1][ii]);
             const float G = out ? 0.0f : u[ii] * m[ii];
             col += G;
             rows[ii] = sum_r(G * dj);
           }
           col = sum_kq(col);
           if (kq == 0) sm.col[it][j] = col;
-          if (r == 0) *reinterpret_cast<float4 *>(&sm.row[jt][i0]) = make_float4(rows[0], rows[1], rows[2], rows[3]);
+          if (r == 0) *reinterpret_cast<float4 *>(&sm.row[JB][i0]) = make_float4(rows[0], rows[1], rows[2], rows[3]);
         }
       }
-      const int pc = 16 * pt + 4 * kq;
-      float Dv[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dd4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (p.D) {
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii) Dv[ii] = p.D_per_channel ? p.D[h * kP + pc + ii] : p.D[h];
-      }
+      const float wj = sm.we[k][j];
+      float rs = 0.0f;
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
-        const int j = 16 * PR::jt(4 * a) + r;
-        const float wj = sm.we[k][j], dj = dt[j];
-        float xf[4], gf[4], o[4], rs = 0.0f;
-        four(&sm.x[tile_at<kP>(j, pc)], xf);
-        four(&sm.g[tile_at<kP>(j, pc)], gf);
+        const int pc = 32 * ph + 16 * a + 4 * kq;
+        float xv4[4], gv4[4], o[4], gx[4];
+        four(&sm.x[tile_at<kP>(j, pc)], xv4);
+        four(&sm.g[tile_at<kP>(j, pc)], gv4);
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii) {
           const float sv = st[a][ii] * wj;
-          rs = fmaf(xf[ii], sv, rs);
-          dd4[ii] = fmaf(gf[ii], xf[ii], dd4[ii]);
-          o[ii] = fmaf(dj, pr[a][ii] + sv, Dv[ii] * gf[ii]);
+          rs = fmaf(xv4[ii], sv, rs);
+          o[ii] = dj * (pr[a][ii] + sv);
         }
-        rs = sum_kq(rs);
-        if (kq == 0) sm.r[pt][j] = rs;
+        if (p.D) {   // and these tokens' part of each channel's dD
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii) {
+            o[ii] = fmaf(p.D_per_channel ? p.D[h * kP + pc + ii] : p.D[h], gv4[ii], o[ii]);
+            gx[ii] = sum_r(gv4[ii] * xv4[ii]);
+          }
+          if (r == 0) *reinterpret_cast<float4 *>(&sm.dd[JB][pc]) = make_float4(gx[0], gx[1], gx[2], gx[3]);
+        }
         if (j < len)
           *reinterpret_cast<uint2 *>(p.dx + (t0 + j) * p.dxs + h * kP + pc) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
       }
-      if (p.D) {   // these tokens' part of each channel's sum
-#pragma unroll
-        for (int ii = 0; ii < 4; ++ii) dd4[ii] = sum_r(dd4[ii]);
-        if (r == 0) *reinterpret_cast<float4 *>(&sm.dd[decltype(hc)::value][pc]) = make_float4(dd4[0], dd4[1], dd4[2], dd4[3]);
-      }
-    };
-    if (half == 0) pairs_and_dx(std::integral_constant<int, 0>{});
-    else pairs_and_dx(std::integral_constant<int, 1>{});
+      rs = sum_kq(rs);
+      if (kq == 0) sm.r[ph][j] = rs;
+    });
 
     // ---- H^T g and dH^T x: lane holds (n = 16 nt + 4 kq + ii, token = 16 ti + r)
     __builtin_amdgcn_sched_barrier(0);
@@ -576,7 +575,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     // ---- add up the head's partial sums (read before the next barrier, after
     // which the next head writes its own)
     if (w == (k & 7)) {
-      const float rs = (sm.r[0][l] + sm.r[1][l]) + (sm.r[2][l] + sm.r[3][l]);
+      const float rs = sm.r[0][l] + sm.r[1][l];
       const float direct = (sm.col[0][l] + sm.col[1][l]) + (sm.col[2][l] + sm.col[3][l]) + rs;
       float into = (sm.row[0][l] + sm.row[1][l]) + (sm.row[2][l] + sm.row[3][l]);
 #pragma unroll
@@ -584,7 +583,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       sm.rs[k][l] = rs;
       sm.direct[k][l] = direct;
       sm.into[k][l] = into;
-      if (p.D) sm.ddc[k][l] = sm.dd[0][l] + sm.dd[1][l];
+      if (p.D) sm.ddc[k][l] = (sm.dd[0][l] + sm.dd[1][l]) + (sm.dd[2][l] + sm.dd[3][l]);
       if (l == 0) {
         float hh = 0.0f;
 #pragma unroll
@@ -634,22 +633,20 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   *reinterpret_cast<uint4 *>(Vh + 8 * tid) = zero;
   *reinterpret_cast<uint4 *>(Vl + 8 * tid) = zero;
   __syncthreads();
-  auto put_V = [&](auto hc) {
-    using PR = Pairs<decltype(hc)::value>;
+  for_block([&](auto block) {
+    constexpr int JB = decltype(block)::value;
 #pragma unroll
-    for (int t = 0; t < 5; ++t) {
-      if (pt != (t & 3)) continue;
-      const f32x4 &v = V[t >> 2];
+    for (int it = JB; it < 4; ++it) {
+      if (ph != ((it + JB) & 1)) continue;
+      const f32x4 &v = V[(it - JB) >> 1];
       uint2 vh, vl;
       split_bf2(v[0], v[1], vh.x, vl.x);
       split_bf2(v[2], v[3], vh.y, vl.y);
-      const int o = tile_at<kQ>(16 * PR::jt(t) + r, 16 * PR::it(t) + 4 * kq);
+      const int o = tile_at<kQ>(16 * JB + r, 16 * it + 4 * kq);
       *reinterpret_cast<uint2 *>(&Vh[o]) = vh;
       *reinterpret_cast<uint2 *>(&Vl[o]) = vl;
     }
-  };
-  if (half == 0) put_V(std::integral_constant<int, 0>{});
-  else put_V(std::integral_constant<int, 1>{});
+  });
   __syncthreads();
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) {
