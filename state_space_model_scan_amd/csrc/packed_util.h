@@ -135,7 +135,7 @@ __device__ __forceinline__ float sum_kq(float v) {
 // sum over the sixteen r lanes of a row kq: rotations of the row
 template <int N>
 __device__ __forceinline__ float row_rotate(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xf, 0xf, false));
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x120 + N, 0xf, 0xf, true));
 }
 __device__ __forceinline__ float sum_r(float v) {
   v += row_rotate<8>(v);

@@ -241,6 +241,7 @@ struct ChunkLds {
   float ch[kMaxHeads][kQ], cl[kMaxHeads][kQ], dt[kMaxHeads][kQ], e0[kMaxHeads][kQ], eb[kMaxHeads][kQ], we[kMaxHeads][kQ];
   // one head's partial sums, and what the heads' steps need of them
   float row[4][kQ], col[4][kQ], q[N / 16][kQ], r[2][kQ], dd[4][kP], hh[8];
+  float D[kMaxHeads][kP];   // (a load of D among the products would wait for the next head's tiles)
   float direct[kMaxHeads][kQ], into[kMaxHeads][kQ], rs[kMaxHeads][kQ], ddc[kMaxHeads][kP], hhs[kMaxHeads];
 };
 
@@ -306,8 +307,13 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   float sc = 0.0f;
   auto load_head = [&](int64_t h) {
     const int t = tid >> 3, p0 = (tid & 7) * 8;
-    xv = t < len ? ld8_raw(p.x + (t0 + t) * p.xs + h * kP + p0) : zero;
-    gv = t < len ? ld8_raw(p.g + (t0 + t) * p.gs + h * kP + p0) : zero;
+    // (not a choice between two values: with `zero` in memory the compiler
+    // chose between two addresses and loaded single words)
+    xv = gv = make_uint4(0, 0, 0, 0);
+    if (t < len) {
+      xv = ld8_raw(p.x + (t0 + t) * p.xs + h * kP + p0);
+      gv = ld8_raw(p.g + (t0 + t) * p.gs + h * kP + p0);
+    }
     if (tid < HPIECES) {
       hv = *reinterpret_cast<const uint4 *>(p.codes + entry * p.code_entry + h * p.code_head + 16 * tid);
       sc = p.scales[entry * p.scale_entry + h * p.scale_head + 16 * tid / N];
@@ -344,6 +350,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     sm.dt[k][l] = d;
     sm.e0[k][l] = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
     sm.eb[k][l] = exp_diff(cs.hi, cs.lo, __shfl(cs.hi, l & 48), __shfl(cs.lo, l & 48));
+    if (p.D) sm.D[k][l] = p.D_per_channel ? p.D[h * kP + l] : p.D[h];
     sm.we[k][l] = exp_diff(__shfl(cs.hi, 63), __shfl(cs.lo, 63), cs.hi, cs.lo);
   }
   if (tid < kQ) {   // no pair tile above the diagonal adds to these
@@ -495,7 +502,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
         }
       }
       const float wj = sm.we[k][j];
-      float rs = 0.0f;
+      float rs = 0.0f, gxs = 0.0f;
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         const int pc = 32 * ph + 16 * a + 4 * kq;
@@ -508,19 +515,38 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
           rs = fmaf(xv4[ii], sv, rs);
           o[ii] = dj * (pr[a][ii] + sv);
         }
-        if (p.D) {   // and these tokens' part of each channel's dD
+        if (p.D) {
+          const float4 D4 = *reinterpret_cast<const float4 *>(&sm.D[k][pc]);
+          o[0] = fmaf(D4.x, gv4[0], o[0]);
+          o[1] = fmaf(D4.y, gv4[1], o[1]);
+          o[2] = fmaf(D4.z, gv4[2], o[2]);
+          o[3] = fmaf(D4.w, gv4[3], o[3]);
+        }
+        // and these tokens' part of dD: of each channel's, or of the head's
+        if (p.D_per_channel) {
 #pragma unroll
           for (int ii = 0; ii < 4; ++ii) {
-            o[ii] = fmaf(p.D_per_channel ? p.D[h * kP + pc + ii] : p.D[h], gv4[ii], o[ii]);
             gx[ii] = sum_r(gv4[ii] * xv4[ii]);
           }
           if (r == 0) *reinterpret_cast<float4 *>(&sm.dd[JB][pc]) = make_float4(gx[0], gx[1], gx[2], gx[3]);
+        } else if (p.D) {
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii) {
+            gxs = fmaf(gv4[ii], xv4[ii], gxs);
+          }
         }
         if (j < len)
           *reinterpret_cast<uint2 *>(p.dx + (t0 + j) * p.dxs + h * kP + pc) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
       }
       rs = sum_kq(rs);
       if (kq == 0) sm.r[ph][j] = rs;
+      if (p.D && !p.D_per_channel) {   // (sixteen token sums of each channel half, in the places of 32 channels)
+        gxs = sum_kq(gxs);
+        if (kq == 0) {
+          sm.dd[JB][32 * ph + r] = gxs;
+          sm.dd[JB][32 * ph + 16 + r] = 0.0f;
+        }
+      }
     });
 
     // ---- H^T g and dH^T x: lane holds (n = 16 nt + 4 kq + ii, token = 16 ti + r)
@@ -859,7 +885,7 @@ extern "C" int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *a, void *stream_ptr) 
   p.seg_chunks = pl.seg_chunks; p.nseg = pl.nseg; p.entries = pl.entries;
   p.hb_heads = pl.hb_heads; p.hb_per_group = pl.hb_per_group;
   p.step = {f.dt_softplus, f.dt_limit, f.dt_min, f.dt_max};
-  p.D_per_channel = f.D_per_channel;
+  p.D_per_channel = f.D && f.D_per_channel;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   hipError_t e = f.dstate == 32 ? launch_bwd<32>(p, pl, stream)
                  : f.dstate == 64 ? launch_bwd<64>(p, pl, stream) : launch_bwd<128>(p, pl, stream);
