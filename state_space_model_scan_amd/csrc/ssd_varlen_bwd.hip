@@ -769,6 +769,25 @@ struct BwdPlan {
   size_t off_state, off_decay, off_bc, off_sum, off_dd, bytes;
 };
 
+// Time in us of the adjoint pass with segments of seg chunks.  Storing every
+// chunk's dH (32 KB at dstate 128, beside 24 KB read) goes at about 4 TB/s; a
+// workgroup's chain takes 2.2 us a chunk, or 1.6 where nothing is stored, in
+// the launch that finds the segments' ends.  Measured (us of the whole
+// backward, one segment / chosen): 8 x 2048 tokens x 80 heads 775 / 775 (1);
+// 1 x 2048 x 80 183 / 160 (6); 1 x 16384 x 16 669 / 241 (24); 1 x 16384 x 80
+// 1173 / 865 (10).
+double adjoint_us(int64_t blocks, int64_t nchunks, int64_t seg, int64_t dstate, int64_t cus) {
+  const int64_t G = (nchunks + seg - 1) / seg;
+  const double len = static_cast<double>(seg) + 0.8, state = static_cast<double>(kP) * dstate * sizeof(float);
+  const double store = static_cast<double>(blocks) * nchunks * (state + kP * kQ * 2 + 2.0 * dstate * kQ) / 4e6;
+  double t = rounds_us(blocks * G, len, 2.2, 2.2, 3, cus);
+  if (t < store) t = store;
+  if (G > 1)
+    t += rounds_us(blocks * (G - 1), len, 1.6, 1.6, 3, cus) + 5.0 +
+         blocks * state * (static_cast<double>(G) * (G - 1) / 2 / 1e7 + (G - 1) / 5e6);
+  return t;
+}
+
 BwdPlan bwd_plan(const ssd_varlen_args_t *a, int cus) {
   BwdPlan pl{};
   pl.entries = ssd_checkpoint_slots(a->total, a->nseq);
@@ -780,12 +799,16 @@ BwdPlan bwd_plan(const ssd_varlen_args_t *a, int cus) {
   if (a->seq_segments >= 1) {
     G = a->seq_segments;
   } else {
-    const int64_t full_rows = (pl.entries + nchunks - 1) / nchunks;
-    const int64_t busy = (full_rows < a->nseq ? full_rows : a->nseq) * a->nheads;
-    const int64_t want = 3LL * cus;
-    if (busy < want) G = (want + busy - 1) / busy;
-    if (G > nchunks / 2) G = nchunks / 2;
-    if (G < 1) G = 1;
+    const int64_t rows = (pl.entries + nchunks - 1) / nchunks;
+    const int64_t blocks = (rows < a->nseq ? rows : a->nseq) * a->nheads;
+    double best = 1e300;
+    for (int64_t k = 1; k <= 64 && (k == 1 || 2 * k <= nchunks); ++k) {
+      const double t = adjoint_us(blocks, nchunks, (nchunks + k - 1) / k, a->dstate, cus);
+      if (t < best) {
+        best = t;
+        G = k;
+      }
+    }
   }
   if (G > nchunks) G = nchunks;
   if (G > 65535) G = 65535;
