@@ -260,10 +260,11 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_bwd_kernel(const ConvVarP
     int64_t s = find_seq(p.cu, p.nseq, t0);
     int64_t end = p.cu[s + 1];
     int64_t pos = t0 - p.cu[s];
-    for (int64_t tb = t0; tb < walk + kW - 1; tb += kStep) {
-      Vec<IO, NV> xv[kStep], gv[kStep];
+    constexpr int STEP = NV == 1 ? 4 * kStep : kStep;   // single channels: as many bytes in flight
+    for (int64_t tb = t0; tb < walk + kW - 1; tb += STEP) {
+      Vec<IO, NV> xv[STEP], gv[STEP];
 #pragma unroll
-      for (int i = 0; i < kStep; ++i) {
+      for (int i = 0; i < STEP; ++i) {
         if (tb + i < walk) {
           xv[i].load(p.x, (tb + i) * p.xs + c0);
           gv[i].load(p.dout, (tb + i) * p.dos + c0);
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_bwd_kernel(const ConvVarP
         }
       }
 #pragma unroll
-      for (int i = 0; i < kStep; ++i) {
+      for (int i = 0; i < STEP; ++i) {
         const int64_t t = tb + i;
         if (t < walk) {
           while (t >= end && s + 1 < p.nseq) {

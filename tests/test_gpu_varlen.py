@@ -477,3 +477,102 @@ def test_captured_training_step():
             assert torch.equal(a, b)
         for a, b in zip(want, step()):
             assert torch.equal(a, b)
+
+
+def test_example_trains_and_serves():
+    log("[together] example")
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "mamba2_mixer.py")
+    spec = importlib.util.spec_from_file_location("mamba2_mixer", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    mixer = ex.Mixer()
+    losses = ex.train(mixer, steps=20)
+    assert losses[-1] < 0.7 * losses[0], losses
+    got, want = ex.serve(mixer)
+    # bf16 activations: the step's conv output is not rounded, its gate is inside; a few roundings of 2^-8
+    assert (got.float() - want.float()).norm() <= 8 * 2.0 ** -8 * want.float().norm()
+
+
+# ---- far offsets and broadcast inputs -------------------------------------
+
+def test_offsets_past_32_bits():
+    """Cache entries and tokens whose byte offsets pass 2^32 (and element
+    offsets 2^31): the last entry of a cache of 9 GB, rows 9 MB apart."""
+    log("[far] cache entry")
+    h, n, entries = 80, 128, 3400
+    state = torch.empty(entries, h, R.P, n, device="cuda")
+    assert state.numel() > 1 << 31
+    g = _gen(2)
+    t, cu = _scan_case(2, (70,), h, 1, n)
+    first = _randn(g, 1, h, R.P, n)
+    state[entries - 1] = first[0].cuda()
+    ref, mag, last, lastm, _ = R.scan_fwd(t, cu, first)
+    d, kw = _call(t)
+    out = binding.ssd_varlen_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], _ints(cu), 70, D=d["D"], dt_bias=d["dt_bias"],
+                                 ssm_state=state, cache_seqlens=_ints([9]), slots=_ints([entries - 1]), **kw)
+    R.close(out, ref, mag, bf, "out")
+    R.close(state[entries - 1:], last, lastm, f32, "state")
+    ch = h * R.P + 2 * n
+    xbc, dt = _randn(g, 1, ch, dtype=bf), _randn(g, 1, h, dtype=bf) - 3
+    w, A = _randn(g, ch, 4, scale=0.5), -1 - torch.rand(h, generator=g)
+    ring = torch.zeros(entries, ch, 4, dtype=bf, device="cuda")
+    ref, mag, _, state1, statem = _step_ref(xbc, dt, A, w, ring[-1:].cpu(), state[-1:].cpu(), [3], [0], torch.zeros(ch),
+                                            torch.zeros(h), None, None, True, None, 1, True)
+    out = binding.conv1d_ssd_update(xbc.cuda(), dt.cuda(), A.cuda(), w.cuda(), ring, state, _ints([3]), dt_softplus=True,
+                                    slots=_ints([entries - 1]))
+    R.close(out, ref, mag, bf, "step out", STEP)
+    R.close(state[entries - 1:], state1, statem, f32, "step state", STEP)
+    del state, ring
+    log("[far] tokens")
+    row, T = 1 << 22, 600
+    far = torch.zeros(T, row, dtype=bf, device="cuda")
+    assert far.numel() > 1 << 31
+    t, cu = _scan_case(4, (T,), 2, 1, 32)
+    d, kw = _call(t)
+    x = far[:, 8:8 + 128].view(T, 2, R.P)
+    x.copy_(d["x"])
+    ref, mag, *_ = R.scan_fwd(t, cu)
+    out = binding.ssd_varlen_fwd(x, d["dt"], d["A"], d["B"], d["C"], _ints(cu), T, D=d["D"], dt_bias=d["dt_bias"], **kw)
+    R.close(out, ref, mag, bf, "far x")
+    w = _randn(g, 128, 4)
+    ref, mag, _ = R.conv_fwd(t["x"].view(T, 128), w, None, cu, True)
+    got = binding.causal_conv1d_varlen_fwd(far[:, 8:8 + 128], w.cuda(), _ints(cu), activation="silu", out=far[:, 1024:1024 + 128])
+    R.close(got, ref, mag, bf, "far conv", R.SHORT)
+
+
+def test_broadcast_inputs():
+    """Inputs expanded over tokens, groups or heads: gradients of the expanded
+    tensors, as for dense ones."""
+    t, cu = _scan_case(4, (70, 3), 4, 2, 32)
+    t["B"], t["A"] = t["B"][:, :1].expand(-1, 2, -1), t["A"][:1].expand(4)
+    d, kw = _call(t)
+    codes = torch.zeros(binding.ssd_checkpoint_slots(73, 2), 4, R.P, 32, dtype=torch.int8, device="cuda")
+    scales = torch.ones(codes.shape[:3], device="cuda")
+    dout = _randn(_gen(1), 1, 4, R.P, dtype=bf).expand(73, -1, -1)
+    B, A = t["B"][:, :1].contiguous().cuda().expand(-1, 2, -1), t["A"][:1].contiguous().cuda().expand(4)
+    args = (d["x"], d["dt"], A, B, d["C"], _ints(cu), 70)
+    binding.ssd_varlen_fwd(*args, D=d["D"], dt_bias=d["dt_bias"], checkpoints=(codes, scales), **kw)
+    got = binding.ssd_varlen_bwd(*args, dout[:1].contiguous().cuda().expand(73, -1, -1), (codes, scales), D=d["D"],
+                                 dt_bias=d["dt_bias"], **kw)
+    ref = R.scan_bwd(t, cu, dout, codes.cpu(), scales.cpu())
+    for k in ("dx", "ddt", "dB", "dC"):
+        R.close(got[k], *ref[k], bf, k)
+    for k in ("dA", "dD", "ddt_bias"):
+        R.close(got[k], *ref[k], f32, k)
+
+
+def test_refused_on_the_gpu():
+    """What needs device tensors to be refused: outputs that are not writable in
+    place, and a workspace that is too small."""
+    t, cu = _scan_case(4, (200,), 2, 1, 32)
+    d, kw = _call(t)
+    args = (d["x"], d["dt"], d["A"], d["B"], d["C"], _ints(cu), 200)
+    with pytest.raises(ValueError, match="written in place"):
+        binding.ssd_varlen_fwd(*args, out=torch.empty(2, 200, R.P, dtype=bf, device="cuda").transpose(0, 1), **kw)
+    with pytest.raises(ValueError, match="status 5"):
+        binding.ssd_varlen_fwd(*args, seq_segments=2, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"), **kw)
+    with pytest.raises(ValueError, match="status 3"):
+        bad = torch.zeros(200, 1, 48, dtype=bf, device="cuda")
+        binding.ssd_varlen_fwd(d["x"], d["dt"], d["A"], bad, bad, _ints(cu), 200, **kw)
