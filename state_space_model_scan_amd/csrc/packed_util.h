@@ -62,7 +62,22 @@ __device__ __forceinline__ TwoSum running_sum(float d, float A) {
   add_lane<0x143, 0xc>(s);   // the first half's to the second
   return s;
 }
-// exp(a - b)
+// exp of an unevaluated sum, to the hardware exp2's own rounding: the rounding
+// of the product with log2 e, which an exponent of -10 makes ten times 2^-24,
+// is recovered with an fma.
+__device__ __forceinline__ float exp_sum(TwoSum s) {
+  constexpr float kLog2eLo = 1.9259630e-8f;   // log2 e - kLog2e
+  const float t = s.hi * kLog2e;
+  const float rest = fmaf(s.hi, kLog2e, -t) + fmaf(s.hi, kLog2eLo, s.lo * kLog2e);
+  const float e = fast_exp2(t);
+  return fmaf(e, rest * kLn2, e);
+}
+// a - b
+__device__ __forceinline__ TwoSum diff(TwoSum a, TwoSum b) {
+  const float t = a.hi - b.hi, v = t - a.hi;
+  return {t, ((a.hi - (t - v)) - (b.hi + v)) + (a.lo - b.lo)};
+}
+// exp(a - b), without that recovery
 __device__ __forceinline__ float exp_diff(float ah, float al, float bh, float bl) {
   return fast_exp2(((ah - bh) + (al - bl)) * kLog2e);
 }
@@ -172,15 +187,32 @@ struct TileLoad {
                     static_cast<uint32_t>(tile_at<ROW_LEN>(row, (piece % G) * 8) - row * ROW_LEN));
     }
   }
+  // In assembly, because the compiler cannot tell the two halves of a double
+  // buffer apart and waits for the loads at the first LDS read after them; the
+  // reader of the tile waits itself (loads_landed, then a barrier).  Such a
+  // load writes no register.  The compiler's own counted waits stay right:
+  // loads return in order, so an unknown one can only make them wait longer.
+  // The wait states are those a load needs after a vector instruction wrote its
+  // scalar address (five) or a scalar one m0 (one).
   __device__ __forceinline__ void fetch(uint16_t *tile, const uint16_t *from, int w) const {
+    const uint32_t lds = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint16_t *)tile));
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (w + 4 * i < ALL)
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void *)(reinterpret_cast<const char *>(from) + at[i]),
-            (__attribute__((address_space(3))) void *)(tile + (w + 4 * i) * 512), 16, 0, 0);
+        asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2"
+                     :
+                     : "s"(__builtin_amdgcn_readfirstlane(lds + (w + 4 * i) * 1024)), "v"(at[i]), "s"(from)
+                     : "m0", "memory");
   }
 };
+
+// This wave's part of the tiles is in LDS (every wave's after a barrier), and
+// what else it loaded is there.
+__device__ __forceinline__ void loads_landed() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0); the compiler counts on from here
+  asm volatile("" ::: "memory");
+}
 
 // A barrier for LDS alone: what is on its way from global memory stays so.
 __device__ __forceinline__ void lds_barrier() {

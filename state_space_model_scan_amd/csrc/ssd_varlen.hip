@@ -17,13 +17,13 @@
 // of a (sequence, head) follow each other.  So:
 // - a workgroup of four waves walks a head's chunks, and 79 KB of LDS let two
 //   run on a compute unit, each in its own phase (one workgroup of eight
-//   waves for two heads, which shares B and C, took 707 us where this takes
-//   650: 32768 tokens, 80 heads);
+//   waves for two heads, which shares B and C, took 707 us where this took
+//   650 and now takes 638: 32768 tokens, 80 heads);
 // - the next chunk's x and B go from global memory straight into the other
 //   half of a double buffer in LDS while this chunk is computed, its C as soon
-//   as this chunk's outputs are done (no registers, and the latency, about a
-//   third of a chunk's time before, is hidden), and its steps are summed at
-//   this chunk's end;
+//   as this chunk's outputs are done (no registers, and no wait but the one at
+//   the top of the chunk and z's), and its steps are summed at this chunk's
+//   end;
 // - tiles stay as they lie in memory, token by token, and are read across by
 //   the transposing LDS load, so nothing is rearranged on the way;
 // - three barriers a chunk: data there, M there, C done with.
@@ -139,17 +139,21 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
     if constexpr (FULL) lc.fetch(sm.C, Cb + c * kQ * p.cs, w);
   };
   // a chunk's raw steps, and what the chunk needs of them (wave 0)
-  auto raw_steps = [&](int64_t c) { return l < chunk_len(c) ? bf2f(dtb[(c * kQ + l) * p.dts]) : 0.0f; };
-  auto put_steps = [&](int64_t c, int b, float raw) {
+  auto raw_steps = [&](int64_t c) {   // (of the last token beyond the end; as loaded: a conversion would wait for it)
+    const int len = chunk_len(c);
+    return static_cast<uint32_t>(dtb[(c * kQ + (l < len ? l : len - 1)) * p.dts]);
+  };
+  auto put_steps = [&](int64_t c, int b, uint32_t raw) {
+    asm volatile("" : "+v"(raw));   // or it is converted, and waited for, where it is loaded
     float v;
-    const float d = chunk_step(p.step, raw, bias, l < chunk_len(c), v);
+    const float d = chunk_step(p.step, bf2f(static_cast<uint16_t>(raw)), bias, l < chunk_len(c), v);
     const TwoSum cs = running_sum(d, Ah);
-    const float eh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cs.hi), 63));
-    const float el = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cs.lo), 63));
+    const TwoSum end = {__int_as_float(__builtin_amdgcn_readlane(__float_as_int(cs.hi), 63)),
+                        __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cs.lo), 63))};
     sm.cs[b][l] = cs.hi * kLog2e;
     sm.dt[b][l] = d;
-    sm.e[b][l] = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
-    sm.w[b][l] = exp_diff(eh, el, cs.hi, cs.lo) * d;
+    sm.e[b][l] = exp_sum(cs);
+    sm.w[b][l] = exp_sum(diff(end, cs)) * d;
   };
 
   // ---- state, transposed: wave w holds S[p = 16w + r][n = 32 kk + 8kq + 4a + i]
@@ -209,9 +213,9 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
     const int len = chunk_len(c);
     // this wave's part of the chunk's tiles is there; after the barrier every
     // wave's, and the last chunk's readers are done
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    loads_landed();
     __syncthreads();
-    float raw = 0.0f;
+    uint32_t raw = 0;
     const bool more = c + 1 < c_end;
     if (w == 0 && more) raw = raw_steps(c + 1);
     uint2 zv[4] = {};
@@ -342,6 +346,9 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
               const int o = (kq < 2 ? m_tile(tb, 2 * kk) : m_tile(tb, 2 * kk + 1)) * kTile + m_at(r, 8 * (kq & 1));
               acc[tb] = mfma(xt[kk], ld8(&sm.M[part][o]), acc[tb]);
             }
+      // z, asked for before the next tiles, is there with them; left to the
+      // compiler this wait comes behind C's loads, which it would wait for too
+      loads_landed();
       // ---- out = (Y + D x) * silu(z), four channels of a token
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {

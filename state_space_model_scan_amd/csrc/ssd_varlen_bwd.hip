@@ -111,12 +111,16 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
     lg.fetch(sm.g[b], gb + c * kQ * p.gs, w);
     lc.fetch(sm.C[b], Cb + c * kQ * p.cs, w);
   };
-  auto raw_steps = [&](int64_t c) { return l < chunk_len(c) ? bf2f(dtb[(c * kQ + l) * p.dts]) : 0.0f; };
+  auto raw_steps = [&](int64_t c) {   // (of the last token beyond the end; as loaded: a conversion would wait for it)
+    const int len = chunk_len(c);
+    return static_cast<uint32_t>(dtb[(c * kQ + (l < len ? l : len - 1)) * p.dts]);
+  };
   // tokens beyond the chunk's end repeat its last one and weigh nothing
-  auto put_steps = [&](int64_t c, int b, float raw) {
+  auto put_steps = [&](int64_t c, int b, uint32_t raw) {
+    asm volatile("" : "+v"(raw));   // or it is converted, and waited for, where it is loaded
     float v;
-    const TwoSum cs = running_sum(chunk_step(p.step, raw, bias, l < chunk_len(c), v), Ah);
-    const float e = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
+    const TwoSum cs = running_sum(chunk_step(p.step, bf2f(static_cast<uint16_t>(raw)), bias, l < chunk_len(c), v), Ah);
+    const float e = exp_sum(cs);
     sm.e[b][l] = l < chunk_len(c) ? e : 0.0f;
     if (l == 63) sm.end[b] = e;
   };
@@ -158,10 +162,10 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
   float decay = 1.0f;
   for (int64_t c = c_end - 1; c >= c_begin; --c) {
     const int b = static_cast<int>((c_end - 1 - c) & 1);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    loads_landed();
     __syncthreads();   // the chunk's tiles are there; the other half's readers are done
     const bool more = c > c_begin;
-    float raw = 0.0f;
+    uint32_t raw = 0;
     if (w == 0 && more) raw = raw_steps(c - 1);
     if (more) fetch(c - 1, b ^ 1);
     if constexpr (STORE) {
@@ -348,10 +352,10 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     sm.ch[k][l] = cs.hi;
     sm.cl[k][l] = cs.lo;
     sm.dt[k][l] = d;
-    sm.e0[k][l] = exp_diff(cs.hi, cs.lo, 0.0f, 0.0f);
-    sm.eb[k][l] = exp_diff(cs.hi, cs.lo, __shfl(cs.hi, l & 48), __shfl(cs.lo, l & 48));
+    sm.e0[k][l] = exp_sum(cs);
+    sm.eb[k][l] = exp_sum(diff(cs, {__shfl(cs.hi, l & 48), __shfl(cs.lo, l & 48)}));
     if (p.D) sm.D[k][l] = p.D_per_channel ? p.D[h * kP + l] : p.D[h];
-    sm.we[k][l] = exp_diff(__shfl(cs.hi, 63), __shfl(cs.lo, 63), cs.hi, cs.lo);
+    sm.we[k][l] = exp_sum(diff({__shfl(cs.hi, 63), __shfl(cs.lo, 63)}, cs));
   }
   if (tid < kQ) {   // no pair tile above the diagonal adds to these
     for (int k = 0; k < 4; ++k) sm.row[k][tid] = sm.col[k][tid] = 0.0f;
