@@ -5,10 +5,10 @@
 // element in 16 bits), the backward reads two and writes one.  A wave owns 64
 // runs of NV neighbouring channels (16 bytes each where the rows allow it, so
 // a token's load is one KiB) and walks a run of tokens with the last inputs in
-// registers.  The tokens before the run are read again: 3 of kFwdRun + 3.
+// registers.  The three tokens before a run are read again.
 // What a token may see is decided by wave-uniform scalars: its place in its
-// sequence, found once per run by a binary search of cu_seqlens and then
-// counted.  The run's loads are issued together before the first is used.
+// sequence, found once per run in cu_seqlens and then counted.  The run's loads
+// are issued together before the first is used.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -24,6 +24,8 @@ namespace {
 constexpr int kW = SSM_CONV_WIDTH;
 constexpr int kFwdRun = 12;        // tokens of a wave's run, forward
 constexpr int kBwdRun = 32;        // tokens of a wave's run, backward
+constexpr int kShortRun = 4;       // the same where the waves are few, forward
+constexpr int kShortBwdRun = 8;    // and backward
 constexpr int kBwdVec = 4;        // channels of a lane, backward, 16 bits
 constexpr int kStep = 4;           // tokens whose loads are in flight together, backward
 constexpr int kRows = 4;           // waves (runs) of a workgroup
@@ -61,14 +63,10 @@ struct ConvVarParams {
 
 // The sequence of token t: the last s with cu[s] <= t (uniform).
 __device__ __forceinline__ int64_t find_seq(const int32_t *cu, int64_t nseq, int64_t t) {
-  int64_t lo = 0, hi = nseq;
-  while (hi - lo > 1) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (cu[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  return lo;
+  return wave_search(nseq, [&](int64_t s) { return cu[s] <= t; });
 }
+// Its first token (a negative one stands for 0).
+__device__ __forceinline__ int64_t first_of(const int32_t *cu, int64_t s) { return cu[s] < 0 ? 0 : cu[s]; }
 
 // The input `back` tokens before a sequence's first one, from its ring.
 template <int IO, int NV>
@@ -81,45 +79,97 @@ __device__ __forceinline__ void ring_input(const ConvVarParams &p, int64_t s, in
   for (int k = 0; k < NV; ++k) v[k] = there ? load_io<IO>(p.ring, at + k * p.ring_len) : 0.0f;
 }
 
+// The weights of the workgroup's 64 NV channels, through LDS: a lane's own NV
+// rows are 16 NV bytes apart from the next lane's, and read from memory they
+// cost a wave more of the L1's time than a run's inputs and outputs.  The row
+// of channel c is kept at place_of(c), which spreads the lanes' reads over the
+// banks.
+struct __attribute__((aligned(4))) Row {   // of weights, at any address of a float
+  float v[kW];
+};
 template <int NV>
-__device__ __forceinline__ void load_params(const ConvVarParams &p, int64_t c0, float (&w)[kW][NV], float (&b)[NV]) {
+struct Weights {
+  float4 w[NV > 1 ? 64 * NV : 1];
+  static __device__ __forceinline__ int place_of(int c) { return c ^ ((c / NV) & (NV - 1)); }
+  static __device__ __forceinline__ float4 row(const ConvVarParams &p, int64_t c) {
+    const Row r = reinterpret_cast<const Row *>(p.w)[c];
+    return make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
+  }
+  // (a barrier belongs between the two)
+  __device__ __forceinline__ void fill(const ConvVarParams &p, int64_t first) {
+    if constexpr (NV > 1) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const float *wr = p.w + (c0 + k) * kW;
+      for (int i = 0; i < NV / kRows; ++i) {
+        const int c = i * 64 * kRows + threadIdx.x;
+        if (first + c < p.channels) w[place_of(c)] = row(p, first + c);
+      }
+    }
+  }
+  __device__ __forceinline__ void take(const ConvVarParams &p, int64_t c0, int lane, float (&wr)[kW][NV], float (&b)[NV]) const {
 #pragma unroll
-    for (int j = 0; j < kW; ++j) w[j][k] = wr[j];
-    b[k] = p.bias ? p.bias[c0 + k] : 0.0f;
+    for (int k = 0; k < NV; ++k) {
+      const float4 v = NV > 1 ? w[place_of(lane * NV + k)] : row(p, c0 + k);
+      wr[0][k] = v.x; wr[1][k] = v.y; wr[2][k] = v.z; wr[3][k] = v.w;
+      b[k] = p.bias ? p.bias[c0 + k] : 0.0f;
+    }
+  }
+};
+
+// A sequence's last inputs into its ring.  The run with the sequence's first
+// token does it, which has read what the ring held before.
+template <int IO, int NV>
+__device__ __forceinline__ void keep_inputs(const ConvVarParams &p, int64_t s, int64_t first, int64_t end, int64_t c0) {
+  const int64_t slot = p.slots ? p.slots[s] : s;
+  if (end <= first || slot < 0 || slot >= p.nslots) return;
+  const int64_t seen = p.seen && p.seen[s] > 0 ? p.seen[s] : 0;
+#pragma unroll 1
+  for (int64_t t = end - first > p.ring_len ? end - p.ring_len : first; t < end; t += 4) {   // four loads in flight
+    Vec<IO, NV> v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t + i < end) v[i].load(p.x, (t + i) * p.xs + c0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t + i < end) {
+        const int64_t at = (slot * p.channels + c0) * p.ring_len +
+                           static_cast<uint64_t>(seen + t + i - first) % static_cast<uint32_t>(p.ring_len);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) store_one<IO>(p.ring, at + k * p.ring_len, v[i].get(k));
+      }
   }
 }
 
-template <int IO, int NV>
-__global__ void __launch_bounds__(64 * kRows) conv_var_fwd_kernel(const ConvVarParams p) {
+template <int IO, int NV, int RUN>
+__global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvVarParams p) {
   const int lane = threadIdx.x & 63;
   const int row = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRows + row) * kFwdRun;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRows + row) * RUN;
   const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * NV;
+  __shared__ Weights<NV> weights;
+  weights.fill(p, c0 - lane * NV);
+  int64_t s = t0 < p.total ? find_seq(p.cu, p.nseq, t0) : 0;
+  if constexpr (NV > 1) __syncthreads();
   if (t0 >= p.total || c0 >= p.channels) return;
-  const int n = static_cast<int>(p.total - t0 < kFwdRun ? p.total - t0 : kFwdRun);
+  const int n = static_cast<int>(p.total - t0 < RUN ? p.total - t0 : RUN);
 
-  Vec<IO, NV> in[kFwdRun + kW - 1];
+  Vec<IO, NV> in[RUN + kW - 1];
 #pragma unroll
-  for (int i = 0; i < kFwdRun + kW - 1; ++i) {
+  for (int i = 0; i < RUN + kW - 1; ++i) {
     const int64_t t = t0 + i - (kW - 1);
     if (t >= 0 && i < n + kW - 1) in[i].load(p.x, t * p.xs + c0);
     else in[i].zero();
   }
   float w[kW][NV], bias[NV];
-  load_params<NV>(p, c0, w, bias);
-  int64_t s = find_seq(p.cu, p.nseq, t0);
+  weights.take(p, c0, lane, w, bias);
   int64_t end = p.cu[s + 1];
-  int64_t pos = t0 - p.cu[s];
-  if (n == kFwdRun && pos >= kW - 1 && t0 + kFwdRun <= end) {
+  int64_t pos = t0 - first_of(p.cu, s);
+  if (n == RUN && pos >= kW - 1 && t0 + RUN <= end) {
     // the whole run and what it sees are inside one sequence: no branch
     // between the loads and their use (with the edge tests of every token in
     // between the compiler kept few loads in flight: 216 us where this takes
-    // 88 at 16384 x 5376 bf16)
+    // 88 at 16384 x 5376 bf16; 79 now)
 #pragma unroll
-    for (int i = 0; i < kFwdRun; ++i) {
+    for (int i = 0; i < RUN; ++i) {
       float acc[NV];
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
@@ -139,7 +189,7 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_fwd_kernel(const ConvVarP
     while (t0 + from >= end && s + 1 < p.nseq) {
       ++s;
       end = p.cu[s + 1];
-      pos = t0 + from - p.cu[s];
+      pos = t0 + from - first_of(p.cu, s);
     }
     const int to = (s + 1 < p.nseq && end - t0 < n) ? static_cast<int>(end - t0) : n;
     float win[kW - 1][NV];   // the last inputs, oldest first
@@ -155,6 +205,7 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_fwd_kernel(const ConvVarP
         ring_input<IO, NV>(p, s, back - static_cast<int>(pos), c0, h);
       }
     }
+    if (p.ring && pos == 0) keep_inputs<IO, NV>(p, s, t0 + from, end < p.total ? end : p.total, c0);
     // (the run's inputs once more, four tokens at a time: sharing the
     // registers above with this path doubled the kernel's)
 #pragma unroll 1
@@ -187,35 +238,6 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_fwd_kernel(const ConvVarP
   }
 }
 
-// The last inputs of every sequence into its ring (a launch of its own: the
-// forward's first tokens still read the ring's old entries).
-template <int IO>
-__global__ void __launch_bounds__(256) conv_var_ring_kernel(const ConvVarParams p) {
-  const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + threadIdx.x;
-  if (c >= p.channels) return;
-  for (int64_t s = blockIdx.x; s < p.nseq; s += gridDim.x) {
-    int64_t lo = p.cu[s], hi = p.cu[s + 1];
-    lo = lo < 0 ? 0 : lo;
-    hi = hi > p.total ? p.total : hi;
-    const int64_t slot = p.slots ? p.slots[s] : s;
-    if (hi <= lo || slot < 0 || slot >= p.nslots) continue;
-    int64_t seen = p.seen ? p.seen[s] : 0;
-    if (seen < 0) seen = 0;
-    const int64_t from = hi - lo > p.ring_len ? hi - p.ring_len : lo;
-    using Raw = typename std::conditional<IO != 0, uint16_t, uint32_t>::type;
-    const Raw *x = static_cast<const Raw *>(p.x) + c;
-    Raw *ring = static_cast<Raw *>(p.ring) + (slot * p.channels + c) * p.ring_len;
-    for (int64_t t = from; t < hi; t += 4) {   // four loads in flight
-      Raw v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = t + i < hi ? x[(t + i) * p.xs] : Raw(0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (t + i < hi) ring[static_cast<uint64_t>(seen + t + i - lo) % static_cast<uint32_t>(p.ring_len)] = v[i];
-    }
-  }
-}
-
 // Backward.  At token t the pre-activation is formed again from x, and
 // da_t = dout_t act'(pre_t) goes to the gradients of the inputs it saw: the
 // run's pending dx of tokens t-3..t are in registers, and token t-3's is
@@ -223,14 +245,18 @@ __global__ void __launch_bounds__(256) conv_var_ring_kernel(const ConvVarParams 
 // the run's last ones; their weight gradients belong to the next run.  The
 // weight and bias gradients of the workgroup's four runs meet in LDS and go
 // out as one row of partial sums.
-template <int IO, int NV>
+template <int IO, int NV, int RUN>
 __global__ void __launch_bounds__(64 * kRows) conv_var_bwd_kernel(const ConvVarParams p) {
   __shared__ float sum[kRows - 1][kW + 1][NV][64];
   const int lane = threadIdx.x & 63;
   const int row = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRows + row) * kBwdRun;
+  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kRows + row) * RUN;
   const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * NV;
   const bool live = c0 < p.channels;
+  __shared__ Weights<NV> weights;
+  weights.fill(p, c0 - lane * NV);
+  const int64_t of_first = t0 < p.total ? find_seq(p.cu, p.nseq, t0) : 0;
+  if constexpr (NV > 1) __syncthreads();
   float dw[kW + 1][NV];
 #pragma unroll
   for (int j = 0; j <= kW; ++j)
@@ -238,10 +264,10 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_bwd_kernel(const ConvVarP
     for (int k = 0; k < NV; ++k) dw[j][k] = 0.0f;
 
   if (live && t0 < p.total) {
-    const int64_t stop = t0 + kBwdRun < p.total ? t0 + kBwdRun : p.total;              // end of the run
+    const int64_t stop = t0 + RUN < p.total ? t0 + RUN : p.total;              // end of the run
     const int64_t walk = stop + kW - 1 < p.total ? stop + kW - 1 : p.total;            // and of the walk
     float w[kW][NV], bias[NV];
-    load_params<NV>(p, c0, w, bias);
+    weights.take(p, c0, lane, w, bias);
     // the last three inputs, oldest first, and the pending gradients
     float win[kW][NV], pend[kW][NV];
 #pragma unroll
@@ -257,7 +283,7 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_bwd_kernel(const ConvVarP
     for (int j = 0; j < kW; ++j)
 #pragma unroll
       for (int k = 0; k < NV; ++k) pend[j][k] = 0.0f;
-    int64_t s = find_seq(p.cu, p.nseq, t0);
+    int64_t s = of_first;
     int64_t end = p.cu[s + 1];
     int64_t pos = t0 - p.cu[s];
     constexpr int STEP = NV == 1 ? 4 * kStep : kStep;   // single channels: as many bytes in flight
@@ -362,8 +388,18 @@ __global__ void __launch_bounds__(256) conv_var_reduce_kernel(const float *part,
   const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane, cols = (kW + 1) * channels;
   double v = 0.0;
-  if (col < cols)
-    for (int64_t r = rows * q / 4; r < rows * (q + 1) / 4; ++r) v += part[r * cols + col];
+  if (col < cols) {
+    const int64_t to = rows * (q + 1) / 4;
+    int64_t r = rows * q / 4;
+    for (; r + 8 <= to; r += 8) {   // eight loads in flight
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = part[(r + i) * cols + col];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += f[i];
+    }
+    for (; r < to; ++r) v += part[r * cols + col];
+  }
   sum[q][lane] = v;
   __syncthreads();
   if (q == 0 && col < cols) {
@@ -383,12 +419,43 @@ ConvVarParams conv_params(const causal_conv1d_varlen_args_t *a) {
   return p;
 }
 
-int64_t bwd_blocks(int64_t total) { return (total + kRows * kBwdRun - 1) / (kRows * kBwdRun); }
+// Waves of a launch whose runs are `run` tokens long.
+int64_t run_waves(const causal_conv1d_varlen_args_t *a, int nv, int run) {
+  return (a->total + run - 1) / run * ((a->channels + 64 * nv - 1) / (64 * nv));
+}
+// A launch of few waves lasts as long as one of its runs with an edge, so runs
+// are short below eight long ones a compute unit.  Measured short / long (us),
+// forward: 500 x 1024 7.9 / 11.2, 3500 x 2304 15.4 / 16.9, and above the limit
+// 8192 x 2304 24.6 / 22.6, 16384 x 5376 94 / 79; backward: 500 x 1024 12.4 /
+// 24.7, 3500 x 2304 24.3 / 30.4, and above it 8192 x 2304 40.9 / 39.7, 16384 x
+// 5376 172 / 126.
+constexpr int kFewWaves = 8;
+int fwd_run(const causal_conv1d_varlen_args_t *a, int nv) {
+  return run_waves(a, nv, kFwdRun) < kFewWaves * static_cast<int64_t>(cu_count_cached()) ? kShortRun : kFwdRun;
+}
+int bwd_run(const causal_conv1d_varlen_args_t *a, int nv) {
+  return run_waves(a, nv, kBwdRun) < kFewWaves * static_cast<int64_t>(cu_count_cached()) ? kShortBwdRun : kBwdRun;
+}
+int64_t blocks_of(int64_t total, int run) { return (total + kRows * run - 1) / (kRows * run); }
 
 // 16-byte accesses need whole and aligned rows of them
 bool wide_rows(int32_t io, int64_t channels, const void *p, int64_t stride) {
   const int nv = io == SSM_F32 ? 4 : 8;
   return channels % nv == 0 && aligned16(p) && stride % nv == 0;
+}
+
+// launch(io, channels of a lane): VEC of 16 bits, 4 of 32, or single ones.
+template <int VEC, typename F>
+void by_type(int32_t io, bool wide, std::integral_constant<int, VEC>, F &&launch) {
+  using std::integral_constant;
+  const integral_constant<int, 1> one;
+  const integral_constant<int, VEC> vec;
+  const integral_constant<int, SSM_BF16> bf16;
+  const integral_constant<int, SSM_F16> f16;
+  const integral_constant<int, SSM_F32> f32;
+  if (io == SSM_BF16) wide ? launch(bf16, vec) : launch(bf16, one);
+  else if (io == SSM_F16) wide ? launch(f16, vec) : launch(f16, one);
+  else wide ? launch(f32, integral_constant<int, 4>{}) : launch(f32, one);
 }
 
 }  // namespace
@@ -406,34 +473,27 @@ extern "C" int causal_conv1d_varlen_fwd(const causal_conv1d_varlen_args_t *a, vo
   const bool wide = wide_rows(a->io_dtype, a->channels, a->x, a->x_stride) &&
                     wide_rows(a->io_dtype, a->channels, a->out, a->out_stride);
   const int nv = !wide ? 1 : a->io_dtype == SSM_F32 ? 4 : 8;
-  const int64_t gx = (a->total + kRows * kFwdRun - 1) / (kRows * kFwdRun);
-  const int64_t gy = (a->channels + 64 * nv - 1) / (64 * nv);
+  const int run = fwd_run(a, nv);
+  const int64_t gx = blocks_of(a->total, run), gy = (a->channels + 64 * nv - 1) / (64 * nv);
   if (gy > 65535) return SSM_ERR_SHAPE;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * kRows);
-  auto launch = [&](auto fn) { hipLaunchKernelGGL(fn, grid, block, 0, stream, p); };
-  if (a->io_dtype == SSM_BF16) wide ? launch(conv_var_fwd_kernel<1, 8>) : launch(conv_var_fwd_kernel<1, 1>);
-  else if (a->io_dtype == SSM_F16) wide ? launch(conv_var_fwd_kernel<2, 8>) : launch(conv_var_fwd_kernel<2, 1>);
-  else wide ? launch(conv_var_fwd_kernel<0, 4>) : launch(conv_var_fwd_kernel<0, 1>);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return hip_fail(e);
-  if (a->conv_state) {
-    const int64_t cy = (a->channels + 255) / 256;
-    if (cy > 65535) return SSM_ERR_SHAPE;
-    const dim3 rgrid(static_cast<unsigned>(a->nseq < 65536 ? a->nseq : 65536), static_cast<unsigned>(cy));
-    if (a->io_dtype == SSM_F32) hipLaunchKernelGGL(conv_var_ring_kernel<0>, rgrid, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL(conv_var_ring_kernel<1>, rgrid, dim3(256), 0, stream, p);
-    e = hipGetLastError();
-    if (e != hipSuccess) return hip_fail(e);
-  }
-  return SSM_OK;
+  auto launch = [&](auto io, auto vec) {
+    constexpr int IO = decltype(io)::value, NV = decltype(vec)::value;
+    const auto fn = run == kFwdRun ? conv_var_fwd_kernel<IO, NV, kFwdRun> : conv_var_fwd_kernel<IO, NV, kShortRun>;
+    hipLaunchKernelGGL(fn, grid, block, 0, stream, p);
+  };
+  by_type(a->io_dtype, wide, std::integral_constant<int, 8>{}, launch);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? SSM_OK : hip_fail(e);
 }
 
 extern "C" int causal_conv1d_varlen_bwd_workspace_size(const causal_conv1d_varlen_args_t *a, size_t *bytes) {
   const int st = causal_conv1d_varlen_bwd_validate(a);
   if (st != SSM_OK) return st;
   if (!bytes) return SSM_ERR_NULL;
-  *bytes = static_cast<size_t>(bwd_blocks(a->total)) * (kW + 1) * a->channels * sizeof(float);
+  // the shorter runs' partial sums, whichever the call's strides let it take
+  *bytes = static_cast<size_t>(blocks_of(a->total, bwd_run(a, kBwdVec))) * (kW + 1) * a->channels * sizeof(float);
   return SSM_OK;
 }
 
@@ -450,14 +510,17 @@ extern "C" int causal_conv1d_varlen_bwd(const causal_conv1d_varlen_args_t *a, vo
                     wide_rows(a->io_dtype, a->channels, a->dout, a->dout_stride) &&
                     wide_rows(a->io_dtype, a->channels, a->dx, a->dx_stride);
   const int nv = !wide ? 1 : a->io_dtype == SSM_F32 ? 4 : kBwdVec;
-  const int64_t gx = bwd_blocks(a->total), gy = (a->channels + 64 * nv - 1) / (64 * nv);
+  const int run = bwd_run(a, nv);
+  const int64_t gx = blocks_of(a->total, run), gy = (a->channels + 64 * nv - 1) / (64 * nv);
   if (gy > 65535) return SSM_ERR_SHAPE;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * kRows);
-  auto launch = [&](auto fn) { hipLaunchKernelGGL(fn, grid, block, 0, stream, p); };
-  if (a->io_dtype == SSM_BF16) wide ? launch(conv_var_bwd_kernel<1, kBwdVec>) : launch(conv_var_bwd_kernel<1, 1>);
-  else if (a->io_dtype == SSM_F16) wide ? launch(conv_var_bwd_kernel<2, kBwdVec>) : launch(conv_var_bwd_kernel<2, 1>);
-  else wide ? launch(conv_var_bwd_kernel<0, 4>) : launch(conv_var_bwd_kernel<0, 1>);
+  auto launch = [&](auto io, auto vec) {
+    constexpr int IO = decltype(io)::value, NV = decltype(vec)::value;
+    const auto fn = run == kBwdRun ? conv_var_bwd_kernel<IO, NV, kBwdRun> : conv_var_bwd_kernel<IO, NV, kShortBwdRun>;
+    hipLaunchKernelGGL(fn, grid, block, 0, stream, p);
+  };
+  by_type(a->io_dtype, wide, std::integral_constant<int, kBwdVec>{}, launch);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return hip_fail(e);
   const int64_t cols = (kW + 1) * a->channels;

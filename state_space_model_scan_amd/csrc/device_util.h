@@ -233,6 +233,23 @@ __device__ __forceinline__ float dot_bcast(float c, const float (&x)[N]) {
   return y;
 }
 
+// The last i in [0, n) with at_or_before(i), where that holds up to some i and
+// 0 stands for none.  All 64 lanes probe at once, so one round of loads finds
+// it among 64 and two among 4096; every lane has to be there.
+template <typename F>
+__device__ __forceinline__ int64_t wave_search(int64_t n, F &&at_or_before) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0;
+  while (n > 1) {
+    const int64_t step = (n + 63) >> 6, mine = lane * step;
+    const bool yes = mine < n && (lane == 0 || at_or_before(lo + mine));
+    const int64_t skip = (__popcll(__ballot(yes)) - 1) * step;
+    lo += skip;
+    n = n - skip < step ? n - skip : step;
+  }
+  return lo;
+}
+
 template <int... I, typename F>
 __device__ __forceinline__ void static_for(std::integer_sequence<int, I...>, F &&f) {
   (f(std::integral_constant<int, I>{}), ...);

@@ -90,6 +90,28 @@ def test_conv_bwd(io, channels, lens):
             R.close(got["dbias"], *ref["dbias"], f32, "dbias", R.SHORT)
 
 
+@pytest.mark.parametrize("io,channels", [(bf, 4096), (f32, 1003)])
+def test_conv_of_many_tokens(io, channels):
+    """As many tokens and channels as the longer runs are taken for, from and to
+    a ring; sequences that end inside a run, and ones shorter than it."""
+    lens = (3000, 1, 0, 701, 2, 899)
+    log(f"[conv many] {io} channels={channels}")
+    g, cu = _gen(channels), R.sequences(lens)
+    x, w, b = _randn(g, cu[-1], channels, dtype=io), _randn(g, channels, 4, scale=0.5), _randn(g, channels)
+    dout, ring, seen = _randn(g, cu[-1], channels, dtype=io), _randn(g, 6, channels, 5, dtype=io), [0, 7, 1, 2, 0, 3]
+    ref, mag, after = R.conv_fwd(x, w, b, cu, True, ring, seen, list(range(6)))
+    dring = ring.cuda()
+    out = binding.causal_conv1d_varlen_fwd(x.cuda(), w.cuda(), _ints(cu), bias=b.cuda(), activation="silu", conv_state=dring,
+                                           cache_seqlens=_ints(seen))
+    R.close(out, ref, mag, io, "out", R.SHORT)
+    assert torch.equal(dring.cpu().view(torch.uint8), after.view(torch.uint8)), "ring"
+    ref = R.conv_bwd(x, w, b, cu, dout, True)
+    got = binding.causal_conv1d_varlen_bwd(x.cuda(), w.cuda(), _ints(cu), dout.cuda(), bias=b.cuda(), activation="silu")
+    R.close(got["dx"], *ref["dx"], io, "dx", R.SHORT)
+    for k in ("dweight", "dbias"):   # 32 tokens in a row in 32 bits, four such runs, some 8 roundings of a term: below 2^-18
+        R.close(got[k], *ref[k], f32, k, 2 * R.SHORT)
+
+
 def test_conv_keeps_to_its_sequence():
     """Infinities and NaN of one sequence reach no other, forward or backward."""
     cu = [0, 4, 9, 15]
