@@ -277,12 +277,10 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
 
   // the entry's sequence: the last s whose first entry is at or before it
   const int64_t entry = blockIdx.x;
-  int lo = 0, hi = static_cast<int>(p.nseq);
-  while (hi - lo > 1) {
-    const int mid = lo + ((hi - lo) >> 1), at = p.cu[mid];
-    if (static_cast<int64_t>((at < 0 ? 0 : at) / kQ) + mid <= entry) lo = mid;
-    else hi = mid;
-  }
+  const int64_t lo = wave_search(p.nseq, [&](int64_t i) {
+    const int at = p.cu[i];
+    return (at < 0 ? 0 : at) / kQ + i <= entry;
+  });
   const Seq q = sequence(p.cu, p.total, p.max_seqlen, lo);
   const int64_t chunk = entry - q.entry;
   const int64_t hpg = p.per_group;
