@@ -169,10 +169,9 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
     if (w == 0 && more) raw = raw_steps(c - 1);
     if (more) fetch(c - 1, b ^ 1);
     if constexpr (STORE) {
-      // in the order (n / 32, (n / 4) % 4, (n / 16) % 2, n % 4) along a row,
-      // so that a lane's eight states of two tiles are 16 bytes and the four
-      // kq lanes of a row 64
-      uint16_t *dh = p.ws_dh + ((q.entry + c) * p.nheads + h) * 2 * kP * N + (16 * w + r) * N + 8 * kq;
+      // as the lanes hold it: a lane's eight states of two tiles are 16 bytes,
+      // and a wave's store one KiB in a row
+      uint16_t *dh = p.ws_dh + ((q.entry + c) * p.nheads + h) * 2 * kP * N + (16 * w * N + 8 * l);
 #pragma unroll
       for (int nt = 0; nt < NT; nt += 2) {
         uint4 hi, lo;
@@ -180,8 +179,8 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
         split_bf2(acc[nt][2], acc[nt][3], hi.y, lo.y);
         split_bf2(acc[nt + 1][0], acc[nt + 1][1], hi.z, lo.z);
         split_bf2(acc[nt + 1][2], acc[nt + 1][3], hi.w, lo.w);
-        *reinterpret_cast<uint4 *>(dh + 16 * nt) = hi;
-        *reinterpret_cast<uint4 *>(dh + kP * N + 16 * nt) = lo;
+        *reinterpret_cast<uint4 *>(dh + 256 * nt) = hi;
+        *reinterpret_cast<uint4 *>(dh + kP * N + 256 * nt) = lo;
       }
     }
     const float end = sm.end[b];
@@ -421,7 +420,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     for (int b = 0; b < BC; ++b) {
       const int piece = tid + 512 * b;
       if (piece < kP * G8) {   // out of adjoint_kernel's order
-        const int row = piece / G8, n0 = ((piece % G8) >> 2) * 32 + (piece & 3) * 4;
+        const int row = piece / (64 * KN) * 16 + (piece & 15), n0 = piece / 64 % KN * 32 + (piece >> 4 & 3) * 4;
         const int o0 = tile_at<N>(row, n0), o1 = tile_at<N>(row, n0 + 16);
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
