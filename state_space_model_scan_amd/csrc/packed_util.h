@@ -207,10 +207,14 @@ struct TileLoad {
 };
 
 // This wave's part of the tiles is in LDS (every wave's after a barrier), and
-// what else it loaded is there.
+// what else it loaded before its last LATER stores is there: loads and stores
+// are counted together and return in order, so stores that follow the loads
+// need not have ended.
+template <int LATER = 0>
 __device__ __forceinline__ void loads_landed() {
+  static_assert(LATER < 16, "the count's low bits");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0); the compiler counts on from here
+  __builtin_amdgcn_s_waitcnt(0x0f70 | LATER);   // vmcnt(LATER); the compiler counts on from here
   asm volatile("" ::: "memory");
 }
 

@@ -18,17 +18,21 @@
 // - a workgroup of four waves walks a head's chunks, and 79 KB of LDS let two
 //   run on a compute unit, each in its own phase (one workgroup of eight
 //   waves for two heads, which shares B and C, took 707 us where this took
-//   650 and now takes 638: 32768 tokens, 80 heads);
+//   650: 32768 tokens, 80 heads);
 // - the next chunk's x and B go from global memory straight into the other
 //   half of a double buffer in LDS while this chunk is computed, its C as soon
-//   as this chunk's outputs are done (no registers, and no wait but the one at
-//   the top of the chunk and z's), and its steps are summed at this chunk's
-//   end;
+//   as C has been read, before the outputs are stored, and its steps are summed
+//   at this chunk's end.  A wave waits for loads twice a chunk, and for stores
+//   not at all (with C behind the stores, and so waiting for them, 654 us);
+// - what the loop does is fixed by template values (gated or not, with or
+//   without the 8-bit states: 630 -> 601 us for the first, and a prompts' batch
+//   of 24 x 32 heads 53 -> 50 us for the second): a branch ends what the
+//   compiler may interleave;
 // - tiles stay as they lie in memory, token by token, and are read across by
 //   the transposing LDS load, so nothing is rearranged on the way;
-// - three barriers a chunk: data there, M there, C done with.
+// - three barriers a chunk: data there, M there, C done with.  Now 599 us.
 // With few (sequence, head) pairs the sequence is cut into segments; a first
-// launch finds their end states from zero (packed_scan_kernel<N, false>), and
+// launch finds their end states from zero (FULL false), and
 // the second starts every segment from the states carried over.
 #include <hip/hip_runtime.h>
 
@@ -88,7 +92,7 @@ __device__ __forceinline__ bf16x8 frag_states(int l, uint16_t *tile, int row0, i
   return __builtin_bit_cast(bf16x8, make_uint4(uu.x, uu.y, uv.x, uv.y));
 }
 
-template <int N, bool FULL>
+template <int N, bool FULL, bool GATED = false, bool KEEP = false>
 __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const ScanParams p) {
   constexpr int KN = N / 32;   // K steps over dstate
   constexpr int NT = N / 16;   // state tiles along dstate
@@ -110,43 +114,48 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
   if (slot >= p.cache_slots) slot = -1;
   const bool cached = p.cache && slot >= 0 && p.seen && p.seen[s] > 0;
 
-  const uint16_t *xb = p.x + q.first * p.xs + h * kP;
-  const uint16_t *zb = p.z ? p.z + q.first * p.zs + h * kP : nullptr;
-  const uint16_t *Bb = p.B + q.first * p.bs + g * N, *Cb = p.C + q.first * p.cs + g * N;
-  const uint16_t *dtb = p.dt + q.first * p.dts + h;
-  uint16_t *ob = p.out + q.first * p.os + h * kP;
+  // the segment's chunks and, from its first token, the tokens and the rows;
+  // what the loop counts and steps through is 32 bits or a pointer, for a
+  // wave's scalar instructions hold up its others
+  const int nchunks = static_cast<int>(c_end - c_begin), ntokens = static_cast<int>(q.len - c_begin * kQ);
+  const int64_t first = q.first + c_begin * kQ;
+  const uint16_t *xb = p.x + first * p.xs + h * kP;   // of the next tiles
+  const uint16_t *Bb = p.B + first * p.bs + g * N, *Cb = p.C + first * p.cs + g * N;
+  const uint16_t *dtb = p.dt + first * p.dts + h;
+  const uint16_t *zb = GATED ? p.z + first * p.zs + h * kP : nullptr;   // of this chunk
+  uint16_t *ob = p.out + first * p.os + h * kP;
   const float Ah = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.0f;
   float *state_ws = p.ws_state + static_cast<int64_t>(sh) * kP * N;   // segment k's at k * SH * kP * N
   const int srow = (16 * w + r) * N + (FULL ? 8 : 4) * kq;   // this lane's first state element in a (p, n) block
 
-  auto chunk_len = [&](int64_t c) { return static_cast<int>(q.len - c * kQ < kQ ? q.len - c * kQ : kQ); };
   TileLoad<kP> lx;
   TileLoad<N> lb, lc;
-  lx.place(p.xs, chunk_len(c_begin), w, l);
-  lb.place(p.bs, chunk_len(c_begin), w, l);
-  if constexpr (FULL) lc.place(p.cs, chunk_len(c_begin), w, l);
-  auto fetch = [&](int64_t c, int b) {
-    const int len = chunk_len(c);
-    if (len < kQ && c > c_begin) {   // the sequence's end
-      lx.place(p.xs, len, w, l);
-      lb.place(p.bs, len, w, l);
-      if constexpr (FULL) lc.place(p.cs, len, w, l);
-    }
-    lx.fetch(sm.x[b], xb + c * kQ * p.xs, w);
-    lb.fetch(sm.B[b], Bb + c * kQ * p.bs, w);
+  auto place = [&](int len) {
+    lx.place(p.xs, len, w, l);
+    lb.place(p.bs, len, w, l);
+    if constexpr (FULL) lc.place(p.cs, len, w, l);
   };
-  auto fetch_C = [&](int64_t c) {
-    if constexpr (FULL) lc.fetch(sm.C, Cb + c * kQ * p.cs, w);
+  place(ntokens < kQ ? ntokens : kQ);
+  auto fetch = [&](int b) {
+    lx.fetch(sm.x[b], xb, w);
+    lb.fetch(sm.B[b], Bb, w);
+    xb += kQ * p.xs;
+    Bb += kQ * p.bs;
+  };
+  auto fetch_C = [&] {
+    if constexpr (FULL) lc.fetch(sm.C, Cb, w);
+    Cb += kQ * p.cs;
   };
   // a chunk's raw steps, and what the chunk needs of them (wave 0)
-  auto raw_steps = [&](int64_t c) {   // (of the last token beyond the end; as loaded: a conversion would wait for it)
-    const int len = chunk_len(c);
-    return static_cast<uint32_t>(dtb[(c * kQ + (l < len ? l : len - 1)) * p.dts]);
+  auto raw_steps = [&](int len) {   // (of the last token beyond the end; as loaded: a conversion would wait for it)
+    const uint32_t raw = dtb[(l < len ? l : len - 1) * p.dts];
+    dtb += kQ * p.dts;
+    return raw;
   };
-  auto put_steps = [&](int64_t c, int b, uint32_t raw) {
+  auto put_steps = [&](int len, int b, uint32_t raw) {
     asm volatile("" : "+v"(raw));   // or it is converted, and waited for, where it is loaded
     float v;
-    const float d = chunk_step(p.step, bf2f(static_cast<uint16_t>(raw)), bias, l < chunk_len(c), v);
+    const float d = chunk_step(p.step, bf2f(static_cast<uint16_t>(raw)), bias, l < len, v);
     const TwoSum cs = running_sum(d, Ah);
     const TwoSum end = {__int_as_float(__builtin_amdgcn_readlane(__float_as_int(cs.hi), 63)),
                         __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cs.lo), 63))};
@@ -202,34 +211,47 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
   }
   float seg_decay = 1.0f;
 
-  if (c_begin < c_end) {
-    fetch(c_begin, 0);
-    fetch_C(c_begin);
-    if (w == 0) put_steps(c_begin, 0, raw_steps(c_begin));
+  // the entering states' 8-bit form, this lane's piece of it
+  int8_t *codes = nullptr;
+  float *scales = nullptr;
+  if constexpr (KEEP) {
+    const int64_t row = ((q.entry + c_begin) * p.nheads + h) * kP + 16 * w + r;
+    codes = p.codes + row * N + 8 * kq;
+    scales = p.scales + row;
   }
-  for (int64_t c = c_begin; c < c_end; ++c) {
-    const int b = static_cast<int>((c - c_begin) & 1);
-    const int64_t t0 = c * kQ;
-    const int len = chunk_len(c);
-    // this wave's part of the chunk's tiles is there; after the barrier every
-    // wave's, and the last chunk's readers are done
-    loads_landed();
-    __syncthreads();
+
+  if (nchunks > 0) {
+    const int len = ntokens < kQ ? ntokens : kQ;
+    fetch(0);
+    fetch_C();
+    if (w == 0) put_steps(len, 0, raw_steps(len));
+  }
+  loads_landed();
+  for (int c = 0, left = ntokens; c < nchunks; ++c, left -= kQ) {
+    const int b = c & 1;
+    const int len = left < kQ ? left : kQ, next = left - kQ < kQ ? left - kQ : kQ;
+    // every wave's part of the chunk's tiles is there, and the last chunk's
+    // readers are done
+    lds_barrier();
     uint32_t raw = 0;
-    const bool more = c + 1 < c_end;
-    if (w == 0 && more) raw = raw_steps(c + 1);
+    const bool more = c + 1 < nchunks;
+    if (w == 0 && more) raw = raw_steps(next);
     uint2 zv[4] = {};
-    if (FULL && zb) {
+    if constexpr (GATED) {
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb)
-        if (16 * tb + r < len) zv[tb] = *reinterpret_cast<const uint2 *>(zb + (t0 + 16 * tb + r) * p.zs + pc);
+        if (16 * tb + r < len) zv[tb] = *reinterpret_cast<const uint2 *>(zb + (16 * tb + r) * p.zs + pc);
+      zb += kQ * p.zs;
     }
-    if (more) fetch(c + 1, b ^ 1);
+    if (more) {
+      if (next < kQ) place(next);   // the sequence's end
+      fetch(b ^ 1);
+    }
     const float *cs = sm.cs[b], *dt = sm.dt[b], *e0 = sm.e[b], *we = sm.w[b];
     uint16_t *X = sm.x[b], *B = sm.B[b];
 
     if constexpr (FULL) {
-      if (p.codes) {
+      if constexpr (KEEP) {
         // the chunk's entering state in 8 bits: this lane holds 4 NT states of
         // row 16w + r, the row's others are 16, 32 and 48 lanes away
         uint32_t top = 0;
@@ -246,16 +268,17 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
         top = o > top ? o : top;
         float inv;
         const float scale = row_scale(top, inv);
-        const int64_t row = ((q.entry + c) * p.nheads + h) * kP + 16 * w + r;
 #pragma unroll
         for (int kk = 0; kk < KN; ++kk) {
           uint32_t word[2] = {0, 0};
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             word[i >> 2] |= (static_cast<uint32_t>(static_cast<int>(rintf(accs[2 * kk + (i >> 2)][i & 3] * inv))) & 0xffu) << (8 * (i & 3));
-          *reinterpret_cast<uint2 *>(p.codes + row * N + 32 * kk + 8 * kq) = make_uint2(word[0], word[1]);
+          *reinterpret_cast<uint2 *>(codes + 32 * kk) = make_uint2(word[0], word[1]);
         }
-        if (kq == 0) p.scales[row] = scale;
+        if (kq == 0) *scales = scale;
+        codes += p.nheads * kP * N;
+        scales += p.nheads * kP;
       }
 
       // ---- M, from G^T = B C^T: lane holds (t = 16 wt + r, tau = 16 tb + 4kq + i),
@@ -346,37 +369,47 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
               const int o = (kq < 2 ? m_tile(tb, 2 * kk) : m_tile(tb, 2 * kk + 1)) * kTile + m_at(r, 8 * (kq & 1));
               acc[tb] = mfma(xt[kk], ld8(&sm.M[part][o]), acc[tb]);
             }
-      // z, asked for before the next tiles, is there with them; left to the
-      // compiler this wait comes behind C's loads, which it would wait for too
+      // z and the next steps are there, and the next tiles (whose loads followed
+      // theirs); asked for behind C's loads, they would wait for those too
       loads_landed();
+      if (more) {
+        lds_barrier();   // C's readers are done
+        fetch_C();
+      }
       // ---- out = (Y + D x) * silu(z), four channels of a token
+      if (p.D) {
 #pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        const int t = 16 * tb + r;
-        float y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = acc[tb][i];
-        if (p.D) {
+        for (int tb = 0; tb < 4; ++tb) {
           float xv[4];
-          four(&X[tile_at<kP>(t, pc)], xv);
+          four(&X[tile_at<kP>(16 * tb + r, pc)], xv);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = fmaf(Dv[i], xv[i], y[i]);
+          for (int i = 0; i < 4; ++i) acc[tb][i] = fmaf(Dv[i], xv[i], acc[tb][i]);
         }
-        if (zb) {
+      }
+      if constexpr (GATED) {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
           const float zf[4] = {__uint_as_float(zv[tb].x << 16), __uint_as_float(zv[tb].x & 0xffff0000u),
                                __uint_as_float(zv[tb].y << 16), __uint_as_float(zv[tb].y & 0xffff0000u)};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] *= silu_f(zf[i]);
+          for (int i = 0; i < 4; ++i) acc[tb][i] *= silu_f(zf[i]);
         }
-        if (t < len)
-          *reinterpret_cast<uint2 *>(ob + (t0 + t) * p.os + pc) = make_uint2(pack_bf2(y[0], y[1]), pack_bf2(y[2], y[3]));
+      }
+      uint16_t *to = ob + r * p.os + pc;
+      ob += kQ * p.os;
+      auto put = [&](int tb) {
+        *reinterpret_cast<uint2 *>(to + 16 * tb * p.os) = make_uint2(pack_bf2(acc[tb][0], acc[tb][1]), pack_bf2(acc[tb][2], acc[tb][3]));
+      };
+      if (len == kQ) {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) put(tb);
+      } else {
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb)
+          if (16 * tb + r < len) put(tb);
       }
     }
 
-    if (FULL && more) {
-      lds_barrier();   // C's readers are done
-      fetch_C(c + 1);
-    }
     // ---- S^T <- exp(cs_end) S^T + B^T (X w), X w in three bf16 parts
     const float dec = e0[kQ - 1];
     if constexpr (!FULL) seg_decay *= dec;
@@ -409,7 +442,10 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) accs[nt] = mfma(bt[nt], f2, accs[nt]);
     }
-    if (w == 0 && more) put_steps(c + 1, b ^ 1, raw);
+    if (w == 0 && more) put_steps(next, b ^ 1, raw);
+    // C is there, whatever the four stores after it do (a chunk with one after
+    // it is whole)
+    loads_landed<FULL ? 4 : 0>();
   }
 
   float *end = nullptr;
@@ -428,11 +464,18 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
 
 using VarFn = void (*)(const ScanParams);
 
-VarFn var_fn(int64_t dstate, bool full) {
+template <int N>
+VarFn var_fn_n(bool full, bool gated, bool keep) {
+  if (!full) return packed_scan_kernel<N, false>;
+  if (keep) return gated ? packed_scan_kernel<N, true, true, true> : packed_scan_kernel<N, true, false, true>;
+  return gated ? packed_scan_kernel<N, true, true, false> : packed_scan_kernel<N, true, false, false>;
+}
+VarFn var_fn(int64_t dstate, bool full, const ScanParams &p) {
+  const bool gated = p.z != nullptr, keep = p.codes != nullptr;
   switch (dstate) {
-    case 32: return full ? packed_scan_kernel<32, true> : packed_scan_kernel<32, false>;
-    case 64: return full ? packed_scan_kernel<64, true> : packed_scan_kernel<64, false>;
-    default: return full ? packed_scan_kernel<128, true> : packed_scan_kernel<128, false>;
+    case 32: return var_fn_n<32>(full, gated, keep);
+    case 64: return var_fn_n<64>(full, gated, keep);
+    default: return var_fn_n<128>(full, gated, keep);
   }
 }
 
@@ -445,7 +488,7 @@ unsigned var_lds(int64_t dstate, bool full) {
 }
 
 hipError_t launch_var(int64_t dstate, bool full, dim3 grid, hipStream_t stream, const ScanParams &p) {
-  const VarFn fn = var_fn(dstate, full);
+  const VarFn fn = var_fn(dstate, full, p);
   const unsigned lds = var_lds(dstate, full);
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(fn), hipFuncAttributeMaxDynamicSharedMemorySize,
                                            static_cast<int>(lds));

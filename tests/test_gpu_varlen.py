@@ -213,6 +213,24 @@ def test_scan_continues_and_splits(segments):
     _check_scan(t, cu, "continued", first=first, segments=segments)
 
 
+@pytest.mark.parametrize("n", [32, 64, 128])
+@pytest.mark.parametrize("z", [False, True])
+@pytest.mark.parametrize("D", [None, "head"])
+def test_scan_serving(n, z, D):
+    """Without 8-bit states: to a cache, and with neither."""
+    t, cu = _scan_case(13 * n + z, (130, 0, 1, 64, 70), 3, 1, n, z=z, D=D)
+    log(f"[scan serving] n={n} z={z} D={D}")
+    ref, mag, last, lastm, _ = R.scan_fwd(t, cu)
+    d, kw = _call(t, strided=True)
+    args = (d["x"], d["dt"], d["A"], d["B"], d["C"], _ints(cu), 130)
+    state = torch.full((5, 3, R.P, n), float("nan"), device="cuda")
+    out = binding.ssd_varlen_fwd(*args, D=d["D"], z=d["z"], dt_bias=d["dt_bias"], ssm_state=state, **kw)
+    R.close(out, ref, mag, bf, "out")
+    full = [0, 2, 3, 4]   # the empty sequence's entry is compared in the test of continued ones
+    R.close(state[full], last[full], lastm[full], f32, "state")
+    assert torch.equal(binding.ssd_varlen_fwd(*args, D=d["D"], z=d["z"], dt_bias=d["dt_bias"], **kw), out)
+
+
 def test_scan_without_a_cache_entry():
     """An entry outside the cache: a fresh sequence, nothing written."""
     t, cu = _scan_case(5, (10, 20), 2, 1, 32)
