@@ -113,13 +113,16 @@ inline int split_first_segment(int64_t blocks, int64_t nck, int64_t units, doubl
 // Time in us of `blocks` workgroups of `chunks` chunks: a chunk takes t1 with
 // one workgroup on a compute unit and tn with `per` of them.  Workgroups that
 // all start together and run long keep in step and use the same units at the
-// same time: up to 12% more (86 chunks each in one round 6.3 us a chunk, 27 in
-// three rounds 5.5).
+// same time: up to 12% more (86 chunks each in one round took 6.3 us a chunk
+// where 27 in three rounds took 5.5).
 inline double rounds_us(int64_t blocks, double chunks, double t1, double tn, int64_t per, int64_t cus) {
   const int64_t slots = per * cus, rest = blocks % slots;
   if (blocks <= slots) tn *= 1.0 + 0.12 * (chunks < 64.0 ? chunks / 64.0 : 1.0);
   double t = static_cast<double>(blocks / slots) * chunks * tn;
-  if (rest > 0) t += chunks * (rest <= cus ? t1 : t1 + (tn - t1) * static_cast<double>(rest - cus) / (slots - cus));
+  if (rest > 0) {   // as long as on the unit with the most of them
+    const int64_t most = (rest + cus - 1) / cus;
+    t += chunks * (most == 1 ? t1 : t1 + (tn - t1) * static_cast<double>(most - 1) / (per - 1));
+  }
   return t;
 }
 

@@ -505,15 +505,15 @@ struct VarPlan {
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// The whole call with segments of seg chunks.  The chunk times (full pass 4.5
-// and 5.6 us, state pass 1.5 and 2.7) are those measured at dstate 128; a
+// The whole call with segments of seg chunks.  The chunk times (full pass 3.4
+// and 4.6 us, state pass 1.5 and 2.7) are those measured at dstate 128; a
 // smaller one changes their ratios little.  Each segment costs about 0.8
 // chunks to start, segment k reads the k end states before it (32 KB each, from
 // the caches mostly), and a second launch about 5 us.
 double split_us(int64_t blocks, int64_t nchunks, int64_t seg, int64_t dstate, int64_t cus) {
   const int64_t G = (nchunks + seg - 1) / seg;
   const double len = static_cast<double>(seg) + 0.8;
-  double t = rounds_us(blocks * G, len, 4.5, 5.6, 2, cus);
+  double t = rounds_us(blocks * G, len, 3.4, 4.6, 2, cus);
   if (G > 1) {
     const double block_bytes = static_cast<double>(blocks) * kP * dstate * sizeof(float);
     t += rounds_us(blocks * (G - 1), len, 1.5, 2.7, 3, cus) + 5.0 +
@@ -524,9 +524,9 @@ double split_us(int64_t blocks, int64_t nchunks, int64_t seg, int64_t dstate, in
 
 // Segments of the longest sequence; a shorter one has fewer.  The library's own
 // count is the one that split_us finds fastest.  Measured at dstate 128 (us,
-// chosen / best of a sweep): 1 x 32768 tokens x 80 heads 644 (19) / 644;
-// 4 x 2048 x 80 178 (1) / 164 (3); 8 x 2048 x 80 316 (2) / 316; 1 x 2048 x 80
-// 60 (6) / 60; 1 x 16384 x 16 109 (26) / 109.
+// chosen / best of a sweep): 1 x 32768 tokens x 80 heads 579 (19) / 579;
+// 4 x 2048 x 80 144 (3) / 144; 8 x 2048 x 80 256 (1) / 256; 1 x 2048 x 80
+// 53 (6) / 53; 1 x 16384 x 16 98 (32) / 96 (26).
 VarPlan var_plan(const ssd_varlen_args_t *a, int cus) {
   VarPlan pl{};
   int64_t nchunks = (a->max_seqlen + kQ - 1) / kQ;

@@ -774,9 +774,9 @@ struct BwdPlan {
 // chunk's dH (32 KB at dstate 128, beside 24 KB read) goes at about 4 TB/s; a
 // workgroup's chain takes 2.2 us a chunk, or 1.6 where nothing is stored, in
 // the launch that finds the segments' ends.  Measured (us of the whole
-// backward, one segment / chosen): 8 x 2048 tokens x 80 heads 775 / 775 (1);
-// 1 x 2048 x 80 183 / 160 (6); 1 x 16384 x 16 669 / 241 (24); 1 x 16384 x 80
-// 1173 / 865 (10).
+// backward, one segment / chosen): 8 x 2048 tokens x 80 heads 705 / 705 (1);
+// 1 x 2048 x 80 173 / 159 (6); 1 x 16384 x 16 598 / 234 (24); 1 x 16384 x 80
+// 1024 / 809 (10).
 double adjoint_us(int64_t blocks, int64_t nchunks, int64_t seg, int64_t dstate, int64_t cus) {
   const int64_t G = (nchunks + seg - 1) / seg;
   const double len = static_cast<double>(seg) + 0.8, state = static_cast<double>(kP) * dstate * sizeof(float);
