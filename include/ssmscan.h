@@ -633,7 +633,8 @@ int causal_conv1d_varlen_bwd_validate(const causal_conv1d_varlen_args_t *args);
 int causal_conv1d_varlen_bwd_workspace_size(const causal_conv1d_varlen_args_t *args, size_t *bytes);
 
 /* Arguments of ssd_varlen_fwd.  x, B, C, z and out must be 16-byte aligned,
- * their strides multiples of 8. */
+ * their strides multiples of 8; those of x, B, C and the backward's dout at
+ * most 2^24 elements. */
 typedef struct ssd_varlen_args {
   int64_t total, nseq, max_seqlen;              /* max_seqlen: at least the longest sequence */
   int64_t nheads, headdim, dstate, ngroups;

@@ -259,6 +259,9 @@ int conv_varlen_common(const causal_conv1d_varlen_args_t *a) {
 }
 
 // what the packed scan's forward and backward share
+// The longest stride with which a chunk's tokens are reached by 32-bit byte offsets.
+constexpr int64_t kFarRow = (int64_t{1} << 31) / (2 * SSD_CHUNK);
+
 int ssd_varlen_common(const ssd_varlen_args_t *a) {
   if (!a) return SSM_ERR_NULL;
   if (!positive(a->total) || !positive(a->nseq) || a->max_seqlen < 0 || !positive(a->nheads) ||
@@ -275,9 +278,7 @@ int ssd_varlen_common(const ssd_varlen_args_t *a) {
       !product_fits(a->total, a->C_stride, 1) || !product_fits(a->total, a->dt_stride, 1) ||
       !product_fits(a->total / SSD_CHUNK + a->nseq, hp, a->dstate))
     return SSM_ERR_SHAPE;
-  // a chunk's tokens are reached by 32-bit byte offsets
-  const int64_t far = (int64_t{1} << 31) / (2 * SSD_CHUNK);
-  if (a->x_stride > far || a->B_stride > far || a->C_stride > far) return SSM_ERR_SHAPE;
+  if (a->x_stride > kFarRow || a->B_stride > kFarRow || a->C_stride > kFarRow) return SSM_ERR_SHAPE;
   if (!flag_ok(a->D_per_channel) || !flag_ok(a->dt_softplus) || !flag_ok(a->dt_limit)) return SSM_ERR_UNSUPPORTED;
   if (a->dt_limit && !(a->dt_min <= a->dt_max)) return SSM_ERR_SHAPE;
   if (a->seq_segments < 0) return SSM_ERR_SHAPE;
@@ -350,6 +351,7 @@ extern "C" int ssd_varlen_bwd_validate(const ssd_varlen_bwd_args_t *a) {
       !product_fits(f.nheads, a->scale_head_stride > 0 ? a->scale_head_stride : 1, 1))
     return SSM_ERR_SHAPE;
   if ((a->code_entry_stride | a->code_head_stride) & 15) return SSM_ERR_UNSUPPORTED;
+  if (a->dout_stride > kFarRow) return SSM_ERR_SHAPE;
   if (a->dout_stride < hp || a->dx_stride < hp || a->ddt_stride < f.nheads || a->dB_stride < gn || a->dC_stride < gn ||
       !product_fits(f.total, a->dout_stride, 1) || !product_fits(f.total, a->dx_stride, 1) ||
       !product_fits(f.total, a->ddt_stride, 1) || !product_fits(f.total, a->dB_stride, 1) ||

@@ -126,6 +126,17 @@ def test_scan_bwd_refusals(kw, want):
     assert _st("ssd_varlen_bwd", _scan_bwd(**kw)) == want
 
 
+def test_rows_too_far_apart_for_32_bit_offsets_are_refused():
+    for key in ("x_stride", "B_stride", "C_stride"):
+        for make, name in ((_scan, "ssd_varlen_fwd"), (_scan_bwd, "ssd_varlen_bwd")):
+            for stride, want in ((1 << 24, _lib.SSM_OK), ((1 << 24) + 8, S)):
+                a = make()
+                setattr(a if name == "ssd_varlen_fwd" else a.fwd, key, stride)
+                assert _st(name, a) == want
+    assert _st("ssd_varlen_bwd", _scan_bwd(dout_stride=1 << 24)) == _lib.SSM_OK
+    assert _st("ssd_varlen_bwd", _scan_bwd(dout_stride=(1 << 24) + 8)) == S
+
+
 def test_scan_bwd_needs_gradients_of_what_is_given():
     for key, grad in (("D", "dD"), ("dt_bias", "ddt_bias")):
         a = _scan_bwd({key: FAKE})
