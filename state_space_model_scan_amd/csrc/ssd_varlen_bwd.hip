@@ -306,30 +306,36 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   const uint4 zero = make_uint4(0, 0, 0, 0);
   uint4 xv, gv, hv, dv[2][BC];
   float sc = 0.0f;
-  auto load_head = [&](int64_t h) {
-    const int t = tid >> 3, p0 = (tid & 7) * 8;
-    // (not a choice between two values: with `zero` in memory the compiler
-    // chose between two addresses and loaded single words)
-    xv = gv = make_uint4(0, 0, 0, 0);
-    if (t < len) {
-      xv = ld8_raw(p.x + (t0 + t) * p.xs + h * kP + p0);
-      gv = ld8_raw(p.g + (t0 + t) * p.gs + h * kP + p0);
-    }
+  // what is the same for the wave steps from head to head, what is the lane's stays
+  const int my_t = tid >> 3, my_p = (tid & 7) * 8, my_row = my_t < len ? my_t : len - 1;
+  const uint32_t x_at = static_cast<uint32_t>(my_row) * static_cast<uint32_t>(p.xs) + my_p;
+  const uint32_t g_at = static_cast<uint32_t>(my_row) * static_cast<uint32_t>(p.gs) + my_p;
+  const uint16_t *xh = p.x + t0 * p.xs + h0 * kP, *gh = p.g + t0 * p.gs + h0 * kP;
+  const int8_t *code_h = p.codes + entry * p.code_entry + h0 * p.code_head;
+  const float *scale_h = p.scales + entry * p.scale_entry + h0 * p.scale_head;
+  const uint16_t *dh_h = p.ws_dh + (entry * p.nheads + h0) * 2 * kP * N;
+  auto load_head = [&] {   // tokens beyond the chunk's end repeat the last one here
+    xv = ld8_raw(xh + x_at);
+    gv = ld8_raw(gh + g_at);
     if (tid < HPIECES) {
-      hv = *reinterpret_cast<const uint4 *>(p.codes + entry * p.code_entry + h * p.code_head + 16 * tid);
-      sc = p.scales[entry * p.scale_entry + h * p.scale_head + 16 * tid / N];
+      hv = *reinterpret_cast<const uint4 *>(code_h + 16 * tid);
+      sc = scale_h[16 * tid / N];
     }
-    const uint16_t *dh = p.ws_dh + (entry * p.nheads + h) * 2 * kP * N;
 #pragma unroll
     for (int k = 0; k < BC; ++k) {
       const int piece = tid + 512 * k;
       if (piece < kP * G8) {
-        dv[0][k] = ld8_raw(dh + 8 * piece);
-        dv[1][k] = ld8_raw(dh + kP * N + 8 * piece);
+        dv[0][k] = ld8_raw(dh_h + 8 * piece);
+        dv[1][k] = ld8_raw(dh_h + kP * N + 8 * piece);
       }
     }
+    xh += kP;
+    gh += kP;
+    code_h += p.code_head;
+    scale_h += p.scale_head;
+    dh_h += 2 * kP * N;
   };
-  load_head(h0);
+  load_head();
 
   // ---- B, C, and every head's steps
 #pragma unroll
@@ -385,8 +391,8 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     }
   });
 
-  for (int k = 0; k < nh; ++k) {
-    const int64_t h = h0 + k;
+  uint16_t *dx_h = p.dx + t0 * p.dxs + h0 * kP;
+  for (int k = 0; k < nh; ++k, dx_h += kP) {
     // the lane anew for every head: the tiles' addresses are then formed where
     // they are used; kept over the loop they would take the registers
     asm volatile("" : "+v"(l));
@@ -395,9 +401,9 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     const float *dt = sm.dt[k];
     // ---- stage the head (its tiles' last readers passed the barrier before)
     {
-      const int t = tid >> 3, p0 = (tid & 7) * 8;
-      *reinterpret_cast<uint4 *>(&sm.x[tile_at<kP>(t, p0)]) = xv;
-      *reinterpret_cast<uint4 *>(&sm.g[tile_at<kP>(t, p0)]) = gv;
+      if (my_t >= len) xv = gv = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4 *>(&sm.x[tile_at<kP>(my_t, my_p)]) = xv;
+      *reinterpret_cast<uint4 *>(&sm.g[tile_at<kP>(my_t, my_p)]) = gv;
     }
     if (tid < HPIECES) {
       // codes as unsigned bytes (code + 128), one conversion each
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       }
     }
     __syncthreads();
-    if (k + 1 < nh) load_head(h + 1);
+    if (k + 1 < nh) load_head();
 
     // ---- the pairs, and dx: pair tiles lie as (i = 16 it + 4 kq + ii,
     // j = 16 JB + r), dx as (p = 16 (2 ph + a) + 4 kq + ii, j = 16 JB + r)
@@ -503,11 +509,12 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
         }
       }
       const float wj = sm.we[k][j];
-      float rs = 0.0f, gxs = 0.0f;
+      float rs = 0.0f, gxs = 0.0f, dxv[2][4];
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
         const int pc = 32 * ph + 16 * a + 4 * kq;
-        float xv4[4], gv4[4], o[4], gx[4];
+        float xv4[4], gv4[4], gx[4];
+        float (&o)[4] = dxv[a];
         four(&sm.x[tile_at<kP>(j, pc)], xv4);
         four(&sm.g[tile_at<kP>(j, pc)], gv4);
 #pragma unroll
@@ -536,8 +543,12 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
             gxs = fmaf(gv4[ii], xv4[ii], gxs);
           }
         }
-        if (j < len)
-          *reinterpret_cast<uint2 *>(p.dx + (t0 + j) * p.dxs + h * kP + pc) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+      }
+      uint16_t *to = dx_h + j * p.dxs + 32 * ph + 4 * kq;
+      if (j < len) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+          *reinterpret_cast<uint2 *>(to + 16 * a) = make_uint2(pack_bf2(dxv[a][0], dxv[a][1]), pack_bf2(dxv[a][2], dxv[a][3]));
       }
       rs = sum_kq(rs);
       if (kq == 0) sm.r[ph][j] = rs;
@@ -849,10 +860,11 @@ hipError_t launch_bwd(const BwdParams &p, const BwdPlan &pl, hipStream_t stream)
   hipLaunchKernelGGL((adjoint_kernel<N, true>), dim3(sh, pl.nseg), dim3(256), 0, stream, p);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   const unsigned lds = sizeof(ChunkLds<N>);
-  e = hipFuncSetAttribute(reinterpret_cast<const void *>(&chunk_kernel<N>), hipFuncAttributeMaxDynamicSharedMemorySize,
+  const auto chunk = chunk_kernel<N>;
+  e = hipFuncSetAttribute(reinterpret_cast<const void *>(chunk), hipFuncAttributeMaxDynamicSharedMemorySize,
                           static_cast<int>(lds));
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(chunk_kernel<N>, dim3(static_cast<unsigned>(pl.entries), static_cast<unsigned>(p.ngroups * pl.hb_per_group)),
+  hipLaunchKernelGGL(chunk, dim3(static_cast<unsigned>(pl.entries), static_cast<unsigned>(p.ngroups * pl.hb_per_group)),
                      dim3(512), lds, stream, p);
   return hipGetLastError();
 }
