@@ -268,95 +268,173 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_bwd_kernel(const ConvVarP
     const int64_t walk = stop + kW - 1 < p.total ? stop + kW - 1 : p.total;            // and of the walk
     float w[kW][NV], bias[NV];
     weights.take(p, c0, lane, w, bias);
-    // the last three inputs, oldest first, and the pending gradients
-    float win[kW][NV], pend[kW][NV];
-#pragma unroll
-    for (int j = 0; j < kW - 1; ++j) {
-      const int64_t t = t0 - (kW - 1) + j;
-      Vec<IO, NV> v;
-      if (t >= 0) v.load(p.x, t * p.xs + c0);
-      else v.zero();
-#pragma unroll
-      for (int k = 0; k < NV; ++k) win[j][k] = v.get(k);
-    }
-#pragma unroll
-    for (int j = 0; j < kW; ++j)
-#pragma unroll
-      for (int k = 0; k < NV; ++k) pend[j][k] = 0.0f;
     int64_t s = of_first;
     int64_t end = p.cu[s + 1];
     int64_t pos = t0 - p.cu[s];
-    constexpr int STEP = NV == 1 ? 4 * kStep : kStep;   // single channels: as many bytes in flight
-    for (int64_t tb = t0; tb < walk + kW - 1; tb += STEP) {
-      Vec<IO, NV> xv[STEP], gv[STEP];
+    if (pos >= kW - 1 && walk - t0 == RUN + kW - 1 && walk <= end) {
+      // the run and all that it sees are inside one sequence.  Token i's input
+      // and pending gradient are in place i % 4, so nothing moves along and
+      // nothing is tested (16384 x 5376 bf16: 126 us where the general walk
+      // takes 131).  Single channels ask for the next four tokens before they
+      // compute four (16384 x 1003: 40 us for 58); several channels would need
+      // 144 registers for that, which leaves three waves a SIMD (144 us).
+      static_assert(kW == 4 && RUN % 8 == 0, "places, and blocks in pairs");
+      float in[4][NV], pend[4][NV];
+      Vec<IO, NV> x0[4], g0[4], x1[4], g1[4];
+      auto ask = [&](Vec<IO, NV> (&xv)[4], Vec<IO, NV> (&gv)[4], int i0) {
 #pragma unroll
-      for (int i = 0; i < STEP; ++i) {
-        if (tb + i < walk) {
-          xv[i].load(p.x, (tb + i) * p.xs + c0);
-          gv[i].load(p.dout, (tb + i) * p.dos + c0);
-        } else {
-          xv[i].zero();
-          gv[i].zero();
+        for (int q = 0; q < 4; ++q)
+          if (q < 3 || i0 < RUN) {
+            xv[q].load(p.x, (t0 + i0 + q) * p.xs + c0);
+            gv[q].load(p.dout, (t0 + i0 + q) * p.dos + c0);
+          }
+      };
+      // token i0 + q, which completes token i0 + q - 3
+      auto token = [&](const Vec<IO, NV> &x, const Vec<IO, NV> &g, int i0, auto place, auto own) {
+        constexpr int Q = decltype(place)::value;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          in[Q][k] = x.get(k);
+          float pre = bias[k];
+#pragma unroll
+          for (int back = 0; back < kW; ++back) pre = fmaf(w[kW - 1 - back][k], in[(Q - back) & 3][k], pre);
+          float da = g.get(k);
+          if (p.silu) {
+            const float sg = fast_rcp(1.0f + fast_exp2(-pre * kLog2e));
+            da *= fmaf(pre * sg, 1.0f - sg, sg);
+          }
+          pend[Q][k] = w[kW - 1][k] * da;
+#pragma unroll
+          for (int back = 1; back < kW; ++back) pend[(Q - back) & 3][k] = fmaf(w[kW - 1 - back][k], da, pend[(Q - back) & 3][k]);
+          if constexpr (decltype(own)::value) {
+#pragma unroll
+            for (int back = 0; back < kW; ++back) dw[kW - 1 - back][k] = fmaf(da, in[(Q - back) & 3][k], dw[kW - 1 - back][k]);
+            dw[kW][k] += da;
+          }
         }
+        if (Q == 3 || i0 > 0) put<IO, NV>(p.dx, (t0 + i0 + Q - 3) * p.dxs + c0, pend[(Q + 1) & 3]);
+      };
+      auto block = [&](const Vec<IO, NV> (&xv)[4], const Vec<IO, NV> (&gv)[4], int i0, auto own) {
+        static_for(std::make_integer_sequence<int, decltype(own)::value ? 4 : 3>{},
+                   [&](auto q) { token(xv[decltype(q)::value], gv[decltype(q)::value], i0, q, own); });
+      };
+#pragma unroll
+      for (int j = 0; j < kW - 1; ++j) {
+        x1[j].load(p.x, (t0 - (kW - 1) + j) * p.xs + c0);
+      }
+      if constexpr (NV == 1) ask(x0, g0, 0);
+#pragma unroll
+      for (int j = 0; j < kW - 1; ++j)
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          in[j + 1][k] = x1[j].get(k);
+          pend[j + 1][k] = 0.0f;   // of tokens before the run, which others complete
+        }
+      if constexpr (NV == 1) {
+#pragma unroll 1
+        for (int i = 0; i < RUN; i += 8) {
+          ask(x1, g1, i + 4);
+          block(x0, g0, i, std::true_type{});
+          ask(x0, g0, i + 8);
+          block(x1, g1, i + 4, std::true_type{});
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < RUN; i += 4) {
+          ask(x0, g0, i);
+          block(x0, g0, i, std::true_type{});
+        }
+        ask(x0, g0, RUN);
+      }
+      block(x0, g0, RUN, std::false_type{});
+    } else {
+      // the last three inputs, oldest first, and the pending gradients
+      float win[kW][NV], pend[kW][NV];
+#pragma unroll
+      for (int j = 0; j < kW - 1; ++j) {
+        const int64_t t = t0 - (kW - 1) + j;
+        Vec<IO, NV> v;
+        if (t >= 0) v.load(p.x, t * p.xs + c0);
+        else v.zero();
+#pragma unroll
+        for (int k = 0; k < NV; ++k) win[j][k] = v.get(k);
       }
 #pragma unroll
-      for (int i = 0; i < STEP; ++i) {
-        const int64_t t = tb + i;
-        if (t < walk) {
-          while (t >= end && s + 1 < p.nseq) {
-            ++s;
-            end = p.cu[s + 1];
-            pos = t - p.cu[s];
+      for (int j = 0; j < kW; ++j)
+#pragma unroll
+        for (int k = 0; k < NV; ++k) pend[j][k] = 0.0f;
+      constexpr int STEP = NV == 1 ? 4 * kStep : kStep;   // single channels: as many bytes in flight
+      for (int64_t tb = t0; tb < walk + kW - 1; tb += STEP) {
+        Vec<IO, NV> xv[STEP], gv[STEP];
+#pragma unroll
+        for (int i = 0; i < STEP; ++i) {
+          if (tb + i < walk) {
+            xv[i].load(p.x, (tb + i) * p.xs + c0);
+            gv[i].load(p.dout, (tb + i) * p.dos + c0);
+          } else {
+            xv[i].zero();
+            gv[i].zero();
           }
-          float da[NV];
-#pragma unroll
-          for (int k = 0; k < NV; ++k) {
-            win[kW - 1][k] = xv[i].get(k);
-            da[k] = fmaf(w[kW - 1][k], win[kW - 1][k], bias[k]);
-          }
-#pragma unroll
-          for (int back = 1; back < kW; ++back)
-            if (pos >= back) {
-#pragma unroll
-              for (int k = 0; k < NV; ++k) da[k] = fmaf(w[kW - 1 - back][k], win[kW - 1 - back][k], da[k]);
-            }
-#pragma unroll
-          for (int k = 0; k < NV; ++k) {
-            const float pre = da[k];
-            float d = gv[i].get(k);
-            if (p.silu) {
-              const float sg = fast_rcp(1.0f + fast_exp2(-pre * kLog2e));
-              d *= fmaf(pre * sg, 1.0f - sg, sg);
-            }
-            da[k] = d;
-          }
-          const bool mine = t < stop;
-#pragma unroll
-          for (int back = 0; back < kW; ++back)
-            if (pos >= back) {
-#pragma unroll
-              for (int k = 0; k < NV; ++k) {
-                pend[kW - 1 - back][k] = fmaf(w[kW - 1 - back][k], da[k], pend[kW - 1 - back][k]);
-                if (mine) dw[kW - 1 - back][k] = fmaf(da[k], win[kW - 1 - back][k], dw[kW - 1 - back][k]);
-              }
-            }
-          if (mine) {
-#pragma unroll
-            for (int k = 0; k < NV; ++k) dw[kW][k] += da[k];
-          }
-          ++pos;
         }
-        const int64_t done = t - (kW - 1);   // its gradient is complete
-        if (done >= t0 && done < stop) put<IO, NV>(p.dx, done * p.dxs + c0, pend[0]);
 #pragma unroll
-        for (int j = 0; j < kW - 1; ++j)
+        for (int i = 0; i < STEP; ++i) {
+          const int64_t t = tb + i;
+          if (t < walk) {
+            while (t >= end && s + 1 < p.nseq) {
+              ++s;
+              end = p.cu[s + 1];
+              pos = t - p.cu[s];
+            }
+            float da[NV];
 #pragma unroll
-          for (int k = 0; k < NV; ++k) {
-            pend[j][k] = pend[j + 1][k];
-            win[j][k] = win[j + 1][k];
+            for (int k = 0; k < NV; ++k) {
+              win[kW - 1][k] = xv[i].get(k);
+              da[k] = fmaf(w[kW - 1][k], win[kW - 1][k], bias[k]);
+            }
+#pragma unroll
+            for (int back = 1; back < kW; ++back)
+              if (pos >= back) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) da[k] = fmaf(w[kW - 1 - back][k], win[kW - 1 - back][k], da[k]);
+              }
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+              const float pre = da[k];
+              float d = gv[i].get(k);
+              if (p.silu) {
+                const float sg = fast_rcp(1.0f + fast_exp2(-pre * kLog2e));
+                d *= fmaf(pre * sg, 1.0f - sg, sg);
+              }
+              da[k] = d;
+            }
+            const bool mine = t < stop;
+#pragma unroll
+            for (int back = 0; back < kW; ++back)
+              if (pos >= back) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                  pend[kW - 1 - back][k] = fmaf(w[kW - 1 - back][k], da[k], pend[kW - 1 - back][k]);
+                  if (mine) dw[kW - 1 - back][k] = fmaf(da[k], win[kW - 1 - back][k], dw[kW - 1 - back][k]);
+                }
+              }
+            if (mine) {
+#pragma unroll
+              for (int k = 0; k < NV; ++k) dw[kW][k] += da[k];
+            }
+            ++pos;
           }
+          const int64_t done = t - (kW - 1);   // its gradient is complete
+          if (done >= t0 && done < stop) put<IO, NV>(p.dx, done * p.dxs + c0, pend[0]);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) pend[kW - 1][k] = 0.0f;
+          for (int j = 0; j < kW - 1; ++j)
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+              pend[j][k] = pend[j + 1][k];
+              win[j][k] = win[j + 1][k];
+            }
+#pragma unroll
+          for (int k = 0; k < NV; ++k) pend[kW - 1][k] = 0.0f;
+        }
       }
     }
   }
@@ -426,7 +504,7 @@ int64_t run_waves(const causal_conv1d_varlen_args_t *a, int nv, int run) {
 // A launch of few waves lasts as long as one of its runs with an edge, so runs
 // are short below eight long ones a compute unit.  Measured short / long (us),
 // forward: 500 x 1024 7.9 / 11.2, 3500 x 2304 15.4 / 16.9, and above the limit
-// 8192 x 2304 24.6 / 22.6, 16384 x 5376 94 / 79; backward: 500 x 1024 12.4 /
+// 8192 x 2304 24.6 / 22.6, 16384 x 5376 94 / 79; backward: 500 x 1024 12.5 /
 // 24.7, 3500 x 2304 24.3 / 30.4, and above it 8192 x 2304 40.9 / 39.7, 16384 x
 // 5376 172 / 126.
 constexpr int kFewWaves = 8;
