@@ -68,13 +68,21 @@ __device__ __forceinline__ int64_t find_seq(const int32_t *cu, int64_t nseq, int
 // Its first token (a negative one stands for 0).
 __device__ __forceinline__ int64_t first_of(const int32_t *cu, int64_t s) { return cu[s] < 0 ? 0 : cu[s]; }
 
+// Where a sequence's ring is, and how many tokens went before.
+struct RingOf {
+  int64_t slot;
+  int seen;
+};
+__device__ __forceinline__ RingOf ring_of(const ConvVarParams &p, int64_t s) {
+  if (!p.ring) return {-1, 0};
+  return {p.slots ? p.slots[s] : s, p.seen ? p.seen[s] : 0};
+}
 // The input `back` tokens before a sequence's first one, from its ring.
 template <int IO, int NV>
-__device__ __forceinline__ void ring_input(const ConvVarParams &p, int64_t s, int back, int64_t c0, float (&v)[NV]) {
-  const int pos = (p.ring && p.seen ? p.seen[s] : 0) - back;
-  const int64_t slot = p.slots ? p.slots[s] : s;
-  const bool there = pos >= 0 && slot >= 0 && slot < p.nslots;
-  const int64_t at = there ? (slot * p.channels + c0) * p.ring_len + static_cast<uint32_t>(pos) % static_cast<uint32_t>(p.ring_len) : 0;
+__device__ __forceinline__ void ring_input(const ConvVarParams &p, const RingOf &ring, int back, int64_t c0, float (&v)[NV]) {
+  const int pos = ring.seen - back;
+  const bool there = pos >= 0 && ring.slot >= 0 && ring.slot < p.nslots;
+  const int64_t at = there ? (ring.slot * p.channels + c0) * p.ring_len + static_cast<uint32_t>(pos) % static_cast<uint32_t>(p.ring_len) : 0;
 #pragma unroll
   for (int k = 0; k < NV; ++k) v[k] = there ? load_io<IO>(p.ring, at + k * p.ring_len) : 0.0f;
 }
@@ -118,10 +126,9 @@ struct Weights {
 // A sequence's last inputs into its ring.  The run with the sequence's first
 // token does it, which has read what the ring held before.
 template <int IO, int NV>
-__device__ __forceinline__ void keep_inputs(const ConvVarParams &p, int64_t s, int64_t first, int64_t end, int64_t c0) {
-  const int64_t slot = p.slots ? p.slots[s] : s;
+__device__ __forceinline__ void keep_inputs(const ConvVarParams &p, const RingOf &ring, int64_t first, int64_t end, int64_t c0) {
+  const int64_t slot = ring.slot, seen = ring.seen > 0 ? ring.seen : 0;
   if (end <= first || slot < 0 || slot >= p.nslots) return;
-  const int64_t seen = p.seen && p.seen[s] > 0 ? p.seen[s] : 0;
 #pragma unroll 1
   for (int64_t t = end - first > p.ring_len ? end - p.ring_len : first; t < end; t += 4) {   // four loads in flight
     Vec<IO, NV> v[4];
@@ -161,6 +168,7 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
   }
   float w[kW][NV], bias[NV];
   weights.take(p, c0, lane, w, bias);
+  RingOf ring = ring_of(p, s);   // (asked for with the two below, not behind them)
   int64_t end = p.cu[s + 1];
   int64_t pos = t0 - first_of(p.cu, s);
   if (n == RUN && pos >= kW - 1 && t0 + RUN <= end) {
@@ -190,6 +198,7 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
       ++s;
       end = p.cu[s + 1];
       pos = t0 + from - first_of(p.cu, s);
+      ring = ring_of(p, s);
     }
     const int to = (s + 1 < p.nseq && end - t0 < n) ? static_cast<int>(end - t0) : n;
     float win[kW - 1][NV];   // the last inputs, oldest first
@@ -202,10 +211,10 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
 #pragma unroll
         for (int k = 0; k < NV; ++k) h[k] = v.get(k);
       } else {
-        ring_input<IO, NV>(p, s, back - static_cast<int>(pos), c0, h);
+        ring_input<IO, NV>(p, ring, back - static_cast<int>(pos), c0, h);
       }
     }
-    if (p.ring && pos == 0) keep_inputs<IO, NV>(p, s, t0 + from, end < p.total ? end : p.total, c0);
+    if (p.ring && pos == 0) keep_inputs<IO, NV>(p, ring, t0 + from, end < p.total ? end : p.total, c0);
     // (the run's inputs once more, four tokens at a time: sharing the
     // registers above with this path doubled the kernel's)
 #pragma unroll 1
