@@ -159,6 +159,36 @@ __device__ __forceinline__ float sum_r(float v) {
   return v + row_rotate<1>(v);
 }
 __device__ __forceinline__ float sum_wave(float v) { return sum_kq(sum_r(v)); }
+// sum over the kq lanes of a column after this one
+__device__ __forceinline__ float sum_later_kq(float v, int kq) {
+  const uint32_t a = __float_as_uint(v);
+  const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);   // each pair of rows: the first, the second
+  const float second = __uint_as_float(x[1]);
+  const uint32_t b = __float_as_uint(__uint_as_float(x[0]) + second);
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return (kq & 1 ? 0.0f : second) + (kq < 2 ? __uint_as_float(y[1]) : 0.0f);
+}
+// sum over the lanes of a row of 16 from this one on
+__device__ __forceinline__ float row_suffix(float v) {
+  v += from_lane<0x101, 0xf>(v);
+  v += from_lane<0x102, 0xf>(v);
+  v += from_lane<0x104, 0xf>(v);
+  return v + from_lane<0x108, 0xf>(v);
+}
+// sum over the lanes before this one, in its row of 16 or in the wave
+template <int LANES>
+__device__ __forceinline__ float sums_before(float v) {
+  v = LANES == 16 ? from_lane<0x111, 0xf>(v) : from_lane<0x138, 0xf>(v);   // one lane on
+  v += from_lane<0x111, 0xf>(v);
+  v += from_lane<0x112, 0xf>(v);
+  v += from_lane<0x114, 0xf>(v);
+  v += from_lane<0x118, 0xf>(v);
+  if constexpr (LANES == 64) {
+    v += from_lane<0x142, 0xa>(v);
+    v += from_lane<0x143, 0xc>(v);
+  }
+  return v;
+}
 
 // four bf16 of one 8-byte piece
 __device__ __forceinline__ void four(const uint16_t *p, float (&v)[4]) {

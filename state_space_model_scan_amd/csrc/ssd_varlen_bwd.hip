@@ -13,9 +13,13 @@
 // and, for the steps, with G_ij = S_ij L_ij M_ij, q_i = e_i g_i . (H C_i) and
 // r_j = w_j x_j . (dH B_j):
 //   direct_j = sum_i G_ij + r_j
-//   dcs_i    = sum_j G_ij dt'_j + q_i - dt'_i direct_i,
-//   dcs_end += sum_j dt'_j r_j + exp(cs_end) <dH, H>
-//   da_t = sum_{k >= t} dcs_k,  ddt'_t = direct_t + A da_t,  dA = sum dt' da.
+//   da_t = sum_{i >= t > j} G_ij dt'_j + sum_{i >= t} q_i + sum_{j < t} dt'_j r_j + exp(cs_end) <dH, H>
+//   ddt'_t = direct_t + A da_t,  dA = sum dt' da.
+// da_t is the gradient of token t's decay exponent, and these are the paths
+// that pass it.  (As sums from t on of d cs, every path between two tokens at or
+// after t would be added at its end and taken off again at its start, a token's
+// way into its own output first of all: what their roundings leave is then the
+// whole of a gradient that has to vanish, as for a sequence of one token.)
 //
 // Three launches.  (1) adjoint_kernel walks every (sequence, head)'s chunks
 // backwards and leaves each chunk's dH, as a bf16 head and tail (16
@@ -252,7 +256,12 @@ struct ChunkLds {
   // one head's partial sums, and what the heads' steps need of them
   float row[4][kQ], col[4][kQ], q[N / 16][kQ], r[2][kQ], dd[4][kP], hh[8];
   float D[kMaxHeads][kP];   // (a load of D among the products would wait for the next head's tiles)
-  float direct[kMaxHeads][kQ], into[kMaxHeads][kQ], rs[kMaxHeads][kQ], ddc[kMaxHeads][kP], hhs[kMaxHeads];
+  // (a token's block is the 16-token one it is in.)  direct and r; the paths
+  // through the token: inside its block; and of those to the token, from the
+  // blocks before and the entering state, and from it to the blocks after
+  float direct[kMaxHeads][kQ], rs[kMaxHeads][kQ], inside[kMaxHeads][kQ], into[kMaxHeads][kQ], from[kMaxHeads][kQ];
+  float past[kMaxHeads][4];   // paths from before block k to after it
+  float ddc[kMaxHeads][kP], hhs[kMaxHeads];
 };
 
 // One workgroup of eight waves.  For a head, between two barriers:
@@ -508,8 +517,18 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
             V[t >> 1][ii] = fmaf(out ? 0.0f : m[ii] * L[ii], dj, V[t >> 1][ii]);
             const float G = out ? 0.0f : u[ii] * m[ii];
             col += G;
-            rows[ii] = sum_r(G * dj);
+            rows[ii] = G * dj;
           }
+          if (it == JB) {   // of row i, the pairs from before token i to it or after it
+            rows[2] += rows[3];
+            rows[1] += rows[2];
+            rows[0] += rows[1];
+            const float after = sum_later_kq(rows[0], kq);
+#pragma unroll
+            for (int ii = 0; ii < 4; ++ii) rows[ii] = r < 4 * kq + ii ? rows[ii] + after : 0.0f;
+          }
+#pragma unroll
+          for (int ii = 0; ii < 4; ++ii) rows[ii] = sum_r(rows[ii]);
           col = sum_kq(col);
           if (kq == 0) sm.col[it][j] = col;
           if (r == 0) *reinterpret_cast<float4 *>(&sm.row[JB][i0]) = make_float4(rows[0], rows[1], rows[2], rows[3]);
@@ -618,17 +637,34 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     }
     __syncthreads();
     // ---- add up the head's partial sums (read before the next barrier, after
-    // which the next head writes its own)
-    if (w == (k & 7)) {
+    // which the next head writes its own), each wave a part: by one wave alone
+    // they held up the others at that barrier (8 x 2048 tokens, 80 heads: 712 us
+    // for 684)
+    const int own = l >> 4, part = (w - k) & 7;
+    if (part == 0) {
       const float rs = sm.r[0][l] + sm.r[1][l];
-      const float direct = (sm.col[0][l] + sm.col[1][l]) + (sm.col[2][l] + sm.col[3][l]) + rs;
-      float into = (sm.row[0][l] + sm.row[1][l]) + (sm.row[2][l] + sm.row[3][l]);
+      float from = 0.0f;
+#pragma unroll
+      for (int it = 1; it < 4; ++it) from += it > own ? sm.col[it][l] : 0.0f;
+      sm.rs[k][l] = rs;
+      sm.direct[k][l] = from + sm.col[own][l] + rs;
+      sm.inside[k][l] = sm.row[own][l];
+      sm.from[k][l] = from;
+    } else if (part < 5) {
+      // to this token from before block part - 1 (at most its own)
+      const int b = part - 1;
+      float into = 0.0f;
 #pragma unroll
       for (int a = 0; a < NT; ++a) into += sm.q[a][l];
-      sm.rs[k][l] = rs;
-      sm.direct[k][l] = direct;
-      sm.into[k][l] = into;
+#pragma unroll
+      for (int a = 0; a < 3; ++a)
+        if (a < b) into += own > a ? sm.row[a][l] : 0.0f;
+      if (b == 3) sm.into[k][l] = into;
+      const float past = sum_wave(own > b ? into : 0.0f);
+      if (l == 0) sm.past[k][b] = past;
+    } else if (part == 5) {
       if (p.D) sm.ddc[k][l] = (sm.dd[0][l] + sm.dd[1][l]) + (sm.dd[2][l] + sm.dd[3][l]);
+    } else if (part == 6) {
       if (l == 0) {
         float hh = 0.0f;
 #pragma unroll
@@ -644,15 +680,9 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     const int64_t h = h0 + k;
     const float Ah = p.A[h], d = sm.dt[k][l], rs = sm.rs[k][l], direct = sm.direct[k][l];
     const float raw = l < len ? bf2f(p.dt[(t0 + l) * p.dts + h]) : 0.0f;
-    float dcs = sm.into[k][l] - d * direct;
-    const float into_end = fmaf(sm.e0[k][kQ - 1], sm.hhs[k], sum_wave(d * rs));
-    if (l == kQ - 1) dcs += into_end;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const float o = __shfl_down(dcs, off);
-      if (l + off < 64) dcs += o;
-    }
-    float v, dd = fmaf(Ah, dcs, direct);
+    const float da = ((sm.inside[k][l] + sums_before<16>(d * sm.from[k][l])) + (row_suffix(sm.into[k][l]) + sm.past[k][l >> 4])) +
+                     fmaf(sm.e0[k][kQ - 1], sm.hhs[k], sums_before<64>(d * rs));
+    float v, dd = fmaf(Ah, da, direct);
     chunk_step(p.step, raw, p.dt_bias ? p.dt_bias[h] : 0.0f, true, v);
     if (p.step.limit) {
       const float sp = p.step.softplus ? softplus_acc(v) : v;
@@ -661,7 +691,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     if (p.step.softplus) dd *= fast_rcp(1.0f + fast_exp2(-v * kLog2e));
     if (l >= len) dd = 0.0f;
     else p.ddt[(t0 + l) * p.ddts + h] = static_cast<uint16_t>(float_to_half_bits<1>(dd));
-    const float dA = sum_wave(d * dcs), db = sum_wave(dd);
+    const float dA = sum_wave(d * da), db = sum_wave(dd);
     if (l == 0) {
       p.ws_sum[(entry * p.nheads + h) * 2] = dA;
       p.ws_sum[(entry * p.nheads + h) * 2 + 1] = db;

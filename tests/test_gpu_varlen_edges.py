@@ -1,0 +1,102 @@
+"""Places where the packed-token operators can go wrong without their ordinary
+tests seeing it: gradients that vanish, sequences that start at the end of a
+run, edges outside the tokens, explicit streams.  References and tolerances as
+in varlen_ref.py."""
+import pytest
+import torch
+
+from state_space_model_scan_amd import binding
+from tests import varlen_ref as R
+from tests.harness import log
+
+pytestmark = pytest.mark.gpu
+bf, f16, f32, i32 = torch.bfloat16, torch.float16, torch.float32, torch.int32
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _randn(g, *shape, dtype=f32, scale=1.0):
+    return (scale * torch.randn(shape, generator=g)).to(dtype)
+
+
+def _ints(v):
+    return torch.tensor(v, dtype=i32, device="cuda")
+
+
+# ---- the decays' gradient -------------------------------------------------
+
+def _steps_case(seed, lens, h, G, n, decay):
+    """Positive steps, decays of about exp(-decay) a token, and the checkpoints
+    of sequences that start from nothing."""
+    g, T = _gen(seed), sum(lens)
+    t = dict(x=_randn(g, T, h, R.P, dtype=bf), A=-decay * (0.5 + torch.rand(h, generator=g)), B=_randn(g, T, G, n, dtype=bf),
+             C=_randn(g, T, G, n, dtype=bf), dt=(0.75 + 0.5 * torch.rand(T, h, generator=g)).to(bf))
+    cu = R.sequences(lens)
+    entries = binding.ssd_checkpoint_slots(T, len(lens))
+    codes, scales = torch.full((entries, h, R.P, n), 3, dtype=torch.int8), torch.full((entries, h, R.P), float("nan"))
+    for e, (S, _) in R.scan_fwd(t, cu)[4].items():
+        codes[e], scales[e] = R.to_8_bits(S.float())
+    return t, cu, _randn(g, T, h, R.P, dtype=bf), codes, scales, _randn(g, len(lens), h, R.P, n)
+
+
+def _bwd(t, cu, dout, codes, scales, dlast):
+    longest = max(b - a for a, b in zip(cu, cu[1:]))
+    return binding.ssd_varlen_bwd(*(t[k].cuda() for k in ("x", "dt", "A", "B", "C")), _ints(cu), longest, dout.cuda(),
+                                  (codes.cuda(), scales.cuda()), dfinal_states=None if dlast is None else dlast.cuda())
+
+
+def _through(t, cu, dout, codes, scales, dlast):
+    """The gradient of every token's decay exponent, sum over its paths, and
+    the sum of the paths' magnitudes: nothing in it cancels by construction."""
+    x, B, C, A, g, d = (v.to(R.f64) for v in (t["x"], t["B"], t["C"], t["A"], dout, t["dt"]))
+    rep = x.shape[1] // B.shape[1]
+    up = lambda v: v.repeat_interleave(rep, 0)[:, None, :]  # noqa: E731
+    keep = torch.exp(d * A)[..., None, None]
+    da, dam = torch.zeros_like(d), torch.zeros_like(d)
+    for s in range(len(cu) - 1):
+        adj = torch.zeros(codes.shape[1:], dtype=R.f64) if dlast is None else dlast[s].to(R.f64).clone()
+        adjm = adj.abs()
+        for c in range((cu[s + 1] - cu[s] - 1) // R.Q, -1, -1):
+            ks = range(cu[s] + c * R.Q, min(cu[s + 1], cu[s] + (c + 1) * R.Q))
+            e = R.entry(cu, s, c)
+            S = codes[e].to(R.f64) * scales[e].to(R.f64)[..., None]
+            M, past = S.abs(), []
+            for k in ks:
+                past.append((S, M))
+                add = (d[k][:, None] * x[k])[:, :, None] * up(B[k])
+                S, M = keep[k] * S + add, keep[k] * M + add.abs()
+            for k in reversed(ks):
+                add = g[k][:, :, None] * up(C[k])
+                adj, adjm = keep[k] * (adj + add), keep[k] * (adjm + add.abs())
+                S, M = past[k - ks[0]]
+                da[k], dam[k] = (adj * S).sum((1, 2)), (adjm * M).sum((1, 2))
+    return da, dam
+
+
+@pytest.mark.parametrize("n", [32, 64, 128])
+@pytest.mark.parametrize("final", [False, True])
+def test_no_decay_gradient_of_single_tokens(n, final):
+    """A sequence of one token from nothing has no state that decays: dA is 0."""
+    log(f"[decay] single tokens n={n} final={final}")
+    *a, dlast = _steps_case(n, (1, 1, 0, 1, 1, 1), 6, 2, n, 1.0)
+    got = _bwd(*a, dlast if final else None)
+    assert torch.equal(got["dA"].cpu(), torch.zeros(6)), got["dA"]
+
+
+@pytest.mark.parametrize("decay", [0.1, 1.0, 10.0])
+@pytest.mark.parametrize("lens", [(2, 2, 1, 2), (17, 40), (64, 65), (200,)])
+def test_decay_gradient_of_short_memories(lens, decay):
+    """dA and ddt against the sum of their paths' magnitudes.  At exp(-10) a
+    token a path through a decay weighs less than a rounding (2^-24) of the paths
+    that do not pass one would, times the bound: those may not enter dA."""
+    log(f"[decay] lens={lens} decay={decay}")
+    t, cu, dout, codes, scales, dlast = _steps_case(3 + len(lens), lens, 4, 2, 64, decay)
+    da, dam = _through(t, cu, dout, codes, scales, dlast)
+    d = t["dt"].to(R.f64)
+    got = _bwd(t, cu, dout, codes, scales, dlast)
+    R.close(got["dA"], (d * da).sum(0), (d * dam).sum(0), f32, "dA")
+    ref = R.scan_bwd(t, cu, dout, codes, scales, dlast)
+    R.close(got["ddt"], *ref["ddt"], bf, "ddt")
+    assert (ref["dA"][0] - (d * da).sum(0)).abs().max() <= 2.0 ** -40 * (d * dam).sum()
