@@ -14,6 +14,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "conv_runs.h"
 #include "device_util.h"
 #include "host_util.h"
 #include "ssmscan.h"
@@ -22,6 +23,7 @@ namespace ssm {
 namespace {
 
 constexpr int kW = SSM_CONV_WIDTH;
+static_assert(kW == kTaps, "one width");
 constexpr int kFwdRun = 12;        // tokens of a wave's run, forward
 constexpr int kBwdRun = 32;        // tokens of a wave's run, backward
 constexpr int kShortRun = 4;       // the same where the waves are few, forward
@@ -124,7 +126,7 @@ struct Weights {
 };
 
 // A sequence's last inputs into its ring.  The run with the sequence's first
-// token does it, which has read what the ring held before.
+// token does it, which alone reads what the ring held before (run_pieces).
 template <int IO, int NV>
 __device__ __forceinline__ void keep_inputs(const ConvVarParams &p, const RingOf &ring, int64_t first, int64_t end, int64_t c0) {
   const int64_t slot = ring.slot, seen = ring.seen > 0 ? ring.seen : 0;
@@ -154,7 +156,7 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
   const int64_t c0 = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * NV;
   __shared__ Weights<NV> weights;
   weights.fill(p, c0 - lane * NV);
-  int64_t s = t0 < p.total ? find_seq(p.cu, p.nseq, t0) : 0;
+  const int64_t s = t0 < p.total ? find_seq(p.cu, p.nseq, t0) : 0;
   if constexpr (NV > 1) __syncthreads();
   if (t0 >= p.total || c0 >= p.channels) return;
   const int n = static_cast<int>(p.total - t0 < RUN ? p.total - t0 : RUN);
@@ -169,8 +171,7 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
   float w[kW][NV], bias[NV];
   weights.take(p, c0, lane, w, bias);
   RingOf ring = ring_of(p, s);   // (asked for with the two below, not behind them)
-  int64_t end = p.cu[s + 1];
-  int64_t pos = t0 - first_of(p.cu, s);
+  const int64_t end = p.cu[s + 1], pos = t0 - first_of(p.cu, s);
   if (n == RUN && pos >= kW - 1 && t0 + RUN <= end) {
     // the whole run and what it sees are inside one sequence: no branch
     // between the loads and their use (with the edge tests of every token in
@@ -192,29 +193,23 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
   }
   // A run with an edge in it, sequence by sequence: what lies before the
   // piece's first token once, then its tokens with the last inputs rolling.
-  int from = 0;
-  while (true) {
-    while (t0 + from >= end && s + 1 < p.nseq) {
-      ++s;
-      end = p.cu[s + 1];
-      pos = t0 + from - first_of(p.cu, s);
-      ring = ring_of(p, s);
-    }
-    const int to = (s + 1 < p.nseq && end - t0 < n) ? static_cast<int>(end - t0) : n;
+  run_pieces([&](int64_t i) { return static_cast<int64_t>(p.cu[i]); }, p.nseq, p.total, t0, n, s,
+             [&](int64_t of, int from, int to, int64_t place, int64_t edge) {
+    if (of != s) ring = ring_of(p, of);
     float win[kW - 1][NV];   // the last inputs, oldest first
 #pragma unroll
     for (int back = 1; back < kW; ++back) {
       float (&h)[NV] = win[kW - 1 - back];
-      if (pos >= back) {
+      if (place >= back) {
         Vec<IO, NV> v;
         v.load(p.x, (t0 + from - back) * p.xs + c0);
 #pragma unroll
         for (int k = 0; k < NV; ++k) h[k] = v.get(k);
       } else {
-        ring_input<IO, NV>(p, ring, back - static_cast<int>(pos), c0, h);
+        ring_input<IO, NV>(p, ring, back - static_cast<int>(place), c0, h);
       }
     }
-    if (p.ring && pos == 0) keep_inputs<IO, NV>(p, ring, t0 + from, end < p.total ? end : p.total, c0);
+    if (p.ring && place == 0) keep_inputs<IO, NV>(p, ring, t0 + from, edge < p.total ? edge : p.total, c0);
     // (the run's inputs once more, four tokens at a time: sharing the
     // registers above with this path doubled the kernel's)
 #pragma unroll 1
@@ -242,9 +237,7 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
         put<IO, NV>(p.out, (t0 + i + q) * p.os + c0, acc);
       }
     }
-    if (to >= n) break;
-    from = to;
-  }
+  });
 }
 
 // Backward.  At token t the pre-activation is formed again from x, and

@@ -100,3 +100,50 @@ def test_decay_gradient_of_short_memories(lens, decay):
     ref = R.scan_bwd(t, cu, dout, codes, scales, dlast)
     R.close(got["ddt"], *ref["ddt"], bf, "ddt")
     assert (ref["dA"][0] - (d * da).sum(0)).abs().max() <= 2.0 ** -40 * (d * dam).sum()
+
+
+# ---- the convolution's ring -----------------------------------------------
+
+@pytest.mark.parametrize("io,channels,total", [(bf, 1000, 12000), (f16, 4096, 6000), (f32, 67, 9000), (bf, 67, 70000)])
+def test_conv_ring_of_sequences_that_start_anywhere(io, channels, total):
+    """Continued sequences that start at every place of a run and of a
+    workgroup's runs, in more workgroups than run at once, short runs and long
+    ones, vectors and single channels: the tokens that see the ring see it as it
+    was before the call."""
+    log(f"[conv ring] {io} channels={channels} total={total}")
+    g, lens = _gen(channels), []
+    pick = torch.randint(0, 6, (total,), generator=g).tolist()
+    while sum(lens) < total:
+        lens.append((4, 5, 7, 13, 50, 121)[pick[len(lens)]])
+    cu, nseq = R.sequences(lens), len(lens)
+    T = cu[-1]
+    x, w, b = _randn(g, T, channels, dtype=io), _randn(g, channels, 4, scale=0.5), _randn(g, channels)
+    ring = _randn(g, nseq, channels, 4, dtype=io)
+    seen = [3 + s % 9 for s in range(nseq)]
+    assert {c % 48 for c in cu[:-1]} == set(range(48))
+    # the tokens that see the ring, and some that do not
+    near = sorted({c + k for c, n in zip(cu, lens) for k in range(min(n, 5))})
+    at = torch.tensor(near)
+    first, before = torch.zeros(T, dtype=torch.long), torch.zeros(nseq, 3, channels, dtype=R.f64)
+    of = torch.zeros(T, dtype=torch.long)
+    after = ring.clone()
+    for s, n in enumerate(lens):
+        first[cu[s]:cu[s + 1]], of[cu[s]:cu[s + 1]] = cu[s], s
+        for j in range(3):
+            before[s, j] = ring[s, :, (seen[s] - 3 + j) % 4].to(R.f64)
+        for t in range(n - 4, n):
+            after[s, :, (seen[s] + t) % 4] = x[cu[s] + t]
+    pre, mag = b.to(R.f64).expand(len(near), channels).clone(), b.to(R.f64).abs().expand(len(near), channels).clone()
+    for k in range(4):
+        src = at - 3 + k
+        inside = (src >= first[at])[:, None]
+        v = torch.where(inside, x[src.clamp(min=0)].to(R.f64), before[of[at], (src - first[at] + 3).clamp(0, 2)])
+        pre += v * w[:, k].to(R.f64)
+        mag += (v * w[:, k].to(R.f64)).abs()
+    ref = R.silu(pre)
+    dx, dw, db, dcu, dseen = x.cuda(), w.cuda(), b.cuda(), _ints(cu), _ints(seen)
+    for _ in range(3):
+        dring = ring.cuda()
+        out = binding.causal_conv1d_varlen_fwd(dx, dw, dcu, bias=db, activation="silu", conv_state=dring, cache_seqlens=dseen)
+        R.close(out[at.cuda()], ref, 1.1 * mag, io, "out", R.SHORT)
+        assert torch.equal(dring.cpu().view(torch.uint8), after.view(torch.uint8)), "ring"

@@ -1,0 +1,121 @@
+"""Host checks of the packed-token operators where a GPU run could not show the
+mistake, or could not run it safely."""
+import os
+import subprocess
+
+from tests.conftest import ROOT
+
+CSRC = os.path.join(ROOT, "state_space_model_scan_amd", "csrc")
+
+RUNS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <map>
+#include <random>
+#include <set>
+#include <vector>
+#include "conv_runs.h"
+using namespace ssm;
+typedef std::vector<int64_t> Edges;
+
+// a run that computes its own tokens and no others
+template <typename Edge, typename Piece>
+void own_tokens(const Edge &edge, int64_t nseq, int64_t total, int64_t t0, int n, int64_t s, Piece &&piece) {
+  for (int from = 0; from < n;) {
+    while (t0 + from >= edge(s + 1) && s + 1 < nseq) ++s;
+    const int64_t left = edge(s + 1) - t0;
+    const int to = s + 1 < nseq && left < n ? (int)left : n;
+    piece(s, from, to, t0 + from - first_token(edge, s), edge(s + 1));
+    from = to;
+  }
+}
+
+// every token computed once, at its place, and no ring of two runs; NULL or what is wrong
+template <bool OWN>
+const char *check(const Edges &cu, int run) {
+  const int64_t nseq = cu.size() - 1, total = cu.back();
+  auto edge = [&](int64_t i) { return cu.at(i); };
+  std::vector<int> done(total, 0);
+  std::map<int64_t, std::set<int64_t>> users;   // sequence -> runs that read or write its ring
+  const char *bad = nullptr;
+  for (int64_t t0 = 0; t0 < total; t0 += run) {
+    int64_t s0 = 0;
+    for (int64_t s = 0; s < nseq; ++s) if (cu[s] <= t0) s0 = s;
+    auto piece = [&](int64_t s, int from, int to, int64_t pos, int64_t end) {
+      if (from >= to || to > run + kTaps - 2 || t0 + to > total) { bad = "a piece's bounds"; return; }
+      if (pos != t0 + from - cu[s] || end != cu[s + 1] || t0 + to > end) { bad = "a piece's place"; return; }
+      for (int i = from; i < to; ++i) ++done[t0 + i];
+      if (pos < kTaps - 1) users[s].insert(t0);
+    };
+    const int n = total - t0 < run ? (int)(total - t0) : run;
+    if (OWN) own_tokens(edge, nseq, total, t0, n, s0, piece);
+    else run_pieces(edge, nseq, total, t0, n, s0, piece);
+  }
+  for (int v : done) if (v != 1) bad = "a token not computed once";
+  for (auto &u : users) if (u.second.size() != 1) bad = "a ring of two runs";
+  return bad;
+}
+
+int main() {
+  std::mt19937 rng(5);
+  long layouts = 0, shared = 0;
+  for (int i = 0; i < 40000; ++i) {
+    Edges cu = {0};
+    const int nseq = 1 + rng() % 9, longest = (int[]){2, 5, 16, 60}[rng() % 4];
+    for (int s = 0; s < nseq; ++s) cu.push_back(cu.back() + (rng() % 4 ? rng() % longest : rng() % 2));
+    if (cu.back() == 0) continue;
+    for (int run : {4, 12}) {
+      ++layouts;
+      if (const char *bad = check<false>(cu, run)) { printf("run %d: %s\n", run, bad); return 1; }
+      if (check<true>(cu, run)) ++shared;
+    }
+  }
+  if (shared < layouts / 20) { printf("the check sees too little: %ld of %ld\n", shared, layouts); return 1; }
+  // edges out of order and out of range: every access stays inside the tokens
+  for (int i = 0; i < 200000; ++i) {
+    const int64_t total = 1 + rng() % 100, nseq = 1 + rng() % 6;
+    Edges cu;
+    for (int s = 0; s <= nseq; ++s) {
+      const int kind = rng() % 8;
+      cu.push_back(kind == 0 ? -(int64_t)(rng() % 20) : kind == 1 ? INT32_MAX : kind == 2 ? INT32_MIN : (int64_t)(rng() % 120));
+    }
+    const int run = rng() % 2 ? 4 : 12;
+    for (int64_t t0 = 0; t0 < total; t0 += run) {
+      bool bad = false;
+      run_pieces([&](int64_t k) { return cu.at(k); }, nseq, total, t0, total - t0 < run ? (int)(total - t0) : run, rng() % nseq,
+                 [&](int64_t s, int from, int to, int64_t pos, int64_t) {
+        if (s < 0 || s >= nseq || from < 0 || from >= to || t0 + to > total) bad = true;
+        for (int back = 1; back < kTaps; ++back) if (pos >= back && t0 + from - back < 0) bad = true;
+      });
+      if (bad) { printf("edges out of order: outside the tokens\n"); return 1; }
+    }
+  }
+  // far from the start, with edges at the ends of their type
+  for (int64_t e : {(int64_t)INT32_MIN, (int64_t)-1, (int64_t)0, (int64_t)INT32_MAX - 3, (int64_t)INT32_MAX}) {
+    const int64_t total = INT32_MAX, t0 = total / 12 * 12;
+    const Edges cu = {e, e, e};
+    bool bad = false;
+    run_pieces([&](int64_t k) { return cu.at(k); }, 2, total, t0, (int)(total - t0), 1, [&](int64_t, int from, int to, int64_t, int64_t) {
+      if (from < 0 || from >= to || t0 + to > total) bad = true;
+    });
+    if (bad) { printf("far edges: outside the tokens\n"); return 1; }
+  }
+  printf("%ld layouts, %ld of them shared between runs of their own tokens\n", layouts, shared);
+  return 0;
+}
+"""
+
+
+def _host_program(tmp_path, text):
+    src, exe = tmp_path / "check.cpp", tmp_path / "check"
+    src.write_text(text)
+    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", f"-I{CSRC}", str(src), "-o", str(exe)], check=True, timeout=120)
+    res = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert res.returncode == 0, res.stdout + res.stderr
+
+
+def test_one_run_reads_and_writes_a_ring(tmp_path):
+    """The packed conv's runs, by the header the kernel uses: every token once,
+    a sequence's ring read and written by one run only (which a split at the
+    runs' ends is not), and nothing outside the tokens whatever the edges."""
+    _host_program(tmp_path, RUNS)
