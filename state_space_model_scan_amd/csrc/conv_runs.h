@@ -22,6 +22,13 @@ SSM_RUN_FN int64_t first_token(const Edge &edge, int64_t s) {
   return at < 0 ? 0 : at;
 }
 
+// Whether the tokens [t0, stop) and the kTaps - 1 before them are tokens of
+// sequence s, that of t0.
+template <typename Edge>
+SSM_RUN_FN bool inside_one(const Edge &edge, int64_t s, int64_t t0, int64_t stop) {
+  return t0 - first_token(edge, s) >= kTaps - 1 && stop <= edge(s + 1);
+}
+
 // The pieces of the run of tokens [t0, t0 + n) that it computes, in order:
 // piece(s, from, to, pos, end) for the tokens t0 + from .. t0 + to - 1 of
 // sequence s, the first of them its token pos, end the edge after it.  s0 is the

@@ -67,8 +67,9 @@ struct ConvVarParams {
 __device__ __forceinline__ int64_t find_seq(const int32_t *cu, int64_t nseq, int64_t t) {
   return wave_search(nseq, [&](int64_t s) { return cu[s] <= t; });
 }
-// Its first token (a negative one stands for 0).
-__device__ __forceinline__ int64_t first_of(const int32_t *cu, int64_t s) { return cu[s] < 0 ? 0 : cu[s]; }
+__device__ __forceinline__ auto edges_of(const int32_t *cu) {
+  return [=](int64_t s) { return static_cast<int64_t>(cu[s]); };
+}
 
 // Where a sequence's ring is, and how many tokens went before.
 struct RingOf {
@@ -171,8 +172,8 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
   float w[kW][NV], bias[NV];
   weights.take(p, c0, lane, w, bias);
   RingOf ring = ring_of(p, s);   // (asked for with the two below, not behind them)
-  const int64_t end = p.cu[s + 1], pos = t0 - first_of(p.cu, s);
-  if (n == RUN && pos >= kW - 1 && t0 + RUN <= end) {
+  const auto edge = edges_of(p.cu);
+  if (n == RUN && inside_one(edge, s, t0, t0 + RUN)) {
     // the whole run and what it sees are inside one sequence: no branch
     // between the loads and their use (with the edge tests of every token in
     // between the compiler kept few loads in flight: 216 us where this takes
@@ -193,8 +194,7 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
   }
   // A run with an edge in it, sequence by sequence: what lies before the
   // piece's first token once, then its tokens with the last inputs rolling.
-  run_pieces([&](int64_t i) { return static_cast<int64_t>(p.cu[i]); }, p.nseq, p.total, t0, n, s,
-             [&](int64_t of, int from, int to, int64_t place, int64_t edge) {
+  run_pieces(edge, p.nseq, p.total, t0, n, s, [&](int64_t of, int from, int to, int64_t place, int64_t end) {
     if (of != s) ring = ring_of(p, of);
     float win[kW - 1][NV];   // the last inputs, oldest first
 #pragma unroll
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
         ring_input<IO, NV>(p, ring, back - static_cast<int>(place), c0, h);
       }
     }
-    if (p.ring && place == 0) keep_inputs<IO, NV>(p, ring, t0 + from, edge < p.total ? edge : p.total, c0);
+    if (p.ring && place == 0) keep_inputs<IO, NV>(p, ring, t0 + from, end < p.total ? end : p.total, c0);
     // (the run's inputs once more, four tokens at a time: sharing the
     // registers above with this path doubled the kernel's)
 #pragma unroll 1
@@ -271,9 +271,10 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_bwd_kernel(const ConvVarP
     float w[kW][NV], bias[NV];
     weights.take(p, c0, lane, w, bias);
     int64_t s = of_first;
-    int64_t end = p.cu[s + 1];
-    int64_t pos = t0 - p.cu[s];
-    if (pos >= kW - 1 && walk - t0 == RUN + kW - 1 && walk <= end) {
+    const auto edge = edges_of(p.cu);
+    int64_t end = edge(s + 1);
+    int64_t pos = t0 - first_token(edge, s);
+    if (walk - t0 == RUN + kW - 1 && inside_one(edge, s, t0, walk)) {
       // the run and all that it sees are inside one sequence.  Token i's input
       // and pending gradient are in place i % 4, so nothing moves along and
       // nothing is tested (16384 x 5376 bf16: 126 us where the general walk
@@ -384,8 +385,8 @@ __global__ void __launch_bounds__(64 * kRows) conv_var_bwd_kernel(const ConvVarP
           if (t < walk) {
             while (t >= end && s + 1 < p.nseq) {
               ++s;
-              end = p.cu[s + 1];
-              pos = t - p.cu[s];
+              end = edge(s + 1);
+              pos = t - first_token(edge, s);
             }
             float da[NV];
 #pragma unroll

@@ -147,3 +147,23 @@ def test_conv_ring_of_sequences_that_start_anywhere(io, channels, total):
         out = binding.causal_conv1d_varlen_fwd(dx, dw, dcu, bias=db, activation="silu", conv_state=dring, cache_seqlens=dseen)
         R.close(out[at.cuda()], ref, 1.1 * mag, io, "out", R.SHORT)
         assert torch.equal(dring.cpu().view(torch.uint8), after.view(torch.uint8)), "ring"
+
+
+@pytest.mark.parametrize("io,channels,total", [(bf, 64, 200), (f32, 67, 200), (bf, 4096, 3000), (bf, 67, 40000)])
+@pytest.mark.parametrize("edge", [-3, -40])
+def test_conv_edge_below_zero(io, channels, total, edge):
+    """A first edge below 0 stands for 0, forward and backward, short runs and
+    long ones.  (The rows before the tokens are there, and not read.)"""
+    log(f"[conv edge] {io} channels={channels} total={total} edge={edge}")
+    g = _gen(total)
+    room = torch.full((total + 64, channels), float("nan"), dtype=io, device="cuda")
+    x = room[64:]
+    x.copy_(_randn(g, total, channels, dtype=io))
+    w, dout = _randn(g, channels, 4, scale=0.5).cuda(), _randn(g, total, channels, dtype=io).cuda()
+    got = []
+    for first in (0, edge):
+        cu = _ints([first, total // 2, total])
+        got.append(binding.causal_conv1d_varlen_bwd(x, w, cu, dout, activation="silu"))
+        got[-1]["out"] = binding.causal_conv1d_varlen_fwd(x, w, cu, activation="silu")
+    for k in ("out", "dx", "dweight"):
+        assert torch.equal(got[0][k], got[1][k]) and torch.isfinite(got[0][k]).all(), k

@@ -87,6 +87,9 @@ int main() {
         if (s < 0 || s >= nseq || from < 0 || from >= to || t0 + to > total) bad = true;
         for (int back = 1; back < kTaps; ++back) if (pos >= back && t0 + from - back < 0) bad = true;
       });
+      // where all of a run and what it sees is read without a test
+      const int64_t s = rng() % nseq;
+      if (inside_one([&](int64_t k) { return cu.at(k); }, s, t0, t0 + run) && t0 - (kTaps - 1) < 0) bad = true;
       if (bad) { printf("edges out of order: outside the tokens\n"); return 1; }
     }
   }
@@ -112,6 +115,29 @@ def _host_program(tmp_path, text):
     subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", f"-I{CSRC}", str(src), "-o", str(exe)], check=True, timeout=120)
     res = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert res.returncode == 0, res.stdout + res.stderr
+
+
+SEEN = r"""
+#include <cstdint>
+#include <cstdio>
+#include <initializer_list>
+#include "conv_runs.h"
+int main() {
+  // a first edge below 0 stands for 0: the run of token 0 sees nothing before it
+  for (int64_t first = -40; first <= 0; ++first) {
+    const int64_t cu[2] = {first, 1000};
+    auto edge = [&](int64_t k) { return cu[k]; };
+    if (ssm::first_token(edge, 0) != 0) return 1;
+    for (int t0 : {0, 1, 2, 3, 8, 32})
+      if (ssm::inside_one(edge, 0, t0, t0 + 35) != (t0 >= 3)) { printf("token %d, edge %d\n", t0, (int)first); return 1; }
+  }
+  return 0;
+}
+"""
+
+
+def test_a_first_edge_below_zero_stands_for_zero(tmp_path):
+    _host_program(tmp_path, SEEN)
 
 
 def test_one_run_reads_and_writes_a_ring(tmp_path):
