@@ -938,6 +938,9 @@ def ssd_scan_workspace_size(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
 # Packed tokens: a Mamba-2 mixer's conv, scan and step.  Their smallest calls
 # take the GPU a few microseconds, so the checks and the marshalling are in
 # C++ (csrc/packed_binding.cpp); each function there returns a status first.
+# A ``stream`` other than the current one takes the whole call: copies of
+# inputs, workspace, new outputs and kernels.  The caller orders it after what
+# made the inputs.
 # ---------------------------------------------------------------------------
 
 def _handle(stream) -> Optional[int]:

@@ -131,10 +131,28 @@ void conv_params(const Tensor &w, const Opt &bias, int64_t channels, at::Device 
   spec(bias, "bias", {channels}, at::kFloat, dev);
 }
 
-void *stream_of(at::Device dev, std::optional<int64_t> given) {
-  if (given) return reinterpret_cast<void *>(*given);
-  return c10::hip::getCurrentHIPStream(dev.index()).stream();
-}
+// The stream of a call, for as long as the call lasts: one that the caller
+// names becomes torch's current one, so that the copies of inputs, the
+// workspace and new outputs are made on it, in order with the kernels, and
+// memory that the call gives back is not handed out to another stream.
+class OnStream {
+ public:
+  OnStream(at::Device dev, std::optional<int64_t> given) : dev_(dev) {
+    if (!given || !dev.is_cuda()) return;
+    before_ = c10::hip::getCurrentHIPStream(dev.index());
+    c10::hip::setCurrentHIPStream(c10::hip::getStreamFromExternal(reinterpret_cast<hipStream_t>(*given), dev.index()));
+  }
+  ~OnStream() {
+    if (before_) c10::hip::setCurrentHIPStream(*before_);
+  }
+  OnStream(const OnStream &) = delete;
+  OnStream &operator=(const OnStream &) = delete;
+  void *handle() const { return c10::hip::getCurrentHIPStream(dev_.index()).stream(); }
+
+ private:
+  at::Device dev_;
+  std::optional<c10::hip::HIPStream> before_;
+};
 
 // the caller's scratch, or as much as the call needs
 template <typename Args>
@@ -185,8 +203,9 @@ struct Conv {
 std::tuple<int, Tensor> conv_fwd(const Tensor &x, const Tensor &w, const Tensor &cu, const Opt &bias, int act,
                                  const Opt &conv_state, const Opt &seen_, const Opt &slots_, const Opt &out_,
                                  std::optional<int64_t> stream) {
-  Conv c(x, w, cu, bias, act);
   const at::Device dev = x.device();
+  const OnStream on(dev, stream);
+  Conv c(x, w, cu, bias, act);
   spec(seen_, "cache_seqlens", {c.a.nseq}, at::kInt, dev);
   spec(slots_, "slots", {c.a.nseq}, at::kInt, dev);
   if (conv_state) {
@@ -204,14 +223,15 @@ std::tuple<int, Tensor> conv_fwd(const Tensor &x, const Tensor &w, const Tensor 
   c.a.out_stride = stride(out);
   c.a.cache_seqlens = i32(seen);
   c.a.slots = i32(slots);
-  return {causal_conv1d_varlen_fwd(&c.a, stream_of(dev, stream)), out};
+  return {causal_conv1d_varlen_fwd(&c.a, on.handle()), out};
 }
 
 std::tuple<int, Tensor, Tensor, Opt> conv_bwd(const Tensor &x, const Tensor &w, const Tensor &cu, const Tensor &dout_,
                                               const Opt &bias, int act, const Opt &dx_, const Opt &ws_,
                                               std::optional<int64_t> stream) {
-  Conv c(x, w, cu, bias, act);
   const at::Device dev = x.device();
+  const OnStream on(dev, stream);
+  Conv c(x, w, cu, bias, act);
   spec(dout_, "dout", x.sizes(), x.scalar_type(), dev);
   on_gpu(dev);
   const Tensor dout = tokens(dout_), dx = tokens_out(dx_, "dx", x.sizes(), x.scalar_type(), dev);
@@ -226,7 +246,7 @@ std::tuple<int, Tensor, Tensor, Opt> conv_bwd(const Tensor &x, const Tensor &w, 
   c.a.dbias = db ? db->data_ptr<float>() : nullptr;
   Opt ws;
   int st = workspace(causal_conv1d_varlen_bwd_workspace_size, c.a, ws_, dev, ws);
-  if (st == SSM_OK) st = causal_conv1d_varlen_bwd(&c.a, stream_of(dev, stream));
+  if (st == SSM_OK) st = causal_conv1d_varlen_bwd(&c.a, on.handle());
   return {st, dx, dw, db};
 }
 
@@ -286,8 +306,9 @@ std::tuple<int, Tensor> scan_fwd(const Tensor &x, const Tensor &dt, const Tensor
                                  bool softplus, std::optional<std::tuple<double, double>> limit, const Opt &state,
                                  const Opt &seen_, const Opt &slots_, const Opt &codes, const Opt &scales, const Opt &out_,
                                  const Opt &ws_, int64_t segments, std::optional<int64_t> stream) {
-  Scan s(x, dt, A, B, C, cu, max_seqlen, D, z, dt_bias, softplus, limit, codes, scales, segments);
   const at::Device dev = x.device();
+  const OnStream on(dev, stream);
+  Scan s(x, dt, A, B, C, cu, max_seqlen, D, z, dt_bias, softplus, limit, codes, scales, segments);
   if (state) {
     if (state->dim() != 4)
       refuse("ssm_state must have shape (entries, nheads, headdim, dstate), got " + tuple_text(state->sizes()));
@@ -310,7 +331,7 @@ std::tuple<int, Tensor> scan_fwd(const Tensor &x, const Tensor &dt, const Tensor
   s.a.slots = i32(slots);
   Opt ws;
   int st = workspace(ssd_varlen_fwd_workspace_size, s.a, ws_, dev, ws);
-  if (st == SSM_OK) st = ssd_varlen_fwd(&s.a, stream_of(dev, stream));
+  if (st == SSM_OK) st = ssd_varlen_fwd(&s.a, on.handle());
   return {st, out};
 }
 
@@ -321,9 +342,10 @@ BwdOut scan_bwd(const Tensor &x, const Tensor &dt, const Tensor &A, const Tensor
                 const Opt &dt_bias, bool softplus, std::optional<std::tuple<double, double>> limit, const Opt &dfin_,
                 bool want_init, const Opt &dx_, const Opt &dB_, const Opt &dC_, const Opt &ddt_, const Opt &ws_,
                 int64_t segments, std::optional<int64_t> stream) {
+  const at::Device dev = x.device();
+  const OnStream on(dev, stream);
   ssd_varlen_bwd_args_t a{};
   Scan s(x, dt, A, B, C, cu, max_seqlen, D, {}, dt_bias, softplus, limit, codes_, scales_, segments);
-  const at::Device dev = x.device();
   const ScalarType io = x.scalar_type(), f = at::kFloat;
   const int64_t h = s.a.nheads, p = s.a.headdim, n = s.a.dstate;
   // any strides from entry to entry and head to head; a channel's states dense
@@ -362,7 +384,7 @@ BwdOut scan_bwd(const Tensor &x, const Tensor &dt, const Tensor &A, const Tensor
   a.dinitial_states = dinit ? dinit->data_ptr<float>() : nullptr;
   Opt ws;
   int st = workspace(ssd_varlen_bwd_workspace_size, a, ws_, dev, ws);
-  if (st == SSM_OK) st = ssd_varlen_bwd(&a, stream_of(dev, stream));
+  if (st == SSM_OK) st = ssd_varlen_bwd(&a, on.handle());
   return {st, dx, ddt, dB, dC, dA, dD, db, dinit};
 }
 
@@ -374,6 +396,7 @@ std::tuple<int, Tensor> step(const Tensor &xBC_, const Tensor &dt_, const Tensor
   a.io_dtype = io_of(xBC_, "xBC", 2);
   const ScalarType io = xBC_.scalar_type(), f = at::kFloat;
   const at::Device dev = xBC_.device();
+  const OnStream on(dev, stream);
   if (state.dim() != 4)
     refuse("ssm_state must be (entries, nheads, headdim, dstate), got shape " + tuple_text(state.sizes()));
   const int64_t e = state.size(0), h = state.size(1), p = state.size(2), n = state.size(3), hp = h * p;
@@ -411,7 +434,7 @@ std::tuple<int, Tensor> step(const Tensor &xBC_, const Tensor &dt_, const Tensor
   a.ssm_state = state.data_ptr<float>(); a.state_slots = e;
   a.cache_seqlens = i32(seen); a.slots = i32(slots);
   a.out = out.data_ptr(); a.out_stride = stride(out);
-  return {conv1d_ssd_update(&a, stream_of(dev, stream)), out};
+  return {conv1d_ssd_update(&a, on.handle()), out};
 }
 
 }  // namespace

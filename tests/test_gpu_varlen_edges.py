@@ -167,3 +167,84 @@ def test_conv_edge_below_zero(io, channels, total, edge):
         got[-1]["out"] = binding.causal_conv1d_varlen_fwd(x, w, cu, activation="silu")
     for k in ("out", "dx", "dweight"):
         assert torch.equal(got[0][k], got[1][k]) and torch.isfinite(got[0][k]).all(), k
+
+
+# ---- a stream of the caller's ---------------------------------------------
+
+def _off(t):
+    """The values of t at a place and with strides that make a wrapper copy them."""
+    room = torch.empty((t.shape[0],) + tuple(t.shape[1:-1]) + (t.shape[-1] + 1,), dtype=t.dtype, device="cuda")
+    room[..., 1:] = t
+    return room[..., 1:]
+
+
+def _busy(a, n=30):
+    for _ in range(n):
+        a = a @ a
+    return a
+
+
+def _packed_calls():
+    """{name: call(stream) -> tensors} of the packed operators, on inputs that
+    have to be copied first."""
+    g, lens, h, G, n = _gen(21), (300, 1, 129), 4, 2, 64
+    cu, T, ch = _ints(R.sequences(lens)), sum(lens), h * R.P + 2 * G * n
+    x, B, C, dout = (_off(_randn(g, T, k, w, dtype=bf).cuda()) for k, w in ((h, R.P), (G, n), (G, n), (h, R.P)))
+    dt, A = _off((_randn(g, T, h, dtype=bf) - 3).cuda()), _off(-1 - 7 * torch.rand(1, h, generator=g).cuda())[0]
+    w, rows, drows = _off(_randn(g, ch, 4).cuda()), _off(_randn(g, T, ch, dtype=bf).cuda()), _off(_randn(g, T, ch, dtype=bf).cuda())
+    rows_t = _randn(g, ch, T, dtype=bf).cuda().t()
+    first = _off(_randn(g, len(lens), h, R.P, n).cuda())
+    codes = torch.zeros(binding.ssd_checkpoint_slots(T, len(lens)), h, R.P, n, dtype=torch.int8, device="cuda")
+    scales = torch.ones(codes.shape[:3], device="cuda")
+    scan = (x, dt, A, B, C, cu, 300)
+    binding.ssd_varlen_fwd(*scan, dt_softplus=True, checkpoints=(codes, scales))
+    codes = _off(codes)
+
+    ring, state = torch.ones(T, ch, 4, dtype=bf, device="cuda"), torch.ones(T, h, R.P, n, device="cuda")
+
+    def step(stream):   # of new requests, which read neither cache
+        out = binding.conv1d_ssd_update(rows_t, dt, A, w, ring, state, None, dt_softplus=True, stream=stream)
+        return [out, ring, state]
+
+    def grads(stream):
+        got = binding.ssd_varlen_bwd(*scan, dout, (codes, scales), dt_softplus=True, dfinal_states=first, seq_segments=3,
+                                     want_dinitial_states=True, stream=stream)
+        return [got[k] for k in sorted(got)]
+
+    def conv_grads(stream):
+        got = binding.causal_conv1d_varlen_bwd(rows_t, w, cu, drows, activation="silu", stream=stream)
+        return [got["dx"], got["dweight"]]
+
+    return {"conv": lambda stream: [binding.causal_conv1d_varlen_fwd(rows_t, w, cu, stream=stream)], "conv_bwd": conv_grads,
+            "scan": lambda stream: [binding.ssd_varlen_fwd(*scan, dt_softplus=True, seq_segments=3, stream=stream)],
+            "scan_bwd": grads, "step": step}
+
+
+def _check_stream(call):
+    want = [v.clone() for v in call(None)]
+    big, sizes = torch.randn(2048, 2048, device="cuda") / 64, [1 << k for k in range(9, 25)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    current = torch.cuda.current_stream()
+    for busy_current in (True, False):
+        if busy_current:   # a copy of an input left on the current stream would come long after the kernels
+            _busy(big)
+        else:              # the call's memory is still in use when it returns
+            side.wait_stream(current)
+            with torch.cuda.stream(side):
+                _busy(big)
+        got = call(side)
+        assert torch.cuda.current_stream() == current
+        junk = [torch.full((s,), float("nan"), device="cuda") for s in sizes for _ in range(3)]
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+        del junk
+
+
+@pytest.mark.parametrize("name", ["conv", "conv_bwd", "scan", "scan_bwd", "step"])
+def test_explicit_stream(name):
+    """stream= of another stream than the current one: inputs that are copied,
+    workspaces and outputs all belong to it."""
+    log(f"[stream] {name}")
+    _check_stream(_packed_calls()[name])
