@@ -12,6 +12,8 @@ activation other than None / "silu" / "swish" raises NotImplementedError.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 from typing import Optional, Tuple, Union
 
 import torch
@@ -35,6 +37,24 @@ def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
 def _stream(device: torch.device, stream=None):
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _whole_call(fn):
+    """fn with a ``stream`` that the caller names as torch's current one for
+    the call, so that the copies of inputs, the workspace and new outputs are
+    made on it, in order with the kernels, and memory that the call gives back
+    is not handed out to another stream."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+    return call
 
 
 # Every wrapper checks each tensor against the sizes that delta (or x) and A
@@ -188,6 +208,7 @@ def _scan_args(u, delta, A, B, C, D, z, delta_bias, delta_softplus, out, last_st
     return args, out, keep
 
 
+@_whole_call
 def ssm_scan_fwd(u: Optional[torch.Tensor], delta: torch.Tensor, A: torch.Tensor,
                  B: torch.Tensor, C: torch.Tensor, D: Optional[torch.Tensor] = None,
                  z: Optional[torch.Tensor] = None, delta_bias: Optional[torch.Tensor] = None,
@@ -247,6 +268,7 @@ def ssm_scan_plan(u: Optional[torch.Tensor], delta: torch.Tensor, A: torch.Tenso
     return {k: getattr(plan, k) for k, _ in _lib.ScanPlan._fields_}
 
 
+@_whole_call
 def ssm_scan_fwd_noalloc(u: Optional[torch.Tensor], delta: torch.Tensor, A: torch.Tensor,
                          B: torch.Tensor, C: torch.Tensor, D: Optional[torch.Tensor] = None,
                          z: Optional[torch.Tensor] = None, delta_bias: Optional[torch.Tensor] = None,
@@ -284,6 +306,7 @@ def _bc_kind_complex(t: torch.Tensor, name: str) -> Tuple[int, int]:
     return kind, g
 
 
+@_whole_call
 def ssm_scan_fwd_complex(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor,
                          B: torch.Tensor, C: torch.Tensor, D: Optional[torch.Tensor] = None,
                          z: Optional[torch.Tensor] = None,
@@ -367,6 +390,7 @@ def checkpoint_count(seqlen: int) -> int:
     return (seqlen + _lib.SSM_CKPT_INTERVAL - 1) // _lib.SSM_CKPT_INTERVAL
 
 
+@_whole_call
 def ssm_scan_bwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                  C: torch.Tensor, dout: torch.Tensor, checkpoints: torch.Tensor,
                  D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
@@ -443,6 +467,7 @@ def ssm_scan_bwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch
     return g
 
 
+@_whole_call
 def ssm_scan_bwd_complex(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                          C: torch.Tensor, dout: torch.Tensor, checkpoints: torch.Tensor,
                          D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
@@ -524,6 +549,7 @@ def ssm_scan_bwd_complex(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, 
     return g
 
 
+@_whole_call
 def causal_conv1d_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
                       out: Optional[torch.Tensor] = None, act: int = _lib.SSM_ACT_NONE,
                       stream=None) -> torch.Tensor:
@@ -572,6 +598,7 @@ def selective_scan_fn(u, delta, A, B, C, D=None, z=None, delta_bias=None,
     return (out, last) if return_last_state else out
 
 
+@_whole_call
 def causal_conv1d_fwd_ex(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
                          seq_idx: Optional[torch.Tensor] = None,
                          initial_states: Optional[torch.Tensor] = None,
@@ -656,6 +683,7 @@ def conv1d_selective_scan_fn(x, conv_weight, conv_bias, delta, A, B, C, D=None, 
 # single-step decode
 # ---------------------------------------------------------------------------
 
+@_whole_call
 def selective_state_update(state: torch.Tensor, x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor,
                            B: torch.Tensor, C: torch.Tensor, D: Optional[torch.Tensor] = None,
                            z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
@@ -708,6 +736,7 @@ def selective_state_update(state: torch.Tensor, x: torch.Tensor, dt: torch.Tenso
     return out
 
 
+@_whole_call
 def causal_conv1d_update(x: torch.Tensor, conv_state: torch.Tensor, weight: torch.Tensor,
                          bias: Optional[torch.Tensor] = None, activation=None,
                          cache_seqlens: Optional[torch.Tensor] = None,
@@ -811,6 +840,7 @@ def _ssd_args(x, dt, A, B, C, D, z, dt_bias, dt_softplus, initial_states, out, f
     return a, out, (x, dt, A, B, C, D, z, dt_bias, initial_states, seq_idx)
 
 
+@_whole_call
 def ssd_scan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                  C: torch.Tensor, D: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
                  dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = False,
@@ -849,6 +879,7 @@ def _nchunks(seqlen: int, chunk_size: int) -> int:
     return -(-seqlen // chunk_size)
 
 
+@_whole_call
 def ssd_chunk_state(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, chunk_size: int,
                     dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = False,
                     seq_idx: Optional[torch.Tensor] = None, dt_limit: Optional[Tuple[float, float]] = None,
@@ -875,6 +906,7 @@ def ssd_chunk_state(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch
     return states, decays
 
 
+@_whole_call
 def ssd_state_passing(states: torch.Tensor, decays: torch.Tensor, initial_states: Optional[torch.Tensor] = None,
                       carried: Optional[torch.Tensor] = None, final_states: Optional[torch.Tensor] = None,
                       stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -902,6 +934,7 @@ def ssd_state_passing(states: torch.Tensor, decays: torch.Tensor, initial_states
     return carried, final_states
 
 
+@_whole_call
 def ssd_chunk_scan(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
                    carried: torch.Tensor, chunk_size: int, D: Optional[torch.Tensor] = None,
                    z: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,

@@ -173,7 +173,7 @@ def test_conv_edge_below_zero(io, channels, total, edge):
 
 def _off(t):
     """The values of t at a place and with strides that make a wrapper copy them."""
-    room = torch.empty((t.shape[0],) + tuple(t.shape[1:-1]) + (t.shape[-1] + 1,), dtype=t.dtype, device="cuda")
+    room = torch.empty(tuple(t.shape[:-1]) + (t.shape[-1] + 1,), dtype=t.dtype, device="cuda")
     room[..., 1:] = t
     return room[..., 1:]
 
@@ -248,3 +248,44 @@ def test_explicit_stream(name):
     workspaces and outputs all belong to it."""
     log(f"[stream] {name}")
     _check_stream(_packed_calls()[name])
+
+
+def _dense_calls():
+    """The same of the operators on dense rows."""
+    g, b, d, l, n, h = _gen(22), 2, 128, 400, 16, 2
+    r = lambda *shape, dtype=bf: _off(_randn(g, *shape, dtype=dtype).cuda())  # noqa: E731
+    u, delta, dout, B, C = r(b, d, l), r(b, d, l) * 0.1, r(b, d, l), r(b, 1, n, l), r(b, 1, n, l)
+    A = _off(-1 - torch.rand(d, n, generator=g).cuda())
+    u, delta, dout = (v.transpose(1, 2).contiguous().transpose(1, 2) for v in (u, delta, dout))
+    fwd = (u, delta, A, B, C)
+    checkpoints = torch.zeros(b, d, binding.checkpoint_count(l), n, device="cuda")
+    binding.ssm_scan_fwd(*fwd, delta_softplus=True, checkpoints=checkpoints)
+    kept = _off(checkpoints)
+    x, dt, Bs, Cs, As = r(b, l, h, R.P), r(b, l, h) - 3, r(b, l, 1, 64), r(b, l, 1, 64), -1 - torch.rand(h, generator=g).cuda()
+    dt = _off(dt)
+    w, bias = r(d, 4, dtype=f32), r(d, dtype=f32)
+    start, xs = _randn(g, b, d, n).cuda(), r(b, d)
+
+    def grads(stream):
+        got = binding.ssm_scan_bwd(*fwd, dout, kept, delta_softplus=True, stream=stream)
+        return [got[k] for k in sorted(got) if got[k] is not None]
+
+    def update(stream):
+        state = out_state   # refilled on the call's own stream
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            state.copy_(start)
+        return [binding.selective_state_update(state, xs, xs, A, B[:, 0, :, 0], C[:, 0, :, 0], dt_softplus=True, stream=stream), state]
+
+    out_state = torch.empty_like(start)
+    return {"scan": lambda s: [binding.ssm_scan_fwd(*fwd, delta_softplus=True, seq_segments=3, stream=s)], "scan_bwd": grads,
+            "conv": lambda s: [binding.causal_conv1d_fwd(u, w, bias, stream=s)],
+            "conv_ex": lambda s: [binding.causal_conv1d_fwd_ex(u, w, bias, stream=s)],
+            "ssd": lambda s: [binding.ssd_scan_fwd(x, dt, As, Bs, Cs, dt_softplus=True, seq_segments=3, stream=s)],
+            "chunk_state": lambda s: list(binding.ssd_chunk_state(x, dt, As, Bs, 64, dt_softplus=True, stream=s)),
+            "update": update}
+
+
+@pytest.mark.parametrize("name", ["scan", "scan_bwd", "conv", "conv_ex", "ssd", "chunk_state", "update"])
+def test_explicit_stream_of_dense_rows(name):
+    log(f"[stream] dense rows: {name}")
+    _check_stream(_dense_calls()[name])

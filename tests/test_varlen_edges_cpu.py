@@ -145,3 +145,34 @@ def test_one_run_reads_and_writes_a_ring(tmp_path):
     a sequence's ring read and written by one run only (which a split at the
     runs' ends is not), and nothing outside the tokens whatever the edges."""
     _host_program(tmp_path, RUNS)
+
+
+def test_a_named_stream_is_the_calls_current_one(monkeypatch):
+    """Every wrapper that takes a stream runs as a whole with it as the current
+    one, whether it is passed by name or by place; without one nothing changes."""
+    import contextlib
+    import inspect
+    import torch
+    from state_space_model_scan_amd import binding
+    entered = []
+
+    @contextlib.contextmanager
+    def stream(s):
+        entered.append(s)
+        yield
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    names = [n for n, f in vars(binding).items() if inspect.isfunction(f) and f.__module__ == binding.__name__ and
+             "stream" in inspect.signature(f).parameters and not n.startswith("_")]
+    packed = {"causal_conv1d_varlen_fwd", "causal_conv1d_varlen_bwd", "ssd_varlen_fwd", "ssd_varlen_bwd", "conv1d_ssd_update"}
+    assert packed < set(names) and len(names) == 18   # (those do it in C++)
+    for name in sorted(set(names) - packed):
+        f = getattr(binding, name)
+        at = list(inspect.signature(f).parameters).index("stream")
+        for args, kw in (((None,) * at, dict(stream="s")), ((None,) * at + ("s",), {}), ((None,) * at, {})):
+            entered.clear()
+            try:
+                f(*args, **kw)
+            except (AttributeError, TypeError, ValueError):
+                pass   # (no tensors)
+            assert entered == (["s"] if kw or len(args) > at else []), (name, args, kw)
