@@ -275,6 +275,7 @@ struct Scan {
     if (max_seqlen < 0 || max_seqlen > total)
       refuse("max_seqlen must be the longest sequence's length, at most " + std::to_string(total) + ", got " +
              std::to_string(max_seqlen));
+    if (codes_.has_value() != scales_.has_value()) refuse("checkpoints must be the codes and their scales, got one of them");
     if (codes_) {
       const int64_t e = ssd_checkpoint_slots(total, a.nseq);
       spec(codes_, "checkpoints[0]", {e, h, p, n}, at::kChar, dev);

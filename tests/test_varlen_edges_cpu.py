@@ -3,6 +3,8 @@ mistake, or could not run it safely."""
 import os
 import subprocess
 
+import pytest
+
 from tests.conftest import ROOT
 
 CSRC = os.path.join(ROOT, "state_space_model_scan_amd", "csrc")
@@ -176,3 +178,19 @@ def test_a_named_stream_is_the_calls_current_one(monkeypatch):
             except (AttributeError, TypeError, ValueError):
                 pass   # (no tensors)
             assert entered == (["s"] if kw or len(args) > at else []), (name, args, kw)
+
+
+@pytest.mark.parametrize("given", ["codes", "scales"])
+def test_checkpoints_without_one_of_their_parts(given):
+    """Refused: codes without scales were an access through nothing, scales
+    without codes were dropped."""
+    import torch
+    from state_space_model_scan_amd import binding
+    bf, T, h, n = torch.bfloat16, 70, 2, 32
+    codes = torch.zeros(binding.ssd_checkpoint_slots(T, 1), h, 64, n, dtype=torch.int8)
+    pair = (codes, None) if given == "codes" else (None, torch.ones(codes.shape[:3]))
+    x, dt, B = torch.zeros(T, h, 64, dtype=bf), torch.zeros(T, h, dtype=bf), torch.zeros(T, 1, n, dtype=bf)
+    with pytest.raises(ValueError, match="codes and their scales"):
+        binding.ssd_varlen_fwd(x, dt, -torch.ones(h), B, B, torch.tensor([0, T], dtype=torch.int32), T, checkpoints=pair)
+    with pytest.raises((ValueError, TypeError)):
+        binding.ssd_varlen_bwd(x, dt, -torch.ones(h), B, B, torch.tensor([0, T], dtype=torch.int32), T, x, pair)
