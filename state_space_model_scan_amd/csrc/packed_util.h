@@ -34,7 +34,9 @@ __device__ __forceinline__ float chunk_step(const StepRule &s, float raw, float 
 
 // Running sum over the wave's lanes of d A, as an unevaluated sum of two
 // floats: decays are exponentials of its differences, whose error would
-// otherwise be the rounding of a sum that reaches 100 and more.
+// otherwise be the rounding of a sum that reaches 100 and more.  (Without
+// contraction: with the product d A inside the first sum's fma, its rounding was
+// counted there and in lo.)
 struct TwoSum {
   float hi, lo;
 };
@@ -45,12 +47,14 @@ __device__ __forceinline__ float from_lane(float v) {
 }
 template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ void add_lane(TwoSum &s) {
+#pragma clang fp contract(off)
   const float oh = from_lane<CTRL, ROW_MASK>(s.hi), ol = from_lane<CTRL, ROW_MASK>(s.lo);
   const float t = s.hi + oh, b = t - s.hi;
   s.lo += ol + ((s.hi - (t - b)) + (oh - b));
   s.hi = t;
 }
 __device__ __forceinline__ TwoSum running_sum(float d, float A) {
+#pragma clang fp contract(off)
   TwoSum s;
   s.hi = d * A;
   s.lo = fmaf(d, A, -s.hi);
@@ -74,6 +78,7 @@ __device__ __forceinline__ float exp_sum(TwoSum s) {
 }
 // a - b
 __device__ __forceinline__ TwoSum diff(TwoSum a, TwoSum b) {
+#pragma clang fp contract(off)
   const float t = a.hi - b.hi, v = t - a.hi;
   return {t, ((a.hi - (t - v)) - (b.hi + v)) + (a.lo - b.lo)};
 }

@@ -289,3 +289,39 @@ def _dense_calls():
 def test_explicit_stream_of_dense_rows(name):
     log(f"[stream] dense rows: {name}")
     _check_stream(_dense_calls()[name])
+
+
+# ---- decays after large steps ---------------------------------------------
+
+def _large_steps(n, large, T=130, h=4):
+    g = _gen(n)
+    t = dict(x=_randn(g, T, h, R.P, dtype=bf), A=-8 - 5 * torch.rand(h, generator=g), B=_randn(g, T, 1, n, dtype=bf),
+             C=_randn(g, T, 1, n, dtype=bf), dt=(0.004 + 0.008 * torch.rand(T, h, generator=g)).to(bf))
+    for k in range(0, T, 16):
+        t["dt"][k:k + 2] = large
+    return t, [0, T]
+
+
+@pytest.mark.parametrize("n", [32, 128])
+@pytest.mark.parametrize("large", [1.0, 100.0, 3000.0])
+def test_state_after_large_steps(n, large):
+    """A chunk's running sum far from zero (to -3e5), and small steps after it:
+    what remains of an input at the chunk's end is that of its own distance, to
+    32 bits, and so are the gradients that the same decays carry."""
+    log(f"[decay] state n={n} large={large}")
+    t, cu = _large_steps(n, large)
+    _, _, last, lastm, held = R.scan_fwd(t, cu)
+    state = torch.empty(1, 4, R.P, n, device="cuda")
+    binding.ssd_varlen_fwd(*(t[k].cuda() for k in ("x", "dt", "A", "B", "C")), _ints(cu), cu[-1], ssm_state=state)
+    R.close(state, last, lastm, f32, "state")
+    entries = binding.ssd_checkpoint_slots(cu[-1], 1)
+    codes, scales = torch.zeros(entries, 4, R.P, n, dtype=torch.int8), torch.ones(entries, 4, R.P)
+    for e, (S, _) in held.items():
+        codes[e], scales[e] = R.to_8_bits(S.float())
+    dout = _randn(_gen(n + 1), cu[-1], 4, R.P, dtype=bf)
+    got, ref = _bwd(t, cu, dout, codes, scales, None), R.scan_bwd(t, cu, dout, codes, scales)
+    for k in ("dx", "dB", "dC"):
+        R.close(got[k], *ref[k], bf, k)
+    da, dam = _through(t, cu, dout, codes, scales, None)
+    d = t["dt"].to(R.f64)
+    R.close(got["dA"], (d * da).sum(0), (d * dam).sum(0), f32, "dA")
