@@ -66,15 +66,18 @@ __device__ __forceinline__ TwoSum running_sum(float d, float A) {
   add_lane<0x143, 0xc>(s);   // the first half's to the second
   return s;
 }
-// exp of an unevaluated sum, to the hardware exp2's own rounding: the rounding
-// of the product with log2 e, which an exponent of -10 makes ten times 2^-24,
-// is recovered with an fma.
-__device__ __forceinline__ float exp_sum(TwoSum s) {
+// s log2 e, as an unevaluated sum: the rounding of the product, which a sum of
+// -10 makes ten times 2^-24, is recovered with an fma.
+__device__ __forceinline__ TwoSum times_log2e(TwoSum s) {
   constexpr float kLog2eLo = 1.9259630e-8f;   // log2 e - kLog2e
   const float t = s.hi * kLog2e;
-  const float rest = fmaf(s.hi, kLog2e, -t) + fmaf(s.hi, kLog2eLo, s.lo * kLog2e);
-  const float e = fast_exp2(t);
-  return fmaf(e, rest * kLn2, e);
+  return {t, fmaf(s.hi, kLog2e, -t) + fmaf(s.hi, kLog2eLo, s.lo * kLog2e)};
+}
+// exp of an unevaluated sum, to the hardware exp2's own rounding.
+__device__ __forceinline__ float exp_sum(TwoSum s) {
+  const TwoSum t = times_log2e(s);
+  const float e = fast_exp2(t.hi);
+  return fmaf(e, t.lo * kLn2, e);
 }
 // a - b
 __device__ __forceinline__ TwoSum diff(TwoSum a, TwoSum b) {

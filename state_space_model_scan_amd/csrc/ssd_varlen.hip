@@ -74,8 +74,8 @@ struct ScanLds {
   uint16_t x[2][kQ * kP];                             // [t][p]
   uint16_t C[FULL ? kQ * N : 8];                      // [t][n]
   uint16_t M[2][FULL ? (kZeroTile + 1) * kTile : 8];    // head, tail
-  // running sum (times log2 e), step, exp(cs), and the state update's weight, per token
-  float cs[2][kQ], dt[2][kQ], e[2][kQ], w[2][kQ];
+  // running sum times log2 e (two floats), step, exp(cs), and the state update's weight, per token
+  float cs[2][kQ], cl[2][kQ], dt[2][kQ], e[2][kQ], w[2][kQ];
 };
 
 // The transposed operand of B for state tile a of the k step kk: lane m's row
@@ -159,7 +159,9 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
     const TwoSum cs = running_sum(d, Ah);
     const TwoSum end = {__int_as_float(__builtin_amdgcn_readlane(__float_as_int(cs.hi), 63)),
                         __int_as_float(__builtin_amdgcn_readlane(__float_as_int(cs.lo), 63))};
-    sm.cs[b][l] = cs.hi * kLog2e;
+    const TwoSum turns = times_log2e(cs);
+    sm.cs[b][l] = turns.hi;
+    sm.cl[b][l] = turns.lo;
     sm.dt[b][l] = d;
     sm.e[b][l] = exp_sum(cs);
     sm.w[b][l] = exp_sum(diff(end, cs)) * d;
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
       if (next < kQ) place(next);   // the sequence's end
       fetch(b ^ 1);
     }
-    const float *cs = sm.cs[b], *dt = sm.dt[b], *e0 = sm.e[b], *we = sm.w[b];
+    const float *cs = sm.cs[b], *cl = sm.cl[b], *dt = sm.dt[b], *e0 = sm.e[b], *we = sm.w[b];
     uint16_t *X = sm.x[b], *B = sm.B[b];
 
     if constexpr (FULL) {
@@ -299,16 +301,17 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
         for (int kk = 0; kk < KN; ++kk)
 #pragma unroll
           for (int tb = 0; tb <= WT; ++tb) acc[tb] = mfma(frag<N>(l, B, 16 * tb, 32 * kk), cop[kk], acc[tb]);
-        const float cst = cs[t];
+        const float cst = cs[t], clt = cl[t];
 #pragma unroll
         for (int tb = 0; tb <= WT; ++tb) {
           const float4 cs4 = *reinterpret_cast<const float4 *>(&cs[16 * tb + 4 * kq]);
+          const float4 cl4 = *reinterpret_cast<const float4 *>(&cl[16 * tb + 4 * kq]);
           const float4 dt4 = *reinterpret_cast<const float4 *>(&dt[16 * tb + 4 * kq]);
-          const float csv[4] = {cs4.x, cs4.y, cs4.z, cs4.w}, dtv[4] = {dt4.x, dt4.y, dt4.z, dt4.w};
+          const float csv[4] = {cs4.x, cs4.y, cs4.z, cs4.w}, clv[4] = {cl4.x, cl4.y, cl4.z, cl4.w}, dtv[4] = {dt4.x, dt4.y, dt4.z, dt4.w};
           float m[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float v = acc[tb][i] * fast_exp2(cst - csv[i]) * dtv[i];
+            const float v = acc[tb][i] * fast_exp2((cst - csv[i]) + (clt - clv[i])) * dtv[i];
             m[i] = (tb < WT || 4 * kq + i <= r) ? v : 0.0f;
           }
           uint2 hi, lo;

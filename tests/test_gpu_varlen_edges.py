@@ -325,3 +325,14 @@ def test_state_after_large_steps(n, large):
     da, dam = _through(t, cu, dout, codes, scales, None)
     d = t["dt"].to(R.f64)
     R.close(got["dA"], (d * da).sum(0), (d * dam).sum(0), f32, "dA")
+
+
+@pytest.mark.parametrize("n", [32, 128])
+@pytest.mark.parametrize("large", [1.0, 100.0, 3000.0])
+def test_outputs_after_large_steps(n, large):
+    """The same for the outputs, whose decays are between two tokens."""
+    log(f"[decay] outputs n={n} large={large}")
+    t, cu = _large_steps(n, large)
+    ref, mag, *_ = R.scan_fwd(t, cu)
+    out = binding.ssd_varlen_fwd(*(t[k].cuda() for k in ("x", "dt", "A", "B", "C")), _ints(cu), cu[-1])
+    R.close(out, ref, mag, bf, "out")
