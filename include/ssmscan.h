@@ -634,7 +634,8 @@ int causal_conv1d_varlen_bwd_workspace_size(const causal_conv1d_varlen_args_t *a
 
 /* Arguments of ssd_varlen_fwd.  x, B, C, z and out must be 16-byte aligned,
  * their strides multiples of 8; those of x, B, C and the backward's dout at
- * most 2^24 elements. */
+ * most 2^24 elements.  ssm_state, checkpoints and workspace must be 16-byte
+ * aligned too. */
 typedef struct ssd_varlen_args {
   int64_t total, nseq, max_seqlen;              /* max_seqlen: at least the longest sequence */
   int64_t nheads, headdim, dstate, ngroups;
@@ -683,6 +684,7 @@ int64_t ssd_checkpoint_slots(int64_t total, int64_t nseq);
  * and the gradients, caller-allocated and fully overwritten. */
 typedef struct ssd_varlen_bwd_args {
   ssd_varlen_args_t fwd;
+  /* (dout, dx, dB, dC and the states' gradients as x: 16-byte aligned) */
   int64_t code_entry_stride, code_head_stride;  /* multiples of 16; as the forward writes: h p n, p n */
   int64_t scale_entry_stride, scale_head_stride;  /* h p, p */
   const void *dout; int64_t dout_stride;        /* (total, h, p) io */
@@ -729,7 +731,7 @@ typedef struct conv1d_ssd_update_args {
   int32_t dt_softplus, dt_limit;
   float dt_min, dt_max;
   void *conv_state; int64_t state_len;          /* ring cache, width <= state_len <= SSM_MAX_CONV_STATE */
-  float *ssm_state;                             /* cache */
+  float *ssm_state;                             /* cache, 16-byte aligned */
   int64_t state_slots;                          /* entries of both caches */
   const int32_t *cache_seqlens;                 /* (batch) or NULL (every request is new) */
   const int32_t *slots;                         /* (batch) or NULL */

@@ -95,15 +95,12 @@ __device__ __forceinline__ void ring_input(const ConvVarParams &p, const RingOf 
 // cost a wave more of the L1's time than a run's inputs and outputs.  The row
 // of channel c is kept at place_of(c), which spreads the lanes' reads over the
 // banks.
-struct __attribute__((aligned(4))) Row {   // of weights, at any address of a float
-  float v[kW];
-};
 template <int NV>
 struct Weights {
   float4 w[NV > 1 ? 64 * NV : 1];
   static __device__ __forceinline__ int place_of(int c) { return c ^ ((c / NV) & (NV - 1)); }
   static __device__ __forceinline__ float4 row(const ConvVarParams &p, int64_t c) {
-    const Row r = reinterpret_cast<const Row *>(p.w)[c];
+    const Row4 r = reinterpret_cast<const Row4 *>(p.w)[c];
     return make_float4(r.v[0], r.v[1], r.v[2], r.v[3]);
   }
   // (a barrier belongs between the two)

@@ -233,6 +233,11 @@ __device__ __forceinline__ float dot_bcast(float c, const float (&x)[N]) {
   return y;
 }
 
+// Four floats at any address of a float (a row of the short conv's weights).
+struct __attribute__((aligned(4))) Row4 {
+  float v[4];
+};
+
 // The last i in [0, n) with at_or_before(i), where that holds up to some i and
 // 0 stands for none.  All 64 lanes probe at once, so one round of loads finds
 // it among 64 and two among 4096; every lane has to be there.

@@ -79,6 +79,12 @@ int io_of(const Tensor &t, const char *name, int64_t ndim) {
 
 Tensor dense(const Tensor &t) { return t.contiguous(); }
 Opt dense(const Opt &t) { return t ? Opt(t->contiguous()) : Opt(); }
+// ... and 16-byte aligned
+Opt dense16(const Opt &t) {
+  if (!t) return {};
+  const Tensor d = t->contiguous();
+  return reinterpret_cast<uintptr_t>(d.data_ptr()) % 16 == 0 ? d : d.clone();
+}
 
 // t as the library takes a packed tensor: whatever a token holds dense, any
 // stride from token to token; with vec, the first element 16-byte aligned and
@@ -361,7 +367,7 @@ BwdOut scan_bwd(const Tensor &x, const Tensor &dt, const Tensor &A, const Tensor
   spec(dout_, "dout", x.sizes(), io, dev);
   spec(dfin_, "dfinal_states", {s.a.nseq, h, p, n}, f, dev);
   const Tensor dout = tokens(dout_, 8);
-  const Opt dfin = dense(dfin_);
+  const Opt dfin = dense16(dfin_);
   on_gpu(dev);
   const Tensor dx = tokens_out(dx_, "dx", x.sizes(), io, dev, 8), ddt = tokens_out(ddt_, "ddt", dt.sizes(), io, dev);
   const Tensor dB = tokens_out(dB_, "dB", B.sizes(), io, dev, 8), dC = tokens_out(dC_, "dC", C.sizes(), io, dev, 8);

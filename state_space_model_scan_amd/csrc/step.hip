@@ -81,15 +81,14 @@ __global__ void __launch_bounds__(256) step_kernel(const StepParams p) {
     const bool isx = i < ROWS;
     const int64_t c = isx ? static_cast<int64_t>(h) * kP + row0 + i
                           : hp + (i - ROWS < N ? static_cast<int64_t>(g) * N + (i - ROWS) : (p.ngroups + g) * N + (i - ROWS - N));
-    const float4 w = *reinterpret_cast<const float4 *>(p.w + c * kW);
-    const float wk[kW] = {w.x, w.y, w.z, w.w};
+    const Row4 w = reinterpret_cast<const Row4 *>(p.w)[c];
     const int64_t rbase = ((slot < 0 ? 0 : slot) * channels + c) * p.ring_len;
     float v = p.wb ? p.wb[c] : 0.0f;
     const float now = load_io<IO>(p.xBC, b * p.xs + c);
-    v = fmaf(wk[kW - 1], now, v);
+    v = fmaf(w.v[kW - 1], now, v);
 #pragma unroll
     for (int back = 1; back < kW; ++back)
-      if (seen >= back) v = fmaf(wk[kW - 1 - back], load_io<IO>(p.ring, rbase + static_cast<uint32_t>(seen - back) % p.ring_len), v);
+      if (seen >= back) v = fmaf(w.v[kW - 1 - back], load_io<IO>(p.ring, rbase + static_cast<uint32_t>(seen - back) % p.ring_len), v);
     if (p.silu) v = silu_f(v);
     su[i] = v;
     if (slot >= 0 && (isx || (static_cast<uint32_t>(h) == g * p.per_group && row0 == 0))) {

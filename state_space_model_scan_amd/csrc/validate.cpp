@@ -385,7 +385,7 @@ extern "C" int conv1d_ssd_update_validate(const conv1d_ssd_update_args_t *a) {
       !product_fits(a->state_slots, hp, a->dstate) || !product_fits(a->state_slots, c, a->state_len))
     return SSM_ERR_SHAPE;
   if (!a->xBC || !a->dt || !a->A || !a->conv_weight || !a->conv_state || !a->ssm_state || !a->out) return SSM_ERR_NULL;
-  if ((bits(a->ssm_state) | bits(a->conv_weight)) & 15u) return SSM_ERR_UNSUPPORTED;
+  if (bits(a->ssm_state) & 15u) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 

@@ -336,3 +336,35 @@ def test_outputs_after_large_steps(n, large):
     ref, mag, *_ = R.scan_fwd(t, cu)
     out = binding.ssd_varlen_fwd(*(t[k].cuda() for k in ("x", "dt", "A", "B", "C")), _ints(cu), cu[-1])
     R.close(out, ref, mag, bf, "out")
+
+
+# ---- dense inputs at any address ------------------------------------------
+
+def _shifted(t):
+    """t, dense, four bytes behind a 16-byte address."""
+    room = torch.empty(t.numel() + 1, dtype=f32, device="cuda")
+    v = room[1:].view(t.shape)
+    v.copy_(t)
+    assert v.is_contiguous() and v.data_ptr() % 16 == 4
+    return v
+
+
+def test_parameters_at_any_address():
+    """Weights and gradients that lie in one flat buffer, as a sharded optimiser
+    keeps them."""
+    log("[address]")
+    g, h, n, b = _gen(2), 3, 32, 5
+    ch = h * R.P + 2 * n
+    xbc, dt, A = _randn(g, b, ch, dtype=bf).cuda(), _randn(g, b, h, dtype=bf).cuda(), -1 - torch.rand(h, generator=g).cuda()
+    w, bias = _randn(g, ch, 4).cuda(), _randn(g, ch).cuda()
+    outs = []
+    for wk, bk in ((w, bias), (_shifted(w), _shifted(bias))):
+        ring, state = torch.zeros(b, ch, 4, dtype=bf, device="cuda"), torch.zeros(b, h, R.P, n, device="cuda")
+        outs.append((binding.conv1d_ssd_update(xbc, dt, A, wk, ring, state, None, conv_bias=bk, dt_softplus=True), state))
+        outs[-1] += (binding.causal_conv1d_varlen_fwd(xbc, wk, _ints([0, b]), bias=bk),)
+    assert all(torch.equal(p, q) for p, q in zip(*outs))
+    t, cu, dout, codes, scales, dlast = _steps_case(1, (70, 3), 2, 1, 32, 1.0)
+    want = _bwd(t, cu, dout, codes, scales, dlast)
+    got = binding.ssd_varlen_bwd(*(t[k].cuda() for k in ("x", "dt", "A", "B", "C")), _ints(cu), 70, dout.cuda(),
+                                 (codes.cuda(), scales.cuda()), dfinal_states=_shifted(dlast.cuda()))
+    assert all(torch.equal(want[k], got[k]) for k in want)

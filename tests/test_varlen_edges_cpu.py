@@ -194,3 +194,9 @@ def test_checkpoints_without_one_of_their_parts(given):
         binding.ssd_varlen_fwd(x, dt, -torch.ones(h), B, B, torch.tensor([0, T], dtype=torch.int32), T, checkpoints=pair)
     with pytest.raises((ValueError, TypeError)):
         binding.ssd_varlen_bwd(x, dt, -torch.ones(h), B, B, torch.tensor([0, T], dtype=torch.int32), T, x, pair)
+
+
+def test_weights_at_any_address():
+    from state_space_model_scan_amd import _lib
+    from tests.test_varlen_cpu import FAKE, _step, _st
+    assert _st("conv1d_ssd_update", _step(conv_weight=FAKE + 4)) == _lib.SSM_OK
