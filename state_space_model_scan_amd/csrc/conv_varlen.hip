@@ -553,7 +553,7 @@ extern "C" int causal_conv1d_varlen_fwd(const causal_conv1d_varlen_args_t *a, vo
   const int nv = !wide ? 1 : a->io_dtype == SSM_F32 ? 4 : 8;
   const int run = fwd_run(a, nv);
   const int64_t gx = blocks_of(a->total, run), gy = (a->channels + 64 * nv - 1) / (64 * nv);
-  if (gy > 65535) return SSM_ERR_SHAPE;
+  if (gy > 65535 || !grid_fits(gx, 64 * kRows)) return SSM_ERR_SHAPE;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * kRows);
   auto launch = [&](auto io, auto vec) {
@@ -590,7 +590,7 @@ extern "C" int causal_conv1d_varlen_bwd(const causal_conv1d_varlen_args_t *a, vo
   const int nv = !wide ? 1 : a->io_dtype == SSM_F32 ? 4 : kBwdVec;
   const int run = bwd_run(a, nv);
   const int64_t gx = blocks_of(a->total, run), gy = (a->channels + 64 * nv - 1) / (64 * nv);
-  if (gy > 65535) return SSM_ERR_SHAPE;
+  if (gy > 65535 || !grid_fits(gx, 64 * kRows)) return SSM_ERR_SHAPE;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), block(64 * kRows);
   auto launch = [&](auto io, auto vec) {

@@ -19,6 +19,9 @@ int cu_count_cached();
 // cached per kernel.
 int blocks_per_cu(const void *f, int block);
 
+// A launch's grid fits in x: the device counts its threads in 32 bits.
+inline bool grid_fits(int64_t blocks, int64_t threads) { return blocks <= 0xffffffffLL / threads; }
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // ---------------------------------------------------------------------------

@@ -579,11 +579,11 @@ extern "C" int ssd_varlen_fwd_workspace_size(const ssd_varlen_args_t *a, size_t 
 extern "C" int ssd_varlen_fwd(const ssd_varlen_args_t *a, void *stream_ptr) {
   const int st = ssd_varlen_fwd_validate(a);
   if (st != SSM_OK) return st;
+  const int64_t blocks = a->nseq * a->nheads;
+  if (!grid_fits(blocks, 256)) return SSM_ERR_SHAPE;
   const VarPlan pl = var_plan(a, cu_count_cached());
   if (pl.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < pl.ws_bytes)) return SSM_ERR_WORKSPACE;
   if (pl.ws_bytes > 0 && !aligned16(a->workspace)) return SSM_ERR_UNSUPPORTED;
-  const int64_t blocks = a->nseq * a->nheads;
-  if (blocks > 0x7fffffffLL) return SSM_ERR_SHAPE;
   ScanParams p{};
   p.x = static_cast<const uint16_t *>(a->x); p.xs = a->x_stride;
   p.dt = static_cast<const uint16_t *>(a->dt); p.dts = a->dt_stride;

@@ -924,11 +924,13 @@ extern "C" int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *a, void *stream_ptr) 
   if (st != SSM_OK) return st;
   const ssd_varlen_args_t &f = a->fwd;
   const BwdPlan pl = bwd_plan(&f, cu_count_cached());
+  // sum_kernel's workgroups for dB and dC, where there are head blocks to add
+  const int64_t bc_blocks = pl.hb_per_group > 1 ? (f.total * f.ngroups * f.dstate + 1023) / 1024 : 0;
+  if (!grid_fits(f.nseq * f.nheads, 256) || !grid_fits(pl.entries, 512) || f.ngroups * pl.hb_per_group > 65535 ||
+      !grid_fits(2 * bc_blocks + f.nheads * kP, 256))
+    return SSM_ERR_SHAPE;
   if (!a->workspace || a->workspace_bytes < pl.bytes) return SSM_ERR_WORKSPACE;
   if (!aligned16(a->workspace)) return SSM_ERR_UNSUPPORTED;
-  if (f.nseq * f.nheads > 0x7fffffffLL || pl.entries > 0x7fffffffLL || f.ngroups * pl.hb_per_group > 65535 ||
-      f.total * f.ngroups * f.dstate > (0x3fffffffLL << 10))
-    return SSM_ERR_SHAPE;
   char *ws = static_cast<char *>(a->workspace);
   BwdParams p{};
   p.x = static_cast<const uint16_t *>(f.x); p.xs = f.x_stride;
@@ -969,7 +971,7 @@ extern "C" int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *a, void *stream_ptr) 
   q.dA = a->dA; q.ddt_bias = f.dt_bias ? a->ddt_bias : nullptr; q.dD = a->dD;
   q.total = f.total; q.row = f.ngroups * f.dstate; q.entries = pl.entries; q.nheads = f.nheads;
   q.hb = pl.hb_per_group;
-  q.bc_blocks = p.ws_bc ? (f.total * q.row + 1023) / 1024 : 0;
+  q.bc_blocks = bc_blocks;
   q.sum_blocks = (2 * f.nheads + 7) / 8;
   q.dd_cols = f.D ? f.nheads * (f.D_per_channel ? kP : 1) : 0;
   const int64_t blocks = 2 * q.bc_blocks + q.sum_blocks + (q.dd_cols + 7) / 8;

@@ -1,5 +1,6 @@
 """Host checks of the packed-token operators where a GPU run could not show the
 mistake, or could not run it safely."""
+import ctypes
 import os
 import subprocess
 
@@ -200,3 +201,20 @@ def test_weights_at_any_address():
     from state_space_model_scan_amd import _lib
     from tests.test_varlen_cpu import FAKE, _step, _st
     assert _st("conv1d_ssd_update", _step(conv_weight=FAKE + 4)) == _lib.SSM_OK
+
+
+def test_grids_that_the_device_cannot_count_are_refused():
+    """A launch has less than 2^32 threads in x: refused before anything is
+    launched, with the shape's status and not the runtime's."""
+    from state_space_model_scan_amd import _lib
+    from tests.test_varlen_cpu import _conv, _scan, _scan_bwd
+
+    def st(name, a):
+        return getattr(_lib.lib(), name)(ctypes.byref(a), None)
+
+    assert st("causal_conv1d_varlen_fwd", _conv(total=900_000_000)) == _lib.SSM_ERR_SHAPE
+    many = dict(total=1 << 23, nseq=1 << 22, max_seqlen=4)   # 2^24 (sequence, head) pairs, 2^22 + 2^17 checkpoint entries
+    assert st("ssd_varlen_fwd", _scan(**many)) == _lib.SSM_ERR_SHAPE
+    assert st("ssd_varlen_bwd", _scan_bwd(many)) == _lib.SSM_ERR_SHAPE
+    many.update(nseq=(1 << 22) - 1)
+    assert st("ssd_varlen_bwd", _scan_bwd(many)) == _lib.SSM_ERR_WORKSPACE
