@@ -67,6 +67,11 @@ __device__ __forceinline__ void split_bf2(float a, float b, uint32_t &hi, uint32
   hi = pack_bf2(a, b);
   lo = pack_bf2(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xffff0000u));
 }
+// ... and what head and tail leave of a and b: with it all 24 bits
+__device__ __forceinline__ uint32_t third_bf2(float a, float b, uint32_t hi, uint32_t lo) {
+  return pack_bf2(a - __uint_as_float(hi << 16) - __uint_as_float(lo << 16),
+                  b - __uint_as_float(hi & 0xffff0000u) - __uint_as_float(lo & 0xffff0000u));
+}
 // the 16-bit halves of two words side by side (one byte permute): the low
 // halves (HIGH = false) or the high halves of a and b, a's in the low half
 template <bool HIGH>

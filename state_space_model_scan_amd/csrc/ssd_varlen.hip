@@ -427,8 +427,7 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
         const float a = bf2f(raw_bits(xw, i)) * we[32 * kk + 8 * kq + i];
         const float d = bf2f(raw_bits(xw, i + 1)) * we[32 * kk + 8 * kq + i + 1];
         split_bf2(a, d, x0[i / 2], x1[i / 2]);
-        x2[i / 2] = pack_bf2(a - __uint_as_float(x0[i / 2] << 16) - __uint_as_float(x1[i / 2] << 16),
-                             d - __uint_as_float(x0[i / 2] & 0xffff0000u) - __uint_as_float(x1[i / 2] & 0xffff0000u));
+        x2[i / 2] = third_bf2(a, d, x0[i / 2], x1[i / 2]);
       }
       const bf16x8 f0 = __builtin_bit_cast(bf16x8, make_uint4(x0[0], x0[1], x0[2], x0[3]));
       const bf16x8 f1 = __builtin_bit_cast(bf16x8, make_uint4(x1[0], x1[1], x1[2], x1[3]));

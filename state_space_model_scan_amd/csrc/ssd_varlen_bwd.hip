@@ -22,8 +22,7 @@
 // whole of a gradient that has to vanish, as for a sequence of one token.)
 //
 // Three launches.  (1) adjoint_kernel walks every (sequence, head)'s chunks
-// backwards and leaves each chunk's dH, as a bf16 head and tail (16
-// significant bits), in the workspace; with few (sequence, head) pairs the
+// backwards and leaves each chunk's dH in the workspace; with few (sequence, head) pairs the
 // sequence is cut into segments as in the forward.  (2) chunk_kernel takes one
 // chunk and a block of heads of one group: everything but dH is local to the
 // chunk.  S is formed once for the group.  dB's and dC's pair products are
@@ -33,9 +32,16 @@
 // blocks' dB and dC and the chunks' dA, dD and ddt_bias, in a fixed order.
 //
 // Precision: x, B, C, g and the dequantised H (seven bits times a power of
-// two) are exact in bf16; dH, S L and the summed M L dt' enter as head and
-// tail, two products each, as the forward's derived operands do: one rounding
-// to bf16 would put 2^-9 into dA and ddt_bias, which are 32-bit sums.
+// two) are exact in bf16.  dA and ddt_bias are 32-bit sums, so what they take
+// from a product is formed from all 24 bits: dH enters r and <dH, H> in three
+// parts (with a head and a tail, 2^-17 of it, r alone put 1e-6 into dA).  What
+// only reaches an output in bf16 enters as head and tail: dH in dB, S L and the
+// summed M L dt'.  The matrix unit rounds an accumulator that is below the
+// products' sum towards minus infinity (measured on the device), so that sums of
+// products would all be off to one side, and the sums over tokens with them: dA
+// by 9e-7 at 8 x 2048 tokens, whatever the sign of g.  So every second token's B
+// and every second state's H enter negated, and the adjoint changes its sign from
+// chunk to chunk (7e-8).
 //
 // Operand layout of the 16x16x32 product as in ssd.hip.  Tiles are kept
 // row-major in LDS, and an operand that runs along the other index is read
@@ -63,7 +69,7 @@ struct BwdParams {
   const float *scales;
   uint16_t *dx, *ddt, *dB, *dC;
   float *dinit;
-  uint16_t *ws_dh;               // (entries, heads, 2, p, n): head, tail
+  float *ws_dh;                  // (entries, heads, p, n), as adjoint_kernel's lanes hold it
   float *ws_state, *ws_decay;    // adjoint segments
   float *ws_bc;                  // (2, head blocks of a group, total, groups, n) or NULL (one block: dB, dC directly)
   float *ws_sum;                 // (entries, heads, 2): dA, ddt_bias
@@ -82,6 +88,9 @@ struct BwdParams {
 // the forward holds the state.  STORE: write every chunk's dH; otherwise find
 // the segment's adjoint from zero and its decay.
 // ---------------------------------------------------------------------------
+// The sign with which an entry's dH is kept (see Precision).
+__device__ __forceinline__ float entry_sign(int64_t entry) { return entry & 1 ? -1.0f : 1.0f; }
+
 template <int N>
 struct AdjointLds {
   uint16_t C[2][kQ * N], g[2][kQ * kP];   // [t][n], [t][p]; the next chunk's are on their way into the other half
@@ -125,7 +134,7 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
     float v;
     const TwoSum cs = running_sum(chunk_step(p.step, bf2f(static_cast<uint16_t>(raw)), bias, l < chunk_len(c), v), Ah);
     const float e = exp_sum(cs);
-    sm.e[b][l] = l < chunk_len(c) ? e : 0.0f;
+    sm.e[b][l] = l < chunk_len(c) ? entry_sign(q.entry + c - 1) * e : 0.0f;
     if (l == 63) sm.end[b] = e;
   };
   if (c_begin < c_end) {
@@ -163,6 +172,11 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
       }
     }
   }
+  {
+    const float sign = entry_sign(q.entry + c_end - 1);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) acc[nt] *= sign;
+  }
   float decay = 1.0f;
   for (int64_t c = c_end - 1; c >= c_begin; --c) {
     const int b = static_cast<int>((c_end - 1 - c) & 1);
@@ -184,8 +198,7 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
       for (int i = 0; i < 8; i += 2) {
         const float x = bf2f(raw_bits(gt, i)) * e[i], y = bf2f(raw_bits(gt, i + 1)) * e[i + 1];
         split_bf2(x, y, g0[i / 2], g1[i / 2]);
-        g2[i / 2] = pack_bf2(x - __uint_as_float(g0[i / 2] << 16) - __uint_as_float(g1[i / 2] << 16),
-                             y - __uint_as_float(g0[i / 2] & 0xffff0000u) - __uint_as_float(g1[i / 2] & 0xffff0000u));
+        g2[i / 2] = third_bf2(x, y, g0[i / 2], g1[i / 2]);
       }
       part[kk][0] = __builtin_bit_cast(bf16x8, make_uint4(g0[0], g0[1], g0[2], g0[3]));
       part[kk][1] = __builtin_bit_cast(bf16x8, make_uint4(g1[0], g1[1], g1[2], g1[3]));
@@ -195,25 +208,21 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
     // workgroup is at about the same place of its chunk, so stores that all come
     // at its start leave the memory idle for the rest of it (213 us for 196 at
     // 8 x 2048 tokens, 80 heads; without any store 108).
-    uint16_t *dh = STORE ? p.ws_dh + ((q.entry + c) * p.nheads + h) * 2 * kP * N + (16 * w * N + 8 * l) : nullptr;
+    float *dh = STORE ? p.ws_dh + ((q.entry + c) * p.nheads + h) * kP * N + (16 * w * N + 4 * l) : nullptr;
 #pragma unroll
     for (int nt = 0; nt < NT; nt += 2) {
       if constexpr (STORE) {
-        // as the lanes hold it: a lane's eight states of two tiles are 16 bytes,
-        // and a wave's store one KiB in a row
+        // as the lanes hold it: a lane's four states of a tile are 16 bytes, and
+        // a wave's store one KiB in a row
         __builtin_amdgcn_sched_barrier(0);
-        uint4 hi, lo;
-        split_bf2(acc[nt][0], acc[nt][1], hi.x, lo.x);
-        split_bf2(acc[nt][2], acc[nt][3], hi.y, lo.y);
-        split_bf2(acc[nt + 1][0], acc[nt + 1][1], hi.z, lo.z);
-        split_bf2(acc[nt + 1][2], acc[nt + 1][3], hi.w, lo.w);
-        *reinterpret_cast<uint4 *>(dh + 256 * nt) = hi;
-        *reinterpret_cast<uint4 *>(dh + kP * N + 256 * nt) = lo;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<float4 *>(dh + 256 * (nt + j)) = make_float4(acc[nt + j][0], acc[nt + j][1], acc[nt + j][2], acc[nt + j][3]);
       }
       bf16x8 ct[2][kQ / 32];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        acc[nt + j] *= end;
+        acc[nt + j] *= -end;
 #pragma unroll
         for (int kk = 0; kk < kQ / 32; ++kk) ct[j][kk] = frag_t<N>(l, sm.C[b], 32 * kk, 16 * (nt + j));
       }
@@ -234,9 +243,12 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
     if (tid == 0) p.ws_decay[(seg - 1) * SH + sh] = decay;
   }
   if (to) {
+    const float sign = entry_sign(q.entry + c_begin - 1);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      acc[nt] *= sign;
       *reinterpret_cast<float4 *>(to + 16 * nt) = make_float4(acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+    }
   }
 }
 
@@ -246,7 +258,7 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
 
 template <int N>
 struct ChunkLds {
-  uint16_t B[kQ * N], C[kQ * N];          // [t][n]
+  uint16_t B[kQ * N], C[kQ * N];          // [t][n]; from head to head B's place holds dH's third part [p][n]
   uint16_t x[kQ * kP], g[kQ * kP];        // [t][p]
   uint16_t H[kP * N];                     // [p][n]
   uint16_t dh[2][kP * N > kQ * kQ ? kP * N : kQ * kQ];   // [p][n] head, tail; at the end M L dt' [j][i]
@@ -283,8 +295,9 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   constexpr int KN = N / 32;          // k steps over n
   constexpr int IT = NT / 2;          // token tiles of a wave in the (n, token) products
   constexpr int G8 = N / 8;
-  constexpr int BC = (kQ * G8 + 511) / 512;     // 16-byte pieces of a B, C or dH tile per thread
+  constexpr int BC = (kQ * G8 + 511) / 512;     // 16-byte pieces of a B or C tile per thread
   constexpr int HPIECES = kP * N / 16;          // 16-code pieces of H
+  static_assert(kP == kQ, "dH's third part in B's place");
   extern __shared__ __attribute__((aligned(16))) char smem[];
   ChunkLds<N> &sm = *reinterpret_cast<ChunkLds<N> *>(smem);
   const int tid = threadIdx.x, lane = tid & 63;
@@ -320,7 +333,8 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
 
   // ---- this thread's pieces of a head's tiles, loaded one head ahead
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 xv, gv, hv, dv[2][BC];
+  uint4 xv, gv, hv;
+  float4 dv[KN];   // of dH: kP N / 4 pieces of four
   float sc = 0.0f;
   // what is the same for the wave steps from head to head, what is the lane's stays
   const int my_t = tid >> 3, my_p = (tid & 7) * 8, my_row = my_t < len ? my_t : len - 1;
@@ -329,7 +343,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   const uint16_t *xh = p.x + t0 * p.xs + h0 * kP, *gh = p.g + t0 * p.gs + h0 * kP;
   const int8_t *code_h = p.codes + entry * p.code_entry + h0 * p.code_head;
   const float *scale_h = p.scales + entry * p.scale_entry + h0 * p.scale_head;
-  const uint16_t *dh_h = p.ws_dh + (entry * p.nheads + h0) * 2 * kP * N;
+  const float *dh_h = p.ws_dh + (entry * p.nheads + h0) * kP * N;
   auto load_head = [&] {   // tokens beyond the chunk's end repeat the last one here
     xv = ld8_raw(xh + x_at);
     gv = ld8_raw(gh + g_at);
@@ -338,18 +352,12 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       sc = scale_h[16 * tid / N];
     }
 #pragma unroll
-    for (int k = 0; k < BC; ++k) {
-      const int piece = tid + 512 * k;
-      if (piece < kP * G8) {
-        dv[0][k] = ld8_raw(dh_h + 8 * piece);
-        dv[1][k] = ld8_raw(dh_h + kP * N + 8 * piece);
-      }
-    }
+    for (int k = 0; k < KN; ++k) dv[k] = *reinterpret_cast<const float4 *>(dh_h + 4 * (tid + 512 * k));
     xh += kP;
     gh += kP;
     code_h += p.code_head;
     scale_h += p.scale_head;
-    dh_h += 2 * kP * N;
+    dh_h += kP * N;
   };
   load_head();
 
@@ -406,8 +414,18 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       for (int it = JB; it < 4; ++it) S[it - JB] = mfma(frag<N>(l, sm.C, 16 * it, 32 * kk), bf, S[it - JB]);
     }
   });
+  // the wave's block of B, which every head's dH is multiplied with
+  bf16x8 Bj[KN];
+#pragma unroll
+  for (int kk = 0; kk < KN; ++kk) {
+    const uint4 b = __builtin_bit_cast(uint4, frag<N>(l, sm.B, 16 * jb, 32 * kk));
+    const uint32_t sign = ((l ^ static_cast<int>(entry)) & 1) * 0x80008000u;   // negated for every second token, and as dH
+    Bj[kk] = __builtin_bit_cast(bf16x8, make_uint4(b.x ^ sign, b.y ^ sign, b.z ^ sign, b.w ^ sign));
+  }
+  __syncthreads();   // and B's place is free
 
   uint16_t *dx_h = p.dx + t0 * p.dxs + h0 * kP;
+  const float sign = entry_sign(entry);   // dH's
   for (int k = 0; k < nh; ++k, dx_h += kP) {
     // the lane anew for every head: the tiles' addresses are then formed where
     // they are used; kept over the loop they would take the registers
@@ -433,23 +451,24 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
           const uint32_t word = raw_word(hv, 2 * hf + (i >> 1)) ^ 0x80808080u;
           const int sh = (i & 1) * 16;
           o[i] = pack_bf2(fmaf(static_cast<float>((word >> sh) & 0xffu), sc, off),
-                          fmaf(static_cast<float>((word >> (sh + 8)) & 0xffu), sc, off));
+                          fmaf(static_cast<float>((word >> (sh + 8)) & 0xffu), -sc, -off));   // every second state negated
         }
         *reinterpret_cast<uint4 *>(&sm.H[tile_at<N>(row, n0 + 8 * hf)]) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
 #pragma unroll
-    for (int b = 0; b < BC; ++b) {
-      const int piece = tid + 512 * b;
-      if (piece < kP * G8) {   // out of adjoint_kernel's order
-        const int row = piece / (64 * KN) * 16 + (piece & 15), n0 = piece / 64 % KN * 32 + (piece >> 4 & 3) * 4;
-        const int o0 = tile_at<N>(row, n0), o1 = tile_at<N>(row, n0 + 16);
+    for (int b = 0; b < KN; ++b) {   // out of adjoint_kernel's order: 16 x 16 tiles, four states a lane
+      const int tile = (tid >> 6) + 8 * b;
+      const int o = tile_at<N>(tile / NT * 16 + (tid & 15), tile % NT * 16 + (tid >> 4 & 3) * 4);
+      const float4 v = dv[b];
+      uint2 part[3];
+      split_bf2(v.x, v.y, part[0].x, part[1].x);
+      split_bf2(v.z, v.w, part[0].y, part[1].y);
+      part[2].x = third_bf2(v.x, v.y, part[0].x, part[1].x);
+      part[2].y = third_bf2(v.z, v.w, part[0].y, part[1].y);
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          *reinterpret_cast<uint2 *>(&sm.dh[a][o0]) = make_uint2(dv[a][b].x, dv[a][b].y);
-          *reinterpret_cast<uint2 *>(&sm.dh[a][o1]) = make_uint2(dv[a][b].z, dv[a][b].w);
-        }
-      }
+      for (int a = 0; a < 2; ++a) *reinterpret_cast<uint2 *>(&sm.dh[a][o]) = part[a];
+      *reinterpret_cast<uint2 *>(&sm.B[o]) = part[2];
     }
     __syncthreads();
     if (k + 1 < nh) load_head();
@@ -463,11 +482,11 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
       f32x4 pr[2] = {zero4, zero4}, st[2] = {zero4, zero4};
 #pragma unroll
       for (int kk = 0; kk < KN; ++kk) {
-        const bf16x8 bf = frag<N>(l, sm.B, 16 * JB, 32 * kk);
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < 3; ++part)
 #pragma unroll
-          for (int a = 0; a < 2; ++a) st[a] = mfma(frag<N>(l, sm.dh[part], 32 * ph + 16 * a, 32 * kk), bf, st[a]);
+          for (int a = 0; a < 2; ++a)
+            st[a] = mfma(frag<N>(l, part < 2 ? sm.dh[part] : sm.B, 32 * ph + 16 * a, 32 * kk), Bj[kk], st[a]);
       }
       bf16x8 xf[2];
 #pragma unroll
@@ -534,7 +553,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
           if (r == 0) *reinterpret_cast<float4 *>(&sm.row[JB][i0]) = make_float4(rows[0], rows[1], rows[2], rows[3]);
         }
       }
-      const float wj = sm.we[k][j];
+      const float wj = r & 1 ? -sm.we[k][j] : sm.we[k][j];   // (as Bj)
       float rs = 0.0f, gxs = 0.0f, dxv[2][4];
 #pragma unroll
       for (int a = 0; a < 2; ++a) {
@@ -603,9 +622,10 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
         for (int kk = 0; kk < 2; ++kk) {
           t = mfma(hf[kk], df[0][kk], t);
           t = mfma(hf[kk], df[1][kk], t);
+          t = mfma(hf[kk], frag_t<N>(l, sm.B, 32 * kk, 16 * nt), t);
         }
         const int ii = r - 4 * kq;
-        const float d = ii == 0 ? t[0] : ii == 1 ? t[1] : ii == 2 ? t[2] : ii == 3 ? t[3] : 0.0f;
+        const float d = ii == 0 ? t[0] : ii == 1 ? -t[1] : ii == 2 ? t[2] : ii == 3 ? -t[3] : 0.0f;
         const float hh = sum_wave(d);
         if (l == 0) sm.hh[w] = hh;
       }
@@ -621,12 +641,12 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
           b = mfma(df[0][kk], xf, b);
           b = mfma(df[1][kk], xf, b);
         }
-        const float e = sm.e0[k][t], wj = sm.we[k][t] * dt[t];
+        const float e = sm.e0[k][t], wj = sm.we[k][t] * dt[t] * sign;
         float cf[4], qs = 0.0f;
         four(&sm.C[tile_at<N>(t, 16 * nt + 4 * kq)], cf);
 #pragma unroll
         for (int ii = 0; ii < 4; ++ii) {
-          const float ce = c[ii] * e;
+          const float ce = ii & 1 ? -c[ii] * e : c[ii] * e;   // (as H)
           dCa[a][ii] += ce;
           dBa[a][ii] = fmaf(b[ii], wj, dBa[a][ii]);
           qs = fmaf(ce, cf[ii], qs);
@@ -669,11 +689,17 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
         float hh = 0.0f;
 #pragma unroll
         for (int a = 0; a < NT; ++a) hh += sm.hh[a];
-        sm.hhs[k] = hh;
+        sm.hhs[k] = sign * hh;
       }
     }
   }
   __syncthreads();
+  uint4 bv[BC];   // B again
+#pragma unroll
+  for (int k = 0; k < BC; ++k) {
+    const int piece = tid + 512 * k, t = piece / G8;
+    bv[k] = piece < kQ * G8 && t < len ? ld8_raw(p.B + (t0 + t) * p.bs + gr * N + (piece % G8) * 8) : zero;
+  }
 
   // ---- the heads' steps: lane = token
   for (int k = w; k < nh; k += 8) {
@@ -704,6 +730,11 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   }
 
   // ---- the pair parts of dB and dC, from the heads' summed M L dt'
+#pragma unroll
+  for (int k = 0; k < BC; ++k) {
+    const int piece = tid + 512 * k;
+    if (piece < kQ * G8) *reinterpret_cast<uint4 *>(&sm.B[tile_at<N>(piece / G8, (piece % G8) * 8)]) = bv[k];
+  }
   uint16_t *Vh = sm.dh[0], *Vl = sm.dh[1];
   *reinterpret_cast<uint4 *>(Vh + 8 * tid) = zero;
   *reinterpret_cast<uint4 *>(Vl + 8 * tid) = zero;
@@ -870,7 +901,7 @@ BwdPlan bwd_plan(const ssd_varlen_args_t *a, int cus) {
   if (per > hpg) per = hpg;
   pl.hb_heads = static_cast<int>((hpg + per - 1) / per);
   pl.hb_per_group = static_cast<int>((hpg + pl.hb_heads - 1) / pl.hb_heads);
-  size_t at = up256(static_cast<size_t>(pl.entries) * a->nheads * 2 * kP * a->dstate * sizeof(uint16_t));
+  size_t at = up256(static_cast<size_t>(pl.entries) * a->nheads * kP * a->dstate * sizeof(float));
   pl.off_state = at;
   if (pl.nseg > 1) at += up256(static_cast<size_t>(pl.nseg - 1) * SH * kP * a->dstate * sizeof(float));
   pl.off_decay = at;
@@ -945,7 +976,7 @@ extern "C" int ssd_varlen_bwd(const ssd_varlen_bwd_args_t *a, void *stream_ptr) 
   p.dB = static_cast<uint16_t *>(a->dB); p.dbs = a->dB_stride;
   p.dC = static_cast<uint16_t *>(a->dC); p.dcs = a->dC_stride;
   p.dinit = a->dinitial_states;
-  p.ws_dh = reinterpret_cast<uint16_t *>(ws);
+  p.ws_dh = reinterpret_cast<float *>(ws);
   p.ws_state = reinterpret_cast<float *>(ws + pl.off_state);
   p.ws_decay = reinterpret_cast<float *>(ws + pl.off_decay);
   p.ws_bc = pl.hb_per_group > 1 ? reinterpret_cast<float *>(ws + pl.off_bc) : nullptr;

@@ -368,3 +368,25 @@ def test_parameters_at_any_address():
     got = binding.ssd_varlen_bwd(*(t[k].cuda() for k in ("x", "dt", "A", "B", "C")), _ints(cu), 70, dout.cuda(),
                                  (codes.cuda(), scales.cuda()), dfinal_states=_shifted(dlast.cuda()))
     assert all(torch.equal(want[k], got[k]) for k in want)
+
+
+@pytest.mark.parametrize("lens,n,G,decay", [((94,) * 12, 32, 4, 0.05), ((700,), 128, 1, 0.01), ((130, 70, 200), 64, 2, 0.02)])
+def test_decay_gradient_to_32_bits(lens, n, G, decay):
+    """dA against 64 bits, over all heads.  Every path's factors have 24 bits and
+    take some eight roundings of 2^-24 (products, decays, partial sums), and the
+    paths have any sign, as their roundings do: sqrt(8) 2^-24 of the whole, 2^-21
+    with what the draw can add.  Inputs with a mean, so that roundings to one
+    side would add up."""
+    log(f"[decay] 32 bits lens={lens} n={n}")
+    h = 16
+    t, cu, dout, codes, scales, _ = _steps_case(n, lens, h, G, n, decay)
+    for k in ("x", "B", "C"):
+        t[k] = R.silu(t[k].float()).to(bf)
+    for e, (S, _) in R.scan_fwd(t, cu)[4].items():
+        codes[e], scales[e] = R.to_8_bits(S.float())
+    da, _ = _through(t, cu, dout, codes, scales, None)
+    ref = (t["dt"].to(R.f64) * da).sum(0)
+    got = _bwd(t, cu, dout, codes, scales, None)["dA"].cpu().to(R.f64)
+    off = ((got - ref).norm() / ref.norm()).item()
+    log(f"  relative error {off:.2e}")
+    assert off <= 2.0 ** -21
