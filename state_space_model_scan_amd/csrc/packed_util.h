@@ -27,7 +27,7 @@ struct StepRule {
 // chunk's end).
 __device__ __forceinline__ float chunk_step(const StepRule &s, float raw, float bias, bool live, float &v) {
   v = raw + bias;
-  float d = s.softplus ? softplus_acc(v) : v;
+  float d = s.softplus ? softplus_step(v) : v;
   if (s.limit) d = fminf(fmaxf(d, s.lo), s.hi);
   return live ? d : 0.0f;
 }

@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
     float v, dd = fmaf(Ah, da, direct);
     chunk_step(p.step, raw, p.dt_bias ? p.dt_bias[h] : 0.0f, true, v);
     if (p.step.limit) {
-      const float sp = p.step.softplus ? softplus_acc(v) : v;
+      const float sp = p.step.softplus ? softplus_step(v) : v;
       if (!(sp >= p.step.lo && sp <= p.step.hi)) dd = 0.0f;
     }
     if (p.step.softplus) dd *= fast_rcp(1.0f + fast_exp2(-v * kLog2e));

@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(256) step_kernel(const StepParams p) {
     }
   }
   float step = load_io<IO>(p.dt, b * p.dts + h) + (p.dt_bias ? p.dt_bias[h] : 0.0f);
-  if (p.softplus) step = softplus_acc(step);
+  if (p.softplus) step = softplus_step(step);
   if (p.dt_limit) step = fminf(fmaxf(step, p.dt_min), p.dt_max);
   const float keep = fast_exp2(step * p.A[h] * kLog2e);
   __syncthreads();

@@ -390,3 +390,31 @@ def test_decay_gradient_to_32_bits(lens, n, G, decay):
     off = ((got - ref).norm() / ref.norm()).item()
     log(f"  relative error {off:.2e}")
     assert off <= 2.0 ** -21
+
+
+@pytest.mark.parametrize("single", [False, True])
+def test_steps_to_32_bits(single):
+    """softplus(dt + bias) from a state that one token leaves, dt' x B with x and B
+    of 1: exp2, log2 and reciprocal of the hardware are off by 2^-23 each, and six
+    operations round by 2^-24: below 2^-21, at steps down to 1e-6."""
+    log(f"[steps] single={single}")
+    g, T, h, n = _gen(1), 400, 64, 32
+    dt, bias = (3 * torch.randn(T, h, generator=g) - 3).to(bf), -2 - 4 * torch.rand(h, generator=g)
+    A, state = -torch.ones(h), torch.empty(T, h, R.P, n, device="cuda")
+    if single:
+        xbc = torch.ones(T, h * R.P + 2 * n, dtype=bf, device="cuda")
+        w = torch.zeros(h * R.P + 2 * n, 4, device="cuda")
+        w[:, 3] = 1
+        ring = torch.zeros(T, h * R.P + 2 * n, 4, dtype=bf, device="cuda")
+        binding.conv1d_ssd_update(xbc, dt.cuda(), A.cuda(), w, ring, state, None, dt_bias=bias.cuda(), dt_softplus=True,
+                                  activation=None)
+    else:
+        one = torch.ones(T, h, R.P, dtype=bf, device="cuda")
+        B = torch.ones(T, 1, n, dtype=bf, device="cuda")
+        binding.ssd_varlen_fwd(one, dt.cuda(), A.cuda(), B, B, torch.arange(T + 1, dtype=i32, device="cuda"), 1,
+                               dt_bias=bias.cuda(), dt_softplus=True, ssm_state=state)
+    v = (dt.float() + bias).to(R.f64)   # the sum is rounded to 32 bits, as a token's own logit
+    ref = torch.log1p(torch.exp(-v.abs())) + v.clamp(min=0)
+    off = ((state[:, :, 5, 7].cpu().to(R.f64) - ref) / ref).abs().max().item()
+    log(f"  relative error {off:.2e}")
+    assert ref.min() < 2e-6 and off <= 2.0 ** -21
