@@ -668,7 +668,12 @@ typedef struct ssd_varlen_args {
 } ssd_varlen_args_t;
 
 /* ssd_scan_fwd over packed tokens: the same recurrence for every sequence,
- * from the cached state (or zero) to the cached state. */
+ * from the cached state (or zero) to the cached state.
+ *
+ * Values that are not finite stay in their sequence.  Here they reach no token
+ * before their own, except that one in x can make its channel's outputs NaN for
+ * up to 31 tokens before it; in ssd_varlen_bwd they can reach every token of
+ * their chunk and of the chunks before. */
 int ssd_varlen_fwd(const ssd_varlen_args_t *args, void *hip_stream);
 int ssd_varlen_fwd_validate(const ssd_varlen_args_t *args);
 int ssd_varlen_fwd_workspace_size(const ssd_varlen_args_t *args, size_t *bytes);

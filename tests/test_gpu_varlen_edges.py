@@ -418,3 +418,58 @@ def test_steps_to_32_bits(single):
     off = ((state[:, :, 5, 7].cpu().to(R.f64) - ref) / ref).abs().max().item()
     log(f"  relative error {off:.2e}")
     assert ref.min() < 2e-6 and off <= 2.0 ** -21
+
+
+# ---- values that are not finite -------------------------------------------
+
+@pytest.mark.parametrize("n", [32, 128])
+@pytest.mark.parametrize("which", ["x", "B", "C", "dt", "dout"])
+def test_scan_keeps_to_its_sequence(which, n):
+    """Infinities and NaN of one sequence reach no token and no state of another,
+    forward or backward, whatever lies in the same 64 tokens of memory."""
+    log(f"[not finite] {which} n={n}")
+    lens, h = (70, 30, 3, 100), 4
+    t, cu, dout, codes, scales, _ = _steps_case(n, lens, h, 2, n, 1.0)
+    runs = []
+    for bad in (False, True):
+        v = {k: u.clone() for k, u in dict(t, dout=dout).items()}
+        if bad:
+            part = v[which][cu[1]:cu[2]]
+            part[3::7], part[5::7] = float("nan"), float("inf")
+        state = torch.empty(4, h, R.P, n, device="cuda")
+        out = binding.ssd_varlen_fwd(*(v[k].cuda() for k in ("x", "dt", "A", "B", "C")), _ints(cu), 100, ssm_state=state)
+        runs.append((out, state, _bwd(v, cu, v["dout"], codes, scales, None)))
+    others = torch.ones(cu[-1], dtype=torch.bool)
+    others[cu[1]:cu[2]] = False
+    others = others.cuda()
+    (a, sa, ga), (b, sb, gb) = runs
+    assert torch.equal(a[others], b[others]) and torch.equal(sa[[0, 2, 3]], sb[[0, 2, 3]])
+    for k in ("dx", "ddt", "dB", "dC"):
+        assert torch.equal(ga[k][others], gb[k][others]), k
+    assert not all(torch.isfinite(gb[k].float()).all() for k in ("dx", "ddt", "dB", "dC"))
+
+
+@pytest.mark.parametrize("n", [32, 128])
+def test_values_that_are_not_finite_inside_a_sequence(n):
+    """In the forward a B, C or dt that is not finite reaches no token before its
+    own, and an x no other channel and none of the tokens before its block of 32;
+    its own and later ones are not finite either."""
+    log(f"[not finite] inside n={n}")
+    t, cu, *_ = _steps_case(n, (130,), 4, 2, n, 1.0)
+    at = 64 + 40
+    for which in ("x", "B", "C", "dt"):
+        outs = []
+        for bad in (False, True):
+            v = {k: u.clone() for k, u in t.items()}
+            if bad:
+                (v["x"][at, 1, 9:10] if which == "x" else v[which][at]).fill_(float("nan"))
+            outs.append(binding.ssd_varlen_fwd(*(v[k].cuda() for k in ("x", "dt", "A", "B", "C")), _ints(cu), 130).cpu())
+        a, b = outs
+        if which == "x":
+            rest = torch.ones(4, R.P, dtype=torch.bool)
+            rest[1, 9] = False
+            assert torch.equal(a[:, rest], b[:, rest]) and torch.equal(a[:at // 32 * 32], b[:at // 32 * 32])
+            assert torch.isnan(b[at:, 1, 9]).all()
+        else:
+            assert torch.equal(a[:at], b[:at]) and torch.isnan(b[at]).all(), which
+            assert which == "C" or torch.isnan(b[at:]).all(), which
