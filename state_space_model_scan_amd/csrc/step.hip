@@ -162,7 +162,12 @@ extern "C" int conv1d_ssd_update(const conv1d_ssd_update_args_t *a, void *stream
   p.silu = a->act == SSM_ACT_SILU;
   p.softplus = a->dt_softplus;
   p.dt_limit = a->dt_limit; p.dt_min = a->dt_min; p.dt_max = a->dt_max;
-  const int rows = a->batch * a->nheads >= 4 * cu_count_cached() ? 64 : 16;
+  // Where the heads alone do not fill the chip four workgroups share one, each
+  // of which forms B's and C's convolution again: 16 rows / 64 (us) of 256
+  // (request, head) pairs 6.1 / 7.1 at dstate 128, 4.5 / 4.9 at 64, 3.9 / 3.8 at
+  // 32, and of 512 10.9 / 8.5, 5.9 / 5.8, 4.8 / 4.3; of 32 4.4 / 6.2, of 1024
+  // 17.5 / 12.8.
+  const int rows = a->batch * a->nheads >= 2 * cu_count_cached() ? 64 : 16;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   const dim3 grid(static_cast<unsigned>(a->nheads), kP / rows, static_cast<unsigned>(a->batch));
   if (a->io_dtype == SSM_BF16) launch_step_n<1>(a->dstate, rows, grid, stream, p);
