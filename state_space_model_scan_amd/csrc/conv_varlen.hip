@@ -5,7 +5,8 @@
 // element in 16 bits), the backward reads two and writes one.  A wave owns 64
 // runs of NV neighbouring channels (16 bytes each where the rows allow it, so
 // a token's load is one KiB) and walks a run of tokens with the last inputs in
-// registers.  The three tokens before a run are read again.
+// registers.  The three tokens before a run are read again.  85 us and 126 us at
+// 16384 x 5376 bf16 are 4.2 TB/s of what they have to move.
 // What a token may see is decided by wave-uniform scalars: its place in its
 // sequence, found once per run in cu_seqlens and then counted.  The run's loads
 // are issued together before the first is used.
@@ -173,8 +174,8 @@ __global__ void __launch_bounds__(64 * kRows, 4) conv_var_fwd_kernel(const ConvV
   if (n == RUN && inside_one(edge, s, t0, t0 + RUN)) {
     // the whole run and what it sees are inside one sequence: no branch
     // between the loads and their use (with the edge tests of every token in
-    // between the compiler kept few loads in flight: 216 us where this takes
-    // 88 at 16384 x 5376 bf16; 79 now)
+    // between the compiler kept few loads in flight: 216 us where this took
+    // 88 at 16384 x 5376 bf16; 85 now)
 #pragma unroll
     for (int i = 0; i < RUN; ++i) {
       float acc[NV];
@@ -503,10 +504,10 @@ int64_t run_waves(const causal_conv1d_varlen_args_t *a, int nv, int run) {
 }
 // A launch of few waves lasts as long as one of its runs with an edge, so runs
 // are short below eight long ones a compute unit.  Measured short / long (us),
-// forward: 500 x 1024 7.9 / 11.2, 3500 x 2304 15.4 / 16.9, and above the limit
-// 8192 x 2304 24.6 / 22.6, 16384 x 5376 94 / 79; backward: 500 x 1024 12.5 /
-// 24.7, 3500 x 2304 24.3 / 30.4, and above it 8192 x 2304 40.9 / 39.7, 16384 x
-// 5376 172 / 126.
+// forward, 16 sequences from and to their rings: 500 x 1024 9.5 / 13.0, 3500 x
+// 2304 16.9 / 18.9, and above the limit 8192 x 2304 37 / 27, 16384 x 5376 108 /
+// 76; backward: 500 x 1024 13.4 / 26.7, 3500 x 2304 24 / 33, and above it 8192 x
+// 2304 45 / 39, 16384 x 5376 160 / 123.
 constexpr int kFewWaves = 8;
 int fwd_run(const causal_conv1d_varlen_args_t *a, int nv) {
   return run_waves(a, nv, kFwdRun) < kFewWaves * static_cast<int64_t>(cu_count_cached()) ? kShortRun : kFwdRun;

@@ -112,7 +112,8 @@ __device__ __forceinline__ float row_scale(uint32_t amax_bits, float &inv) {
 // 16-byte groups are permuted by g = the row's last three bits rotated, so
 // that eight consecutive rows at one column (an operand read row by row) have
 // eight values of g, and four consecutive rows (a transposing read: 32 bytes
-// of each) four values of g / 2: neither meets in a bank.
+// of each) four values of g / 2.  Rows r and r + 8 of an operand still meet:
+// conflicts are 42 to 52% of the LDS's active cycles in the scan and its gradient.
 template <int ROW_LEN>
 __device__ __forceinline__ int tile_at(int row, int col) {
   constexpr int GROUPS = ROW_LEN / 8;

@@ -10,8 +10,8 @@
 //   S        <- exp(cs_end) S + X^T diag(exp(cs_end - cs) dt') B
 // with M and S entering their products as a bf16 head and tail.  The weighted
 // X of the state update enters in three parts (all 24 bits) and the running
-// sum is kept in two floats: the state is a 32-bit output, and its 8-bit form
-// is decided by it.
+// sum is kept in two floats, whose difference gives every decay: the state is a
+// 32-bit output, and its 8-bit form is decided by it.
 //
 // What bounds it is the chain of a chunk's dependent steps, not HBM: the chunks
 // of a (sequence, head) follow each other.  So:
@@ -30,7 +30,8 @@
 //   compiler may interleave;
 // - tiles stay as they lie in memory, token by token, and are read across by
 //   the transposing LDS load, so nothing is rearranged on the way;
-// - three barriers a chunk: data there, M there, C done with.  Now 599 us.
+// - three barriers a chunk: data there, M there, C done with.
+// Now 595 us; the 24 prompts 50.
 // With few (sequence, head) pairs the sequence is cut into segments; a first
 // launch finds their end states from zero (FULL false), and
 // the second starts every segment from the states carried over.
@@ -508,8 +509,9 @@ struct VarPlan {
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // The whole call with segments of seg chunks.  The chunk times (full pass 3.4
-// and 4.6 us, state pass 1.5 and 2.7) are those measured at dstate 128; a
-// smaller one changes their ratios little.  Each segment costs about 0.8
+// and 4.6 us, state pass 1.5 and 2.7) are those measured at dstate 128.  A
+// smaller one takes less of each, in about their ratios: the choices below hold
+// at 64 too, and at 32 are up to 17% from the best.  Each segment costs about 0.8
 // chunks to start, segment k reads the k end states before it (32 KB each, from
 // the caches mostly), and a second launch about 5 us.
 double split_us(int64_t blocks, int64_t nchunks, int64_t seg, int64_t dstate, int64_t cus) {
@@ -525,10 +527,11 @@ double split_us(int64_t blocks, int64_t nchunks, int64_t seg, int64_t dstate, in
 }
 
 // Segments of the longest sequence; a shorter one has fewer.  The library's own
-// count is the one that split_us finds fastest.  Measured at dstate 128 (us,
-// chosen / best of a sweep): 1 x 32768 tokens x 80 heads 579 (19) / 579;
-// 4 x 2048 x 80 144 (3) / 144; 8 x 2048 x 80 256 (1) / 256; 1 x 2048 x 80
-// 53 (6) / 53; 1 x 16384 x 16 98 (32) / 96 (26).
+// count is the one that split_us finds fastest.  Measured (us, chosen / best of
+// a sweep), at dstate 128, 64 and 32: 1 x 32768 tokens x 80 heads 590 / 576,
+// 418 / 418, 344 / 327; 4 x 2048 x 80 141 / 137, 102 / 101, 78 / 72; 1 x 2048 x 80
+// 55 / 52, 41 / 39, 34 / 29; 1 x 16384 x 16 97 / 95, 63 / 63, 47 / 47; 5 x 200 x 8
+// 16 / 16, 13 / 13, 11 / 11.
 VarPlan var_plan(const ssd_varlen_args_t *a, int cus) {
   VarPlan pl{};
   int64_t nchunks = (a->max_seqlen + kQ - 1) / kQ;

@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(256, 3) adjoint_kernel(const BwdParams p) {
     }
     // Two tiles at a time: their states out, then their products.  Every
     // workgroup is at about the same place of its chunk, so stores that all come
-    // at its start leave the memory idle for the rest of it (213 us for 196 at
-    // 8 x 2048 tokens, 80 heads; without any store 108).
+    // at its start leave the memory idle for the rest of it (213 us where this
+    // took 196 at 8 x 2048 tokens, 80 heads, and without any store 108; 186 now).
     float *dh = STORE ? p.ws_dh + ((q.entry + c) * p.nheads + h) * kP * N + (16 * w * N + 4 * l) : nullptr;
 #pragma unroll
     for (int nt = 0; nt < NT; nt += 2) {
@@ -285,10 +285,12 @@ struct ChunkLds {
 //     every second tile's sums.  Wave w takes block w of the first half, wave
 //     4 + w block 3 - w of the second, so that the two waves of a SIMD have
 //     five tiles together (four waves to a tile, ten to a SIMD, took 659 us
-//     where this takes 600 at 8 x 2048 tokens, 80 heads);
+//     where this took 600 at 8 x 2048 tokens, 80 heads);
 //   and the state products of its n tile, dH^T x and H^T g.
 // The partial sums over tiles meet in LDS; the steps' gradients, chains of
-// lane sums, wait until the end and are then done for all heads at once.
+// lane sums, wait until the end and are then done for all heads at once.  545 us
+// at 8 x 2048 tokens, 80 heads, of them 45 for dH's third part; vector
+// instructions issue 52% of the time, one workgroup a compute unit.
 template <int N>
 __global__ void __launch_bounds__(512, 2) chunk_kernel(const BwdParams p) {
   constexpr int NT = N / 16;          // n tiles
@@ -852,10 +854,11 @@ struct BwdPlan {
 // Time in us of the adjoint pass with segments of seg chunks.  Storing every
 // chunk's dH (32 KB at dstate 128, beside 24 KB read) goes at about 4 TB/s; a
 // workgroup's chain takes 2.2 us a chunk, or 1.6 where nothing is stored, in
-// the launch that finds the segments' ends.  Measured (us of the whole
-// backward, one segment / chosen): 8 x 2048 tokens x 80 heads 705 / 705 (1);
-// 1 x 2048 x 80 173 / 159 (6); 1 x 16384 x 16 598 / 234 (24); 1 x 16384 x 80
-// 1024 / 809 (10).
+// the launch that finds the segments' ends, at dstate 128.  Measured (us of the
+// whole backward, one segment / chosen / best of a sweep), at dstate 128, 64 and
+// 32: 4 x 2048 tokens x 80 heads 403 / 403 / 403, 270 / 269 / 270, 216 / 215 / 216;
+// 1 x 2048 x 80 168 / 158 / 158, 120 / 111 / 109, 101 / 90 / 91; 1 x 16384 x 16
+// 508 / 234 / 230, 378 / 148 / 146, 301 / 117 / 117.
 double adjoint_us(int64_t blocks, int64_t nchunks, int64_t seg, int64_t dstate, int64_t cus) {
   const int64_t G = (nchunks + seg - 1) / seg;
   const double len = static_cast<double>(seg) + 0.8, state = static_cast<double>(kP) * dstate * sizeof(float);
