@@ -414,11 +414,12 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
       }
     }
 
-    // ---- S^T <- exp(cs_end) S^T + B^T (X w), X w in three bf16 parts
+    // ---- S^T <- exp(cs_end) S^T + B^T (X w), X w in three bf16 parts.  The
+    // matrix unit rounds its accumulator four times a product, so the small parts
+    // come first and the state is added at the end, with one rounding.
     const float dec = e0[kQ - 1];
     if constexpr (!FULL) seg_decay *= dec;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) accs[nt] *= dec;
+    bf16x8 part[3][2];
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       const uint4 xw = __builtin_bit_cast(uint4, xt[kk]);
@@ -430,20 +431,32 @@ __global__ void __launch_bounds__(256, FULL ? 2 : 3) packed_scan_kernel(const Sc
         split_bf2(a, d, x0[i / 2], x1[i / 2]);
         x2[i / 2] = third_bf2(a, d, x0[i / 2], x1[i / 2]);
       }
-      const bf16x8 f0 = __builtin_bit_cast(bf16x8, make_uint4(x0[0], x0[1], x0[2], x0[3]));
-      const bf16x8 f1 = __builtin_bit_cast(bf16x8, make_uint4(x1[0], x1[1], x1[2], x1[3]));
-      const bf16x8 f2 = __builtin_bit_cast(bf16x8, make_uint4(x2[0], x2[1], x2[2], x2[3]));
-      // part by part over all tiles: a product never waits for the one before
-      bf16x8 bt[NT];
+      part[0][kk] = __builtin_bit_cast(bf16x8, make_uint4(x0[0], x0[1], x0[2], x0[3]));
+      part[1][kk] = __builtin_bit_cast(bf16x8, make_uint4(x1[0], x1[1], x1[2], x1[3]));
+      part[2][kk] = __builtin_bit_cast(bf16x8, make_uint4(x2[0], x2[1], x2[2], x2[3]));
+    }
+    constexpr int AT = 2;   // tiles at a time (4 and 8 take registers: 606 and 709 us where this takes 602)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        bt[nt] = FULL ? frag_states<N>(l, B, 32 * kk, nt >> 1, nt & 1) : frag_t<N>(l, B, 32 * kk, 16 * nt);
-        accs[nt] = mfma(bt[nt], f0, accs[nt]);
+    for (int n0 = 0; n0 < NT; n0 += AT) {
+      bf16x8 bt[AT][2];
+      f32x4 sum[AT];
+#pragma unroll
+      for (int a = 0; a < AT; ++a) {
+        sum[a] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+          bt[a][kk] = FULL ? frag_states<N>(l, B, 32 * kk, (n0 + a) >> 1, a & 1) : frag_t<N>(l, B, 32 * kk, 16 * (n0 + a));
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) accs[nt] = mfma(bt[nt], f1, accs[nt]);
+      for (int k = 2; k >= 0; --k)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) accs[nt] = mfma(bt[nt], f2, accs[nt]);
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int a = 0; a < AT; ++a) sum[a] = mfma(bt[a][kk], part[k][kk], sum[a]);
+#pragma unroll
+      for (int a = 0; a < AT; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) accs[n0 + a][i] = fmaf(accs[n0 + a][i], dec, sum[a][i]);
     }
     if (w == 0 && more) put_steps(next, b ^ 1, raw);
     // C is there, whatever the four stores after it do (a chunk with one after

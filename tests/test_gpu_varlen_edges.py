@@ -473,3 +473,23 @@ def test_values_that_are_not_finite_inside_a_sequence(n):
         else:
             assert torch.equal(a[:at], b[:at]) and torch.isnan(b[at]).all(), which
             assert which == "C" or torch.isnan(b[at:]).all(), which
+
+
+@pytest.mark.parametrize("decay", [0.0, 0.003, 0.05])
+def test_states_to_32_bits(decay):
+    """The last state against 64 bits, over all its elements, after many chunks
+    whose terms have a mean.  A term has the roundings of its step's decay (exp2
+    and four operations) and of its products: sqrt(6) 2^-24 / sqrt(3) if they fall
+    as they may; the sums' add one of each chunk's nine, as partial sums are as
+    large as the state.  Together sqrt(6 + 9) 2^-24 / sqrt(3) = 1.3e-7, here with
+    steps that are given and one segment: 2^-23."""
+    log(f"[state] decay={decay}")
+    g, T, h, n = _gen(7), 1500, 3, 128
+    t = dict(x=R.silu(_randn(g, T, h, R.P)).to(bf), A=-decay * (0.5 + torch.rand(h, generator=g)),
+             B=R.silu(_randn(g, T, 1, n)).to(bf), C=_randn(g, T, 1, n, dtype=bf), dt=(0.75 + 0.5 * torch.rand(T, h, generator=g)).to(bf))
+    last = R.scan_fwd(t, [0, T])[2]
+    state = torch.empty(1, h, R.P, n, device="cuda")
+    binding.ssd_varlen_fwd(*(t[k].cuda() for k in ("x", "dt", "A", "B", "C")), _ints([0, T]), T, ssm_state=state, seq_segments=1)
+    off = ((state.cpu().to(R.f64) - last).norm() / last.norm()).item()
+    log(f"  relative error {off:.2e}")
+    assert off <= 2.0 ** -23
