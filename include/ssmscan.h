@@ -751,6 +751,174 @@ typedef struct conv1d_ssd_update_args {
 int conv1d_ssd_update(const conv1d_ssd_update_args_t *args, void *hip_stream);
 int conv1d_ssd_update_validate(const conv1d_ssd_update_args_t *args);
 
+/* ---------------------------------------------------------------------------
+ * A gated recurrent block: its recurrence over packed tokens, in serving and
+ * in training, and its norm.  Packed tokens, strides, cu_seqlens, caches, slots
+ * and cache_seqlens as above, except that tokens before cu_seqlens[0] and from
+ * cu_seqlens[nseq] on (a padded batch) belong to no sequence: their outputs are
+ * left as they were, and their gradients are 0.
+ * ------------------------------------------------------------------------- */
+
+#define GATED_CHUNK 64   /* packed tokens from one kept state to the next */
+
+/* Arguments of gated_scan_varlen_fwd. */
+typedef struct gated_scan_varlen_args {
+  int64_t total, nseq, channels;
+  int32_t io_dtype;
+  const void *x; int64_t x_stride;              /* (total, channels) io */
+  const void *r; int64_t r_stride;              /* (total, channels) io: recurrence gate before its sigmoid */
+  const void *i; int64_t i_stride;              /* (total, channels) io: input gate before its sigmoid */
+  const float *A;                               /* (channels) fp32, <= 0: log of the decay at an open gate */
+  const float *r_bias, *i_bias;                 /* (channels) fp32 or NULL */
+  const int32_t *cu_seqlens;                    /* (nseq + 1) */
+  void *out; int64_t out_stride;                /* (total, channels) io */
+  float *state; int64_t state_slots;            /* (state_slots, channels) cache or NULL: read and written */
+  const int32_t *cache_seqlens, *slots;         /* (nseq) or NULL */
+  /* The state before every GATED_CHUNK-th packed token, for
+   * gated_scan_varlen_bwd (NULL: not kept); rows of tokens of no sequence are
+   * 0. */
+  float *checkpoints;                           /* (gated_checkpoint_slots(total), channels) */
+  void *workspace; size_t workspace_bytes;      /* gated_scan_varlen_fwd_workspace_size */
+} gated_scan_varlen_args_t;
+
+/* A gated linear recurrence over packed tokens.  For every token t of a
+ * sequence and channel c, with sigma the logistic function,
+ *
+ *     rho  = sigma(r[t,c] + r_bias[c]),   iota = sigma(i[t,c] + i_bias[c])
+ *     a    = exp(A[c] rho)
+ *     h   <- a h + sqrt(1 - a^2) iota x[t,c]
+ *     out[t,c] = h
+ *
+ * with h starting at the sequence's cached state (or zero) and its last value
+ * stored there; an empty sequence leaves its entry as it is.  The state is
+ * fp32.  Where A[c] > 0 the weight sqrt(1 - a^2) is taken as 0.  `out` must not
+ * overlap an input.  Values that are not finite stay in their sequence and
+ * channel and reach no earlier token.  Results are bit-for-bit repeatable. */
+int gated_scan_varlen_fwd(const gated_scan_varlen_args_t *args, void *hip_stream);
+int gated_scan_varlen_fwd_validate(const gated_scan_varlen_args_t *args);
+int gated_scan_varlen_fwd_workspace_size(const gated_scan_varlen_args_t *args, size_t *bytes);
+
+/* Kept states of packed tokens: ceil(total / GATED_CHUNK). */
+int64_t gated_checkpoint_slots(int64_t total);
+
+/* Arguments of gated_scan_varlen_bwd: the forward's (fwd.checkpoints are those
+ * that the forward wrote; fwd.out, state, state_slots, cache_seqlens, slots and
+ * workspace are ignored), and the gradients, caller-allocated and fully
+ * overwritten. */
+typedef struct gated_scan_varlen_bwd_args {
+  gated_scan_varlen_args_t fwd;
+  const float *initial_states;                  /* (nseq, channels) fp32: the states that the sequences started from, or NULL (zero) */
+  const void *dout; int64_t dout_stride;        /* (total, channels) io */
+  const float *dfinal_states;                   /* (nseq, channels) fp32: gradient of the last states, or NULL (zero) */
+  void *dx; int64_t dx_stride;                  /* (total, channels) io */
+  void *dr; int64_t dr_stride;                  /* (total, channels) io */
+  void *di; int64_t di_stride;                  /* (total, channels) io */
+  float *dA;                                    /* (channels) fp32 */
+  float *dr_bias, *di_bias;                     /* (channels) fp32, required iff r_bias, i_bias */
+  float *dinitial_states;                       /* (nseq, channels) fp32 or NULL */
+  void *workspace; size_t workspace_bytes;      /* gated_scan_varlen_bwd_workspace_size */
+} gated_scan_varlen_bwd_args_t;
+
+/* Gradients of gated_scan_varlen_fwd.  With G the adjoint of the state,
+ *   G_t = dout_t + a_{t+1} G_{t+1}   (dfinal_states behind the last token),
+ * and m = sqrt(1 - a^2):
+ *   q   = G rho (a h_{t-1} - (a^2 / m) iota x)   (rho / m taken as 0 where m = 0)
+ *   dA  = sum_t q,   dr = A (1 - rho) q,   dr_bias = sum_t dr
+ *   dx  = G m iota,  di = G m x iota (1 - iota),   di_bias = sum_t di
+ * An empty sequence passes dfinal_states on to dinitial_states.  Sums are taken
+ * in a fixed order (bit-for-bit repeatable).  Values that are not finite stay
+ * in their sequence and channel (apart from the sums over the tokens). */
+int gated_scan_varlen_bwd(const gated_scan_varlen_bwd_args_t *args, void *hip_stream);
+int gated_scan_varlen_bwd_validate(const gated_scan_varlen_bwd_args_t *args);
+int gated_scan_varlen_bwd_workspace_size(const gated_scan_varlen_bwd_args_t *args, size_t *bytes);
+
+/* Arguments of gated_scan_update. */
+typedef struct gated_scan_update_args {
+  int64_t batch, channels;
+  int32_t io_dtype;
+  const void *x; int64_t x_stride;              /* (batch, channels) io, and so r, i and out */
+  const void *r; int64_t r_stride;
+  const void *i; int64_t i_stride;
+  const float *A;                               /* (channels) fp32 */
+  const float *r_bias, *i_bias;                 /* (channels) fp32 or NULL */
+  float *state; int64_t state_slots;            /* (state_slots, channels) cache */
+  const int32_t *cache_seqlens;                 /* (batch) or NULL (every request is new) */
+  const int32_t *slots;                         /* (batch) or NULL */
+  void *out; int64_t out_stride;
+} gated_scan_update_args_t;
+
+/* One token of every request through gated_scan_varlen_fwd's recurrence
+ * against the cached states, which are updated.  An entry outside the cache (a
+ * padding row) gives the output of a new request and writes nothing. */
+int gated_scan_update(const gated_scan_update_args_t *args, void *hip_stream);
+int gated_scan_update_validate(const gated_scan_update_args_t *args);
+
+#define RMS_SCALE_BLOCK 128     /* columns that share a scale in 8 bits */
+#define RMS_MAX_GROUP 16384     /* largest group_size */
+
+/* Arguments of rms_norm_fwd.  A *_stride is the number of elements from a row to
+ * the next; a row's columns are dense. */
+typedef struct rms_norm_args {
+  int64_t rows, cols, group_size;               /* group_size divides cols */
+  int32_t io_dtype, residual_dtype;             /* residual_dtype: io_dtype or SSM_F32 */
+  float eps;
+  const void *x; int64_t x_stride;              /* (rows, cols) io */
+  const void *z; int64_t z_stride;              /* (rows, cols) io gate, or NULL */
+  const void *residual; int64_t residual_stride;  /* (rows, cols) residual_dtype, or NULL; not with z */
+  const float *weight;                          /* (cols) fp32 */
+  void *residual_out; int64_t residual_out_stride;  /* as residual, required iff residual; may be residual itself */
+  /* either */
+  void *out; int64_t out_stride;                /* (rows, cols) io */
+  /* or */
+  void *codes; int64_t codes_stride;            /* (rows, cols) e4m3 */
+  float *scales;                                /* (rows, ceil(cols / RMS_SCALE_BLOCK)) fp32 */
+} rms_norm_args_t;
+
+/* Root-mean-square norm of every group of group_size neighbouring columns of a
+ * row, after the residual's addition or behind a gate:
+ *
+ *     v = x,  or  residual_out = round(x + residual) and v = residual_out,
+ *         or  v = x silu(z)
+ *     y = v / sqrt(mean(v^2) + eps) weight
+ *
+ * (of what the residual stream holds, so that rms_norm_bwd, which reads it, is
+ * the gradient of what was computed).  y goes to `out`, or in 8 bits to `codes`:
+ * y is code * scale, the code rounded to nearest (ties to even) and the scale,
+ * one for RMS_SCALE_BLOCK columns of a row, the smallest power of two with which
+ * none of them is over 448 (at least 2^-100; NaN where one of them is not
+ * finite).  8 bits need one group a row, or a group_size that is a multiple of
+ * RMS_SCALE_BLOCK. */
+int rms_norm_fwd(const rms_norm_args_t *args, void *hip_stream);
+int rms_norm_fwd_validate(const rms_norm_args_t *args);
+
+/* Arguments of rms_norm_bwd. */
+typedef struct rms_norm_bwd_args {
+  int64_t rows, cols, group_size;
+  int32_t io_dtype, x_dtype;                    /* x_dtype: io_dtype or SSM_F32 */
+  float eps;
+  const void *x; int64_t x_stride;              /* (rows, cols) x_dtype: the forward's x, or its residual_out */
+  const void *z; int64_t z_stride;              /* (rows, cols) io, or NULL; not with ds, and x_dtype is io_dtype */
+  const float *weight;                          /* (cols) fp32 */
+  const void *dy; int64_t dy_stride;            /* (rows, cols) io */
+  const void *ds; int64_t ds_stride;            /* (rows, cols) x_dtype: the gradient that reaches residual_out, or NULL */
+  void *dx; int64_t dx_stride;                  /* (rows, cols) io */
+  void *dresidual; int64_t dresidual_stride;    /* (rows, cols) x_dtype: dx before its rounding to io, or NULL */
+  void *dz; int64_t dz_stride;                  /* (rows, cols) io, required iff z */
+  float *dweight;                               /* (cols) fp32 */
+  void *workspace; size_t workspace_bytes;      /* rms_norm_bwd_workspace_size */
+} rms_norm_bwd_args_t;
+
+/* Gradients of rms_norm_fwd.  With rstd = 1 / sqrt(mean(v^2) + eps), hat = v rstd
+ * and g = dy weight:
+ *   dv = rstd (g - hat mean(g hat)),  dweight = sum over rows of dy hat
+ *   dx = dv + ds   (the residual's gradient as well),  or with a gate
+ *   dx = dv silu(z),  dz = dv x silu'(z)
+ * Sums are taken in a fixed order (bit-for-bit repeatable).  Outputs must not
+ * overlap inputs. */
+int rms_norm_bwd(const rms_norm_bwd_args_t *args, void *hip_stream);
+int rms_norm_bwd_validate(const rms_norm_bwd_args_t *args);
+int rms_norm_bwd_workspace_size(const rms_norm_bwd_args_t *args, size_t *bytes);
+
 /* Static text for a status code. */
 const char *ssm_status_str(int status);
 

@@ -13,6 +13,13 @@ from .binding import (  # noqa: F401
     causal_conv1d_varlen_fwd,
     conv1d_ssd_update,
     conv1d_selective_scan_fn,
+    gated_checkpoint_slots,
+    gated_scan_update,
+    gated_scan_varlen_bwd,
+    gated_scan_varlen_fwd,
+    rms_norm_bwd,
+    rms_norm_fwd,
+    rms_norm_quant_fwd,
     selective_scan_fn,
     ssd_checkpoint_slots,
     ssd_varlen_bwd,

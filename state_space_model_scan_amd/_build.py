@@ -45,12 +45,14 @@ SOURCES = [
     ("ssd_varlen_bwd.hip", True),
     ("conv_varlen.hip", True),
     ("step.hip", True),
+    ("gated_scan.hip", True),
+    ("rms_norm.hip", True),
     ("bwd.hip", True),
     ("bwd_complex.hip", True),
     ("validate.cpp", False),
 ]
 MICRO_SOURCES = [("microbench.hip", True)]
-# the torch binding of the packed-token operators: host code only, linked
+# the torch binding of the packed-token and the block's operators: host code only, linked
 # against the operators' library beside it
 PACKED_SOURCE = "packed_binding.cpp"
 PACKED_LIB = os.path.join(PKG, "_packed.so")

@@ -18,6 +18,9 @@ SSM_MAX_CONV_STATE = 256
 SSD_HEADDIM = 64
 SSD_CHUNK = 64
 SSM_CKPT_INTERVAL = 32
+GATED_CHUNK = 64
+RMS_SCALE_BLOCK = 128
+RMS_MAX_GROUP = 16384
 
 # Every symbol include/ssmscan.h declares.
 EXPORTS = (
@@ -36,6 +39,12 @@ EXPORTS = (
     "ssd_varlen_fwd", "ssd_varlen_fwd_validate", "ssd_varlen_fwd_workspace_size", "ssd_checkpoint_slots",
     "ssd_varlen_bwd", "ssd_varlen_bwd_validate", "ssd_varlen_bwd_workspace_size",
     "conv1d_ssd_update", "conv1d_ssd_update_validate",
+    "gated_scan_varlen_fwd", "gated_scan_varlen_fwd_validate", "gated_scan_varlen_fwd_workspace_size",
+    "gated_checkpoint_slots",
+    "gated_scan_varlen_bwd", "gated_scan_varlen_bwd_validate", "gated_scan_varlen_bwd_workspace_size",
+    "gated_scan_update", "gated_scan_update_validate",
+    "rms_norm_fwd", "rms_norm_fwd_validate",
+    "rms_norm_bwd", "rms_norm_bwd_validate", "rms_norm_bwd_workspace_size",
     "ssm_status_str", "ssm_last_hip_error", "ssm_abi_version",
 )
 
@@ -170,6 +179,44 @@ class ConvSsdUpdateArgs(ctypes.Structure):
         p cache_seqlens p slots p out q out_stride""")
 
 
+class GatedScanArgs(ctypes.Structure):
+    """Mirror of gated_scan_varlen_args_t."""
+    _fields_ = _fields("""
+        q total q nseq q channels i io_dtype p x q x_stride p r q r_stride p i q i_stride p A p r_bias p i_bias
+        p cu_seqlens p out q out_stride p state q state_slots p cache_seqlens p slots p checkpoints
+        p workspace z workspace_bytes""")
+
+
+class GatedScanBwdArgs(ctypes.Structure):
+    """Mirror of gated_scan_varlen_bwd_args_t."""
+    _fields_ = [("fwd", GatedScanArgs)] + _fields("""
+        p initial_states p dout q dout_stride p dfinal_states p dx q dx_stride p dr q dr_stride p di q di_stride
+        p dA p dr_bias p di_bias p dinitial_states p workspace z workspace_bytes""")
+
+
+class GatedUpdateArgs(ctypes.Structure):
+    """Mirror of gated_scan_update_args_t."""
+    _fields_ = _fields("""
+        q batch q channels i io_dtype p x q x_stride p r q r_stride p i q i_stride p A p r_bias p i_bias
+        p state q state_slots p cache_seqlens p slots p out q out_stride""")
+
+
+class RmsNormArgs(ctypes.Structure):
+    """Mirror of rms_norm_args_t."""
+    _fields_ = _fields("""
+        q rows q cols q group_size i io_dtype i residual_dtype f eps p x q x_stride p z q z_stride
+        p residual q residual_stride p weight p residual_out q residual_out_stride p out q out_stride
+        p codes q codes_stride p scales""")
+
+
+class RmsNormBwdArgs(ctypes.Structure):
+    """Mirror of rms_norm_bwd_args_t."""
+    _fields_ = _fields("""
+        q rows q cols q group_size i io_dtype i x_dtype f eps p x q x_stride p z q z_stride p weight
+        p dy q dy_stride p ds q ds_stride p dx q dx_stride p dresidual q dresidual_stride p dz q dz_stride
+        p dweight p workspace z workspace_bytes""")
+
+
 class SsmError(ValueError):
     """A non-zero status from libssmscan."""
 
@@ -256,7 +303,10 @@ def lib() -> ctypes.CDLL:
         L.ssm_scan_bwd_complex_workspace_size.restype = ctypes.c_int
         for name, args in (("causal_conv1d_varlen_fwd", ConvVarlenArgs), ("causal_conv1d_varlen_bwd", ConvVarlenArgs),
                            ("ssd_varlen_fwd", SsdVarlenArgs), ("ssd_varlen_bwd", SsdVarlenBwdArgs),
-                           ("conv1d_ssd_update", ConvSsdUpdateArgs)):
+                           ("conv1d_ssd_update", ConvSsdUpdateArgs),
+                           ("gated_scan_varlen_fwd", GatedScanArgs), ("gated_scan_varlen_bwd", GatedScanBwdArgs),
+                           ("gated_scan_update", GatedUpdateArgs), ("rms_norm_fwd", RmsNormArgs),
+                           ("rms_norm_bwd", RmsNormBwdArgs)):
             getattr(L, name).argtypes = [ctypes.POINTER(args), _vp]
             getattr(L, name).restype = ctypes.c_int
             getattr(L, name + "_validate").argtypes = [ctypes.POINTER(args)]
@@ -266,6 +316,8 @@ def lib() -> ctypes.CDLL:
                 getattr(L, name + "_workspace_size").restype = ctypes.c_int
         L.ssd_checkpoint_slots.argtypes = [i64, i64]
         L.ssd_checkpoint_slots.restype = i64
+        L.gated_checkpoint_slots.argtypes = [i64]
+        L.gated_checkpoint_slots.restype = i64
         L.ssm_status_str.argtypes = [ctypes.c_int]
         L.ssm_status_str.restype = ctypes.c_char_p
         L.ssm_last_hip_error.argtypes = []

@@ -20,6 +20,9 @@ import torch
 
 from . import _lib
 from ._lib import BwdArgs, ConvArgs, ScanArgs, check
+from .block import (gated_checkpoint_slots, gated_scan_update, gated_scan_varlen_bwd, gated_scan_varlen_fwd,  # noqa: F401
+                    rms_norm_bwd, rms_norm_fwd, rms_norm_quant_fwd)
+from .block import handle as _handle
 
 _IO = {torch.float32: _lib.SSM_F32, torch.bfloat16: _lib.SSM_BF16, torch.float16: _lib.SSM_F16}
 
@@ -975,10 +978,6 @@ def ssd_scan_workspace_size(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_sof
 # inputs, workspace, new outputs and kernels.  The caller orders it after what
 # made the inputs.
 # ---------------------------------------------------------------------------
-
-def _handle(stream) -> Optional[int]:
-    return None if stream is None else stream.cuda_stream
-
 
 def causal_conv1d_varlen_fwd(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: torch.Tensor,
                              bias: Optional[torch.Tensor] = None, activation=None,

@@ -1,5 +1,5 @@
-// packed_binding.cpp -- the torch binding of the packed-token operators
-// (module _packed).  Argument checks and marshalling only: every step of an
+// packed_binding.cpp -- the torch binding of the packed-token operators and of
+// a gated recurrent block's (module _packed).  Argument checks and marshalling only: every step of an
 // operator runs in libssmscan's kernels behind the C ABI.
 //
 // Their smallest calls take the GPU about five microseconds, which is less
@@ -7,6 +7,7 @@
 // returns (status, outputs...); binding.py names the arguments, documents them
 // and turns a status into an exception.  A refused tensor raises ValueError
 // with the text that the other wrappers use.
+#include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/utils/pybind.h>
 
@@ -16,6 +17,8 @@
 #include <sstream>
 #include <string>
 #include <tuple>
+#include <utility>
+#include <vector>
 
 #include "ssmscan.h"
 
@@ -45,6 +48,7 @@ std::string dtype_text(ScalarType t) {
     case at::kInt: return "torch.int32";
     case at::kLong: return "torch.int64";
     case at::kChar: return "torch.int8";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     case at::kDouble: return "torch.float64";
     default: return c10::toString(t);
   }
@@ -144,7 +148,9 @@ void conv_params(const Tensor &w, const Opt &bias, int64_t channels, at::Device 
 class OnStream {
  public:
   OnStream(at::Device dev, std::optional<int64_t> given) : dev_(dev) {
-    if (!given || !dev.is_cuda()) return;
+    if (!dev.is_cuda()) return;
+    guard_.reset_device(dev);   // (kernels are launched on the current device)
+    if (!given) return;
     before_ = c10::hip::getCurrentHIPStream(dev.index());
     c10::hip::setCurrentHIPStream(c10::hip::getStreamFromExternal(reinterpret_cast<hipStream_t>(*given), dev.index()));
   }
@@ -157,6 +163,7 @@ class OnStream {
 
  private:
   at::Device dev_;
+  c10::OptionalDeviceGuard guard_;
   std::optional<c10::hip::HIPStream> before_;
 };
 
@@ -444,13 +451,237 @@ std::tuple<int, Tensor> step(const Tensor &xBC_, const Tensor &dt_, const Tensor
   return {conv1d_ssd_update(&a, on.handle()), out};
 }
 
+// ---------------------------------------------------------------------------
+// a gated recurrent block
+// ---------------------------------------------------------------------------
+
+// x and its two gates, and their parameters
+template <typename Args>
+void gated_inputs(Args &a, const Tensor &x_, const Tensor &r_, const Tensor &i_, const Tensor &A_, const Opt &rb_,
+                  const Opt &ib_, std::vector<Tensor> &held) {
+  const ScalarType io = x_.scalar_type(), f = at::kFloat;
+  a.io_dtype = io_of(x_, "x", 2);
+  const at::Device dev = x_.device();
+  const int64_t c = x_.size(1);
+  spec(r_, "r", x_.sizes(), io, dev);
+  spec(i_, "i", x_.sizes(), io, dev);
+  spec(A_, "A", {c}, f, dev);
+  spec(rb_, "r_bias", {c}, f, dev);
+  spec(ib_, "i_bias", {c}, f, dev);
+  auto keep = [&](Tensor t) -> const Tensor & { held.push_back(std::move(t)); return held.back(); };
+  held.reserve(8);
+  const Tensor &x = keep(tokens(x_)), &r = keep(tokens(r_)), &i = keep(tokens(i_));
+  a.channels = c;
+  a.x = addr(x); a.x_stride = stride(x);
+  a.r = addr(r); a.r_stride = stride(r);
+  a.i = addr(i); a.i_stride = stride(i);
+  a.A = f32(keep(dense(A_)));
+  if (rb_) a.r_bias = f32(keep(dense(*rb_)));
+  if (ib_) a.i_bias = f32(keep(dense(*ib_)));
+}
+
+void gated_state(const Tensor &state, int64_t channels, at::Device dev) {
+  if (state.dim() != 2) refuse("state must have shape (entries, channels), got " + tuple_text(state.sizes()));
+  out_spec(state, "state", {state.size(0), channels}, at::kFloat, dev);
+}
+
+std::tuple<int, Tensor> gated_fwd(const Tensor &x, const Tensor &r, const Tensor &i, const Tensor &A, const Tensor &cu_,
+                                  const Opt &rb, const Opt &ib, const Opt &state, const Opt &seen_, const Opt &slots_,
+                                  const Opt &ckpt, const Opt &out_, const Opt &ws_, std::optional<int64_t> stream) {
+  const at::Device dev = x.device();
+  const OnStream on(dev, stream);
+  gated_scan_varlen_args_t a{};
+  std::vector<Tensor> held;
+  gated_inputs(a, x, r, i, A, rb, ib, held);
+  a.nseq = cu_spec(cu_, dev);
+  a.total = x.size(0);
+  if (state) {
+    gated_state(*state, a.channels, dev);
+    a.state = state->data_ptr<float>();
+    a.state_slots = state->size(0);
+  }
+  spec(seen_, "cache_seqlens", {a.nseq}, at::kInt, dev);
+  spec(slots_, "slots", {a.nseq}, at::kInt, dev);
+  if (ckpt) {
+    out_spec(ckpt, "checkpoints", {gated_checkpoint_slots(a.total), a.channels}, at::kFloat, dev);
+    a.checkpoints = ckpt->data_ptr<float>();
+  }
+  on_gpu(dev);
+  const Tensor cu = dense(cu_), out = tokens_out(out_, "out", x.sizes(), x.scalar_type(), dev);
+  const Opt seen = dense(seen_), slots = dense(slots_);
+  a.cu_seqlens = cu.data_ptr<int32_t>();
+  a.out = out.data_ptr();
+  a.out_stride = stride(out);
+  a.cache_seqlens = i32(seen);
+  a.slots = i32(slots);
+  Opt ws;
+  int st = workspace(gated_scan_varlen_fwd_workspace_size, a, ws_, dev, ws);
+  if (st == SSM_OK) st = gated_scan_varlen_fwd(&a, on.handle());
+  return {st, out};
+}
+
+using GatedGrads = std::tuple<int, Tensor, Tensor, Tensor, Tensor, Opt, Opt, Opt>;
+
+GatedGrads gated_bwd(const Tensor &x, const Tensor &r, const Tensor &i, const Tensor &A, const Tensor &cu_, const Tensor &dout_,
+                     const Tensor &ckpt_, const Opt &rb, const Opt &ib, const Opt &init_, const Opt &dfin_, bool want_init,
+                     const Opt &dx_, const Opt &dr_, const Opt &di_, const Opt &ws_, std::optional<int64_t> stream) {
+  const at::Device dev = x.device();
+  const OnStream on(dev, stream);
+  gated_scan_varlen_bwd_args_t a{};
+  std::vector<Tensor> held;
+  gated_inputs(a.fwd, x, r, i, A, rb, ib, held);
+  const ScalarType io = x.scalar_type(), f = at::kFloat;
+  a.fwd.nseq = cu_spec(cu_, dev);
+  a.fwd.total = x.size(0);
+  const int64_t c = a.fwd.channels;
+  spec(dout_, "dout", x.sizes(), io, dev);
+  spec(ckpt_, "checkpoints", {gated_checkpoint_slots(a.fwd.total), c}, f, dev);
+  spec(init_, "initial_states", {a.fwd.nseq, c}, f, dev);
+  spec(dfin_, "dfinal_states", {a.fwd.nseq, c}, f, dev);
+  on_gpu(dev);
+  const Tensor cu = dense(cu_), dout = tokens(dout_), ckpt = dense(ckpt_);
+  const Opt init = dense(init_), dfin = dense(dfin_);
+  const Tensor dx = tokens_out(dx_, "dx", x.sizes(), io, dev), dr = tokens_out(dr_, "dr", x.sizes(), io, dev);
+  const Tensor di = tokens_out(di_, "di", x.sizes(), io, dev), dA = make({c}, f, dev);
+  Opt drb, dib, dinit;
+  if (rb) drb = make({c}, f, dev);
+  if (ib) dib = make({c}, f, dev);
+  if (want_init) dinit = make({a.fwd.nseq, c}, f, dev);
+  a.fwd.cu_seqlens = cu.data_ptr<int32_t>();
+  a.fwd.checkpoints = ckpt.data_ptr<float>();
+  a.initial_states = f32(init);
+  a.dfinal_states = f32(dfin);
+  a.dout = addr(dout); a.dout_stride = stride(dout);
+  a.dx = dx.data_ptr(); a.dx_stride = stride(dx);
+  a.dr = dr.data_ptr(); a.dr_stride = stride(dr);
+  a.di = di.data_ptr(); a.di_stride = stride(di);
+  a.dA = dA.data_ptr<float>();
+  a.dr_bias = drb ? drb->data_ptr<float>() : nullptr;
+  a.di_bias = dib ? dib->data_ptr<float>() : nullptr;
+  a.dinitial_states = dinit ? dinit->data_ptr<float>() : nullptr;
+  Opt ws;
+  int st = workspace(gated_scan_varlen_bwd_workspace_size, a, ws_, dev, ws);
+  if (st == SSM_OK) st = gated_scan_varlen_bwd(&a, on.handle());
+  return {st, dx, dr, di, dA, drb, dib, dinit};
+}
+
+std::tuple<int, Tensor> gated_step(const Tensor &x, const Tensor &r, const Tensor &i, const Tensor &A, const Tensor &state,
+                                   const Opt &seen_, const Opt &rb, const Opt &ib, const Opt &slots_, const Opt &out_,
+                                   std::optional<int64_t> stream) {
+  const at::Device dev = x.device();
+  const OnStream on(dev, stream);
+  gated_scan_update_args_t a{};
+  std::vector<Tensor> held;
+  gated_inputs(a, x, r, i, A, rb, ib, held);
+  a.batch = x.size(0);
+  gated_state(state, a.channels, dev);
+  spec(seen_, "cache_seqlens", {a.batch}, at::kInt, dev);
+  spec(slots_, "slots", {a.batch}, at::kInt, dev);
+  on_gpu(dev);
+  const Tensor out = tokens_out(out_, "out", x.sizes(), x.scalar_type(), dev);
+  const Opt seen = dense(seen_), slots = dense(slots_);
+  a.state = state.data_ptr<float>();
+  a.state_slots = state.size(0);
+  a.cache_seqlens = i32(seen);
+  a.slots = i32(slots);
+  a.out = out.data_ptr();
+  a.out_stride = stride(out);
+  return {gated_scan_update(&a, on.handle()), out};
+}
+
+std::tuple<int, Tensor, Opt, Opt> norm_fwd(const Tensor &x_, const Tensor &w_, const Opt &res_, const Opt &z_,
+                                           std::optional<int64_t> group, double eps, bool quant, const Opt &out_,
+                                           const Opt &scales_, const Opt &rout_, std::optional<int64_t> stream) {
+  rms_norm_args_t a{};
+  a.io_dtype = a.residual_dtype = io_of(x_, "x", 2);
+  const ScalarType io = x_.scalar_type();
+  const at::Device dev = x_.device();
+  const OnStream on(dev, stream);
+  a.rows = x_.size(0); a.cols = x_.size(1); a.group_size = group.value_or(a.cols); a.eps = static_cast<float>(eps);
+  spec(w_, "weight", {a.cols}, at::kFloat, dev);
+  spec(z_, "z", x_.sizes(), io, dev);
+  if (res_ && z_) refuse("the norm takes a residual or a gate, not both");
+  if (!res_ && rout_) refuse("residual_out goes with a residual");
+  if (res_) {
+    spec(res_, "residual", x_.sizes(), res_->scalar_type() == at::kFloat ? at::kFloat : io, dev);
+    if (res_->scalar_type() == at::kFloat) a.residual_dtype = SSM_F32;
+  }
+  const int64_t blocks = (a.cols + RMS_SCALE_BLOCK - 1) / RMS_SCALE_BLOCK;
+  if (quant) out_spec(scales_, "scales", {a.rows, blocks}, at::kFloat, dev);
+  on_gpu(dev);
+  const Tensor x = tokens(x_), w = dense(w_), out = tokens_out(out_, quant ? "codes" : "out", x_.sizes(), quant ? at::kFloat8_e4m3fn : io, dev);
+  const Opt z = tokens(z_), res = tokens(res_);
+  Opt rout, scales;
+  if (res) rout = tokens_out(rout_, "residual_out", x_.sizes(), res->scalar_type(), dev);
+  a.x = addr(x); a.x_stride = stride(x);
+  a.weight = f32(w);
+  if (z) { a.z = addr(*z); a.z_stride = stride(*z); }
+  if (res) {
+    a.residual = addr(*res); a.residual_stride = stride(*res);
+    a.residual_out = rout->data_ptr(); a.residual_out_stride = stride(*rout);
+  }
+  if (quant) {
+    scales = scales_ ? *scales_ : make({a.rows, blocks}, at::kFloat, dev);
+    a.codes = out.data_ptr(); a.codes_stride = stride(out);
+    a.scales = scales->data_ptr<float>();
+  } else {
+    a.out = out.data_ptr(); a.out_stride = stride(out);
+  }
+  return {rms_norm_fwd(&a, on.handle()), out, scales, rout};
+}
+
+std::tuple<int, Tensor, Opt, Opt, Tensor> norm_bwd(const Tensor &x_, const Tensor &w_, const Tensor &dy_, const Opt &z_,
+                                                   const Opt &ds_, std::optional<int64_t> group, double eps, const Opt &dx_,
+                                                   const Opt &dres_, const Opt &dz_, const Opt &ws_,
+                                                   std::optional<int64_t> stream) {
+  rms_norm_bwd_args_t a{};
+  a.io_dtype = io_of(dy_, "dy", 2);
+  a.x_dtype = io_of(x_, "x", 2);
+  const ScalarType io = dy_.scalar_type(), xt = x_.scalar_type();
+  const at::Device dev = dy_.device();
+  const OnStream on(dev, stream);
+  a.rows = dy_.size(0); a.cols = dy_.size(1); a.group_size = group.value_or(a.cols); a.eps = static_cast<float>(eps);
+  spec(x_, "x", dy_.sizes(), xt == at::kFloat ? at::kFloat : io, dev);
+  spec(w_, "weight", {a.cols}, at::kFloat, dev);
+  spec(z_, "z", dy_.sizes(), io, dev);
+  spec(ds_, "ds", dy_.sizes(), xt, dev);
+  if (z_ && ds_) refuse("the norm takes a residual or a gate, not both");
+  if (z_ && xt != io) refuse("x and the gate must have one dtype, got " + dtype_text(xt) + " and " + dtype_text(io));
+  if (dz_ && !z_) refuse("dz goes with z");
+  if (dres_ && xt == io) refuse("dresidual goes with an x of another dtype than dy's: dx is the residual's gradient");
+  on_gpu(dev);
+  const Tensor x = tokens(x_), w = dense(w_), dy = tokens(dy_), dx = tokens_out(dx_, "dx", dy_.sizes(), io, dev);
+  const Opt z = tokens(z_), ds = tokens(ds_);
+  const Tensor dw = make({a.cols}, at::kFloat, dev);
+  Opt dres, dz;
+  if (xt != io) dres = tokens_out(dres_, "dresidual", dy_.sizes(), xt, dev);
+  if (z) dz = tokens_out(dz_, "dz", dy_.sizes(), io, dev);
+  a.x = addr(x); a.x_stride = stride(x);
+  a.weight = f32(w);
+  a.dy = addr(dy); a.dy_stride = stride(dy);
+  if (z) { a.z = addr(*z); a.z_stride = stride(*z); a.dz = dz->data_ptr(); a.dz_stride = stride(*dz); }
+  if (ds) { a.ds = addr(*ds); a.ds_stride = stride(*ds); }
+  a.dx = dx.data_ptr(); a.dx_stride = stride(dx);
+  if (dres) { a.dresidual = dres->data_ptr(); a.dresidual_stride = stride(*dres); }
+  a.dweight = dw.data_ptr<float>();
+  Opt ws;
+  int st = workspace(rms_norm_bwd_workspace_size, a, ws_, dev, ws);
+  if (st == SSM_OK) st = rms_norm_bwd(&a, on.handle());
+  return {st, dx, dres, dz, dw};
+}
+
 }  // namespace
 
 PYBIND11_MODULE(_packed, m) {
-  m.doc() = "Checks and marshalling of the packed-token operators (see binding.py).";
+  m.doc() = "Checks and marshalling of the packed-token and the gated block's operators (see binding.py).";
   m.def("conv_fwd", &conv_fwd);
   m.def("conv_bwd", &conv_bwd);
   m.def("scan_fwd", &scan_fwd);
   m.def("scan_bwd", &scan_bwd);
   m.def("step", &step);
+  m.def("gated_fwd", &gated_fwd);
+  m.def("gated_bwd", &gated_bwd);
+  m.def("gated_step", &gated_step);
+  m.def("norm_fwd", &norm_fwd);
+  m.def("norm_bwd", &norm_bwd);
 }

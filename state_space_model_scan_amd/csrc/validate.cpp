@@ -389,6 +389,104 @@ extern "C" int conv1d_ssd_update_validate(const conv1d_ssd_update_args_t *a) {
   return SSM_OK;
 }
 
+// A gated recurrent block: its recurrence over packed tokens, and its norm.
+namespace {
+
+bool rows_fit(int64_t rows, int64_t cols, int64_t stride) { return stride >= cols && product_fits(rows, stride, 1); }
+
+int gated_common(const gated_scan_varlen_args_t *a) {
+  if (!a) return SSM_ERR_NULL;
+  if (!positive(a->total) || !positive(a->nseq) || !positive(a->channels)) return SSM_ERR_SHAPE;
+  if (a->total > 0x7fffffffLL || a->nseq > 0x7fffffffLL || a->channels > 0x7fffffffLL) return SSM_ERR_SHAPE;   // int32 edges
+  if (!rows_fit(a->total, a->channels, a->x_stride) || !rows_fit(a->total, a->channels, a->r_stride) ||
+      !rows_fit(a->total, a->channels, a->i_stride) || !product_fits(a->nseq, a->channels, 1))
+    return SSM_ERR_SHAPE;
+  if (!io_ok(a->io_dtype)) return SSM_ERR_UNSUPPORTED;
+  if (!a->x || !a->r || !a->i || !a->A || !a->cu_seqlens) return SSM_ERR_NULL;
+  return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" int64_t gated_checkpoint_slots(int64_t total) { return total / GATED_CHUNK + (total % GATED_CHUNK > 0); }
+
+extern "C" int gated_scan_varlen_fwd_validate(const gated_scan_varlen_args_t *a) {
+  const int st = gated_common(a);
+  if (st != SSM_OK) return st;
+  if (!a->out) return SSM_ERR_NULL;
+  if (!rows_fit(a->total, a->channels, a->out_stride)) return SSM_ERR_SHAPE;
+  if (a->state && (!positive(a->state_slots) || !product_fits(a->state_slots, a->channels, 1))) return SSM_ERR_SHAPE;
+  return SSM_OK;
+}
+
+extern "C" int gated_scan_varlen_bwd_validate(const gated_scan_varlen_bwd_args_t *a) {
+  if (!a) return SSM_ERR_NULL;
+  const gated_scan_varlen_args_t &f = a->fwd;
+  const int st = gated_common(&f);
+  if (st != SSM_OK) return st;
+  if (!f.checkpoints || !a->dout || !a->dx || !a->dr || !a->di || !a->dA || (f.r_bias && !a->dr_bias) ||
+      (f.i_bias && !a->di_bias))
+    return SSM_ERR_NULL;
+  if (!rows_fit(f.total, f.channels, a->dout_stride) || !rows_fit(f.total, f.channels, a->dx_stride) ||
+      !rows_fit(f.total, f.channels, a->dr_stride) || !rows_fit(f.total, f.channels, a->di_stride))
+    return SSM_ERR_SHAPE;
+  return SSM_OK;
+}
+
+extern "C" int gated_scan_update_validate(const gated_scan_update_args_t *a) {
+  if (!a) return SSM_ERR_NULL;
+  if (!positive(a->batch) || !positive(a->channels) || !positive(a->state_slots)) return SSM_ERR_SHAPE;
+  if (a->batch > 0x7fffffffLL || a->channels > 0x7fffffffLL) return SSM_ERR_SHAPE;
+  if (!rows_fit(a->batch, a->channels, a->x_stride) || !rows_fit(a->batch, a->channels, a->r_stride) ||
+      !rows_fit(a->batch, a->channels, a->i_stride) || !rows_fit(a->batch, a->channels, a->out_stride) ||
+      !product_fits(a->state_slots, a->channels, 1))
+    return SSM_ERR_SHAPE;
+  if (!io_ok(a->io_dtype)) return SSM_ERR_UNSUPPORTED;
+  if (!a->x || !a->r || !a->i || !a->A || !a->state || !a->out) return SSM_ERR_NULL;
+  return SSM_OK;
+}
+
+namespace {
+
+int norm_common(int64_t rows, int64_t cols, int64_t group, int32_t io, int32_t wide, float eps) {
+  if (!positive(rows) || !positive(cols) || !positive(group) || cols % group != 0) return SSM_ERR_SHAPE;
+  if (rows > 0x7fffffffLL || cols > 0x7fffffffLL) return SSM_ERR_SHAPE;
+  if (!io_ok(io) || (wide != io && wide != SSM_F32) || group > RMS_MAX_GROUP) return SSM_ERR_UNSUPPORTED;
+  if (!(eps >= 0.0f)) return SSM_ERR_SHAPE;
+  return SSM_OK;
+}
+
+}  // namespace
+
+extern "C" int rms_norm_fwd_validate(const rms_norm_args_t *a) {
+  if (!a) return SSM_ERR_NULL;
+  const int st = norm_common(a->rows, a->cols, a->group_size, a->io_dtype, a->residual_dtype, a->eps);
+  if (st != SSM_OK) return st;
+  if (!a->x || !a->weight || (!a->residual) != (!a->residual_out)) return SSM_ERR_NULL;
+  if ((!a->out && !a->codes) || (!a->codes) != (!a->scales)) return SSM_ERR_NULL;
+  if ((a->z && a->residual) || (a->out && a->codes)) return SSM_ERR_UNSUPPORTED;
+  if (!rows_fit(a->rows, a->cols, a->x_stride) || (a->z && !rows_fit(a->rows, a->cols, a->z_stride)) ||
+      (a->residual && (!rows_fit(a->rows, a->cols, a->residual_stride) || !rows_fit(a->rows, a->cols, a->residual_out_stride))) ||
+      (a->out && !rows_fit(a->rows, a->cols, a->out_stride)) || (a->codes && !rows_fit(a->rows, a->cols, a->codes_stride)))
+    return SSM_ERR_SHAPE;
+  if (a->codes && a->group_size != a->cols && a->group_size % RMS_SCALE_BLOCK != 0) return SSM_ERR_UNSUPPORTED;
+  return SSM_OK;
+}
+
+extern "C" int rms_norm_bwd_validate(const rms_norm_bwd_args_t *a) {
+  if (!a) return SSM_ERR_NULL;
+  const int st = norm_common(a->rows, a->cols, a->group_size, a->io_dtype, a->x_dtype, a->eps);
+  if (st != SSM_OK) return st;
+  if (!a->x || !a->weight || !a->dy || !a->dx || !a->dweight || (!a->z) != (!a->dz)) return SSM_ERR_NULL;
+  if (a->z && (a->ds || a->dresidual || a->x_dtype != a->io_dtype)) return SSM_ERR_UNSUPPORTED;
+  if (!rows_fit(a->rows, a->cols, a->x_stride) || !rows_fit(a->rows, a->cols, a->dy_stride) ||
+      !rows_fit(a->rows, a->cols, a->dx_stride) || (a->ds && !rows_fit(a->rows, a->cols, a->ds_stride)) ||
+      (a->dresidual && !rows_fit(a->rows, a->cols, a->dresidual_stride)) ||
+      (a->z && (!rows_fit(a->rows, a->cols, a->z_stride) || !rows_fit(a->rows, a->cols, a->dz_stride))))
+    return SSM_ERR_SHAPE;
+  return SSM_OK;
+}
+
 extern "C" const char *ssm_status_str(int status) {
   switch (status) {
     case SSM_OK: return "ok";
