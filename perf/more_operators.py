@@ -353,7 +353,8 @@ def _own(st):
             codes, scales, *kept = ssm.rms_norm_quant_fwd(st["x"], st["weight"], **kw)
             r = {"out": _values(codes, scales)}
         else:
-            out, *kept = ssm.rms_norm_fwd(st["x"], st["weight"], **kw)
+            got = ssm.rms_norm_fwd(st["x"], st["weight"], **kw)
+            out, *kept = (got,) if st["residual"] is None else got
             r = {"out": out}
         if st["residual"] is not None:
             r["residual"] = kept[0]
