@@ -1,10 +1,19 @@
 // rms_norm.hip -- root-mean-square norm with the residual's addition or behind
 // a gate, to io or to 8 bits (rms_norm_fwd), and its gradient (rms_norm_bwd).
 //
-// A workgroup takes a row, group by group.
+// Both stream: every element is read once, held in registers, and written once.
+// A group of columns is a unit of its own; L lanes take it (16 to 64 of a wave,
+// or 2 to 8 whole waves), each K vectors of V neighbouring columns (16 bytes,
+// or one element where rows are odd or not aligned), as few lanes as K allows:
+// then a wave has more loads in flight, fewer idle lanes and no barrier.
+//
+// The gradient's workgroups walk the rows of their units, so that a lane's
+// weight gradients stay in its registers; the workgroups' sums are added by a
+// second launch, in a fixed order.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "device_util.h"
 #include "host_util.h"
@@ -13,34 +22,59 @@
 namespace ssm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kMaxThreads = 512;
 
 struct NormParams {
   const void *x, *z, *res, *dy, *ds;
   const float *w;
   void *rout, *out, *dx, *dres, *dz;
   uint8_t *codes;
-  float *scales, *stat, *dw;
-  int64_t rows, cols, group, xs, zs, rs, ros, os, cs, dys, dss, dxs, drs, dzs;
+  float *scales, *part, *dw;
+  int64_t rows, cols, xs, zs, rs, ros, os, cs, dys, dss, dxs, drs, dzs;
+  int group, groups, lanes;   // lanes: of a unit, a power of two
   float eps;
 };
 
-__device__ __forceinline__ float block_sum(float v, float *lds) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+// V elements of a type, 16 bytes of them (or 8 of 16 bits beside 8 of 32, in
+// two loads), or one.
+template <int IO, int V>
+struct Vec {
+  RawV<IO, V> r;
+  __device__ __forceinline__ void load(const void *p, int64_t i) { r.load_vec(p, i); }
+  __device__ __forceinline__ float get(int k) const { return r.get(k); }
+  __device__ __forceinline__ void zero() { r.zero(); }
+};
+template <int IO>
+struct Vec<IO, 1> {
+  float v;
+  __device__ __forceinline__ void load(const void *p, int64_t i) { v = load_io<IO>(p, i); }
+  __device__ __forceinline__ float get(int) const { return v; }
+  __device__ __forceinline__ void zero() { v = 0.0f; }
+};
+template <int IO, int V>
+__device__ __forceinline__ void put(void *p, int64_t i, const float (&v)[V]) {
+  if constexpr (V == 1) store_one<IO>(p, i, v[0]);
+  else store_n<IO, V>(p, i, v, V, true);
+}
+
+// Sum over a unit's lanes; more than a wave of them meet in LDS (`room`: a
+// float for every wave of the workgroup), where every thread has to be there.
+__device__ __forceinline__ float unit_sum(float v, int lanes, float *room) {
+  const int in_wave = lanes < 64 ? lanes : 64;
+  for (int o = 1; o < in_wave; o <<= 1) v += __shfl_xor(v, o);
+  if (lanes <= 64) return v;
+  const int wave = threadIdx.x >> 6, per = lanes >> 6, first = wave & ~(per - 1);
+  if ((threadIdx.x & 63) == 0) room[wave] = v;
   __syncthreads();
   float s = 0.0f;
-  for (int k = 0; k < kThreads / 64; ++k) s += lds[k];
+  for (int k = 0; k < per; ++k) s += room[first + k];
   return s;
 }
 
-// One code of a value: the hardware's rounding to e4m3, ties to even.
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-  return static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v, v, 0, false) & 0xff);
-}
-// The smallest power of two s with amax <= 448 s (448 = 1.75 * 2^8), and 1 / s.
+// The smallest power of two s with amax <= 448 s (448 = 1.75 * 2^8), and 1 / s:
+// a code times a power of two is exact in bf16, and against amax / 448 the
+// coarser scale costs an e4m3 value none of its four significant bits.  At least
+// 2^-100, which keeps every value a normal number.  NaN where amax is not finite.
 __device__ __forceinline__ float e4m3_scale(uint32_t amax, float &inv) {
   if (amax >= 0x7f800000u) {
     inv = 0.0f;
@@ -52,91 +86,292 @@ __device__ __forceinline__ float e4m3_scale(uint32_t amax, float &inv) {
   return __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
-// What is normalised at (row, column): MODE 0 x, 1 x + residual (RES its type), 2 x silu(z).
-template <int IO, int MODE, int RES>
-__device__ __forceinline__ float value_at(const NormParams &p, int64_t row, int64_t c) {
-  const float x = load_io<IO>(p.x, row * p.xs + c);
-  if constexpr (MODE == 1) return round_io<RES>(x + load_io<RES>(p.res, row * p.rs + c));
-  if constexpr (MODE == 2) return x * silu_f(load_io<IO>(p.z, row * p.zs + c));
-  return x;
-}
+enum Mode { kPlain, kAdd, kGate };
 
-template <int IO, int MODE, int RES>
-__global__ void __launch_bounds__(kThreads) norm_fwd_kernel(const NormParams p) {
-  __shared__ float lds[kThreads / 64];
-  __shared__ float v[RMS_MAX_GROUP / kThreads][kThreads];
-  __shared__ uint32_t top[RMS_MAX_GROUP / RMS_SCALE_BLOCK];
-  const int64_t row = blockIdx.x, first = blockIdx.y * p.group;
-  const int n = static_cast<int>(p.group), nb = (n + RMS_SCALE_BLOCK - 1) / RMS_SCALE_BLOCK;
-  float sum = 0.0f;
-  for (int k = threadIdx.x; k < n; k += kThreads) {
-    const float q = value_at<IO, MODE, RES>(p, row, first + k);
-    v[k / kThreads][threadIdx.x] = q;
-    if constexpr (MODE == 1) store_one<RES>(p.rout, row * p.ros + first + k, q);
-    sum = fmaf(q, q, sum);
-  }
-  for (int k = threadIdx.x; k < nb; k += kThreads) top[k] = 0;
-  const float rstd = 1.0f / sqrtf(block_sum(sum, lds) / n + p.eps);
-  for (int k = threadIdx.x; k < n; k += kThreads) {
-    const float y = v[k / kThreads][threadIdx.x] * rstd * p.w[first + k];
-    v[k / kThreads][threadIdx.x] = y;
-    if (p.codes) atomicMax(&top[k / RMS_SCALE_BLOCK], __float_as_uint(y) & 0x7fffffffu);
-    else store_one<IO>(p.out, row * p.os + first + k, y);
-  }
-  if (!p.codes) return;
-  __syncthreads();
-  for (int k = threadIdx.x; k < n; k += kThreads) {
-    float inv;
-    const float scale = e4m3_scale(top[k / RMS_SCALE_BLOCK], inv);
-    p.codes[row * p.cs + first + k] = to_e4m3(v[k / kThreads][threadIdx.x] * inv);
-    if (k % RMS_SCALE_BLOCK == 0)
-      p.scales[row * ((p.cols + RMS_SCALE_BLOCK - 1) / RMS_SCALE_BLOCK) + (first + k) / RMS_SCALE_BLOCK] = scale;
-  }
-}
+// RES: the residual's type.  8 bits: QUANT.
+template <int IO, int MODE, int RES, bool QUANT, int V, int K>
+__global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams p) {
+  __shared__ float room[kMaxThreads / 64];
+  __shared__ uint32_t top[QUANT && V == 1 ? RMS_MAX_GROUP / RMS_SCALE_BLOCK : 1];
+  const int lane = threadIdx.x & (p.lanes - 1);
+  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / p.lanes;
+  const int64_t row = unit / p.groups;
+  const int first = static_cast<int>(unit - row * p.groups) * p.group;
+  const bool there = row < p.rows;
 
-template <int IO, int XT, bool GATE>
-__global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormParams p) {
-  __shared__ float lds[kThreads / 64];
-  const int64_t row = blockIdx.x, first = blockIdx.y * p.group;
-  const int n = static_cast<int>(p.group);
-  float sum = 0.0f, dot = 0.0f;
-  for (int k = threadIdx.x; k < n; k += kThreads) {
-    float v = load_io<XT>(p.x, row * p.xs + first + k);
-    if constexpr (GATE) v *= silu_f(load_io<IO>(p.z, row * p.zs + first + k));
-    sum = fmaf(v, v, sum);
-    dot = fmaf(v, load_io<IO>(p.dy, row * p.dys + first + k) * p.w[first + k], dot);
-  }
-  const float rstd = 1.0f / sqrtf(block_sum(sum, lds) / n + p.eps);
-  const float mean = block_sum(dot, lds) * rstd / n;
-  if (threadIdx.x == 0) p.stat[row * gridDim.y + blockIdx.y] = rstd;
-  for (int k = threadIdx.x; k < n; k += kThreads) {
-    const float x = load_io<XT>(p.x, row * p.xs + first + k);
-    float gate = 1.0f, dgate = 0.0f;
-    if constexpr (GATE) {
-      const float z = load_io<IO>(p.z, row * p.zs + first + k), sg = fast_rcp(1.0f + fast_exp2(-z * kLog2e));
-      gate = z * sg;
-      dgate = sg * fmaf(z, 1.0f - sg, 1.0f);
+  Vec<IO, V> x[K];
+  Vec<MODE == kAdd ? RES : IO, V> r[MODE == kPlain ? 1 : K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * p.lanes + lane) * V;
+    if (there && c < p.group) {
+      x[k].load(p.x, row * p.xs + first + c);
+      if constexpr (MODE == kAdd) r[k].load(p.res, row * p.rs + first + c);
+      if constexpr (MODE == kGate) r[k].load(p.z, row * p.zs + first + c);
+    } else {
+      x[k].zero();
+      if constexpr (MODE != kPlain) r[k].zero();
     }
-    const float dv = rstd * fmaf(-x * gate * rstd, mean, load_io<IO>(p.dy, row * p.dys + first + k) * p.w[first + k]);
-    float dx = dv * gate;
-    if (p.ds) dx += load_io<XT>(p.ds, row * p.dss + first + k);
-    if (p.dres) store_one<XT>(p.dres, row * p.drs + first + k, dx);
-    store_one<IO>(p.dx, row * p.dxs + first + k, dx);
-    if constexpr (GATE) store_one<IO>(p.dz, row * p.dzs + first + k, dv * x * dgate);
+  }
+  float v[K][V], sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float q = x[k].get(i);
+      if constexpr (MODE == kAdd) q = round_io<RES>(q + r[k].get(i));
+      if constexpr (MODE == kGate) q *= silu_f(r[k].get(i));
+      v[k][i] = q;
+      sum = fmaf(q, q, sum);
+    }
+    if constexpr (MODE == kAdd) {
+      const int c = (k * p.lanes + lane) * V;
+      if (there && c < p.group) put<RES, V>(p.rout, row * p.ros + first + c, v[k]);
+    }
+  }
+  sum = unit_sum(sum, p.lanes, room);
+  const float rstd = 1.0f / sqrtf(sum / p.group + p.eps);
+  if constexpr (!QUANT) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * p.lanes + lane) * V;
+      if (!there || c >= p.group) continue;
+      Vec<0, V> w;
+      w.load(p.w, first + c);
+      float y[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[i] = v[k][i] * rstd * w.get(i);
+      put<IO, V>(p.out, row * p.os + first + c, y);
+    }
+  } else {
+    const int64_t blocks = (p.cols + RMS_SCALE_BLOCK - 1) / RMS_SCALE_BLOCK;
+    if constexpr (V == 1) {   // a block's columns are spread over its unit's lanes: its largest through LDS (units of a wave or more: one a workgroup)
+      for (int k = threadIdx.x; k < RMS_MAX_GROUP / RMS_SCALE_BLOCK; k += blockDim.x) top[k] = 0;
+      __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * p.lanes + lane) * V;
+      const bool in = there && c < p.group;
+      uint32_t amax = 0;
+      if (in) {
+        Vec<0, V> w;
+        w.load(p.w, first + c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          v[k][i] *= rstd * w.get(i);
+          const uint32_t b = __float_as_uint(v[k][i]) & 0x7fffffffu;
+          amax = b > amax ? b : amax;
+        }
+      }
+      if constexpr (V == 1) {
+        if (in) atomicMax(&top[c / RMS_SCALE_BLOCK], amax);
+      } else {   // 128 / V neighbouring lanes hold a block
+#pragma unroll
+        for (int o = 1; o < RMS_SCALE_BLOCK / V; o <<= 1) {
+          const uint32_t other = __shfl_xor(amax, o);
+          amax = other > amax ? other : amax;
+        }
+        float inv;
+        const float scale = e4m3_scale(amax, inv);
+        if (in) {
+          uint32_t w[V / 4];
+#pragma unroll
+          for (int i = 0; i < V / 4; ++i) {
+            int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[k][4 * i] * inv, v[k][4 * i + 1] * inv, 0, false);
+            w[i] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[k][4 * i + 2] * inv, v[k][4 * i + 3] * inv, q, true));
+          }
+          uint8_t *at = p.codes + row * p.cs + first + c;
+          if constexpr (V == 8) *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
+          else *reinterpret_cast<uint32_t *>(at) = w[0];
+          if (c % RMS_SCALE_BLOCK == 0) p.scales[row * blocks + (first + c) / RMS_SCALE_BLOCK] = scale;
+        }
+      }
+    }
+    if constexpr (V == 1) {
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int c = k * p.lanes + lane;
+        if (!there || c >= p.group) continue;
+        float inv;
+        const float scale = e4m3_scale(top[c / RMS_SCALE_BLOCK], inv), q = v[k][0] * inv;
+        p.codes[row * p.cs + first + c] = static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false));
+        if (c % RMS_SCALE_BLOCK == 0) p.scales[row * blocks + (first + c) / RMS_SCALE_BLOCK] = scale;
+      }
+    }
   }
 }
 
-template <int IO, int XT, bool GATE>
-__global__ void __launch_bounds__(64) norm_dweight_kernel(const NormParams p) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 64 + threadIdx.x;
-  if (c >= p.cols) return;
-  double v = 0.0;
-  for (int64_t row = 0; row < p.rows; ++row) {
-    float x = load_io<XT>(p.x, row * p.xs + c);
-    if constexpr (GATE) x *= silu_f(load_io<IO>(p.z, row * p.zs + c));
-    v += x * p.stat[row * (p.cols / p.group) + c / p.group] * load_io<IO>(p.dy, row * p.dys + c);
+// XT: x's type.  A workgroup's units are `blockDim.x / lanes` rows of one group
+// of columns at a time; it walks the rows in steps of the whole grid.
+template <int IO, int XT, bool GATE, int V, int K>
+__global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormParams p) {
+  __shared__ float room[2][kMaxThreads / 64];
+  extern __shared__ float sums[];
+  const int lane = threadIdx.x & (p.lanes - 1), here = threadIdx.x / p.lanes, units = blockDim.x / p.lanes;
+  const int first = blockIdx.y * p.group;
+  float w[K][V], dw[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * p.lanes + lane) * V;
+    Vec<0, V> q;
+    if (c < p.group) q.load(p.w, first + c);
+    else q.zero();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[k][i] = q.get(i);
+      dw[k][i] = 0.0f;
+    }
   }
-  p.dw[c] = static_cast<float>(v);
+  const float n = static_cast<float>(p.group);
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * units; base < p.rows; base += static_cast<int64_t>(gridDim.x) * units) {
+    const int64_t row = base + here;
+    const bool there = row < p.rows;
+    Vec<XT, V> x[K], ds[GATE ? 1 : K];
+    Vec<IO, V> dy[K], z[GATE ? K : 1];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * p.lanes + lane) * V;
+      if (there && c < p.group) {
+        x[k].load(p.x, row * p.xs + first + c);
+        dy[k].load(p.dy, row * p.dys + first + c);
+        if constexpr (GATE) z[k].load(p.z, row * p.zs + first + c);
+        else if (p.ds) ds[k].load(p.ds, row * p.dss + first + c);
+        else ds[k].zero();
+      } else {
+        x[k].zero();
+        dy[k].zero();
+        if constexpr (GATE) z[k].zero();
+        else ds[k].zero();
+      }
+    }
+    float sum = 0.0f, dot = 0.0f, sg[GATE ? K : 1][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float v = x[k].get(i);
+        if constexpr (GATE) {
+          const float q = z[k].get(i);
+          sg[k][i] = fast_rcp(1.0f + fast_exp2(-q * kLog2e));
+          v *= q * sg[k][i];
+        }
+        sum = fmaf(v, v, sum);
+        dot = fmaf(v, dy[k].get(i) * w[k][i], dot);
+      }
+    if (p.lanes > 64) __syncthreads();   // (the room's last readers are done)
+    sum = unit_sum(sum, p.lanes, room[0]);
+    dot = unit_sum(dot, p.lanes, room[1]);
+    const float rstd = 1.0f / sqrtf(sum / n + p.eps);
+    const float mean = dot * rstd / n;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * p.lanes + lane) * V;
+      float dx[V], dz[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float xv = x[k].get(i), g = dy[k].get(i);
+        if constexpr (GATE) {
+          const float q = z[k].get(i), s = sg[k][i], gate = q * s, hat = xv * gate * rstd;
+          const float dv = rstd * fmaf(-hat, mean, g * w[k][i]);
+          dw[k][i] = fmaf(g, hat, dw[k][i]);
+          dx[i] = dv * gate;
+          dz[i] = dv * xv * (s * fmaf(q, 1.0f - s, 1.0f));
+        } else {
+          const float hat = xv * rstd;
+          dw[k][i] = fmaf(g, hat, dw[k][i]);
+          dx[i] = fmaf(rstd, fmaf(-hat, mean, g * w[k][i]), ds[k].get(i));
+        }
+      }
+      if (!there || c >= p.group) continue;
+      put<IO, V>(p.dx, row * p.dxs + first + c, dx);
+      if constexpr (GATE) put<IO, V>(p.dz, row * p.dzs + first + c, dz);
+      else if (p.dres) put<XT, V>(p.dres, row * p.drs + first + c, dx);
+    }
+  }
+  // the units' sums, in order
+  if (units > 1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sums[(k * V + i) * blockDim.x + threadIdx.x] = dw[k][i];
+    __syncthreads();
+    for (int at = here; at < K * V; at += units) {   // (a unit's lanes take an element of every lane)
+      float s = 0.0f;
+      for (int u = 0; u < units; ++u) s += sums[at * blockDim.x + u * p.lanes + lane];
+      const int c = (at / V * p.lanes + lane) * V + at % V;
+      if (c < p.group) p.part[static_cast<int64_t>(blockIdx.x) * p.cols + first + c] = s;
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * p.lanes + lane) * V;
+    if (c < p.group) put<0, V>(p.part, static_cast<int64_t>(blockIdx.x) * p.cols + first + c, dw[k]);
+  }
+}
+
+// Sum of the workgroups' rows, four threads a column, each its quarter in
+// order, in 64 bits.
+__global__ void __launch_bounds__(256) norm_sum_kernel(const float *part, float *dw, int64_t rows, int64_t cols) {
+  __shared__ double sum[4][64];
+  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  double v = 0.0;
+  if (col < cols) {
+    const int64_t to = rows * (q + 1) / 4;
+    int64_t r = rows * q / 4;
+    for (; r + 8 <= to; r += 8) {   // eight loads in flight
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = part[(r + i) * cols + col];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += f[i];
+    }
+    for (; r < to; ++r) v += part[r * cols + col];
+  }
+  sum[q][lane] = v;
+  __syncthreads();
+  if (q == 0 && col < cols) dw[col] = static_cast<float>((sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]));
+}
+
+// Vectors of a lane: of 8 columns of 16 bits or 4 of 32, and of single columns.
+constexpr int kVecK[] = {1, 2, 3, 5};
+constexpr int kVec4K[] = {1, 2, 3, 5, 8};
+constexpr int kOneK[] = {4, 16, 32};
+using VecK = std::integer_sequence<int, 1, 2, 3, 5>;
+using Vec4K = std::integer_sequence<int, 1, 2, 3, 5, 8>;
+using OneK = std::integer_sequence<int, 4, 16, 32>;
+static_assert(kMaxThreads * 5 * 8 >= RMS_MAX_GROUP && kMaxThreads * 8 * 4 >= RMS_MAX_GROUP && kMaxThreads * 32 >= RMS_MAX_GROUP,
+              "the largest group fits a workgroup's registers");
+
+// How a call's units are laid on lanes: K vectors of V columns at most a lane.
+struct Lay {
+  int k, lanes, threads;
+};
+template <int N>
+Lay lay_of(int64_t group, int v, const int (&ks)[N], int least, int most_k) {
+  Lay l{};
+  const int64_t vecs = (group + v - 1) / v;
+  l.lanes = least;
+  if (most_k > ks[N - 1]) most_k = ks[N - 1];
+  while (l.lanes < kMaxThreads && (vecs + l.lanes - 1) / l.lanes > most_k) l.lanes *= 2;
+  for (int i = N - 1; i >= 0; --i)
+    if ((vecs + l.lanes - 1) / l.lanes <= ks[i]) l.k = ks[i];
+  l.threads = l.lanes > 256 ? l.lanes : 256;
+  return l;
+}
+// `columns`: of a lane, where the largest groups do not take more.
+Lay lay_of(bool vec, int32_t io, int64_t group, int least, int columns) {
+  if (!vec) return lay_of(group, 1, kOneK, least, columns > 16 ? 16 : 4);
+  return io == SSM_F32 ? lay_of(group, 4, kVec4K, least, columns / 4) : lay_of(group, 8, kVecK, least, columns / 8);
+}
+
+bool wide(int32_t type, const void *p, int64_t stride, int v) {
+  const int64_t bytes = type == SSM_F32 ? 4 : 2;
+  const uintptr_t step = static_cast<uintptr_t>(v * bytes > 16 ? 16 : v * bytes);
+  return stride % v == 0 && reinterpret_cast<uintptr_t>(p) % step == 0;
 }
 
 template <typename F>
@@ -148,6 +383,10 @@ int by_io(int32_t io, F &&launch) {
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SSM_OK : hip_fail(e);
 }
+template <int... Ks, typename F>
+void by_k(std::integer_sequence<int, Ks...>, int k, F &&launch) {
+  ((k == Ks ? launch(std::integral_constant<int, Ks>{}) : void()), ...);
+}
 
 }  // namespace
 }  // namespace ssm
@@ -157,8 +396,18 @@ using namespace ssm;
 extern "C" int rms_norm_fwd(const rms_norm_args_t *a, void *stream_ptr) {
   const int st = rms_norm_fwd_validate(a);
   if (st != SSM_OK) return st;
+  const int32_t io = a->io_dtype;
+  const int v = io == SSM_F32 ? 4 : 8;
+  const bool vec = a->group_size % v == 0 && wide(io, a->x, a->x_stride, v) && (!a->z || wide(io, a->z, a->z_stride, v)) &&
+                   (!a->residual || (wide(a->residual_dtype, a->residual, a->residual_stride, v) &&
+                                     wide(a->residual_dtype, a->residual_out, a->residual_out_stride, v))) &&
+                   (!a->out || wide(io, a->out, a->out_stride, v)) && aligned16(a->weight) &&
+                   (!a->codes || (a->codes_stride % v == 0 && reinterpret_cast<uintptr_t>(a->codes) % v == 0));
   const int64_t groups = a->cols / a->group_size;
-  if (groups > 65535 || !grid_fits(a->rows, kThreads)) return SSM_ERR_SHAPE;
+  // (8 bits: a block of 128 columns in neighbouring lanes, or a workgroup a unit)
+  const Lay l = lay_of(vec, io, a->group_size, !a->codes ? 8 : vec ? RMS_SCALE_BLOCK / v : 256, 40);
+  const int64_t units = l.threads / l.lanes, blocks = (a->rows * groups + units - 1) / units;
+  if (!grid_fits(blocks, l.threads)) return SSM_ERR_SHAPE;
   NormParams p{};
   p.x = a->x; p.xs = a->x_stride;
   p.z = a->z; p.zs = a->z_stride;
@@ -166,23 +415,71 @@ extern "C" int rms_norm_fwd(const rms_norm_args_t *a, void *stream_ptr) {
   p.rout = a->residual_out; p.ros = a->residual_out_stride;
   p.w = a->weight; p.out = a->out; p.os = a->out_stride;
   p.codes = static_cast<uint8_t *>(a->codes); p.cs = a->codes_stride; p.scales = a->scales;
-  p.rows = a->rows; p.cols = a->cols; p.group = a->group_size; p.eps = a->eps;
-  const dim3 grid(static_cast<unsigned>(a->rows), static_cast<unsigned>(groups));
+  p.rows = a->rows; p.cols = a->cols; p.eps = a->eps;
+  p.group = static_cast<int>(a->group_size); p.groups = static_cast<int>(groups); p.lanes = l.lanes;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
-  return by_io(a->io_dtype, [&](auto io) {
-    constexpr int IO = decltype(io)::value;
-    if (a->z) hipLaunchKernelGGL((norm_fwd_kernel<IO, 2, IO>), grid, dim3(kThreads), 0, stream, p);
-    else if (!a->residual) hipLaunchKernelGGL((norm_fwd_kernel<IO, 0, IO>), grid, dim3(kThreads), 0, stream, p);
-    else if (a->residual_dtype == a->io_dtype) hipLaunchKernelGGL((norm_fwd_kernel<IO, 1, IO>), grid, dim3(kThreads), 0, stream, p);
-    else hipLaunchKernelGGL((norm_fwd_kernel<IO, 1, SSM_F32>), grid, dim3(kThreads), 0, stream, p);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(l.threads);
+  return by_io(io, [&](auto type) {
+    constexpr int IO = decltype(type)::value;
+    constexpr int V = IO == 0 ? 4 : 8;
+    auto go = [&](auto mode, auto res, auto quant) {
+      constexpr int MODE = decltype(mode)::value, RES = decltype(res)::value;
+      constexpr bool QUANT = decltype(quant)::value;
+      if (vec)
+        by_k(std::conditional_t<IO == 0, Vec4K, VecK>{}, l.k, [&](auto k) {
+          hipLaunchKernelGGL((norm_fwd_kernel<IO, MODE, RES, QUANT, V, decltype(k)::value>), grid, block, 0, stream, p);
+        });
+      else
+        by_k(OneK{}, l.k, [&](auto k) {
+          hipLaunchKernelGGL((norm_fwd_kernel<IO, MODE, RES, QUANT, 1, decltype(k)::value>), grid, block, 0, stream, p);
+        });
+    };
+    auto quant = [&](auto mode, auto res) {
+      if (a->codes) go(mode, res, std::true_type{});
+      else go(mode, res, std::false_type{});
+    };
+    if (a->z) quant(std::integral_constant<int, kGate>{}, type);
+    else if (!a->residual) quant(std::integral_constant<int, kPlain>{}, type);
+    else if (a->residual_dtype == io) quant(std::integral_constant<int, kAdd>{}, type);
+    else quant(std::integral_constant<int, kAdd>{}, std::integral_constant<int, SSM_F32>{});
   });
 }
+
+namespace {
+
+struct BwdPlan {
+  bool vec;
+  Lay lay;
+  int64_t blocks, groups;   // blocks: workgroups that share a group's rows
+};
+// The workspace's size goes by the sizes alone; a call whose strides allow no
+// vectors takes another lay with as many blocks or fewer.
+int64_t most_blocks(int64_t rows, int64_t groups) {
+  const int64_t want = (4 * static_cast<int64_t>(cu_count_cached()) + groups - 1) / groups;
+  return want < rows ? want : rows;
+}
+BwdPlan bwd_plan(const rms_norm_bwd_args_t *a) {
+  BwdPlan b{};
+  const int32_t io = a->io_dtype, xt = a->x_dtype;
+  const int v = io == SSM_F32 ? 4 : 8;
+  b.vec = a->group_size % v == 0 && wide(xt, a->x, a->x_stride, v) && wide(io, a->dy, a->dy_stride, v) &&
+          wide(io, a->dx, a->dx_stride, v) && (!a->z || (wide(io, a->z, a->z_stride, v) && wide(io, a->dz, a->dz_stride, v))) &&
+          (!a->ds || wide(xt, a->ds, a->ds_stride, v)) && (!a->dresidual || wide(xt, a->dresidual, a->dresidual_stride, v)) &&
+          aligned16(a->weight);
+  b.groups = a->cols / a->group_size;
+  b.lay = lay_of(b.vec, io, a->group_size, 8, a->z ? 16 : 24);
+  const int64_t units = b.lay.threads / b.lay.lanes, need = (a->rows + units - 1) / units, most = most_blocks(a->rows, b.groups);
+  b.blocks = need < most ? need : most;
+  return b;
+}
+
+}  // namespace
 
 extern "C" int rms_norm_bwd_workspace_size(const rms_norm_bwd_args_t *a, size_t *bytes) {
   const int st = rms_norm_bwd_validate(a);
   if (st != SSM_OK) return st;
   if (!bytes) return SSM_ERR_NULL;
-  *bytes = static_cast<size_t>(a->rows) * (a->cols / a->group_size) * sizeof(float);
+  *bytes = static_cast<size_t>(most_blocks(a->rows, a->cols / a->group_size)) * a->cols * sizeof(float);
   return SSM_OK;
 }
 
@@ -190,9 +487,9 @@ extern "C" int rms_norm_bwd(const rms_norm_bwd_args_t *a, void *stream_ptr) {
   size_t need = 0;
   const int st = rms_norm_bwd_workspace_size(a, &need);
   if (st != SSM_OK) return st;
-  const int64_t groups = a->cols / a->group_size;
-  if (groups > 65535 || !grid_fits(a->rows, kThreads)) return SSM_ERR_SHAPE;
   if (!a->workspace || a->workspace_bytes < need) return SSM_ERR_WORKSPACE;
+  const BwdPlan b = bwd_plan(a);
+  if (b.groups > 65535) return SSM_ERR_SHAPE;
   NormParams p{};
   p.x = a->x; p.xs = a->x_stride;
   p.z = a->z; p.zs = a->z_stride;
@@ -201,21 +498,32 @@ extern "C" int rms_norm_bwd(const rms_norm_bwd_args_t *a, void *stream_ptr) {
   p.dx = a->dx; p.dxs = a->dx_stride;
   p.dres = a->dresidual; p.drs = a->dresidual_stride;
   p.dz = a->dz; p.dzs = a->dz_stride;
-  p.w = a->weight; p.dw = a->dweight; p.stat = static_cast<float *>(a->workspace);
-  p.rows = a->rows; p.cols = a->cols; p.group = a->group_size; p.eps = a->eps;
-  const dim3 grid(static_cast<unsigned>(a->rows), static_cast<unsigned>(groups));
-  const dim3 cols(static_cast<unsigned>((a->cols + 63) / 64));
+  p.w = a->weight; p.part = static_cast<float *>(a->workspace);
+  p.rows = a->rows; p.cols = a->cols; p.eps = a->eps;
+  p.group = static_cast<int>(a->group_size); p.groups = static_cast<int>(b.groups); p.lanes = b.lay.lanes;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
-  return by_io(a->io_dtype, [&](auto io) {
-    constexpr int IO = decltype(io)::value;
-    auto both = [&](auto xt, auto gate) {
+  const dim3 grid(static_cast<unsigned>(b.blocks), static_cast<unsigned>(b.groups)), block(b.lay.threads);
+  const int v = !b.vec ? 1 : a->io_dtype == SSM_F32 ? 4 : 8;
+  const size_t lds = b.lay.threads > b.lay.lanes ? static_cast<size_t>(b.lay.threads) * b.lay.k * v * sizeof(float) : 0;
+  return by_io(a->io_dtype, [&](auto type) {
+    constexpr int IO = decltype(type)::value;
+    constexpr int V = IO == 0 ? 4 : 8;
+    auto go = [&](auto xt, auto gate) {
       constexpr int XT = decltype(xt)::value;
       constexpr bool GATE = decltype(gate)::value;
-      hipLaunchKernelGGL((norm_bwd_kernel<IO, XT, GATE>), grid, dim3(kThreads), 0, stream, p);
-      hipLaunchKernelGGL((norm_dweight_kernel<IO, XT, GATE>), cols, dim3(64), 0, stream, p);
+      if (b.vec)
+        by_k(std::conditional_t<IO == 0, Vec4K, VecK>{}, b.lay.k, [&](auto k) {
+          hipLaunchKernelGGL((norm_bwd_kernel<IO, XT, GATE, V, decltype(k)::value>), grid, block, lds, stream, p);
+        });
+      else
+        by_k(OneK{}, b.lay.k, [&](auto k) {
+          hipLaunchKernelGGL((norm_bwd_kernel<IO, XT, GATE, 1, decltype(k)::value>), grid, block, lds, stream, p);
+        });
     };
-    if (a->z) both(io, std::true_type{});
-    else if (a->x_dtype == a->io_dtype) both(io, std::false_type{});
-    else both(std::integral_constant<int, SSM_F32>{}, std::false_type{});
+    if (a->z) go(type, std::true_type{});
+    else if (a->x_dtype == a->io_dtype) go(type, std::false_type{});
+    else go(std::integral_constant<int, SSM_F32>{}, std::false_type{});
+    hipLaunchKernelGGL(norm_sum_kernel, dim3(static_cast<unsigned>((p.cols + 63) / 64)), dim3(256), 0, stream, p.part, a->dweight,
+                       b.blocks, p.cols);
   });
 }
