@@ -761,7 +761,7 @@ int conv1d_ssd_update_validate(const conv1d_ssd_update_args_t *args);
 
 #define GATED_CHUNK 64   /* packed tokens from one kept state to the next */
 
-/* Arguments of gated_scan_varlen_fwd. */
+/* Arguments of gated_scan_varlen_fwd.  Strides of at most 2^24 elements. */
 typedef struct gated_scan_varlen_args {
   int64_t total, nseq, channels;
   int32_t io_dtype;
@@ -801,7 +801,7 @@ int gated_scan_varlen_fwd_workspace_size(const gated_scan_varlen_args_t *args, s
 /* Kept states of packed tokens: ceil(total / GATED_CHUNK). */
 int64_t gated_checkpoint_slots(int64_t total);
 
-/* Arguments of gated_scan_varlen_bwd: the forward's (fwd.checkpoints are those
+/* Arguments of gated_scan_varlen_bwd, strides as there: the forward's (fwd.checkpoints are those
  * that the forward wrote; fwd.out, state, state_slots, cache_seqlens, slots and
  * workspace are ignored), and the gradients, caller-allocated and fully
  * overwritten. */

@@ -15,6 +15,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "column_sum.h"
 #include "device_util.h"
 #include "host_util.h"
 #include "ssmscan.h"
@@ -312,28 +313,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormPara
   }
 }
 
-// Sum of the workgroups' rows, four threads a column, each its quarter in
-// order, in 64 bits.
-__global__ void __launch_bounds__(256) norm_sum_kernel(const float *part, float *dw, int64_t rows, int64_t cols) {
-  __shared__ double sum[4][64];
-  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
-  const int64_t col = static_cast<int64_t>(blockIdx.x) * 64 + lane;
-  double v = 0.0;
-  if (col < cols) {
-    const int64_t to = rows * (q + 1) / 4;
-    int64_t r = rows * q / 4;
-    for (; r + 8 <= to; r += 8) {   // eight loads in flight
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = part[(r + i) * cols + col];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v += f[i];
-    }
-    for (; r < to; ++r) v += part[r * cols + col];
-  }
-  sum[q][lane] = v;
-  __syncthreads();
-  if (q == 0 && col < cols) dw[col] = static_cast<float>((sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]));
+// The workgroups' sums, added.
+__global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float *part, float *dw, int64_t rows, int64_t cols) {
+  const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31);
+  const double v = column_sum(part, rows, cols, col);
+  if (threadIdx.x < 32 && col < cols) dw[col] = static_cast<float>(v);
 }
 
 // Vectors of a lane: of 8 columns of 16 bits or 4 of 32, and of single columns.
@@ -523,7 +507,7 @@ extern "C" int rms_norm_bwd(const rms_norm_bwd_args_t *a, void *stream_ptr) {
     if (a->z) go(type, std::true_type{});
     else if (a->x_dtype == a->io_dtype) go(type, std::false_type{});
     else go(std::integral_constant<int, SSM_F32>{}, std::false_type{});
-    hipLaunchKernelGGL(norm_sum_kernel, dim3(static_cast<unsigned>((p.cols + 63) / 64)), dim3(256), 0, stream, p.part, a->dweight,
+    hipLaunchKernelGGL(norm_sum_kernel, dim3(static_cast<unsigned>((p.cols + 31) / 32)), dim3(kSumThreads), 0, stream, p.part, a->dweight,
                        b.blocks, p.cols);
   });
 }

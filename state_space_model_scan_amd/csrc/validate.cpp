@@ -393,13 +393,15 @@ extern "C" int conv1d_ssd_update_validate(const conv1d_ssd_update_args_t *a) {
 namespace {
 
 bool rows_fit(int64_t rows, int64_t cols, int64_t stride) { return stride >= cols && product_fits(rows, stride, 1); }
+// ... and a wave's 16 tokens are reached by 32-bit offsets.
+bool near_rows(int64_t rows, int64_t cols, int64_t stride) { return rows_fit(rows, cols, stride) && stride <= kFarRow; }
 
 int gated_common(const gated_scan_varlen_args_t *a) {
   if (!a) return SSM_ERR_NULL;
   if (!positive(a->total) || !positive(a->nseq) || !positive(a->channels)) return SSM_ERR_SHAPE;
   if (a->total > 0x7fffffffLL || a->nseq > 0x7fffffffLL || a->channels > 0x7fffffffLL) return SSM_ERR_SHAPE;   // int32 edges
-  if (!rows_fit(a->total, a->channels, a->x_stride) || !rows_fit(a->total, a->channels, a->r_stride) ||
-      !rows_fit(a->total, a->channels, a->i_stride) || !product_fits(a->nseq, a->channels, 1))
+  if (!near_rows(a->total, a->channels, a->x_stride) || !near_rows(a->total, a->channels, a->r_stride) ||
+      !near_rows(a->total, a->channels, a->i_stride) || !product_fits(a->nseq, a->channels, 1))
     return SSM_ERR_SHAPE;
   if (!io_ok(a->io_dtype)) return SSM_ERR_UNSUPPORTED;
   if (!a->x || !a->r || !a->i || !a->A || !a->cu_seqlens) return SSM_ERR_NULL;
@@ -414,7 +416,7 @@ extern "C" int gated_scan_varlen_fwd_validate(const gated_scan_varlen_args_t *a)
   const int st = gated_common(a);
   if (st != SSM_OK) return st;
   if (!a->out) return SSM_ERR_NULL;
-  if (!rows_fit(a->total, a->channels, a->out_stride)) return SSM_ERR_SHAPE;
+  if (!near_rows(a->total, a->channels, a->out_stride)) return SSM_ERR_SHAPE;
   if (a->state && (!positive(a->state_slots) || !product_fits(a->state_slots, a->channels, 1))) return SSM_ERR_SHAPE;
   return SSM_OK;
 }
@@ -427,8 +429,8 @@ extern "C" int gated_scan_varlen_bwd_validate(const gated_scan_varlen_bwd_args_t
   if (!f.checkpoints || !a->dout || !a->dx || !a->dr || !a->di || !a->dA || (f.r_bias && !a->dr_bias) ||
       (f.i_bias && !a->di_bias))
     return SSM_ERR_NULL;
-  if (!rows_fit(f.total, f.channels, a->dout_stride) || !rows_fit(f.total, f.channels, a->dx_stride) ||
-      !rows_fit(f.total, f.channels, a->dr_stride) || !rows_fit(f.total, f.channels, a->di_stride))
+  if (!near_rows(f.total, f.channels, a->dout_stride) || !near_rows(f.total, f.channels, a->dx_stride) ||
+      !near_rows(f.total, f.channels, a->dr_stride) || !near_rows(f.total, f.channels, a->di_stride))
     return SSM_ERR_SHAPE;
   return SSM_OK;
 }

@@ -193,6 +193,35 @@ def test_scan_bwd_of_many_tokens():
         R.close(v, *ref[k], f32, k)
 
 
+# (as a call is cut: by tokens and channels; sequences that end anywhere, and more of them than a wave has lanes)
+CUTS = [(4200, 1030, 5), (3100, 4097, 3), (1700, 200, 3), (900, 1000, 200), (130, 1000, 2)]
+
+
+@pytest.mark.parametrize("io", [f32, bf])
+@pytest.mark.parametrize("T,C,nseq", CUTS)
+def test_every_cut(io, T, C, nseq):
+    log(f"[gated cuts] {io} {T}x{C} in {nseq}")
+    t, g = _case(T + C, T, C, io)
+    cuts = sorted(torch.randint(0, T + 1, (nseq - 1,), generator=g).tolist())
+    cu = [0] + cuts + [T]
+    dout = _randn(g, T, C, dtype=io)
+    state, slots = _randn(g, nseq, C), torch.randperm(nseq, generator=g).tolist()
+    args, kw = _dev(t)
+    kept, dstate = torch.empty(-(-T // 64), C, device="cuda"), state.cuda()
+    out = binding.gated_scan_varlen_fwd(*args, _ints(cu), state=dstate, cache_seqlens=_ints([1] * nseq), slots=_ints(slots),
+                                        checkpoints=kept, **kw)
+    ref, err, after, e_after = R.scan_cached(t, cu, state, [1] * nseq, slots)
+    R.close(out, ref, err, io, "out")
+    R.close(dstate, after, e_after, f32, "cache")
+    h0 = state[slots]
+    dfin = _randn(g, nseq, C)
+    got = binding.gated_scan_varlen_bwd(*args, _ints(cu), dout.cuda(), kept, initial_states=h0.cuda(), dfinal_states=dfin.cuda(),
+                                        want_dinitial_states=True, **kw)
+    want = R.scan_bwd(t, cu, dout, h0, dfin)
+    for k, v in got.items():
+        R.close(v, *want[k], io if k in ("dx", "dr", "di") else f32, k)
+
+
 @pytest.mark.parametrize("C", [72, 65])
 def test_padding(C):
     """Tokens before the first sequence and behind the last: their outputs stay,
