@@ -2,10 +2,12 @@
 // a gate, to io or to 8 bits (rms_norm_fwd), and its gradient (rms_norm_bwd).
 //
 // Both stream: every element is read once, held in registers, and written once.
-// A group of columns is a unit of its own; L lanes take it (16 to 64 of a wave,
-// or 2 to 8 whole waves), each K vectors of V neighbouring columns (16 bytes,
-// or one element where rows are odd or not aligned), as few lanes as K allows:
-// then a wave has more loads in flight, fewer idle lanes and no barrier.
+// A group of columns is a unit of its own; L lanes take it (8 to 64 of a wave,
+// or 2 to 8 whole waves), each K vectors of V neighbouring columns (16 bytes),
+// as few lanes as K allows: then a wave has more loads in flight, fewer idle
+// lanes and no barrier.  Vectors are read and written at any address: rows of
+// 1003 elements have no other, and single elements took 20.6 us for 8192 of them
+// with a residual.
 //
 // The gradient's workgroups walk the rows of their units, so that a lane's
 // weight gradients stay in its registers; the workgroups' sums are added by a
@@ -36,26 +38,46 @@ struct NormParams {
   float eps;
 };
 
-// V elements of a type, 16 bytes of them (or 8 of 16 bits beside 8 of 32, in
-// two loads), or one.
+// V neighbouring elements at any address of one, or the first `n` of them (the
+// others 0).
+template <int BYTES, int ALIGN>
+struct __attribute__((packed, aligned(ALIGN))) Words {
+  uint32_t w[BYTES / 4];
+};
 template <int IO, int V>
 struct Vec {
+  static constexpr int kSize = IO == 0 ? 4 : 2;
+  using At = Words<V * kSize, kSize>;
   RawV<IO, V> r;
-  __device__ __forceinline__ void load(const void *p, int64_t i) { r.load_vec(p, i); }
+  template <bool TAIL>
+  __device__ __forceinline__ void load(const void *p, int64_t i, int n) {
+    if (!TAIL || n >= V) {
+      const At q = *reinterpret_cast<const At *>(static_cast<const char *>(p) + i * kSize);
+#pragma unroll
+      for (int k = 0; k < RawV<IO, V>::kWords; ++k) r.w[k] = q.w[k];
+    } else {
+      r.load_elems(p, i, n);
+    }
+  }
   __device__ __forceinline__ float get(int k) const { return r.get(k); }
   __device__ __forceinline__ void zero() { r.zero(); }
 };
-template <int IO>
-struct Vec<IO, 1> {
-  float v;
-  __device__ __forceinline__ void load(const void *p, int64_t i) { v = load_io<IO>(p, i); }
-  __device__ __forceinline__ float get(int) const { return v; }
-  __device__ __forceinline__ void zero() { v = 0.0f; }
-};
-template <int IO, int V>
-__device__ __forceinline__ void put(void *p, int64_t i, const float (&v)[V]) {
-  if constexpr (V == 1) store_one<IO>(p, i, v[0]);
-  else store_n<IO, V>(p, i, v, V, true);
+template <int IO, int V, bool TAIL>
+__device__ __forceinline__ void put(void *p, int64_t i, const float (&v)[V], int n) {
+  using At = typename Vec<IO, V>::At;
+  if (TAIL && n < V) {
+    store_n<IO, V>(p, i, v, n, false);
+    return;
+  }
+  At q;
+  if constexpr (IO == 0) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) q.w[k] = __float_as_uint(v[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) q.w[k] = float_to_half_bits<IO>(v[2 * k]) | (float_to_half_bits<IO>(v[2 * k + 1]) << 16);
+  }
+  *reinterpret_cast<At *>(static_cast<char *>(p) + i * Vec<IO, V>::kSize) = q;
 }
 
 // Sum over a unit's lanes; more than a wave of them meet in LDS (`room`: a
@@ -89,11 +111,12 @@ __device__ __forceinline__ float e4m3_scale(uint32_t amax, float &inv) {
 
 enum Mode { kPlain, kAdd, kGate };
 
-// RES: the residual's type.  8 bits: QUANT.
-template <int IO, int MODE, int RES, bool QUANT, int V, int K>
+// RES: the residual's type.  8 bits: QUANT.  TAIL: a unit's columns are no
+// multiple of V.
+template <int IO, int MODE, int RES, bool QUANT, bool TAIL, int K>
 __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams p) {
+  constexpr int V = IO == 0 ? 4 : 8;
   __shared__ float room[kMaxThreads / 64];
-  __shared__ uint32_t top[QUANT && V == 1 ? RMS_MAX_GROUP / RMS_SCALE_BLOCK : 1];
   const int lane = threadIdx.x & (p.lanes - 1);
   const int64_t unit = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) / p.lanes;
   const int64_t row = unit / p.groups;
@@ -104,11 +127,11 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams 
   Vec<MODE == kAdd ? RES : IO, V> r[MODE == kPlain ? 1 : K];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (k * p.lanes + lane) * V;
-    if (there && c < p.group) {
-      x[k].load(p.x, row * p.xs + first + c);
-      if constexpr (MODE == kAdd) r[k].load(p.res, row * p.rs + first + c);
-      if constexpr (MODE == kGate) r[k].load(p.z, row * p.zs + first + c);
+    const int c = (k * p.lanes + lane) * V, n = p.group - c;
+    if (there && n > 0) {
+      x[k].template load<TAIL>(p.x, row * p.xs + first + c, n);
+      if constexpr (MODE == kAdd) r[k].template load<TAIL>(p.res, row * p.rs + first + c, n);
+      if constexpr (MODE == kGate) r[k].template load<TAIL>(p.z, row * p.zs + first + c, n);
     } else {
       x[k].zero();
       if constexpr (MODE != kPlain) r[k].zero();
@@ -126,88 +149,63 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const NormParams 
       sum = fmaf(q, q, sum);
     }
     if constexpr (MODE == kAdd) {
-      const int c = (k * p.lanes + lane) * V;
-      if (there && c < p.group) put<RES, V>(p.rout, row * p.ros + first + c, v[k]);
+      const int c = (k * p.lanes + lane) * V, n = p.group - c;
+      if (there && n > 0) put<RES, V, TAIL>(p.rout, row * p.ros + first + c, v[k], n);
     }
   }
   sum = unit_sum(sum, p.lanes, room);
   const float rstd = 1.0f / sqrtf(sum / p.group + p.eps);
-  if constexpr (!QUANT) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * p.lanes + lane) * V;
-      if (!there || c >= p.group) continue;
-      Vec<0, V> w;
-      w.load(p.w, first + c);
-      float y[V];
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * p.lanes + lane) * V, n = p.group - c;
+    const bool in = there && n > 0;
+    Vec<0, V> w;
+    if (in) w.template load<TAIL>(p.w, first + c, n);
+    else w.zero();
 #pragma unroll
-      for (int i = 0; i < V; ++i) y[i] = v[k][i] * rstd * w.get(i);
-      put<IO, V>(p.out, row * p.os + first + c, y);
-    }
-  } else {
-    const int64_t blocks = (p.cols + RMS_SCALE_BLOCK - 1) / RMS_SCALE_BLOCK;
-    if constexpr (V == 1) {   // a block's columns are spread over its unit's lanes: its largest through LDS (units of a wave or more: one a workgroup)
-      for (int k = threadIdx.x; k < RMS_MAX_GROUP / RMS_SCALE_BLOCK; k += blockDim.x) top[k] = 0;
-      __syncthreads();
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * p.lanes + lane) * V;
-      const bool in = there && c < p.group;
+    for (int i = 0; i < V; ++i) v[k][i] = v[k][i] * rstd * w.get(i);
+    if constexpr (!QUANT) {
+      if (in) put<IO, V, TAIL>(p.out, row * p.os + first + c, v[k], n);
+    } else {   // 128 / V neighbouring lanes hold a block
       uint32_t amax = 0;
-      if (in) {
-        Vec<0, V> w;
-        w.load(p.w, first + c);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          v[k][i] *= rstd * w.get(i);
-          const uint32_t b = __float_as_uint(v[k][i]) & 0x7fffffffu;
-          amax = b > amax ? b : amax;
-        }
+      for (int i = 0; i < V; ++i) {
+        const uint32_t b = __float_as_uint(v[k][i]) & 0x7fffffffu;
+        amax = in && (!TAIL || i < n) && b > amax ? b : amax;
       }
-      if constexpr (V == 1) {
-        if (in) atomicMax(&top[c / RMS_SCALE_BLOCK], amax);
-      } else {   // 128 / V neighbouring lanes hold a block
 #pragma unroll
-        for (int o = 1; o < RMS_SCALE_BLOCK / V; o <<= 1) {
-          const uint32_t other = __shfl_xor(amax, o);
-          amax = other > amax ? other : amax;
-        }
-        float inv;
-        const float scale = e4m3_scale(amax, inv);
-        if (in) {
-          uint32_t w[V / 4];
-#pragma unroll
-          for (int i = 0; i < V / 4; ++i) {
-            int q = __builtin_amdgcn_cvt_pk_fp8_f32(v[k][4 * i] * inv, v[k][4 * i + 1] * inv, 0, false);
-            w[i] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[k][4 * i + 2] * inv, v[k][4 * i + 3] * inv, q, true));
-          }
-          uint8_t *at = p.codes + row * p.cs + first + c;
-          if constexpr (V == 8) *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
-          else *reinterpret_cast<uint32_t *>(at) = w[0];
-          if (c % RMS_SCALE_BLOCK == 0) p.scales[row * blocks + (first + c) / RMS_SCALE_BLOCK] = scale;
-        }
+      for (int o = 1; o < RMS_SCALE_BLOCK / V; o <<= 1) {
+        const uint32_t other = __shfl_xor(amax, o);
+        amax = other > amax ? other : amax;
       }
-    }
-    if constexpr (V == 1) {
-      __syncthreads();
+      float inv;
+      const float scale = e4m3_scale(amax, inv);
+      if (!in) continue;
+      Words<V, 1> q;
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const int c = k * p.lanes + lane;
-        if (!there || c >= p.group) continue;
-        float inv;
-        const float scale = e4m3_scale(top[c / RMS_SCALE_BLOCK], inv), q = v[k][0] * inv;
-        p.codes[row * p.cs + first + c] = static_cast<uint8_t>(__builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false));
-        if (c % RMS_SCALE_BLOCK == 0) p.scales[row * blocks + (first + c) / RMS_SCALE_BLOCK] = scale;
+      for (int i = 0; i < V / 4; ++i) {
+        const int h = __builtin_amdgcn_cvt_pk_fp8_f32(v[k][4 * i] * inv, v[k][4 * i + 1] * inv, 0, false);
+        q.w[i] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(v[k][4 * i + 2] * inv, v[k][4 * i + 3] * inv, h, true));
       }
+      uint8_t *at = p.codes + row * p.cs + first + c;
+      if (!TAIL || n >= V) {
+        *reinterpret_cast<Words<V, 1> *>(at) = q;
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i < n) at[i] = static_cast<uint8_t>(q.w[i / 4] >> (8 * (i % 4)));
+      }
+      if (c % RMS_SCALE_BLOCK == 0)
+        p.scales[row * ((p.cols + RMS_SCALE_BLOCK - 1) / RMS_SCALE_BLOCK) + (first + c) / RMS_SCALE_BLOCK] = scale;
     }
   }
 }
 
 // XT: x's type.  A workgroup's units are `blockDim.x / lanes` rows of one group
 // of columns at a time; it walks the rows in steps of the whole grid.
-template <int IO, int XT, bool GATE, int V, int K>
+template <int IO, int XT, bool GATE, bool TAIL, int K>
 __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormParams p) {
+  constexpr int V = IO == 0 ? 4 : 8;
   __shared__ float room[2][kMaxThreads / 64];
   extern __shared__ float sums[];
   const int lane = threadIdx.x & (p.lanes - 1), here = threadIdx.x / p.lanes, units = blockDim.x / p.lanes;
@@ -215,9 +213,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormPara
   float w[K][V], dw[K][V];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (k * p.lanes + lane) * V;
+    const int c = (k * p.lanes + lane) * V, n = p.group - c;
     Vec<0, V> q;
-    if (c < p.group) q.load(p.w, first + c);
+    if (n > 0) q.template load<TAIL>(p.w, first + c, n);
     else q.zero();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -225,7 +223,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormPara
       dw[k][i] = 0.0f;
     }
   }
-  const float n = static_cast<float>(p.group);
+  const float count = static_cast<float>(p.group);
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * units; base < p.rows; base += static_cast<int64_t>(gridDim.x) * units) {
     const int64_t row = base + here;
     const bool there = row < p.rows;
@@ -233,12 +231,12 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormPara
     Vec<IO, V> dy[K], z[GATE ? K : 1];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = (k * p.lanes + lane) * V;
-      if (there && c < p.group) {
-        x[k].load(p.x, row * p.xs + first + c);
-        dy[k].load(p.dy, row * p.dys + first + c);
-        if constexpr (GATE) z[k].load(p.z, row * p.zs + first + c);
-        else if (p.ds) ds[k].load(p.ds, row * p.dss + first + c);
+      const int c = (k * p.lanes + lane) * V, n = p.group - c;
+      if (there && n > 0) {
+        x[k].template load<TAIL>(p.x, row * p.xs + first + c, n);
+        dy[k].template load<TAIL>(p.dy, row * p.dys + first + c, n);
+        if constexpr (GATE) z[k].template load<TAIL>(p.z, row * p.zs + first + c, n);
+        else if (p.ds) ds[k].template load<TAIL>(p.ds, row * p.dss + first + c, n);
         else ds[k].zero();
       } else {
         x[k].zero();
@@ -264,11 +262,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormPara
     if (p.lanes > 64) __syncthreads();   // (the room's last readers are done)
     sum = unit_sum(sum, p.lanes, room[0]);
     dot = unit_sum(dot, p.lanes, room[1]);
-    const float rstd = 1.0f / sqrtf(sum / n + p.eps);
-    const float mean = dot * rstd / n;
+    const float rstd = 1.0f / sqrtf(sum / count + p.eps);
+    const float mean = dot * rstd / count;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = (k * p.lanes + lane) * V;
+      const int c = (k * p.lanes + lane) * V, n = p.group - c;
       float dx[V], dz[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -285,10 +283,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormPara
           dx[i] = fmaf(rstd, fmaf(-hat, mean, g * w[k][i]), ds[k].get(i));
         }
       }
-      if (!there || c >= p.group) continue;
-      put<IO, V>(p.dx, row * p.dxs + first + c, dx);
-      if constexpr (GATE) put<IO, V>(p.dz, row * p.dzs + first + c, dz);
-      else if (p.dres) put<XT, V>(p.dres, row * p.drs + first + c, dx);
+      if (!there || n <= 0) continue;
+      put<IO, V, TAIL>(p.dx, row * p.dxs + first + c, dx, n);
+      if constexpr (GATE) put<IO, V, TAIL>(p.dz, row * p.dzs + first + c, dz, n);
+      else if (p.dres) put<XT, V, TAIL>(p.dres, row * p.drs + first + c, dx, n);
     }
   }
   // the units' sums, in order
@@ -308,8 +306,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormPara
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (k * p.lanes + lane) * V;
-    if (c < p.group) put<0, V>(p.part, static_cast<int64_t>(blockIdx.x) * p.cols + first + c, dw[k]);
+    const int c = (k * p.lanes + lane) * V, n = p.group - c;
+    if (n > 0) put<0, V, TAIL>(p.part, static_cast<int64_t>(blockIdx.x) * p.cols + first + c, dw[k], n);
   }
 }
 
@@ -320,26 +318,26 @@ __global__ void __launch_bounds__(kSumThreads) norm_sum_kernel(const float *part
   if (threadIdx.x < 32 && col < cols) dw[col] = static_cast<float>(v);
 }
 
-// Vectors of a lane: of 8 columns of 16 bits or 4 of 32, and of single columns.
-constexpr int kVecK[] = {1, 2, 3, 5};
-constexpr int kVec4K[] = {1, 2, 3, 5, 8};
-constexpr int kOneK[] = {4, 16, 32};
-using VecK = std::integer_sequence<int, 1, 2, 3, 5>;
-using Vec4K = std::integer_sequence<int, 1, 2, 3, 5, 8>;
-using OneK = std::integer_sequence<int, 4, 16, 32>;
-static_assert(kMaxThreads * 5 * 8 >= RMS_MAX_GROUP && kMaxThreads * 8 * 4 >= RMS_MAX_GROUP && kMaxThreads * 32 >= RMS_MAX_GROUP,
+// Vectors of a lane: of 8 columns of 16 bits, or 4 of 32.
+constexpr int kWideK[] = {1, 2, 3, 5};
+constexpr int kFloatK[] = {1, 2, 3, 5, 8};
+using WideK = std::integer_sequence<int, 1, 2, 3, 5>;
+using FloatK = std::integer_sequence<int, 1, 2, 3, 5, 8>;
+static_assert(kMaxThreads * 5 * 8 >= RMS_MAX_GROUP && kMaxThreads * 8 * 4 >= RMS_MAX_GROUP,
               "the largest group fits a workgroup's registers");
 
-// How a call's units are laid on lanes: K vectors of V columns at most a lane.
+// How a call's units are laid on lanes.
 struct Lay {
-  int k, lanes, threads;
+  int v, k, lanes, threads;
+  bool tail;
 };
 template <int N>
 Lay lay_of(int64_t group, int v, const int (&ks)[N], int least, int most_k) {
   Lay l{};
   const int64_t vecs = (group + v - 1) / v;
+  l.v = v;
+  l.tail = group % v != 0;
   l.lanes = least;
-  if (most_k > ks[N - 1]) most_k = ks[N - 1];
   while (l.lanes < kMaxThreads && (vecs + l.lanes - 1) / l.lanes > most_k) l.lanes *= 2;
   for (int i = N - 1; i >= 0; --i)
     if ((vecs + l.lanes - 1) / l.lanes <= ks[i]) l.k = ks[i];
@@ -347,15 +345,8 @@ Lay lay_of(int64_t group, int v, const int (&ks)[N], int least, int most_k) {
   return l;
 }
 // `columns`: of a lane, where the largest groups do not take more.
-Lay lay_of(bool vec, int32_t io, int64_t group, int least, int columns) {
-  if (!vec) return lay_of(group, 1, kOneK, least, columns > 16 ? 16 : 4);
-  return io == SSM_F32 ? lay_of(group, 4, kVec4K, least, columns / 4) : lay_of(group, 8, kVecK, least, columns / 8);
-}
-
-bool wide(int32_t type, const void *p, int64_t stride, int v) {
-  const int64_t bytes = type == SSM_F32 ? 4 : 2;
-  const uintptr_t step = static_cast<uintptr_t>(v * bytes > 16 ? 16 : v * bytes);
-  return stride % v == 0 && reinterpret_cast<uintptr_t>(p) % step == 0;
+Lay lay_of(int32_t io, int64_t group, int least, int columns) {
+  return io == SSM_F32 ? lay_of(group, 4, kFloatK, least, columns / 4) : lay_of(group, 8, kWideK, least, columns / 8);
 }
 
 template <typename F>
@@ -381,15 +372,11 @@ extern "C" int rms_norm_fwd(const rms_norm_args_t *a, void *stream_ptr) {
   const int st = rms_norm_fwd_validate(a);
   if (st != SSM_OK) return st;
   const int32_t io = a->io_dtype;
-  const int v = io == SSM_F32 ? 4 : 8;
-  const bool vec = a->group_size % v == 0 && wide(io, a->x, a->x_stride, v) && (!a->z || wide(io, a->z, a->z_stride, v)) &&
-                   (!a->residual || (wide(a->residual_dtype, a->residual, a->residual_stride, v) &&
-                                     wide(a->residual_dtype, a->residual_out, a->residual_out_stride, v))) &&
-                   (!a->out || wide(io, a->out, a->out_stride, v)) && aligned16(a->weight) &&
-                   (!a->codes || (a->codes_stride % v == 0 && reinterpret_cast<uintptr_t>(a->codes) % v == 0));
   const int64_t groups = a->cols / a->group_size;
-  // (8 bits: a block of 128 columns in neighbouring lanes, or a workgroup a unit)
-  const Lay l = lay_of(vec, io, a->group_size, !a->codes ? 8 : vec ? RMS_SCALE_BLOCK / v : 256, 40);
+  // 8 bits: a block of 128 columns in neighbouring lanes of a wave.  Columns of a lane, 40 / 24 / 16 / 8 (us): bf16 16384 x 2560 with a residual 64.3
+  // / 61.0 / 60.5 / 62.5, gated 16384 x 5120 in eight groups 92 / 89 / 97 / 117; fp32
+  // 8192 x 2560 63.3 / 63.4 / 60.0 / 62.6.
+  const Lay l = lay_of(io, a->group_size, !a->codes ? 8 : RMS_SCALE_BLOCK / (io == SSM_F32 ? 4 : 8), io == SSM_F32 ? 16 : 24);
   const int64_t units = l.threads / l.lanes, blocks = (a->rows * groups + units - 1) / units;
   if (!grid_fits(blocks, l.threads)) return SSM_ERR_SHAPE;
   NormParams p{};
@@ -405,18 +392,14 @@ extern "C" int rms_norm_fwd(const rms_norm_args_t *a, void *stream_ptr) {
   const dim3 grid(static_cast<unsigned>(blocks)), block(l.threads);
   return by_io(io, [&](auto type) {
     constexpr int IO = decltype(type)::value;
-    constexpr int V = IO == 0 ? 4 : 8;
     auto go = [&](auto mode, auto res, auto quant) {
       constexpr int MODE = decltype(mode)::value, RES = decltype(res)::value;
       constexpr bool QUANT = decltype(quant)::value;
-      if (vec)
-        by_k(std::conditional_t<IO == 0, Vec4K, VecK>{}, l.k, [&](auto k) {
-          hipLaunchKernelGGL((norm_fwd_kernel<IO, MODE, RES, QUANT, V, decltype(k)::value>), grid, block, 0, stream, p);
-        });
-      else
-        by_k(OneK{}, l.k, [&](auto k) {
-          hipLaunchKernelGGL((norm_fwd_kernel<IO, MODE, RES, QUANT, 1, decltype(k)::value>), grid, block, 0, stream, p);
-        });
+      by_k(std::conditional_t<IO == 0, FloatK, WideK>{}, l.k, [&](auto k) {
+        constexpr int K = decltype(k)::value;
+        if (l.tail) hipLaunchKernelGGL((norm_fwd_kernel<IO, MODE, RES, QUANT, true, K>), grid, block, 0, stream, p);
+        else hipLaunchKernelGGL((norm_fwd_kernel<IO, MODE, RES, QUANT, false, K>), grid, block, 0, stream, p);
+      });
     };
     auto quant = [&](auto mode, auto res) {
       if (a->codes) go(mode, res, std::true_type{});
@@ -432,28 +415,25 @@ extern "C" int rms_norm_fwd(const rms_norm_args_t *a, void *stream_ptr) {
 namespace {
 
 struct BwdPlan {
-  bool vec;
   Lay lay;
   int64_t blocks, groups;   // blocks: workgroups that share a group's rows
 };
-// The workspace's size goes by the sizes alone; a call whose strides allow no
-// vectors takes another lay with as many blocks or fewer.
-int64_t most_blocks(int64_t rows, int64_t groups) {
-  const int64_t want = (4 * static_cast<int64_t>(cu_count_cached()) + groups - 1) / groups;
-  return want < rows ? want : rows;
-}
+int64_t per_group(int64_t blocks, int64_t groups) { return (blocks + groups - 1) / groups; }
+// Two workgroups a compute unit walk many rows best; up to three passes over
+// the rows four of them, as then a pass is what counts (us, two / four): 16384 x
+// 2560 133 / 138, gated 16384 x 5120 in eight groups 172 / 178, but 1500 x 1001 in
+// seven 16.5 / 14.0.  A call of a few passes of one workgroup takes one, which
+// needs no second launch.
 BwdPlan bwd_plan(const rms_norm_bwd_args_t *a) {
   BwdPlan b{};
-  const int32_t io = a->io_dtype, xt = a->x_dtype;
-  const int v = io == SSM_F32 ? 4 : 8;
-  b.vec = a->group_size % v == 0 && wide(xt, a->x, a->x_stride, v) && wide(io, a->dy, a->dy_stride, v) &&
-          wide(io, a->dx, a->dx_stride, v) && (!a->z || (wide(io, a->z, a->z_stride, v) && wide(io, a->dz, a->dz_stride, v))) &&
-          (!a->ds || wide(xt, a->ds, a->ds_stride, v)) && (!a->dresidual || wide(xt, a->dresidual, a->dresidual_stride, v)) &&
-          aligned16(a->weight);
   b.groups = a->cols / a->group_size;
-  b.lay = lay_of(b.vec, io, a->group_size, 8, a->z ? 16 : 24);
-  const int64_t units = b.lay.threads / b.lay.lanes, need = (a->rows + units - 1) / units, most = most_blocks(a->rows, b.groups);
-  b.blocks = need < most ? need : most;
+  // (columns of a lane: gated 16384 x 5120 in eight groups 172 us with 24, 218 with
+  // 16, 645 with 40, which do not fit the registers; 16384 x 2560 129 with 16, 133
+  // with 24, 155 with 40)
+  b.lay = lay_of(a->io_dtype, a->group_size, 8, a->z ? 24 : 16);
+  const int64_t units = b.lay.threads / b.lay.lanes, passes = (a->rows + units - 1) / units, cus = cu_count_cached();
+  const int64_t few = per_group(4 * cus, b.groups);
+  b.blocks = passes <= 4 ? 1 : passes > 3 * few ? per_group(2 * cus, b.groups) : passes < few ? passes : few;
   return b;
 }
 
@@ -463,7 +443,8 @@ extern "C" int rms_norm_bwd_workspace_size(const rms_norm_bwd_args_t *a, size_t 
   const int st = rms_norm_bwd_validate(a);
   if (st != SSM_OK) return st;
   if (!bytes) return SSM_ERR_NULL;
-  *bytes = static_cast<size_t>(most_blocks(a->rows, a->cols / a->group_size)) * a->cols * sizeof(float);
+  const BwdPlan b = bwd_plan(a);
+  *bytes = b.blocks == 1 ? 0 : static_cast<size_t>(b.blocks) * a->cols * sizeof(float);
   return SSM_OK;
 }
 
@@ -471,7 +452,7 @@ extern "C" int rms_norm_bwd(const rms_norm_bwd_args_t *a, void *stream_ptr) {
   size_t need = 0;
   const int st = rms_norm_bwd_workspace_size(a, &need);
   if (st != SSM_OK) return st;
-  if (!a->workspace || a->workspace_bytes < need) return SSM_ERR_WORKSPACE;
+  if (need && (!a->workspace || a->workspace_bytes < need)) return SSM_ERR_WORKSPACE;
   const BwdPlan b = bwd_plan(a);
   if (b.groups > 65535) return SSM_ERR_SHAPE;
   NormParams p{};
@@ -482,31 +463,27 @@ extern "C" int rms_norm_bwd(const rms_norm_bwd_args_t *a, void *stream_ptr) {
   p.dx = a->dx; p.dxs = a->dx_stride;
   p.dres = a->dresidual; p.drs = a->dresidual_stride;
   p.dz = a->dz; p.dzs = a->dz_stride;
-  p.w = a->weight; p.part = static_cast<float *>(a->workspace);
+  p.w = a->weight; p.part = b.blocks == 1 ? a->dweight : static_cast<float *>(a->workspace);
   p.rows = a->rows; p.cols = a->cols; p.eps = a->eps;
   p.group = static_cast<int>(a->group_size); p.groups = static_cast<int>(b.groups); p.lanes = b.lay.lanes;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
   const dim3 grid(static_cast<unsigned>(b.blocks), static_cast<unsigned>(b.groups)), block(b.lay.threads);
-  const int v = !b.vec ? 1 : a->io_dtype == SSM_F32 ? 4 : 8;
-  const size_t lds = b.lay.threads > b.lay.lanes ? static_cast<size_t>(b.lay.threads) * b.lay.k * v * sizeof(float) : 0;
+  const size_t lds = b.lay.threads > b.lay.lanes ? static_cast<size_t>(b.lay.threads) * b.lay.k * b.lay.v * sizeof(float) : 0;
   return by_io(a->io_dtype, [&](auto type) {
     constexpr int IO = decltype(type)::value;
-    constexpr int V = IO == 0 ? 4 : 8;
     auto go = [&](auto xt, auto gate) {
       constexpr int XT = decltype(xt)::value;
       constexpr bool GATE = decltype(gate)::value;
-      if (b.vec)
-        by_k(std::conditional_t<IO == 0, Vec4K, VecK>{}, b.lay.k, [&](auto k) {
-          hipLaunchKernelGGL((norm_bwd_kernel<IO, XT, GATE, V, decltype(k)::value>), grid, block, lds, stream, p);
-        });
-      else
-        by_k(OneK{}, b.lay.k, [&](auto k) {
-          hipLaunchKernelGGL((norm_bwd_kernel<IO, XT, GATE, 1, decltype(k)::value>), grid, block, lds, stream, p);
-        });
+      by_k(std::conditional_t<IO == 0, FloatK, WideK>{}, b.lay.k, [&](auto k) {
+        constexpr int K = decltype(k)::value;
+        if (b.lay.tail) hipLaunchKernelGGL((norm_bwd_kernel<IO, XT, GATE, true, K>), grid, block, lds, stream, p);
+        else hipLaunchKernelGGL((norm_bwd_kernel<IO, XT, GATE, false, K>), grid, block, lds, stream, p);
+      });
     };
     if (a->z) go(type, std::true_type{});
     else if (a->x_dtype == a->io_dtype) go(type, std::false_type{});
     else go(std::integral_constant<int, SSM_F32>{}, std::false_type{});
+    if (b.blocks == 1) return;
     hipLaunchKernelGGL(norm_sum_kernel, dim3(static_cast<unsigned>((p.cols + 31) / 32)), dim3(kSumThreads), 0, stream, p.part, a->dweight,
                        b.blocks, p.cols);
   });
