@@ -757,6 +757,8 @@ int conv1d_ssd_update_validate(const conv1d_ssd_update_args_t *args);
  * and cache_seqlens as above, except that tokens before cu_seqlens[0] and from
  * cu_seqlens[nseq] on (a padded batch) belong to no sequence: their outputs are
  * left as they were, and their gradients are 0.
+ * The scans' workspaces are aligned to 16 bytes
+ * (SSM_ERR_UNSUPPORTED), and serve one call at a time.
  * ------------------------------------------------------------------------- */
 
 #define GATED_CHUNK 64   /* packed tokens from one kept state to the next */
@@ -882,7 +884,8 @@ typedef struct rms_norm_args {
  *     y = v / sqrt(mean(v^2) + eps) weight
  *
  * (of what the residual stream holds, so that rms_norm_bwd, which reads it, is
- * the gradient of what was computed).  y goes to `out`, or in 8 bits to `codes`:
+ * the gradient of what was computed).  The squares and their sum are fp32, as the
+ * values are: where the sum is more than fp32 holds, y is 0.  y goes to `out`, or in 8 bits to `codes`:
  * y is code * scale, the code rounded to nearest (ties to even) and the scale,
  * one for RMS_SCALE_BLOCK columns of a row, the smallest power of two with which
  * none of them is over 448 (at least 2^-100; NaN where one of them is not
@@ -914,7 +917,7 @@ typedef struct rms_norm_bwd_args {
  *   dx = dv + ds   (the residual's gradient as well),  or with a gate
  *   dx = dv silu(z),  dz = dv x silu'(z)
  * Sums are taken in a fixed order (bit-for-bit repeatable).  Outputs must not
- * overlap inputs. */
+ * overlap inputs.  At most 65535 groups a row. */
 int rms_norm_bwd(const rms_norm_bwd_args_t *args, void *hip_stream);
 int rms_norm_bwd_validate(const rms_norm_bwd_args_t *args);
 int rms_norm_bwd_workspace_size(const rms_norm_bwd_args_t *args, size_t *bytes);

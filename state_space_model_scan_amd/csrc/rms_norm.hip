@@ -9,6 +9,10 @@
 // 1003 elements have no other, and single elements took 20.6 us for 8192 of them
 // with a residual.
 //
+// Measured on bf16 (us; bytes over time): 16384 x 5120 gated in eight groups 90
+// (5.6 TB/s, a copy makes 5.1), 4100 x 2560 with a residual to 8 bits 16 (4.6), the
+// gradient of 16384 x 2560 with the residual stream in fp32 128 (5.2): HBM.
+//
 // The gradient's workgroups walk the rows of their units, so that a lane's
 // weight gradients stay in its registers; the workgroups' sums are added by a
 // second launch, in a fixed order.
@@ -454,7 +458,6 @@ extern "C" int rms_norm_bwd(const rms_norm_bwd_args_t *a, void *stream_ptr) {
   if (st != SSM_OK) return st;
   if (need && (!a->workspace || a->workspace_bytes < need)) return SSM_ERR_WORKSPACE;
   const BwdPlan b = bwd_plan(a);
-  if (b.groups > 65535) return SSM_ERR_SHAPE;
   NormParams p{};
   p.x = a->x; p.xs = a->x_stride;
   p.z = a->z; p.zs = a->z_stride;

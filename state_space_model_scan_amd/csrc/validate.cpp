@@ -479,6 +479,7 @@ extern "C" int rms_norm_bwd_validate(const rms_norm_bwd_args_t *a) {
   if (!a) return SSM_ERR_NULL;
   const int st = norm_common(a->rows, a->cols, a->group_size, a->io_dtype, a->x_dtype, a->eps);
   if (st != SSM_OK) return st;
+  if (a->cols / a->group_size > 65535) return SSM_ERR_SHAPE;   // a launch's second dimension
   if (!a->x || !a->weight || !a->dy || !a->dx || !a->dweight || (!a->z) != (!a->dz)) return SSM_ERR_NULL;
   if (a->z && (a->ds || a->dresidual || a->x_dtype != a->io_dtype)) return SSM_ERR_UNSUPPORTED;
   if (!rows_fit(a->rows, a->cols, a->x_stride) || !rows_fit(a->rows, a->cols, a->dy_stride) ||

@@ -221,3 +221,20 @@ def test_norm_bwd_wrapper_refuses(name, value, text):
         binding.rms_norm_bwd(**kw, z=kw["x"], ds=kw["x"])
     with pytest.raises(ValueError, match="one dtype"):
         binding.rms_norm_bwd(torch.zeros(4, 256), kw["weight"], kw["dy"], z=kw["x"])
+
+
+def test_norm_bwd_refuses_more_groups_than_a_launch_takes():
+    wide = {k + "_stride": 65536 for k in ("x", "z", "dy", "ds", "dx", "dresidual", "dz")}
+    assert _st("rms_norm_bwd", _norm_bwd(cols=65536, group_size=1, **wide)) == S
+    assert _st("rms_norm_bwd", _norm_bwd(cols=65535, group_size=1, **wide)) == _lib.SSM_OK
+
+
+def test_scans_refuse_a_workspace_off_16_bytes():
+    """... and one that is too small or missing, before anything is launched."""
+    L, size = _lib.lib(), ctypes.c_size_t()
+    for make, name in ((lambda **kw: _scan(total=1000, **kw), "gated_scan_varlen_fwd"),
+                       (lambda **kw: _scan_bwd(dict(total=1000), **kw), "gated_scan_varlen_bwd")):
+        assert getattr(L, name + "_workspace_size")(ctypes.byref(make()), ctypes.byref(size)) == _lib.SSM_OK and size.value > 0
+        for kw, want in ((dict(), _lib.SSM_ERR_WORKSPACE), (dict(workspace=FAKE, workspace_bytes=size.value - 1), _lib.SSM_ERR_WORKSPACE),
+                         (dict(workspace=FAKE + 8, workspace_bytes=size.value), U)):
+            assert getattr(L, name)(ctypes.byref(make(**kw)), None) == want, (name, kw)
