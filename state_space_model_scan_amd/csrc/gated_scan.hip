@@ -934,10 +934,12 @@ namespace {
 //   2000 x 2560 (32 x 40)   38 / 36 / 34        1000 x 512 (16 x 8)  17 / 15.7 / 14.3
 //   500 x 2560 (8 x 40)     21 / 16.8 / 17.7    256 x 2560 (4 x 40)  17 / 15.4 / 13.8
 //   128 x 2560 (2 x 40: one tile, nothing to wait for)  16 / 12.1 / 12.6
+// fp32's inputs take twice the registers, with which BwdMany's 16 tokens do not fit:
+//   8192 x 2560 fp32 175 / 135 / 124
 enum Cut { kMany, kLong, kSmall };
 Cut bwd_cut(const gated_scan_varlen_args_t &f) {
   const int64_t tiles = parts_of(f.total, GATED_CHUNK), all = tiles * parts_of(f.channels, 64), cus = cu_count_cached();
-  if (all > 12 * cus) return kMany;
+  if (all > 12 * cus) return f.io_dtype == SSM_F32 ? kSmall : kMany;
   return tiles == 2 || (tiles >= 24 && all <= 4 * cus) ? kLong : kSmall;
 }
 Tiling bwd_tiling(const gated_scan_varlen_args_t &f) {
@@ -986,9 +988,12 @@ extern "C" int gated_scan_varlen_bwd(const gated_scan_varlen_bwd_args_t *a, void
   const Cut cut = bwd_cut(f);
   return by_io(f.io_dtype, [&](auto type) {
     constexpr int IO = decltype(type)::value;
-    if (cut == kMany) hipLaunchKernelGGL((gated_bwd_kernel<IO, 1, BwdMany>), dim3(grid), dim3(t.threads), 0, stream, p);
-    else if (cut == kLong) hipLaunchKernelGGL((gated_bwd_kernel<IO, 1, BwdLong>), dim3(grid), dim3(t.threads), 0, stream, p);
-    else hipLaunchKernelGGL((gated_bwd_kernel<IO, 1, BwdSmall>), dim3(grid), dim3(t.threads), 0, stream, p);
+    auto go = [&](auto shape) {
+      hipLaunchKernelGGL((gated_bwd_kernel<IO, 1, decltype(shape)>), dim3(grid), dim3(t.threads), 0, stream, p);
+    };
+    if (cut == kLong) go(BwdLong{});
+    else if (cut == kSmall) go(BwdSmall{});
+    else if constexpr (IO != SSM_F32) go(BwdMany{});
     hipLaunchKernelGGL(gated_sum_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kSumThreads), 0, stream, s);
   });
 }
