@@ -25,7 +25,7 @@
 // copy makes 5.1), gradient 160 (3.7), 65536 x 2560 forward 255 (5.2); a sequence
 // a thread of every channel took 1973, 2961 and 33887.  What bounds them is HBM in
 // the forward of many tokens, in the gradient memory and the vector units in turn
-// (72 instructions an element, 54% of the time busy), and below some 10^7 elements
+// (70 instructions an element, 59% of the time busy), and below some 10^7 elements
 // the workgroups' own length: loads, the pairs' way through LDS, stores.  The step of
 // 256 x 5120 takes 5.5 (3.8), that of one request 2.6: latency.
 //
