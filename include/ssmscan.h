@@ -827,8 +827,8 @@ typedef struct gated_scan_varlen_bwd_args {
  *   q   = G rho (a h_{t-1} - (a^2 / m) iota x)   (rho / m taken as 0 where m = 0)
  *   dA  = sum_t q,   dr = A (1 - rho) q,   dr_bias = sum_t dr
  *   dx  = G m iota,  di = G m x iota (1 - iota),   di_bias = sum_t di
- * An empty sequence passes dfinal_states on to dinitial_states.  Sums are taken
- * in a fixed order (bit-for-bit repeatable).  Values that are not finite stay
+ * An empty sequence passes dfinal_states on to dinitial_states.  Gradients must
+ * not overlap inputs.  Sums are taken in a fixed order (bit-for-bit repeatable).  Values that are not finite stay
  * in their sequence and channel (apart from the sums over the tokens). */
 int gated_scan_varlen_bwd(const gated_scan_varlen_bwd_args_t *args, void *hip_stream);
 int gated_scan_varlen_bwd_validate(const gated_scan_varlen_bwd_args_t *args);
