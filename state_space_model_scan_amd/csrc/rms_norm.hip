@@ -266,7 +266,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormPara
     if (p.lanes > 64) __syncthreads();   // (the room's last readers are done)
     sum = unit_sum(sum, p.lanes, room[0]);
     dot = unit_sum(dot, p.lanes, room[1]);
-    const float rstd = 1.0f / sqrtf(sum / count + p.eps);
+    // 0 for a unit without a row: with eps = 0 its 1 / 0 would reach the weight's gradient, which its lanes share
+    const float rstd = there ? 1.0f / sqrtf(sum / count + p.eps) : 0.0f;
     const float mean = dot * rstd / count;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
