@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormPara
       else if (p.dres) put<XT, V, TAIL>(p.dres, row * p.drs + first + c, dx, n);
     }
   }
-  // the units' sums, in order
+  // the units' sums, in order and in 64 bits
   if (units > 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -302,10 +302,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) norm_bwd_kernel(const NormPara
       for (int i = 0; i < V; ++i) sums[(k * V + i) * blockDim.x + threadIdx.x] = dw[k][i];
     __syncthreads();
     for (int at = here; at < K * V; at += units) {   // (a unit's lanes take an element of every lane)
-      float s = 0.0f;
+      double s = 0.0;
       for (int u = 0; u < units; ++u) s += sums[at * blockDim.x + u * p.lanes + lane];
       const int c = (at / V * p.lanes + lane) * V + at % V;
-      if (c < p.group) p.part[static_cast<int64_t>(blockIdx.x) * p.cols + first + c] = s;
+      if (c < p.group) p.part[static_cast<int64_t>(blockIdx.x) * p.cols + first + c] = static_cast<float>(s);
     }
     return;
   }
@@ -423,12 +423,17 @@ struct BwdPlan {
   Lay lay;
   int64_t blocks, groups;   // blocks: workgroups that share a group's rows
 };
-int64_t per_group(int64_t blocks, int64_t groups) { return (blocks + groups - 1) / groups; }
+int64_t ceil_div(int64_t n, int64_t by) { return (n + by - 1) / by; }
 // Two workgroups a compute unit walk many rows best; up to three passes over
 // the rows four of them, as then a pass is what counts (us, two / four): 16384 x
 // 2560 133 / 138, gated 16384 x 5120 in eight groups 172 / 178, but 1500 x 1001 in
 // seven 16.5 / 14.0.  A call of a few passes of one workgroup takes one, which
 // needs no second launch.
+// A lane adds the weight gradient's terms of at most kLaneRows rows one after
+// another in fp32, the rest is added in 64 bits: more rows take as many times the
+// workgroups (us, without the limit / with it: 140000 x 2560 695 / 441, 131072 x 5120
+// gated in groups of 80 2514 / 2231, 16384 x 5120 in groups of 8 777 / 544).
+constexpr int64_t kLaneRows = 256;
 BwdPlan bwd_plan(const rms_norm_bwd_args_t *a) {
   BwdPlan b{};
   b.groups = a->cols / a->group_size;
@@ -437,8 +442,9 @@ BwdPlan bwd_plan(const rms_norm_bwd_args_t *a) {
   // with 24, 155 with 40)
   b.lay = lay_of(a->io_dtype, a->group_size, 8, a->z ? 24 : 16);
   const int64_t units = b.lay.threads / b.lay.lanes, passes = (a->rows + units - 1) / units, cus = cu_count_cached();
-  const int64_t few = per_group(4 * cus, b.groups);
-  b.blocks = passes <= 4 ? 1 : passes > 3 * few ? per_group(2 * cus, b.groups) : passes < few ? passes : few;
+  const int64_t few = ceil_div(4 * cus, b.groups);
+  b.blocks = passes <= 4 ? 1 : passes > 3 * few ? ceil_div(2 * cus, b.groups) : passes < few ? passes : few;
+  b.blocks *= ceil_div(passes, kLaneRows * b.blocks);
   return b;
 }
 
@@ -471,6 +477,7 @@ extern "C" int rms_norm_bwd(const rms_norm_bwd_args_t *a, void *stream_ptr) {
   p.rows = a->rows; p.cols = a->cols; p.eps = a->eps;
   p.group = static_cast<int>(a->group_size); p.groups = static_cast<int>(b.groups); p.lanes = b.lay.lanes;
   hipStream_t stream = static_cast<hipStream_t>(stream_ptr);
+  if (!grid_fits(b.blocks * b.groups, b.lay.threads)) return SSM_ERR_SHAPE;
   const dim3 grid(static_cast<unsigned>(b.blocks), static_cast<unsigned>(b.groups)), block(b.lay.threads);
   const size_t lds = b.lay.threads > b.lay.lanes ? static_cast<size_t>(b.lay.threads) * b.lay.k * b.lay.v * sizeof(float) : 0;
   return by_io(a->io_dtype, [&](auto type) {

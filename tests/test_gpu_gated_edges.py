@@ -44,3 +44,23 @@ def test_norm_eps(io, kind, eps, T, C, n):
     grads = binding.rms_norm_bwd(s.cuda(), w.cuda(), dy.cuda(), z=_cuda(z), ds=_cuda(res), group_size=n, eps=eps)
     for k, v in grads.items():
         R.close(v, *want[k], {"dweight": f32, "dresidual": f32}.get(k, io), k)
+
+
+# ---- the weight's gradient of many rows -------------------------------------
+
+@pytest.mark.parametrize("T,C,n,gate", [(200001, 512, 1, False), (100003, 1024, 4, True), (70001, 2048, 64, False)])
+def test_norm_weight_gradient_of_many_rows(T, C, n, gate):
+    """Terms of one sign whose fp32 sum, one after another, rounds the same way
+    each time: 1 + 0.45 2^-11 loses its fraction as long as the sum is between
+    2^12 and 2^13."""
+    log(f"[norm rows] {T}x{C} groups of {n} gate {gate}")
+    g = torch.Generator().manual_seed(C)
+    cols = sorted(set(range(2 * n)) | set(range(C - n, C)))
+    x = 1 + torch.rand(T, n, generator=g).repeat(1, C // n)
+    w, dy = 1 + 0.3 * _randn(g, C), torch.full((T, C), 1 + 0.45 * 2.0 ** -11)
+    z = 1 + torch.rand(T, 1, generator=g).expand(T, C) if gate else None
+    want = R.norm_bwd(x[:, cols], w[cols], dy[:, cols], None if z is None else z[:, cols], None, n)["dweight"]
+    got = binding.rms_norm_bwd(x.cuda(), w.cuda(), dy.cuda(), z=_cuda(z), group_size=n)["dweight"]
+    R.close(got[cols], *want, f32, "dweight")
+    again = binding.rms_norm_bwd(x.cuda(), w.cuda(), dy.cuda(), z=_cuda(z), group_size=n)["dweight"]
+    assert torch.equal(got, again)
