@@ -793,7 +793,9 @@ typedef struct gated_scan_varlen_args {
  *
  * with h starting at the sequence's cached state (or zero) and its last value
  * stored there; an empty sequence leaves its entry as it is.  The state is
- * fp32.  Where A[c] > 0 the weight sqrt(1 - a^2) is taken as 0.  `out` must not
+ * fp32.  Where A[c] > 0 the weight sqrt(1 - a^2) is taken as 0, and a state other
+ * than 0 may be infinite up to 128 tokens before its own value is (a tile's decay
+ * is formed before the state is known).  `out` must not
  * overlap an input.  Values that are not finite stay in their sequence and
  * channel and reach no earlier token.  Results are bit-for-bit repeatable. */
 int gated_scan_varlen_fwd(const gated_scan_varlen_args_t *args, void *hip_stream);

@@ -204,8 +204,10 @@ __device__ __forceinline__ int64_t sequence_of(const GatedParams &p, int64_t t) 
 constexpr uint32_t kNothing = 0xffffffffu;
 constexpr float kFresh = -1.0f;   // P of tokens with a sequence's start among them: nothing that entered is left
 
-// (h -> P h + H) behind (h -> p h + v)
-__device__ __forceinline__ float through(float P, float H, float h) { return P < 0.0f ? H : fmaf(P, h, H); }
+// (h -> P h + H) of a state.  Of no state nothing is left, though P be inf, as it
+// is over a tile where A > 0: token by token that stays 0.
+__device__ __forceinline__ float through(float P, float H, float h) { return P < 0.0f || h == 0.0f ? H : fmaf(P, h, H); }
+// P of tokens behind others
 __device__ __forceinline__ float joined(float first, float then) { return then < 0.0f || first < 0.0f ? kFresh : first * then; }
 
 __device__ __forceinline__ void publish(unsigned long long *at, float P, float H) {

@@ -64,3 +64,34 @@ def test_norm_weight_gradient_of_many_rows(T, C, n, gate):
     R.close(got[cols], *want, f32, "dweight")
     again = binding.rms_norm_bwd(x.cuda(), w.cuda(), dy.cuda(), z=_cuda(z), group_size=n)["dweight"]
     assert torch.equal(got, again)
+
+
+# ---- channels that grow -----------------------------------------------------
+
+@pytest.mark.parametrize("io", [f32, bf])
+@pytest.mark.parametrize("T,C", [(700, 72), (4200, 1030)])
+def test_a_growing_channel_of_nothing_stays_nothing(io, T, C):
+    """A > 0: an input weighs nothing, so from no state all of it is 0, though the
+    decay of a tile's tokens overflows; and the others are what they are."""
+    log(f"[gated growing] {io} {T}x{C}")
+    g = torch.Generator().manual_seed(T)
+    t = dict(x=_randn(g, T, C, dtype=io), r=_randn(g, T, C, dtype=io), i=_randn(g, T, C, dtype=io),
+             A=-(0.05 + 3 * torch.rand(C, generator=g)))
+    t["A"][::3] = 2.0
+    rest = [c for c in range(C) if c % 3][:40]
+    cu = [0, 5, T - 9, T]
+    dout = _randn(g, T, C, dtype=io)
+    dout[30:] = 0
+    args = [t[k].cuda() for k in ("x", "r", "i", "A")]
+    kept, state = torch.empty(-(-T // 64), C, device="cuda"), torch.zeros(3, C, device="cuda")
+    out = binding.gated_scan_varlen_fwd(*args, _ints(cu), state=state, cache_seqlens=_ints([1] * 3), checkpoints=kept)
+    assert not out[:, ::3].any() and not state[:, ::3].any() and not kept[:, ::3].any()
+    grads = binding.gated_scan_varlen_bwd(*args, _ints(cu), dout.cuda(), kept)
+    for k, v in grads.items():
+        assert not v[..., ::3].any(), k
+    few = {k: v[..., rest] for k, v in t.items()}
+    ref = R.scan(few, cu)
+    R.close(out[:, rest], ref["after"], ref["err"], io, "out")
+    want = R.scan_bwd(few, cu, dout[:, rest])
+    for k, v in grads.items():
+        R.close(v[..., rest], *want[k], io if k in ("dx", "dr", "di") else f32, k)
