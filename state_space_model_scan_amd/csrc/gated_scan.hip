@@ -508,6 +508,8 @@ __global__ void __launch_bounds__(64 * Sh::W, Sh::Fill) gated_fwd_kernel(const G
 // Of an element's values the gradient needs after the waves have met: a, and
 //   e = m iota     (dx = G e, di = dx x (1 - iota); the input's part of the state is e x)
 //   u = a iota / m (q = G rho a (h_{t-1} - u x), dr = A (1 - rho) q)
+//   1 - iota, and rho with 1 - rho in one register (in two they did not fit: 202 us
+//   for 16384 x 2560 instead of 164; as differences they would lose their bits: 162)
 template <int IO, int NV, typename Sh>
 __global__ void __launch_bounds__(64 * Sh::W, Sh::Fill) gated_bwd_kernel(const GatedParams p) {
   constexpr int T = Sh::T, W = Sh::W, S = 64 * NV;
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(64 * Sh::W, Sh::Fill) gated_bwd_kernel(const G
 #pragma unroll
     for (int q = 0; q < kHeld; ++q) asm("" : "+v"(xh[q]), "+v"(gh[q]));
   };
-  float a[T][NV], e[T][NV], u[T][NV], rho[T][NV], iota[T][NV];
+  float a[T][NV], e[T][NV], u[T][NV], gate[T][NV], shut_i[T][NV];
 #pragma unroll
   for (int q = 0; q < T; ++q) {
 #pragma unroll
@@ -569,8 +571,10 @@ __global__ void __launch_bounds__(64 * Sh::W, Sh::Fill) gated_bwd_kernel(const G
       a[q][n] = g.a;
       e[q][n] = g.m2 * inv_m * g.iota;
       u[q][n] = g.a * inv_m * g.iota;
-      rho[q][n] = g.rho;
-      iota[q][n] = g.iota;
+      gate[q][n] = fold_gate(g.w_r, g.rho);
+      shut_i[q][n] = shut(g.w_i, g.iota);
+      // (formed here: put off, what they are formed from took the registers, 171 us for 16384 x 2560 instead of 164)
+      asm("" : "+v"(a[q][n]), "+v"(e[q][n]), "+v"(u[q][n]), "+v"(gate[q][n]), "+v"(shut_i[q][n]));
     }
     if constexpr (kPairs) {
       if (q & 1) {
@@ -667,10 +671,12 @@ __global__ void __launch_bounds__(64 * Sh::W, Sh::Fill) gated_bwd_kernel(const G
         if (!kInside && (marks.last >> q & 1)) come[n] = at_edge[kInside ? 0 : q][n];
         const float x = held(xh, q, n), adj = held(gh, q, n) + come[n];
         come[n] = a[q][n] * adj;
-        const float w = come[n] * rho[q][n] * u[q][n];
+        float rho, shut_r;
+        unfold_gate(gate[q][n], rho, shut_r);
+        const float w = come[n] * rho * u[q][n];
         dx[n] = adj * e[q][n];
-        dr[n] = fmaf(-ch[n].A, rho[q][n], ch[n].A) * w;
-        di[n] = dx[n] * fmaf(-iota[q][n], x, x);
+        dr[n] = ch[n].A * shut_r * w;
+        di[n] = dx[n] * shut_i[q][n] * x;
         if (!live) dx[n] = dr[n] = di[n] = 0.0f;
         sum[0][n] += live ? w : 0.0f;
         sum[1][n] += dr[n];

@@ -15,11 +15,26 @@ __device__ __forceinline__ Channel channel_of(float A, float r_bias, float i_bia
   return {A, A * kLog2e, A < 0.0f ? A : 0.0f, -r_bias * kLog2e, -i_bias * kLog2e};
 }
 
-// sigma(v + bias), off = -bias log2 e
-__device__ __forceinline__ float sigmoid_off(float v, float off) { return fast_rcp(1.0f + fast_exp2(fmaf(v, -kLog2e, off))); }
+// exp(-(v + bias)), off = -bias log2 e, of which sigma(v + bias) = 1 / (1 + w)
+__device__ __forceinline__ float gate_exp(float v, float off) { return fast_exp2(fmaf(v, -kLog2e, off)); }
+// 1 - sigma = w sigma: as a difference it would be off by sigma's last bit, and at
+// v = 12, where it is 6e-6, keep six bits.  (Clamped in the product's own
+// instruction; inf 0 of a gate whose sigma is 0 becomes 0.)
+__device__ __forceinline__ float shut(float w, float sigma) { return fminf(fmaxf(w * sigma, 0.0f), 1.0f); }
+
+// sigma and 1 - sigma in a register: the smaller one, with a minus where it is
+// sigma itself.
+__device__ __forceinline__ float fold_gate(float w, float sigma) { return w < 1.0f ? w * sigma : -sigma; }
+__device__ __forceinline__ void unfold_gate(float v, float &sigma, float &shut) {
+  const float less = fabsf(v), more = 1.0f - less;
+  const bool is = __float_as_int(v) < 0;
+  sigma = is ? less : more;
+  shut = is ? more : less;
+}
 
 struct Gates {
-  float rho, iota;   // sigma of the two gates
+  float w_r, w_i;    // exp(-v) of the two gates
+  float rho, iota;   // sigma of them
   float a;           // exp(A rho)
   float m2;          // 1 - a^2, 0 where A >= 0
 };
@@ -30,8 +45,10 @@ struct Gates {
 // is as exact (its two roundings, 6e-8 of 1, against 0.39 and more).
 __device__ __forceinline__ Gates gates_of(float r, float i, const Channel &c) {
   Gates g;
-  g.rho = sigmoid_off(r, c.r_off);
-  g.iota = sigmoid_off(i, c.i_off);
+  g.w_r = gate_exp(r, c.r_off);
+  g.w_i = gate_exp(i, c.i_off);
+  g.rho = fast_rcp(1.0f + g.w_r);
+  g.iota = fast_rcp(1.0f + g.w_i);
   g.a = fast_exp2(c.A_log2e * g.rho);
   const float y = c.A_kept * g.rho, y2 = y * y;
   const float s = fmaf(y2, fmaf(y2, -1.0f / 60.0f, -1.0f / 3.0f), -2.0f);

@@ -95,3 +95,46 @@ def test_a_growing_channel_of_nothing_stays_nothing(io, T, C):
     want = R.scan_bwd(few, cu, dout[:, rest])
     for k, v in grads.items():
         R.close(v[..., rest], *want[k], io if k in ("dx", "dr", "di") else f32, k)
+
+
+# ---- gates far open and far closed ------------------------------------------
+
+@pytest.mark.parametrize("io,T,C", [(f32, 1, 40), (f32, 130, 256), (f32, 1700, 200), (f32, 3200, 4096), (bf, 3200, 4096),
+                                    (f16, 3200, 4096), (bf, 500, 72)])
+def test_gradients_of_open_gates(io, T, C):
+    """dr and di carry 1 - sigma of a gate, to a relative bound: with
+    w = exp(-v), sigma = 1 / (1 + w) and 1 - sigma = w sigma, w is off by
+    (3 |v| + 2) u, sigma by (3 |v| + 5) u, the product by one rounding.  Sequences
+    of a single token, so that every element stands by itself."""
+    log(f"[gated open gates] {io} {T}x{C}")
+    g = torch.Generator().manual_seed(T + C)
+
+    def far():
+        v = 8 + 12 * torch.rand(T, C, generator=g)
+        return torch.where(torch.rand(T, C, generator=g) < 0.8, v, -v).to(io)
+
+    t = dict(x=_randn(g, T, C, dtype=io), r=far(), i=far(), A=-(0.05 + 3 * torch.rand(C, generator=g)),
+             r_bias=_randn(g, C, scale=0.25), i_bias=_randn(g, C, scale=0.25))
+    dout = _randn(g, T, C, dtype=io)
+    args, kw = [t[k].cuda() for k in ("x", "r", "i", "A")], {k: t[k].cuda() for k in ("r_bias", "i_bias")}
+    cu = _ints(list(range(T + 1)))
+    kept = torch.zeros(-(-T // 64), C, device="cuda")
+    got = binding.gated_scan_varlen_bwd(*args, cu, dout.cuda(), kept, **kw)
+    cols = sorted(set(range(min(C, 40))) | set(range(C - 8, C)))
+    few = {k: v[..., cols] for k, v in t.items()}
+    flat = {k: v.reshape(1, -1) if v.dim() == 2 else v.repeat(T) for k, v in few.items()}
+    ref = R.scan_bwd(flat, [0, 1], dout[:, cols].reshape(1, -1))
+    A, x = flat["A"].double(), flat["x"].double()
+
+    def open_error(v, bias):   # of 1 - sigma, relative
+        return R.U * (6 * (v.double() + bias.double()).abs() + 8)
+
+    (q, e_q), (dx, e_dx) = ref["dA"], ref["dx"]
+    for name, gate, e_rest in (("dr", "r", A.abs() * e_q), ("di", "i", e_dx * x.abs())):
+        v = flat[gate].double() + flat[gate + "_bias"].double()
+        closed = torch.sigmoid(-v)
+        want = (A * q if name == "dr" else dx * x) * closed
+        err = e_rest * closed + want.abs() * (open_error(flat[gate], flat[gate + "_bias"]) + 4 * R.U)
+        want, err = want.view(T, -1), err.view(T, -1)
+        R.close(got[name][:, cols], want, err, io, name)
+        R.close(got[name + "_bias"][cols], want.sum(0), err.sum(0) + 130 * R.U * want.abs().sum(0), f32, name + "_bias")
