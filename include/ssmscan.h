@@ -910,7 +910,7 @@ typedef struct rms_norm_bwd_args {
   void *dresidual; int64_t dresidual_stride;    /* (rows, cols) x_dtype: dx before its rounding to io, or NULL */
   void *dz; int64_t dz_stride;                  /* (rows, cols) io, required iff z */
   float *dweight;                               /* (cols) fp32 */
-  void *workspace; size_t workspace_bytes;      /* rms_norm_bwd_workspace_size */
+  void *workspace; size_t workspace_bytes;      /* rms_norm_bwd_workspace_size; aligned to 4 bytes */
 } rms_norm_bwd_args_t;
 
 /* Gradients of rms_norm_fwd.  With rstd = 1 / sqrt(mean(v^2) + eps), hat = v rstd

@@ -464,6 +464,7 @@ extern "C" int rms_norm_bwd(const rms_norm_bwd_args_t *a, void *stream_ptr) {
   const int st = rms_norm_bwd_workspace_size(a, &need);
   if (st != SSM_OK) return st;
   if (need && (!a->workspace || a->workspace_bytes < need)) return SSM_ERR_WORKSPACE;
+  if (need && reinterpret_cast<uintptr_t>(a->workspace) % alignof(float) != 0) return SSM_ERR_UNSUPPORTED;
   const BwdPlan b = bwd_plan(a);
   NormParams p{};
   p.x = a->x; p.xs = a->x_stride;
