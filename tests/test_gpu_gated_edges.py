@@ -138,3 +138,106 @@ def test_gradients_of_open_gates(io, T, C):
         want, err = want.view(T, -1), err.view(T, -1)
         R.close(got[name][:, cols], want, err, io, name)
         R.close(got[name + "_bias"][cols], want.sum(0), err.sum(0) + 130 * R.U * want.abs().sum(0), f32, name + "_bias")
+
+
+# ---- the kernels of large 16-bit calls --------------------------------------
+
+# (T, C, nseq): two channels a lane in the forward and 16 tokens a lane in the gradient, with fewer and with more
+# sequences than a wave has lanes; large workgroups of few strips; odd widths
+LARGE = [(4200, 3200, 150), (4200, 3200, 5), (4200, 1030, 5), (3100, 4097, 3), (1700, 200, 3), (130, 1000, 2)]
+
+
+@pytest.mark.parametrize("io", [f16, bf])
+@pytest.mark.parametrize("T,C,nseq", LARGE)
+def test_large_16_bit_calls(io, T, C, nseq):
+    log(f"[gated large] {io} {T}x{C} in {nseq}")
+    g = torch.Generator().manual_seed(T + C + nseq)
+    t = dict(x=_randn(g, T, C, dtype=io), r=_randn(g, T, C, dtype=io), i=_randn(g, T, C, dtype=io),
+             A=-(0.05 + 3 * torch.rand(C, generator=g)), r_bias=_randn(g, C, scale=0.5), i_bias=_randn(g, C, scale=0.5))
+    cu = [0] + sorted(torch.randint(0, T + 1, (nseq - 1,), generator=g).tolist()) + [T]
+    dout, state, dfin = _randn(g, T, C, dtype=io), _randn(g, nseq, C), _randn(g, nseq, C)
+    slots = torch.randperm(nseq, generator=g).tolist()
+    args, kw = [t[k].cuda() for k in ("x", "r", "i", "A")], {k: t[k].cuda() for k in ("r_bias", "i_bias")}
+    kept, dstate = torch.empty(-(-T // 64), C, device="cuda"), state.cuda()
+    out = binding.gated_scan_varlen_fwd(*args, _ints(cu), state=dstate, cache_seqlens=_ints([1] * nseq), slots=_ints(slots),
+                                        checkpoints=kept, **kw)
+    got = binding.gated_scan_varlen_bwd(*args, _ints(cu), dout.cuda(), kept, initial_states=state[slots].cuda(),
+                                        dfinal_states=dfin.cuda(), want_dinitial_states=True, **kw)
+    # channels are independent: some of every strip's
+    cols = sorted(set(range(0, C, 61)) | set(range(min(C, 4))) | set(range(C - 4, C)))
+    few = {k: v[..., cols] for k, v in t.items()}
+    ref, err, after, e_after = R.scan_cached(few, cu, state[:, cols], [1] * nseq, slots)
+    R.close(out[:, cols], ref, err, io, "out")
+    R.close(dstate[:, cols], after, e_after, f32, "cache")
+    want = R.scan_bwd(few, cu, dout[:, cols], state[slots][:, cols], dfin[:, cols])
+    for k, v in got.items():
+        R.close(v[..., cols], *want[k], io if k in ("dx", "dr", "di") else f32, k)
+
+
+# ---- far rows ---------------------------------------------------------------
+
+def test_rows_far_apart():
+    """Token and row strides of 2^24 elements, the largest that the scans take, in
+    every operator that reads or writes such rows."""
+    log("[gated far rows]")
+    C, T, far = 64, 140, 1 << 24
+    g = torch.Generator().manual_seed(2)
+    room = torch.empty((T - 1) * far + 4 * C, dtype=bf, device="cuda")   # 4.7 GB
+
+    def view(k):
+        return room.as_strided((T, C), (far, 1), k * C)
+
+    x, r, i, dout = (_randn(g, T, C, dtype=bf).cuda() for _ in range(4))
+    A, cu, w = -torch.rand(C, generator=g).cuda(), _ints([0, 70, T]), _randn(g, C).cuda()
+    kept = torch.empty(-(-T // 64), C, device="cuda")
+    out = binding.gated_scan_varlen_fwd(x, r, i, A, cu, checkpoints=kept)
+    want = binding.gated_scan_varlen_bwd(x, r, i, A, cu, dout, kept)
+    for k, v in enumerate((x, r, i, dout)):
+        view(k).copy_(v)
+    got = binding.gated_scan_varlen_bwd(view(0), view(1), view(2), A, cu, view(3), kept)
+    for k in want:
+        assert torch.equal(want[k], got[k]), k
+    got = binding.gated_scan_varlen_bwd(x, r, i, A, cu, dout, kept, dx=view(0), dr=view(1), di=view(2))
+    for k in want:
+        assert torch.equal(want[k], got[k]), f"{k} into far rows"
+    # the norm's gradient, and its 8 bits
+    want = binding.rms_norm_bwd(x, w, dout, z=r)
+    for k, v in enumerate((x, dout, r)):
+        view(k).copy_(v)
+    got = binding.rms_norm_bwd(view(0), w, view(1), z=view(2), dx=view(3))
+    for k in want:
+        assert torch.equal(want[k], got[k]), f"norm's {k}"
+    got = binding.rms_norm_bwd(x, w, dout, z=r, dz=view(3))
+    assert torch.equal(want["dz"], got["dz"])
+    codes, scales = binding.rms_norm_quant_fwd(x, w, z=r)
+    bytes_ = room.view(torch.float8_e4m3fn).as_strided((T, C), (2 * far, 1), 0)
+    far_codes, far_scales = binding.rms_norm_quant_fwd(x, w, z=r, codes=bytes_)
+    assert torch.equal(codes.view(torch.uint8), far_codes.contiguous().view(torch.uint8)) and torch.equal(scales, far_scales)
+    # the step on rows far apart
+    state = torch.ones(T, C, device="cuda")
+    want = binding.gated_scan_update(x, r, i, A, state.clone(), None)
+    view(0).copy_(x)
+    assert torch.equal(want, binding.gated_scan_update(view(0), r, i, A, state.clone(), None, out=view(1)))
+    del room
+    # fp32, whose last token of a wave is 15 2^26 bytes from its first
+    room = torch.empty((T // 2 - 1) * far + C, device="cuda").as_strided((T // 2, C), (far, 1))
+    x, r, i, cu = x.float()[:T // 2], r.float()[:T // 2], i.float()[:T // 2], _ints([0, 3, T // 2])
+    want = binding.gated_scan_varlen_fwd(x, r, i, A, cu)
+    room.copy_(x)
+    assert torch.equal(want, binding.gated_scan_varlen_fwd(room, r, i, A, cu))
+    assert torch.equal(want, binding.gated_scan_varlen_fwd(x, r, i, A, cu, out=room))
+
+
+def test_step_on_a_far_entry():
+    """A cache entry whose byte offset passes 2^33, in the step."""
+    log("[gated far entry]")
+    C = 64
+    g = torch.Generator().manual_seed(3)
+    x, r, i = (_randn(g, 2, C, dtype=bf).cuda() for _ in range(3))
+    A, entries = -torch.rand(C, generator=g).cuda(), (1 << 31) // C + 3
+    state = torch.empty(entries, C, device="cuda")   # 8.6 GB
+    state[-1] = 0.5
+    near = torch.full((1, C), 0.5, device="cuda")
+    want = binding.gated_scan_update(x, r, i, A, near, _ints([1, 1]), slots=_ints([0, -1]))
+    got = binding.gated_scan_update(x, r, i, A, state, _ints([1, 1]), slots=_ints([entries - 1, -1]))
+    assert torch.equal(want, got) and torch.equal(state[-1], near[0])
