@@ -220,7 +220,9 @@ __device__ __forceinline__ unsigned long long look(const unsigned long long *at)
 }
 __device__ __forceinline__ bool there(unsigned long long v) { return static_cast<uint32_t>(v) != kNothing; }
 
-// The tile of this workgroup: in the order of the tickets, strip by strip.
+// The tile of this workgroup: in the order of the tickets, strip by strip.  (There
+// are as many tickets as tiles, unless another call draws from the same workspace
+// at the same time, which it must not: a ticket beyond the tiles then does nothing.)
 __device__ __forceinline__ int draw_ticket(const GatedParams &p) {
   if (!p.ticket) return blockIdx.x;
   __shared__ int drawn;
@@ -383,6 +385,7 @@ __global__ void __launch_bounds__(64 * Sh::W, Sh::Fill) gated_fwd_kernel(const G
   const int32_t edge = edges_of(p);
   const int drawn = draw_ticket(p);
   const int k = drawn / p.strips;
+  if (k >= p.tiles) return;
   const int strip = (drawn - k * p.strips) * 64 * NV, c = strip + lane * NV;   // (channels fit 24 bits, as strides do)
   const int64_t t0 = static_cast<int64_t>(k) * Sh::Tile + wave * T;
   const bool on = c < p.channels;
@@ -519,6 +522,7 @@ __global__ void __launch_bounds__(64 * Sh::W, Sh::Fill) gated_bwd_kernel(const G
   const int32_t edge = edges_of(p);
   const int drawn = draw_ticket(p);
   const int back = drawn / p.strips, k = p.tiles - 1 - back;   // the last tile first
+  if (k < 0) return;
   const int strip = (drawn - back * p.strips) * S, c = strip + lane * NV;
   const int64_t t0 = static_cast<int64_t>(k) * Sh::Tile + wave * T;
   const bool on = c < p.channels;
