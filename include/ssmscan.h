@@ -757,8 +757,12 @@ int conv1d_ssd_update_validate(const conv1d_ssd_update_args_t *args);
  * and cache_seqlens as above, except that tokens before cu_seqlens[0] and from
  * cu_seqlens[nseq] on (a padded batch) belong to no sequence: their outputs are
  * left as they were, and their gradients are 0.
- * The scans' workspaces are aligned to 16 bytes
- * (SSM_ERR_UNSUPPORTED), and serve one call at a time.
+ * The scans' workspaces are aligned to 16 bytes (SSM_ERR_UNSUPPORTED), and
+ * serve one call at a time.  A scan's workgroups wait there for what workgroups
+ * of the same call that started before them leave.  The wait is bounded, by some
+ * 10^6 polls: a call that comes to its end, as where another one writes to its
+ * workspace meanwhile, has returned SSM_OK, and the states, outputs and gradients
+ * from there on are NaN.
  * ------------------------------------------------------------------------- */
 
 #define GATED_CHUNK 64   /* packed tokens from one kept state to the next */
@@ -792,12 +796,16 @@ typedef struct gated_scan_varlen_args {
  *     out[t,c] = h
  *
  * with h starting at the sequence's cached state (or zero) and its last value
- * stored there; an empty sequence leaves its entry as it is.  The state is
- * fp32.  Where A[c] > 0 the weight sqrt(1 - a^2) is taken as 0, and a state other
- * than 0 may be infinite up to 128 tokens before its own value is (a tile's decay
- * is formed before the state is known).  `out` must not
- * overlap an input.  Values that are not finite stay in their sequence and
- * channel and reach no earlier token.  Results are bit-for-bit repeatable. */
+ * stored there; an empty sequence leaves its entry as it is.  Every token's input
+ * has the weight sqrt(1 - a^2), a sequence's first one too (there are models whose
+ * first token has the weight 1: their weights do not fit this recurrence).  The
+ * state is fp32; sigma and a are formed in fp32, to (3 |v| + 5) 2^-24 of sigma for
+ * a gate's sum v, and a sigma below 2^-126 counts as 0.  Where A[c] > 0 the weight
+ * sqrt(1 - a^2) is taken as 0, and a state other than 0 may be infinite up to 128
+ * tokens before its own value is (a tile's decay is formed before the state is
+ * known).  `out` must not overlap an input.  Values that are not finite stay in
+ * their sequence and channel and reach no earlier token.  Results are bit-for-bit
+ * repeatable. */
 int gated_scan_varlen_fwd(const gated_scan_varlen_args_t *args, void *hip_stream);
 int gated_scan_varlen_fwd_validate(const gated_scan_varlen_args_t *args);
 int gated_scan_varlen_fwd_workspace_size(const gated_scan_varlen_args_t *args, size_t *bytes);
@@ -830,8 +838,9 @@ typedef struct gated_scan_varlen_bwd_args {
  *   dA  = sum_t q,   dr = A (1 - rho) q,   dr_bias = sum_t dr
  *   dx  = G m iota,  di = G m x iota (1 - iota),   di_bias = sum_t di
  * An empty sequence passes dfinal_states on to dinitial_states.  Gradients must
- * not overlap inputs.  Sums are taken in a fixed order (bit-for-bit repeatable).  Values that are not finite stay
- * in their sequence and channel (apart from the sums over the tokens). */
+ * not overlap inputs.  Sums over the tokens are fp32 over at most 128 of them, then
+ * 64 bits, in a fixed order (bit-for-bit repeatable).  Values that are not finite
+ * stay in their sequence and channel (apart from the sums over the tokens). */
 int gated_scan_varlen_bwd(const gated_scan_varlen_bwd_args_t *args, void *hip_stream);
 int gated_scan_varlen_bwd_validate(const gated_scan_varlen_bwd_args_t *args);
 int gated_scan_varlen_bwd_workspace_size(const gated_scan_varlen_bwd_args_t *args, size_t *bytes);
@@ -887,11 +896,11 @@ typedef struct rms_norm_args {
  *
  * (of what the residual stream holds, so that rms_norm_bwd, which reads it, is
  * the gradient of what was computed).  The squares and their sum are fp32, as the
- * values are: where the sum is more than fp32 holds, y is 0.  y goes to `out`, or in 8 bits to `codes`:
- * y is code * scale, the code rounded to nearest (ties to even) and the scale,
- * one for RMS_SCALE_BLOCK columns of a row, the smallest power of two with which
- * none of them is over 448 (at least 2^-100; NaN where one of them is not
- * finite).  8 bits need one group a row, or a group_size that is a multiple of
+ * values are: where the sum is more than fp32 holds, y is 0; with eps = 0 a group
+ * of zeros gives NaN (0 / 0).  y goes to `out`, or in 8 bits to `codes`: y is
+ * code * scale, the code rounded to nearest (ties to even) and the scale, one for
+ * RMS_SCALE_BLOCK columns of a row, the smallest power of two with which none of
+ * them is over 448 (at least 2^-100; NaN where one of them is not finite).  8 bits need one group a row, or a group_size that is a multiple of
  * RMS_SCALE_BLOCK. */
 int rms_norm_fwd(const rms_norm_args_t *args, void *hip_stream);
 int rms_norm_fwd_validate(const rms_norm_args_t *args);
@@ -918,8 +927,9 @@ typedef struct rms_norm_bwd_args {
  *   dv = rstd (g - hat mean(g hat)),  dweight = sum over rows of dy hat
  *   dx = dv + ds   (the residual's gradient as well),  or with a gate
  *   dx = dv silu(z),  dz = dv x silu'(z)
- * Sums are taken in a fixed order (bit-for-bit repeatable).  Outputs must not
- * overlap inputs.  At most 65535 groups a row. */
+ * dweight's terms are added in fp32 over at most 256 rows, then in 64 bits, in a
+ * fixed order (bit-for-bit repeatable).  Outputs must not overlap inputs.  At most
+ * 65535 groups a row. */
 int rms_norm_bwd(const rms_norm_bwd_args_t *args, void *hip_stream);
 int rms_norm_bwd_validate(const rms_norm_bwd_args_t *args);
 int rms_norm_bwd_workspace_size(const rms_norm_bwd_args_t *args, size_t *bytes);

@@ -22,10 +22,10 @@
 // kept ones, so nothing waits for them.
 //
 // Measured on bf16 (us; bytes over time): 16384 x 2560 forward 78 (4.4 TB/s, a
-// copy makes 5.1), gradient 160 (3.7), 65536 x 2560 forward 255 (5.2); a sequence
-// a thread of every channel took 1973, 2961 and 33887.  What bounds them is HBM in
-// the forward of many tokens, in the gradient memory and the vector units in turn
-// (70 instructions an element, 59% of the time busy), and below some 10^7 elements
+// copy makes 5.1), gradient 163 (3.6), 65536 x 2560 forward 255 to 262 (5.2); a
+// sequence a thread of every channel took 1973, 2961 and 33887.  What bounds them is
+// HBM in the forward of many tokens, in the gradient memory and the vector units in
+// turn (78 instructions an element, 64% of the time busy), and below some 10^7 elements
 // the workgroups' own length: loads, the pairs' way through LDS, stores.  The step of
 // 256 x 5120 takes 5.5 (3.8), that of one request 2.6: latency.
 //
@@ -75,8 +75,6 @@ struct GatedParams {
   int tiles, strips;
 };
 
-// What a lane reads of a token: 32 bits (two 16-bit elements or one of 32), or
-// a single 16-bit element where rows are odd or not aligned.
 // A wave's tokens of a tensor, as a buffer: an address is the buffer's base, a
 // scalar offset (the token's) and a lane's offset (the channels'), which costs a
 // load no vector instruction.  The offsets stay below the buffer's 2^31 bytes, as
@@ -96,7 +94,8 @@ struct Rows {
                                              kBytes, 0x00027000)),
         step(static_cast<uint32_t>(stride) * kSize<IO>) {}
 };
-// Token q's words of a lane.
+// What a lane reads of token q: 32 bits (two 16-bit elements or one of 32), or a
+// single 16-bit element where rows are odd or not aligned.
 template <int IO, int NV>
 __device__ __forceinline__ uint32_t take(const Rows<IO> &r, uint32_t lane, int q) {
   static_assert(IO ? NV <= 2 : NV == 1, "at most 32 bits");
@@ -941,13 +940,14 @@ namespace {
 // a few strips have long chains to wait for, large ones, which have half as many
 // links.  Measured on bf16, BwdMany / BwdLong / BwdSmall (us), with the tiles of 64
 // tokens and the strips of 64 channels:
-//   8000 x 2560 (125 x 40)  88 / 97 / 98        4000 x 512 (63 x 8)  27 / 20 / 27
-//   4000 x 2560 (63 x 40)   56 / 58 / 56        2000 x 512 (32 x 8)  20 / 17 / 17.5
-//   2000 x 2560 (32 x 40)   38 / 36 / 34        1000 x 512 (16 x 8)  17 / 15.7 / 14.3
-//   500 x 2560 (8 x 40)     21 / 16.8 / 17.7    256 x 2560 (4 x 40)  17 / 15.4 / 13.8
-//   128 x 2560 (2 x 40: one tile, nothing to wait for)  16 / 12.1 / 12.6
+//   16384 x 2560 (256 x 40) 162 / 209 / 182     4000 x 512 (63 x 8)  29 / 21 / 28
+//   8000 x 2560 (125 x 40)  94 / 112 / 100      2000 x 512 (32 x 8)  20 / 17.7 / 18.3
+//   4000 x 2560 (63 x 40)   58 / 61 / 57        1000 x 512 (16 x 8)  17 / 16.9 / 15.2
+//   2000 x 2560 (32 x 40)   40 / 38 / 36        256 x 2560 (4 x 40)  17 / 16.2 / 14.5
+//   500 x 2560 (8 x 40)     21 / 17.8 / 18.5
+//   128 x 2560 (2 x 40: one tile, nothing to wait for)  16 / 12.3 / 13.0
 // fp32's inputs take twice the registers, with which BwdMany's 16 tokens do not fit:
-//   8192 x 2560 fp32 175 / 135 / 124
+//   8192 x 2560 fp32 175 / 138 / 125
 enum Cut { kMany, kLong, kSmall };
 Cut bwd_cut(const gated_scan_varlen_args_t &f) {
   const int64_t tiles = parts_of(f.total, GATED_CHUNK), all = tiles * parts_of(f.channels, 64), cus = cu_count_cached();

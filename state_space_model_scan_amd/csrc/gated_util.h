@@ -15,7 +15,9 @@ __device__ __forceinline__ Channel channel_of(float A, float r_bias, float i_bia
   return {A, A * kLog2e, A < 0.0f ? A : 0.0f, -r_bias * kLog2e, -i_bias * kLog2e};
 }
 
-// exp(-(v + bias)), off = -bias log2 e, of which sigma(v + bias) = 1 / (1 + w)
+// exp(-(v + bias)), off = -bias log2 e, of which sigma(v + bias) = 1 / (1 + w).  The
+// exponent is rounded once to a float, so sigma is off by (3 |v| + 5) 2^-24 of it at
+// the most; the sum v + bias in fp32 alone would be off as much as |v| 2^-24 makes.
 __device__ __forceinline__ float gate_exp(float v, float off) { return fast_exp2(fmaf(v, -kLog2e, off)); }
 // 1 - sigma = w sigma: as a difference it would be off by sigma's last bit, and at
 // v = 12, where it is 6e-6, keep six bits.  (Clamped in the product's own
