@@ -241,3 +241,30 @@ def test_step_on_a_far_entry():
     want = binding.gated_scan_update(x, r, i, A, near, _ints([1, 1]), slots=_ints([0, -1]))
     got = binding.gated_scan_update(x, r, i, A, state, _ints([1, 1]), slots=_ints([entries - 1, -1]))
     assert torch.equal(want, got) and torch.equal(state[-1], near[0])
+
+
+# ---- as many sequences as a wave has lanes, and more empty ones than that ----
+
+@pytest.mark.parametrize("C", [1, 40])
+@pytest.mark.parametrize("lens", [(3,) * 62, (1, 2, 0) * 21, (2, 1, 0, 1) * 16, (1,) * 65, (0,) * 100 + (3,) + (0,) * 150 + (70, 1) + (0,) * 90,
+                                  (17,) + (0,) * 200 + (2, 0, 0, 30) * 20 + (0,) * 64], ids=lambda v: str(len(v)))
+def test_counts_of_sequences(lens, C):
+    log(f"[gated counts] {len(lens)} sequences C={C}")
+    g = torch.Generator().manual_seed(len(lens))
+    cu = R.sequences(lens, 2)
+    T, n = cu[-1] + 3, len(lens)
+    t = dict(x=_randn(g, T, C), r=_randn(g, T, C), i=_randn(g, T, C), A=-(0.05 + 3 * torch.rand(C, generator=g)))
+    dout, state, dfin = _randn(g, T, C), _randn(g, n, C), _randn(g, n, C)
+    seen = [k % 3 for k in range(n)]
+    args = [t[k].cuda() for k in ("x", "r", "i", "A")]
+    kept, dstate = torch.empty(-(-T // 64), C, device="cuda"), state.cuda()
+    out = binding.gated_scan_varlen_fwd(*args, _ints(cu), state=dstate, cache_seqlens=_ints(seen), checkpoints=kept)
+    ref, err, after, e_after = R.scan_cached(t, cu, state, seen, list(range(n)))
+    R.close(out[2:-3], ref[2:-3], err[2:-3], f32, "out")
+    R.close(dstate, after, e_after, f32, "cache")
+    h0 = state * (torch.tensor(seen) > 0)[:, None]
+    got = binding.gated_scan_varlen_bwd(*args, _ints(cu), dout.cuda(), kept, initial_states=h0.cuda(), dfinal_states=dfin.cuda(),
+                                        want_dinitial_states=True)
+    want = R.scan_bwd(t, cu, dout, h0, dfin)
+    for k, v in got.items():
+        R.close(v, *want[k], f32, k)
